@@ -18,6 +18,7 @@ STATUS = {0: "GPTQ_OK", 1: "GPTQ_ERR_ARG", 2: "GPTQ_ERR_SHAPE", 3: "GPTQ_ERR_NOM
 
 # name -> (restype, argtypes); the full exported surface of the header.
 _P, _I, _D, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_double, ctypes.c_size_t
+_L, _F = ctypes.c_longlong, ctypes.c_float
 SIGNATURES = {
     "gptq_status_string": (ctypes.c_char_p, [_I]),
     "gptq_fold_workspace_bytes": (_S, [_I]),
@@ -45,6 +46,12 @@ SIGNATURES = {
     "gptq_debias": (_I, [_I, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
     "gptq_gram_workspace_bytes": (_S, [_I]),
     "gptq_gram_add": (_I, [_P, _I, _P, _I, _P, _S, _P]),
+    "gptq_q4tp_linear": (_I, [_I, _P, _L, _I, _P, _P, _P, _I, _I, _P, _I, _P, _L, _P, _L, _P, _P]),
+    "gptq_kv4_write": (_I, [_I, _P, _L, _I, _I, _I, _P, _P, _L, _L, _L, _L, _P, _I, _P]),
+    "gptq_kv4_read": (_I, [_I, _P, _L, _I, _I, _I, _P, _I, _P, _P, _P]),
+    "gptq_kv4_attention_workspace_bytes": (_S, [_I]),
+    "gptq_kv4_attention": (_I, [_I, _P, _L, _L, _I, _P, _L, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _F, _P, _P,
+                                _S, _P, _P]),
     "gptq_launch_count": (ctypes.c_longlong, []),
     "gptq_kernel_kinds": (_I, []),
     "gptq_kernel_kind_name": (ctypes.c_char_p, [_I]),
@@ -574,3 +581,242 @@ def debias(bits, w, h_packed, codes, rungs, tab, lost, scales, ws=None, want_num
                            _ptr(lost), _ptr(scales), _ptr(nd), _ptr(ws), ws.numel(), _stream(torch, stream))
     _check("gptq_debias", code)
     return nd
+
+
+# ------------------------------------------------------------------ serving
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+_serve_words = {}  # device -> the status word its serving calls set
+
+
+def _serve_word(device):
+    import torch
+
+    w = _serve_words.get(device)
+    if w is None:
+        w = _serve_words[device] = torch.zeros(4, dtype=torch.int32, device=device)
+    return w
+
+
+def serve_check(device=None):
+    """Raises GptqError(TIMEOUT) if a bounded device wait of a serving call on
+    `device` (default: the current one) ran out since the last check.  Reads
+    one word back, so it waits for the device's current stream."""
+    import torch
+
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    w = _serve_words.get(device)
+    if w is not None and int(w[0]) != 0:
+        w.zero_()
+        raise GptqError("serving call", 6)
+
+
+def _dtype16(t, name):
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float16:
+        return 1
+    raise ValueError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+
+
+def _strided(t, name, shape, like):
+    """Raise ValueError unless ``t`` has ``shape``, the dtype and device of
+    ``like``, dense last dimension and other strides of a multiple of 8
+    elements (16 bytes) that do not run backwards."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the call's data on {like.device}")
+    st = t.stride()
+    if t.numel() == 0:
+        return st
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if any(s % 8 and n > 1 for s, n in zip(st[:-1], shape[:-1])):
+        raise ValueError(f"{name} must have strides of a multiple of 8 elements, got {st}")
+    return st
+
+
+def _step(st, shape, i):
+    """Stride i; a dimension of one element may carry any (the library wants a multiple of 8)."""
+    return st[i] if shape[i] > 1 else 0
+
+
+def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, out=None, stream=None):
+    """act(x W^T + bias) + residual with W [rows, n] in q4tp form (nibbles,
+    rungs, tab as quantize_group returns them).  x [tokens, n] bf16 or f16
+    (rows may be strided), bias [rows], residual [tokens, rows] and the result
+    [tokens, rows] of x's dtype.  act: a key of ACTIVATIONS."""
+    import torch
+
+    lib = load()
+    dt = _dtype16(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D [tokens, n], got shape {tuple(x.shape)}")
+    tokens, n = x.shape
+    if n <= 0 or n % 32:
+        raise ValueError(f"x must have a multiple of 32 columns, got {n}")
+    dev = x.device
+    st = _strided(x, "x", x.shape, x)
+    _need(tab, "tab", device=dev)
+    if tab.dim() != 2 or tab.shape[1] != 32:
+        raise ValueError(f"tab must be [rows, 32], got shape {tuple(tab.shape)}")
+    rows = tab.shape[0]
+    _need(nibbles, "nibbles", dtype=torch.uint8, numel=rows * n // 2, device=dev)
+    _need(rungs, "rungs", dtype=torch.uint8, numel=rows * (n // 32), device=dev)
+    if bias is not None:
+        _need(bias, "bias", dtype=x.dtype, numel=rows, device=dev)
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    ldr = 0
+    if residual is not None:
+        ldr = _rows_of(residual, "residual", tokens, rows, x)
+    if out is None:
+        out = torch.empty(tokens, rows, dtype=x.dtype, device=dev)
+    ldy = _rows_of(out, "out", tokens, rows, x)
+    code = lib.gptq_q4tp_linear(dt, _ptr(x), st[0] if tokens > 1 else n, tokens, _ptr(nibbles), _ptr(rungs),
+                                _ptr(tab), rows, n, _ptr(bias), ACTIVATIONS[act], _ptr(residual), ldr, _ptr(out),
+                                ldy, _ptr(_serve_word(dev)), _stream(torch, stream))
+    _check("gptq_q4tp_linear", code)
+    return out
+
+
+def _rows_of(t, name, tokens, rows, like):
+    """Row stride of a [tokens, rows] matrix of like's dtype whose rows are dense."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype != like.dtype:
+        raise ValueError(f"{name} must be a {like.dtype} tensor")
+    if t.shape != (tokens, rows):
+        raise ValueError(f"{name} must have shape {(tokens, rows)}, got {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the call's data on {like.device}")
+    st = t.stride()
+    if (rows > 1 and st[1] != 1) or (tokens > 1 and st[0] < rows):
+        raise ValueError(f"{name} must have dense rows that do not overlap, got strides {st}")
+    return st[0] if tokens > 1 else rows
+
+
+def _cache(cache, dim, page_size):
+    """pages, heads of a cache pool after checking it against dim and page_size."""
+    import torch
+
+    _need(cache, "cache", dtype=torch.uint8)
+    if dim not in (64, 128, 256):
+        raise ValueError(f"dim must be 64, 128 or 256, got {dim}")
+    if page_size <= 0 or page_size > 4096 or page_size % 16:
+        raise ValueError(f"page_size must be a multiple of 16 up to 4096, got {page_size}")
+    if cache.dim() != 3 or cache.shape[2] != page_size * dim * 5 // 4:
+        raise ValueError(f"cache must be [pages, heads, {page_size * dim * 5 // 4}] for dim {dim} and pages of "
+                         f"{page_size} tokens, got shape {tuple(cache.shape)}")
+    return cache.shape[0], cache.shape[1]
+
+
+def kv4_cache(pages, heads, dim, page_size, device="cuda"):
+    """An empty 4-bit key/value pool: u8 [pages, heads, page_size * dim * 5 / 4]."""
+    import torch
+
+    cache = torch.zeros(pages, heads, page_size * dim * 5 // 4, dtype=torch.uint8, device=device)
+    _cache(cache, dim, page_size)
+    return cache
+
+
+def kv4_write(cache, k, v, slots, page_size, stream=None):
+    """Quantise k, v [tokens, heads, dim] (bf16 or f16, strided views allowed)
+    into the cache at slots [tokens] i64 (page * page_size + place; negative:
+    left out).  Returns the cache."""
+    import torch
+
+    lib = load()
+    dt = _dtype16(k, "k")
+    if k.dim() != 3:
+        raise ValueError(f"k must be 3-D [tokens, heads, dim], got shape {tuple(k.shape)}")
+    tokens, heads, dim = k.shape
+    pages, ch = _cache(cache, dim, page_size)
+    if heads != ch:
+        raise ValueError(f"k has {heads} heads, the cache {ch}")
+    if cache.device != k.device:
+        raise ValueError(f"cache is on {cache.device}, the call's data on {k.device}")
+    ks, vs = _strided(k, "k", k.shape, k), _strided(v, "v", k.shape, k)
+    _need(slots, "slots", dtype=torch.int64, numel=tokens, device=k.device)
+    code = lib.gptq_kv4_write(dt, _ptr(cache), pages, heads, dim, page_size, _ptr(k), _ptr(v),
+                              _step(ks, k.shape, 0), _step(ks, k.shape, 1), _step(vs, k.shape, 0),
+                              _step(vs, k.shape, 1), _ptr(slots), tokens, _stream(torch, stream))
+    _check("gptq_kv4_write", code)
+    return cache
+
+
+def kv4_read(cache, slots, dim, page_size, dtype, stream=None):
+    """The values k, v [tokens, heads, dim] that the cache holds at slots
+    [tokens] i64, in the dtype it was written in (zeros outside the pool)."""
+    import torch
+
+    lib = load()
+    pages, heads = _cache(cache, dim, page_size)
+    tokens = slots.numel() if isinstance(slots, torch.Tensor) else 0
+    _need(slots, "slots", dtype=torch.int64, device=cache.device)
+    k = torch.empty(tokens, heads, dim, dtype=dtype, device=cache.device)
+    v = torch.empty_like(k)
+    code = lib.gptq_kv4_read(_dtype16(k, "dtype"), _ptr(cache), pages, heads, dim, page_size, _ptr(slots), tokens,
+                             _ptr(k), _ptr(v), _stream(torch, stream))
+    _check("gptq_kv4_read", code)
+    return k, v
+
+
+def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, scale=None, out=None, ws=None,
+                  stream=None):
+    """Causal attention of q [tokens, query heads, dim] (bf16 or f16) over the
+    4-bit cache: softmax(scale q k^T) v per sequence and head, scale default
+    1 / sqrt(dim).  table [seqs, pages per sequence] i32, kv_lens [seqs] i32
+    (the queries' own keys included).  The queries of sequence b are its last
+    tokens, rows q_starts[b] .. q_starts[b + 1] - 1 of q (i32 [seqs + 1], at
+    most max_q each); without q_starts, one a sequence."""
+    import torch
+
+    lib = load()
+    dt = _dtype16(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q must be 3-D [tokens, heads, dim], got shape {tuple(q.shape)}")
+    tq, hq, dim = q.shape
+    dev = q.device
+    pages, heads = _cache(cache, dim, page_size)
+    if heads <= 0 or hq % heads or hq == 0:
+        raise ValueError(f"q has {hq} heads, not a multiple of the cache's {heads}")
+    if cache.device != dev:
+        raise ValueError(f"cache is on {cache.device}, the call's data on {dev}")
+    qs = _strided(q, "q", q.shape, q)
+    _need(table, "table", dtype=torch.int32, device=dev)
+    if table.dim() != 2 or table.shape[1] == 0:
+        raise ValueError(f"table must be 2-D [seqs, pages], got shape {tuple(table.shape)}")
+    seqs = table.shape[0]
+    _need(kv_lens, "kv_lens", dtype=torch.int32, numel=seqs, device=dev)
+    if q_starts is not None:
+        _need(q_starts, "q_starts", dtype=torch.int32, numel=seqs + 1, device=dev)
+    elif tq != seqs or max_q != 1:
+        raise ValueError(f"without q_starts there is one query a sequence: q has {tq} tokens for {seqs} sequences")
+    if max_q <= 0:
+        raise ValueError(f"max_q must be positive, got {max_q}")
+    if out is None:
+        out = torch.empty(tq, hq, dim, dtype=q.dtype, device=dev)
+    else:
+        _need(out, "out", dtype=q.dtype, numel=q.numel(), device=dev)
+    if ws is None:
+        ws = workspace(lib.gptq_kv4_attention_workspace_bytes(dim), dev)
+    _ws(ws, dev)
+    scale = dim ** -0.5 if scale is None else float(scale)
+    code = lib.gptq_kv4_attention(dt, _ptr(q), _step(qs, q.shape, 0), _step(qs, q.shape, 1), tq, _ptr(cache), pages,
+                                  heads, hq // heads, dim, page_size, _ptr(table), table.shape[1], _ptr(kv_lens),
+                                  _ptr(q_starts), seqs, int(max_q), scale, _ptr(out), _ptr(ws), ws.numel(),
+                                  _ptr(_serve_word(dev)), _stream(torch, stream))
+    _check("gptq_kv4_attention", code)
+    return out

@@ -1,7 +1,7 @@
 // C ABI entry points (include/gptq_fold.h): argument checks, workspace
 // carving and the chaining of fold -> ladder -> sweep.  No device memory is
 // allocated here; every buffer is the caller's.
-#include "common.cuh"
+#include "serve.cuh"
 
 #include <math.h>
 #include <string.h>
@@ -62,6 +62,14 @@ gptq_status sweep_q2_run(float* W, int rows, int n, const float* U, const float*
 size_t gram_ws_bytes(int n);
 gptq_status gram_run(float* Hp, int n, const float* X, int T, void* ws, size_t ws_bytes,
                      cudaStream_t s);
+gptq_status q4tp_linear_run(int dtype, const LinearArgs& a, cudaStream_t s);
+gptq_status kv4_write_run(int dtype, uint8_t* cache, long long pages, int heads, int dim, int page_size,
+                          const void* k, const void* v, long long kt, long long kh, long long vt, long long vh,
+                          const long long* slots, int tokens, cudaStream_t s);
+gptq_status kv4_read_run(int dtype, const uint8_t* cache, long long pages, int heads, int dim, int page_size,
+                         const long long* slots, int tokens, void* k, void* v, cudaStream_t s);
+size_t kv4_attention_ws_bytes(int dim);
+gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s);
 }  // namespace gq
 
 using namespace gq;
@@ -72,6 +80,14 @@ bool bad_rows(int rows) { return rows <= 0 || rows > GPTQ_MAX_ROWS; }
 bool ptr_ok(const void* p) { return p != nullptr && aligned16(p); }
 bool opt_ok(const void* p) { return p == nullptr || aligned16(p); }
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
+bool bad_dtype(int d) { return d != GPTQ_BF16 && d != GPTQ_F16; }
+bool bad_tokens(int t) { return t < 0 || t > GPTQ_MAX_TOKENS; }
+// The cache's geometry (gptq_kv4_*).
+bool bad_cache(long long pages, int heads, int dim, int page_size) {
+  return pages <= 0 || pages > (1ll << 31) || heads <= 0 || heads > 1024 || (dim != 64 && dim != 128 && dim != 256) ||
+         page_size <= 0 || page_size > 4096 || page_size % 16 != 0;
+}
+bool bad_stride(long long s) { return s < 0 || s % 8 != 0; }
 }  // namespace
 
 namespace {
@@ -641,6 +657,68 @@ gptq_status gptq_quantize_group_act_order(const float* H_packed, int n, double l
   GQ_TRY(copy_ladder_run(W, rows, n, hraw, wz, tb, ls, s));
   GQ_TRY(static_rungs_run(wz, rows, n, tb, ls, rungs, scales, s));
   return sweep_act_run(wz, rows, n, u, perm, tb, rungs, nibbles, rest, rest_bytes, s);
+}
+
+gptq_status gptq_q4tp_linear(int dtype, const void* X, long long ldx, int tokens, const uint8_t* nibbles,
+                             const uint8_t* rungs, const float* tab, int rows, int n, const void* bias,
+                             int act, const void* residual, long long ldr, void* Y, long long ldy,
+                             uint32_t* status, void* stream) {
+  if (bad_n(n) || bad_rows(rows) || n % GPTQ_GROUP != 0 || bad_tokens(tokens)) return GPTQ_ERR_SHAPE;
+  if (bad_dtype(dtype) || act < GPTQ_ACT_NONE || act > GPTQ_ACT_SILU) return GPTQ_ERR_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (ldx < n || bad_stride(ldx) || ldy < rows || (residual != nullptr && ldr < rows)) return GPTQ_ERR_SHAPE;
+  if (!ptr_ok(X) || !ptr_ok(nibbles) || !ptr_ok(rungs) || !ptr_ok(tab) || !opt_ok(bias) || !opt_ok(residual) ||
+      !ptr_ok(Y))
+    return GPTQ_ERR_ARG;
+  const LinearArgs a{X, ldx, tokens, nibbles, rungs, tab, rows, n, bias, act, residual, ldr, Y, ldy, status};
+  return q4tp_linear_run(dtype, a, as_stream(stream));
+}
+
+gptq_status gptq_kv4_write(int dtype, uint8_t* cache, long long pages, int heads, int dim, int page_size,
+                           const void* K, const void* V, long long kt, long long kh, long long vt,
+                           long long vh, const long long* slots, int tokens, void* stream) {
+  if (bad_cache(pages, heads, dim, page_size) || bad_tokens(tokens)) return GPTQ_ERR_SHAPE;
+  if (bad_dtype(dtype)) return GPTQ_ERR_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (bad_stride(kt) || bad_stride(kh) || bad_stride(vt) || bad_stride(vh)) return GPTQ_ERR_SHAPE;
+  if (!ptr_ok(cache) || !ptr_ok(K) || !ptr_ok(V) || slots == nullptr) return GPTQ_ERR_ARG;
+  return kv4_write_run(dtype, cache, pages, heads, dim, page_size, K, V, kt, kh, vt, vh, slots, tokens,
+                       as_stream(stream));
+}
+
+gptq_status gptq_kv4_read(int dtype, const uint8_t* cache, long long pages, int heads, int dim, int page_size,
+                          const long long* slots, int tokens, void* K, void* V, void* stream) {
+  if (bad_cache(pages, heads, dim, page_size) || bad_tokens(tokens)) return GPTQ_ERR_SHAPE;
+  if (bad_dtype(dtype)) return GPTQ_ERR_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (!ptr_ok(cache) || !ptr_ok(K) || !ptr_ok(V) || slots == nullptr) return GPTQ_ERR_ARG;
+  return kv4_read_run(dtype, cache, pages, heads, dim, page_size, slots, tokens, K, V, as_stream(stream));
+}
+
+size_t gptq_kv4_attention_workspace_bytes(int dim) {
+  return (dim == 64 || dim == 128 || dim == 256) ? kv4_attention_ws_bytes(dim) : 0;
+}
+
+gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
+                               const uint8_t* cache, long long pages, int heads, int group, int dim,
+                               int page_size, const int* table, int table_stride, const int* kv_lens,
+                               const int* q_starts, int seqs, int max_q, float scale, void* out, void* ws,
+                               size_t ws_bytes, uint32_t* status, void* stream) {
+  if (bad_cache(pages, heads, dim, page_size) || bad_tokens(tq) || group <= 0 || group > 1024 || seqs < 0 ||
+      seqs > GPTQ_MAX_TOKENS || table_stride <= 0 || (long long)table_stride * page_size > (1ll << 30) ||
+      max_q <= 0 || max_q > GPTQ_MAX_TOKENS)
+    return GPTQ_ERR_SHAPE;
+  if (bad_dtype(dtype) || !isfinite(scale)) return GPTQ_ERR_ARG;
+  if (q_starts == nullptr && (tq != seqs || max_q != 1)) return GPTQ_ERR_SHAPE;
+  if (tq == 0 || seqs == 0) return GPTQ_OK;
+  if (bad_stride(q_ts) || bad_stride(q_hs)) return GPTQ_ERR_SHAPE;
+  if (!ptr_ok(Q) || !ptr_ok(cache) || table == nullptr || kv_lens == nullptr || !ptr_ok(out) || !ptr_ok(ws))
+    return GPTQ_ERR_ARG;
+  if (ws_bytes < kv4_attention_ws_bytes(dim)) return GPTQ_ERR_NOMEM;
+  const AttnArgs a{Q,     q_ts,         q_hs,    tq,       cache, pages, heads, group, page_size,
+                   table, table_stride, kv_lens, q_starts, seqs,  max_q, scale * 1.4426950408889634f,
+                   out,   static_cast<float*>(ws), status};
+  return kv4_attention_run(dtype, dim, a, as_stream(stream));
 }
 
 }  // extern "C"

@@ -332,6 +332,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   // A function-local static: initialised once, thread-safe.
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -345,6 +347,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   }();
   return fn;
 }
+
+namespace {
 
 using CtxGetCurrentFn = CUresult (*)(CUcontext*);
 

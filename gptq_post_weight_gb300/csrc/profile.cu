@@ -27,7 +27,8 @@ std::atomic<int> g_no_loads{0};
 const char* kNames[K_NKINDS] = {"diag", "build", "potrf", "trsm", "fold_gemm", "ladder",
                                 "sweep_block", "prep_ut", "sweep_gemm", "group", "copy",
                                 "gram_prep", "gram_gemm", "place", "debias",
-                                "debias_gemm", "fold_strip"};
+                                "debias_gemm", "fold_strip", "q4_linear", "kv4_write", "kv4_read",
+                                "kv4_attention", "kv4_join"};
 
 }  // namespace
 

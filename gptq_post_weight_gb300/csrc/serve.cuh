@@ -1,0 +1,143 @@
+// Shared by the serving kernels (q4tp product, 4-bit key/value cache): the
+// two 16-bit element types and the 4-bit codes as numbers of those types.
+#pragma once
+
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "tcgen05.cuh"
+
+namespace gq {
+
+// kMagic16 with a code c in the top four mantissa bits is the number 16 + c;
+// shift(i) puts nibble i of each 16-bit half there.
+template <class T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+  using T2 = __nv_bfloat162;
+  static constexpr uint32_t kMagic16 = 0x41804180u, kMask16 = 0x00780078u;
+  static constexpr int kPos = 3;  // lowest of the top four mantissa bits
+  static __device__ __forceinline__ T2 make2(float a, float b) { return __floats2bfloat162_rn(a, b); }
+  static __device__ __forceinline__ float2 to2(T2 v) { return __bfloat1622float2(v); }
+  static __device__ __forceinline__ __nv_bfloat16 from(float a) { return __float2bfloat16_rn(a); }
+  static __device__ __forceinline__ float to(__nv_bfloat16 a) { return __bfloat162float(a); }
+};
+template <>
+struct Elem<__half> {
+  using T2 = __half2;
+  static constexpr uint32_t kMagic16 = 0x4C004C00u, kMask16 = 0x03C003C0u;
+  static constexpr int kPos = 6;
+  static __device__ __forceinline__ T2 make2(float a, float b) { return __floats2half2_rn(a, b); }
+  static __device__ __forceinline__ float2 to2(T2 v) { return __half22float2(v); }
+  static __device__ __forceinline__ __half from(float a) { return __float2half_rn(a); }
+  static __device__ __forceinline__ float to(__half a) { return __half2float(a); }
+};
+
+template <class T2>
+__device__ __forceinline__ uint32_t bits2(T2 v) {
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+template <class T2>
+__device__ __forceinline__ T2 from_bits2(uint32_t v) {
+  return *reinterpret_cast<T2*>(&v);
+}
+
+// (16 + nibble i of the low half, 16 + nibble i of the high half) as T2.
+template <class T>
+__device__ __forceinline__ typename Elem<T>::T2 code16(uint32_t w, int i) {
+  constexpr int kPos = Elem<T>::kPos;
+  const int sh = 4 * i - kPos;
+  const uint32_t x = sh >= 0 ? (w >> sh) : (w << -sh);
+  return from_bits2<typename Elem<T>::T2>((x & Elem<T>::kMask16) | Elem<T>::kMagic16);
+}
+
+// 16 x 8 x 16 product with f32 accumulation.
+template <class T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Eight elements (x0..x7) as the pairs (x0,x4), (x1,x5), (x2,x6), (x3,x7):
+// the order in which one shift and mask takes the nibbles out of a word.
+__device__ __forceinline__ uint4 pair_order(uint4 v) {
+  uint4 o;
+  o.x = __byte_perm(v.x, v.z, 0x5410);
+  o.y = __byte_perm(v.x, v.z, 0x7632);
+  o.z = __byte_perm(v.y, v.w, 0x5410);
+  o.w = __byte_perm(v.y, v.w, 0x7632);
+  return o;
+}
+
+// One untiled copy global -> shared that completes on `bar` (16-byte aligned
+// addresses, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Arguments of the q4tp product (checked by the C entry; strides in elements).
+struct LinearArgs {
+  const void* x;
+  long long ldx;
+  int tokens;
+  const uint8_t* nibbles;
+  const uint8_t* rungs;
+  const float* tab;
+  int rows, n;
+  const void* bias;
+  int act;
+  const void* residual;
+  long long ldr;
+  void* y;
+  long long ldy;
+  unsigned* status;
+};
+
+// Arguments of the attention over the cache.
+struct AttnArgs {
+  const void* q;
+  long long q_ts, q_hs;  // elements between query tokens and between heads
+  int tq;
+  const uint8_t* cache;
+  long long pages;
+  int heads, group, page_size;
+  const int* table;
+  int table_stride;
+  const int* kv_lens;
+  const int* q_starts;  // null: one query a sequence
+  int seqs, max_q;
+  float scale_log2;  // scale * log2(e)
+  void* out;         // [tq][heads * group][dim]
+  float* part;       // workspace
+  unsigned* status;
+};
+
+// The driver's tensor-map encoder (null when it cannot be had).
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+
+// Geometry of the cache: blocks of 16 tokens, each
+//   K codes [16][dim / 2], K (scale, offset) [16][dim / 32], V codes, V (scale, offset).
+constexpr int KV_BLOCK = 16;
+__host__ __device__ constexpr int kv_block_bytes(int dim) { return 20 * dim; }
+__host__ __device__ constexpr int kv_param_off(int dim) { return 8 * dim; }
+__host__ __device__ constexpr int kv_value_off(int dim) { return 10 * dim; }
+
+}  // namespace gq

@@ -385,6 +385,115 @@ gptq_status gptq_gram_add(float* H_packed, int n, const float* X, int T, void* w
                           size_t ws_bytes, void* stream);
 
 /*
+ * Serving with the quantized weights: the product with q4tp weights, and a
+ * key/value cache in 4 bits with the attention that reads it.  (The pages
+ * stop at the packed weights; these entries have no counterpart there.)
+ *
+ * Element type T of activations, keys, values and outputs: GPTQ_BF16 or
+ * GPTQ_F16.  Calls return once the work is enqueued and read nothing back.
+ * Matrices of T may have a row stride (in elements): bases 16-byte aligned,
+ * strides a multiple of 8.  `status` (device u32, may be NULL) gets bit 1
+ * set if a bounded device wait ran out; the output is then not valid.
+ */
+typedef enum { GPTQ_BF16 = 0, GPTQ_F16 = 1 } gptq_dtype;
+typedef enum {
+  GPTQ_ACT_NONE = 0,
+  GPTQ_ACT_RELU = 1,
+  GPTQ_ACT_GELU = 2,      /* v (1 + erf(v / sqrt 2)) / 2 */
+  GPTQ_ACT_GELU_TANH = 3, /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+  GPTQ_ACT_SILU = 4       /* v / (1 + exp(-v)) */
+} gptq_act;
+
+/* Largest token count of one gptq_q4tp_linear / cache call. */
+#define GPTQ_MAX_TOKENS (1 << 20)
+
+/*
+ * gptq_q4tp_linear -- Y = act(X W^T + bias) + residual with W in q4tp form,
+ *   W[r][c] = (nibble(r, c) - 8) * tab[r][rung(r, c / 32)]:
+ * the nibble plane, rungs and ladder of gptq_q4tp_sweep /
+ * gptq_quantize_group (and gptq_debias).  f32 sums, one rounding to T at the
+ * end.  Up to 16 tokens no weight is rounded either; above that a weight is
+ * rounded once to T (f16: relative to the row's largest rung).  A rung
+ * above 31 counts as scale 0.
+ *
+ *   X        in  T tokens*n, row stride ldx.   0 <= tokens <= GPTQ_MAX_TOKENS.
+ *   nibbles  in  u8 rows*n/2;  rungs in u8 rows*n/32;  tab in f32 rows*32.
+ *   bias     in  T rows (may be NULL);  residual in T tokens*rows, row stride
+ *            ldr (may be NULL; may be Y itself).
+ *   Y        out T tokens*rows, row stride ldy.
+ *   n % 32 == 0; ldx a multiple of 8; ldr, ldy >= rows.
+ */
+gptq_status gptq_q4tp_linear(int dtype, const void* X, long long ldx, int tokens,
+                             const uint8_t* nibbles, const uint8_t* rungs, const float* tab,
+                             int rows, int n, const void* bias, int act, const void* residual,
+                             long long ldr, void* Y, long long ldy, uint32_t* status, void* stream);
+
+/*
+ * The cache: a pool of `pages` pages of page_size tokens (a multiple of 16,
+ * at most 4096) for `heads` key heads of `dim` channels (64, 128 or 256), u8
+ * [pages][heads][page_size * dim * 5 / 4].  A page holds blocks of 16
+ * tokens; a block is K codes [16][dim/2] (channel j of a token in byte j/2,
+ * low nibble for even j), K (s, z) pairs of T [16][dim/32][2], then the same
+ * for V.  With lo, hi the extremes of a group of 32 channels of one token
+ * (f32 arithmetic, one rounding per operation):
+ *   s = T((hi - lo) * (1/15)),  z = T(lo - 16 s),
+ *   code = clamp(rint((x - z) * (1/s)), 16, 31) - 16   (1/0 taken as 0),
+ *   value = T(z + s * (16 + code)), rounded once.
+ * A group with a NaN or an infinity, or whose s or z is not finite in T,
+ * reads back as NaN (f16: no group within +-20000).
+ * Slot = page * page_size + place in the page.
+ */
+
+/*
+ * gptq_kv4_write -- quantise tokens into the cache.  K, V in T
+ * [tokens][heads][dim] with strides in elements (kt, vt between tokens, kh,
+ * vh between heads; multiples of 8), slots in i64 [tokens].  A slot outside
+ * the pool (a negative one: padding) is left out; one slot twice in a call
+ * keeps either token.
+ */
+gptq_status gptq_kv4_write(int dtype, uint8_t* cache, long long pages, int heads, int dim,
+                           int page_size, const void* K, const void* V, long long kt, long long kh,
+                           long long vt, long long vh, const long long* slots, int tokens,
+                           void* stream);
+
+/*
+ * gptq_kv4_read -- the values of the slots: K, V out T [tokens][heads][dim]
+ * (dense).  A slot outside the pool reads zeros.
+ */
+gptq_status gptq_kv4_read(int dtype, const uint8_t* cache, long long pages, int heads, int dim,
+                          int page_size, const long long* slots, int tokens, void* K, void* V,
+                          void* stream);
+
+/*
+ * gptq_kv4_attention -- softmax(scale Q K^T) V over the cache, causal: the
+ * queries of sequence b are its last tokens, query i of nq sees the keys
+ * 0 .. kv_lens[b] - nq + i (none: its output is zero).  Query head h reads
+ * key head h / group.  Scores, softmax and sums in f32; the cache's values
+ * and the probabilities enter the products in T.
+ *
+ *   Q        in  T [tq][heads*group][dim], strides q_ts, q_hs (multiples of 8).
+ *   table    in  i32 [seqs][table_stride]: page of tokens 0.., page_size.., ...
+ *            of each sequence.  An entry outside the pool reads page 0.
+ *   kv_lens  in  i32 [seqs], the queries' own keys included; at most
+ *            table_stride * page_size counts.
+ *   q_starts in  i32 [seqs + 1]: the queries of b are rows q_starts[b] ..
+ *            q_starts[b + 1] - 1 of Q (at most max_q count); NULL: one query a
+ *            sequence (tq == seqs).
+ *   max_q    host bound on the queries of one sequence.
+ *   out      out T [tq][heads*group][dim] (dense).
+ *   ws       >= gptq_kv4_attention_workspace_bytes(dim).
+ * The values of one sequence's keys must be finite where any of its queries
+ * sees them; what the pages hold past kv_lens is never used.
+ */
+size_t gptq_kv4_attention_workspace_bytes(int dim);
+gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
+                               const uint8_t* cache, long long pages, int heads, int group, int dim,
+                               int page_size, const int* table, int table_stride,
+                               const int* kv_lens, const int* q_starts, int seqs, int max_q,
+                               float scale, void* out, void* ws, size_t ws_bytes, uint32_t* status,
+                               void* stream);
+
+/*
  * Tracing: launch accounting and per-kernel timing.  Every kernel launch of
  * the library is counted; between gptq_profile_start and gptq_profile_stop
  * each launch is also bracketed by a pair of CUDA events recorded on the
