@@ -210,8 +210,7 @@ __global__ void __launch_bounds__(ATHREADS)
 
     for (int i = 0; i < nb; ++i) {
       const int slot = (cnt + i) % ST;
-      const bool ok = mbar_wait(&full[warp * ST + slot], (uint32_t)((cnt + i) / ST) & 1u, abort, wc.ns);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!wait_bar_warp(&full[warp * ST + slot], (uint32_t)((cnt + i) / ST) & 1u, abort, wc.ns)) break;
       const uint8_t* blk = ring + slot * BB;
       const int tok0 = (j0 + warp + AW * i) * 16;
 

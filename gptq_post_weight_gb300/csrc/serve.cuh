@@ -84,6 +84,49 @@ __device__ __forceinline__ uint4 pair_order(uint4 v) {
   return o;
 }
 
+// mbar_wait for waits that are short and many: the clock is looked at once in
+// 64 tries, since reading it costs more than such a wait.  CTA scope also on
+// barriers that a cluster's peer arrives on: what those announce is in shared
+// or tensor memory (an acquire at cluster scope took some 1000 cycles each).
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0u) {
+      if (*abort) return false;
+      const uint64_t now = globaltimer();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// The same for waits that are long: sleeps between the tries, so that the
+// polling does not take issue slots and ALU cycles from the warps at work
+// (eight warps polling took a third of a SM's ALU cycles).
+__device__ __forceinline__ bool wait_bar_idle(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  uint64_t t0 = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    __nanosleep(64);
+    if (*abort) return false;
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// The same for a whole warp.
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, limit));
+}
+
 // One untiled copy global -> shared that completes on `bar` (16-byte aligned
 // addresses, a multiple of 16 bytes).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {

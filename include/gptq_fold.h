@@ -412,7 +412,7 @@ typedef enum {
  *   W[r][c] = (nibble(r, c) - 8) * tab[r][rung(r, c / 32)]:
  * the nibble plane, rungs and ladder of gptq_q4tp_sweep /
  * gptq_quantize_group (and gptq_debias).  f32 sums, one rounding to T at the
- * end.  Up to 16 tokens no weight is rounded either; above that a weight is
+ * end.  Up to 8 tokens no weight is rounded either; above that a weight is
  * rounded once to T (f16: relative to the row's largest rung).  A rung
  * above 31 counts as scale 0.
  *

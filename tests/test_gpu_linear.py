@@ -55,7 +55,7 @@ def check(y, p, dtype, act):
     mag = ax @ np.abs(w).T
     u = 2.0 ** (1 - serve.TYPES[dtype][0])
     err = 34 * 143 * 2.0 ** -22 * (ax @ np.abs(sc).T) + (n / 32) * 2.0 ** -23 * mag
-    if tokens > 16:
+    if tokens > 8:
         err = err + 0.5 * u * mag
     if p["bias"] is not None:
         err = err + 2.0 ** -23 * np.abs(p["bias"])
