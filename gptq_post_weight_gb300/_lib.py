@@ -584,31 +584,60 @@ def debias(bits, w, h_packed, codes, rungs, tab, lost, scales, ws=None, want_num
 
 
 # ------------------------------------------------------------------ serving
+#
+# These calls are short, so the host's part of them counts: each wrapper first
+# looks at its arguments in one expression of cheap attributes, and only where
+# that does not hold goes through the checks that name the argument.
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
-_serve_words = {}  # device -> the status word its serving calls set
+_serve = {}  # torch, its dtypes and the raw-stream call, once the first wrapper ran
+_serve_words = {}  # device index -> the status word its serving calls set (tensor, address)
+_attention_ws = {}  # dim -> workspace bytes
 
 
-def _serve_word(device):
+def _serving():
     import torch
 
-    w = _serve_words.get(device)
+    _serve.update(torch=torch, empty=torch.empty, f32=torch.float32, u8=torch.uint8, i32=torch.int32, i64=torch.int64,
+                  dtypes={torch.bfloat16: 0, torch.float16: 1},
+                  raw=getattr(torch._C, "_cuda_getCurrentRawStream", None))
+    load()
+    return _serve
+
+
+def _raw_stream(sv, stream, index):
+    """The call's stream as an integer: the given one, or the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    raw = sv["raw"]
+    return raw(index) if raw is not None else sv["torch"].cuda.current_stream(index).cuda_stream
+
+
+def _serve_word(index):
+    w = _serve_words.get(index)
     if w is None:
-        w = _serve_words[device] = torch.zeros(4, dtype=torch.int32, device=device)
-    return w
+        import torch
+
+        t = torch.zeros(4, dtype=torch.int32, device=torch.device("cuda", index))
+        torch.cuda.current_stream(index).synchronize()  # before a call on any stream may set it
+        w = _serve_words[index] = (t, t.data_ptr())
+    return w[1]
 
 
 def serve_check(device=None):
     """Raises GptqError(TIMEOUT) if a bounded device wait of a serving call on
-    `device` (default: the current one) ran out since the last check.  Reads
-    one word back, so it waits for the device's current stream."""
+    `device` (default: the current one) ran out since the last check.  Waits
+    for the device and reads one word back."""
     import torch
 
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    w = _serve_words.get(device)
-    if w is not None and int(w[0]) != 0:
-        w.zero_()
-        raise GptqError("serving call", 6)
+    device = torch.device("cuda") if device is None else torch.device(device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    w = _serve_words.get(index)
+    if w is not None:
+        torch.cuda.synchronize(index)
+        if int(w[0][0]) != 0:
+            w[0].zero_()
+            raise GptqError("serving call", 6)
 
 
 def _dtype16(t, name):
@@ -616,17 +645,14 @@ def _dtype16(t, name):
 
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch tensor")
-    if t.dtype == torch.bfloat16:
-        return 0
-    if t.dtype == torch.float16:
-        return 1
-    raise ValueError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
 
 
 def _strided(t, name, shape, like):
     """Raise ValueError unless ``t`` has ``shape``, the dtype and device of
     ``like``, dense last dimension and other strides of a multiple of 8
-    elements (16 bytes) that do not run backwards."""
+    elements (16 bytes)."""
     import torch
 
     if not isinstance(t, torch.Tensor):
@@ -639,60 +665,16 @@ def _strided(t, name, shape, like):
         raise ValueError(f"{name} is on {t.device}, the call's data on {like.device}")
     st = t.stride()
     if t.numel() == 0:
-        return st
+        return
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     if any(s % 8 and n > 1 for s, n in zip(st[:-1], shape[:-1])):
         raise ValueError(f"{name} must have strides of a multiple of 8 elements, got {st}")
-    return st
-
-
-def _step(st, shape, i):
-    """Stride i; a dimension of one element may carry any (the library wants a multiple of 8)."""
-    return st[i] if shape[i] > 1 else 0
-
-
-def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, out=None, stream=None):
-    """act(x W^T + bias) + residual with W [rows, n] in q4tp form (nibbles,
-    rungs, tab as quantize_group returns them).  x [tokens, n] bf16 or f16
-    (rows may be strided), bias [rows], residual [tokens, rows] and the result
-    [tokens, rows] of x's dtype.  act: a key of ACTIVATIONS."""
-    import torch
-
-    lib = load()
-    dt = _dtype16(x, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x must be 2-D [tokens, n], got shape {tuple(x.shape)}")
-    tokens, n = x.shape
-    if n <= 0 or n % 32:
-        raise ValueError(f"x must have a multiple of 32 columns, got {n}")
-    dev = x.device
-    st = _strided(x, "x", x.shape, x)
-    _need(tab, "tab", device=dev)
-    if tab.dim() != 2 or tab.shape[1] != 32:
-        raise ValueError(f"tab must be [rows, 32], got shape {tuple(tab.shape)}")
-    rows = tab.shape[0]
-    _need(nibbles, "nibbles", dtype=torch.uint8, numel=rows * n // 2, device=dev)
-    _need(rungs, "rungs", dtype=torch.uint8, numel=rows * (n // 32), device=dev)
-    if bias is not None:
-        _need(bias, "bias", dtype=x.dtype, numel=rows, device=dev)
-    if act not in ACTIVATIONS:
-        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
-    ldr = 0
-    if residual is not None:
-        ldr = _rows_of(residual, "residual", tokens, rows, x)
-    if out is None:
-        out = torch.empty(tokens, rows, dtype=x.dtype, device=dev)
-    ldy = _rows_of(out, "out", tokens, rows, x)
-    code = lib.gptq_q4tp_linear(dt, _ptr(x), st[0] if tokens > 1 else n, tokens, _ptr(nibbles), _ptr(rungs),
-                                _ptr(tab), rows, n, _ptr(bias), ACTIVATIONS[act], _ptr(residual), ldr, _ptr(out),
-                                ldy, _ptr(_serve_word(dev)), _stream(torch, stream))
-    _check("gptq_q4tp_linear", code)
-    return out
 
 
 def _rows_of(t, name, tokens, rows, like):
-    """Row stride of a [tokens, rows] matrix of like's dtype whose rows are dense."""
+    """Raise ValueError unless ``t`` is a [tokens, rows] matrix of like's dtype
+    whose rows are dense and do not overlap."""
     import torch
 
     if not isinstance(t, torch.Tensor) or t.dtype != like.dtype:
@@ -704,7 +686,87 @@ def _rows_of(t, name, tokens, rows, like):
     st = t.stride()
     if (rows > 1 and st[1] != 1) or (tokens > 1 and st[0] < rows):
         raise ValueError(f"{name} must have dense rows that do not overlap, got strides {st}")
-    return st[0] if tokens > 1 else rows
+
+
+def _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out):
+    import torch
+
+    _dtype16(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D [tokens, n], got shape {tuple(x.shape)}")
+    tokens, n = x.shape
+    if n <= 0 or n % 32:
+        raise ValueError(f"x must have a multiple of 32 columns, got {n}")
+    dev = x.device
+    _strided(x, "x", x.shape, x)
+    _need(tab, "tab", device=dev)
+    if tab.dim() != 2 or tab.shape[1] != 32:
+        raise ValueError(f"tab must be [rows, 32], got shape {tuple(tab.shape)}")
+    rows = tab.shape[0]
+    _need(nibbles, "nibbles", dtype=torch.uint8, numel=rows * n // 2, device=dev)
+    _need(rungs, "rungs", dtype=torch.uint8, numel=rows * (n // 32), device=dev)
+    if bias is not None:
+        _need(bias, "bias", dtype=x.dtype, numel=rows, device=dev)
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    if residual is not None:
+        _rows_of(residual, "residual", tokens, rows, x)
+    if out is not None:
+        _rows_of(out, "out", tokens, rows, x)
+    _ptr(x)
+
+
+def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, out=None, stream=None):
+    """act(x W^T + bias) + residual with W [rows, n] in q4tp form (nibbles,
+    rungs, tab as quantize_group returns them).  x [tokens, n] bf16 or f16
+    (rows may be strided), bias [rows], residual [tokens, rows] and the result
+    [tokens, rows] of x's dtype.  act: a key of ACTIVATIONS."""
+    sv = _serve or _serving()
+    try:
+        xt, xs, u8 = x.dtype, x.shape, sv["u8"]
+        dt, dev = sv["dtypes"][xt], x.get_device()
+        tokens, n = xs
+        rows = tab.shape[0]
+        code = ACTIVATIONS[act]
+        st = x.stride()
+        ldx = st[0] if tokens > 1 else n
+        fine = (dev >= 0 and n > 0 and n % 32 == 0 and st[1] == 1 and ldx % 8 == 0 and ldx >= n
+                and tab.dtype is sv["f32"] and tab.shape == (rows, 32) and tab.is_contiguous()
+                and tab.get_device() == dev
+                and nibbles.dtype is u8 and nibbles.numel() == rows * n // 2 and nibbles.is_contiguous()
+                and nibbles.get_device() == dev
+                and rungs.dtype is u8 and rungs.numel() == rows * n // 32 and rungs.is_contiguous()
+                and rungs.get_device() == dev)
+        bp = rp = None
+        ldr = 0
+        if fine and bias is not None:
+            fine = bias.dtype is xt and bias.numel() == rows and bias.is_contiguous() and bias.get_device() == dev
+            bp = bias.data_ptr()
+        if fine and residual is not None:
+            st = residual.stride()
+            ldr = st[0] if tokens > 1 else rows
+            fine = (residual.dtype is xt and residual.shape == (tokens, rows) and (rows == 1 or st[1] == 1)
+                    and ldr >= rows and residual.get_device() == dev)
+            rp = residual.data_ptr()
+        ldy = rows
+        if fine and out is not None:
+            st = out.stride()
+            ldy = st[0] if tokens > 1 else rows
+            fine = (out.dtype is xt and out.shape == (tokens, rows) and (rows == 1 or st[1] == 1) and ldy >= rows
+                    and out.get_device() == dev)
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out)
+        ldx = max(n, -(-n // 8) * 8)  # a dense x without elements, or of one row
+    if out is None:
+        out = sv["empty"]((tokens, rows), dtype=xt, device=x.device)
+    code = _lib.gptq_q4tp_linear(dt, x.data_ptr(), ldx, tokens, nibbles.data_ptr(), rungs.data_ptr(), tab.data_ptr(),
+                                 rows, n, bp, code, rp, ldr, out.data_ptr(), ldy,
+                                 (_serve_words.get(dev) or (0, _serve_word(dev)))[1], _raw_stream(sv, stream, dev))
+    if code:
+        raise GptqError("gptq_q4tp_linear", code)
+    return out
 
 
 def _cache(cache, dim, page_size):
@@ -731,14 +793,10 @@ def kv4_cache(pages, heads, dim, page_size, device="cuda"):
     return cache
 
 
-def kv4_write(cache, k, v, slots, page_size, stream=None):
-    """Quantise k, v [tokens, heads, dim] (bf16 or f16, strided views allowed)
-    into the cache at slots [tokens] i64 (page * page_size + place; negative:
-    left out).  Returns the cache."""
+def _refuse_write(cache, k, v, slots, page_size):
     import torch
 
-    lib = load()
-    dt = _dtype16(k, "k")
+    _dtype16(k, "k")
     if k.dim() != 3:
         raise ValueError(f"k must be 3-D [tokens, heads, dim], got shape {tuple(k.shape)}")
     tokens, heads, dim = k.shape
@@ -747,44 +805,82 @@ def kv4_write(cache, k, v, slots, page_size, stream=None):
         raise ValueError(f"k has {heads} heads, the cache {ch}")
     if cache.device != k.device:
         raise ValueError(f"cache is on {cache.device}, the call's data on {k.device}")
-    ks, vs = _strided(k, "k", k.shape, k), _strided(v, "v", k.shape, k)
+    _strided(k, "k", k.shape, k)
+    _strided(v, "v", k.shape, k)
     _need(slots, "slots", dtype=torch.int64, numel=tokens, device=k.device)
-    code = lib.gptq_kv4_write(dt, _ptr(cache), pages, heads, dim, page_size, _ptr(k), _ptr(v),
-                              _step(ks, k.shape, 0), _step(ks, k.shape, 1), _step(vs, k.shape, 0),
-                              _step(vs, k.shape, 1), _ptr(slots), tokens, _stream(torch, stream))
-    _check("gptq_kv4_write", code)
+    _ptr(k)
+
+
+def kv4_write(cache, k, v, slots, page_size, stream=None):
+    """Quantise k, v [tokens, heads, dim] (bf16 or f16, strided views allowed)
+    into the cache at slots [tokens] i64 (page * page_size + place; negative:
+    left out).  Returns the cache."""
+    sv = _serve or _serving()
+    try:
+        kt, shape, dev = k.dtype, k.shape, k.get_device()
+        dt = sv["dtypes"][kt]
+        tokens, heads, dim = shape
+        pages = cache.shape[0]
+        kts, khs, k1 = k.stride()
+        vts, vhs, v1 = v.stride()
+        fine = (dev >= 0 and dim in (64, 128, 256) and tokens > 1 and heads > 1 and v.dtype is kt and v.shape == shape
+                and k1 == 1 and v1 == 1 and (kts | khs | vts | vhs) % 8 == 0 and v.get_device() == dev
+                and 0 < page_size <= 4096 and page_size % 16 == 0 and cache.dtype is sv["u8"]
+                and cache.shape == (pages, heads, page_size * dim * 5 // 4) and cache.is_contiguous()
+                and cache.get_device() == dev and slots.dtype is sv["i64"] and slots.numel() == tokens
+                and slots.is_contiguous() and slots.get_device() == dev)
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _refuse_write(cache, k, v, slots, page_size)
+        # A dimension of one element may carry any stride (the library wants a multiple of 8).
+        kts, vts = (kts, vts) if tokens > 1 else (0, 0)
+        khs, vhs = (khs, vhs) if heads > 1 else (0, 0)
+    code = _lib.gptq_kv4_write(dt, cache.data_ptr(), pages, heads, dim, page_size, k.data_ptr(), v.data_ptr(), kts,
+                               khs, vts, vhs, slots.data_ptr(), tokens, _raw_stream(sv, stream, dev))
+    if code:
+        raise GptqError("gptq_kv4_write", code)
     return cache
+
+
+def _refuse_read(cache, slots, dim, page_size, dtype):
+    import torch
+
+    _cache(cache, dim, page_size)
+    _need(slots, "slots", dtype=torch.int64, device=cache.device)
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+    _ptr(cache)
 
 
 def kv4_read(cache, slots, dim, page_size, dtype, stream=None):
     """The values k, v [tokens, heads, dim] that the cache holds at slots
     [tokens] i64, in the dtype it was written in (zeros outside the pool)."""
-    import torch
-
-    lib = load()
-    pages, heads = _cache(cache, dim, page_size)
-    tokens = slots.numel() if isinstance(slots, torch.Tensor) else 0
-    _need(slots, "slots", dtype=torch.int64, device=cache.device)
-    k = torch.empty(tokens, heads, dim, dtype=dtype, device=cache.device)
-    v = torch.empty_like(k)
-    code = lib.gptq_kv4_read(_dtype16(k, "dtype"), _ptr(cache), pages, heads, dim, page_size, _ptr(slots), tokens,
-                             _ptr(k), _ptr(v), _stream(torch, stream))
-    _check("gptq_kv4_read", code)
+    sv = _serve or _serving()
+    try:
+        dt, dev = sv["dtypes"][dtype], cache.get_device()
+        pages, heads, size = cache.shape
+        tokens = slots.numel()
+        fine = (dev >= 0 and dim in (64, 128, 256) and 0 < page_size <= 4096 and page_size % 16 == 0
+                and cache.dtype is sv["u8"] and size == page_size * dim * 5 // 4 and cache.is_contiguous()
+                and slots.dtype is sv["i64"] and slots.is_contiguous() and slots.get_device() == dev)
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _refuse_read(cache, slots, dim, page_size, dtype)
+    k = sv["empty"]((tokens, heads, dim), dtype=dtype, device=cache.device)
+    v = sv["empty"]((tokens, heads, dim), dtype=dtype, device=cache.device)
+    code = _lib.gptq_kv4_read(dt, cache.data_ptr(), pages, heads, dim, page_size, slots.data_ptr(), tokens,
+                              k.data_ptr(), v.data_ptr(), _raw_stream(sv, stream, dev))
+    if code:
+        raise GptqError("gptq_kv4_read", code)
     return k, v
 
 
-def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, scale=None, out=None, ws=None,
-                  stream=None):
-    """Causal attention of q [tokens, query heads, dim] (bf16 or f16) over the
-    4-bit cache: softmax(scale q k^T) v per sequence and head, scale default
-    1 / sqrt(dim).  table [seqs, pages per sequence] i32, kv_lens [seqs] i32
-    (the queries' own keys included).  The queries of sequence b are its last
-    tokens, rows q_starts[b] .. q_starts[b + 1] - 1 of q (i32 [seqs + 1], at
-    most max_q each); without q_starts, one a sequence."""
+def _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, out, ws):
     import torch
 
-    lib = load()
-    dt = _dtype16(q, "q")
+    _dtype16(q, "q")
     if q.dim() != 3:
         raise ValueError(f"q must be 3-D [tokens, heads, dim], got shape {tuple(q.shape)}")
     tq, hq, dim = q.shape
@@ -794,7 +890,7 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
         raise ValueError(f"q has {hq} heads, not a multiple of the cache's {heads}")
     if cache.device != dev:
         raise ValueError(f"cache is on {cache.device}, the call's data on {dev}")
-    qs = _strided(q, "q", q.shape, q)
+    _strided(q, "q", q.shape, q)
     _need(table, "table", dtype=torch.int32, device=dev)
     if table.dim() != 2 or table.shape[1] == 0:
         raise ValueError(f"table must be 2-D [seqs, pages], got shape {tuple(table.shape)}")
@@ -806,17 +902,64 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
         raise ValueError(f"without q_starts there is one query a sequence: q has {tq} tokens for {seqs} sequences")
     if max_q <= 0:
         raise ValueError(f"max_q must be positive, got {max_q}")
-    if out is None:
-        out = torch.empty(tq, hq, dim, dtype=q.dtype, device=dev)
-    else:
+    if out is not None:
         _need(out, "out", dtype=q.dtype, numel=q.numel(), device=dev)
+    if ws is not None:
+        _ws(ws, dev)
+    _ptr(q)
+
+
+def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, scale=None, out=None, ws=None,
+                  stream=None):
+    """Causal attention of q [tokens, query heads, dim] (bf16 or f16) over the
+    4-bit cache: softmax(scale q k^T) v per sequence and head, scale default
+    1 / sqrt(dim).  table [seqs, pages per sequence] i32, kv_lens [seqs] i32
+    (the queries' own keys included).  The queries of sequence b are its last
+    tokens, rows q_starts[b] .. q_starts[b + 1] - 1 of q (i32 [seqs + 1], at
+    most max_q each); without q_starts, one a sequence."""
+    sv = _serve or _serving()
+    try:
+        qt, dev, i32 = q.dtype, q.get_device(), sv["i32"]
+        dt = sv["dtypes"][qt]
+        tq, hq, dim = q.shape
+        pages, heads, size = cache.shape
+        seqs, per = table.shape
+        qts, qhs, q1 = q.stride()
+        fine = (dev >= 0 and dim in (64, 128, 256) and tq > 0 and hq > 1 and hq % heads == 0 and q1 == 1
+                and (qts | qhs) % 8 == 0 and 0 < page_size <= 4096 and page_size % 16 == 0 and max_q > 0
+                and cache.dtype is sv["u8"] and size == page_size * dim * 5 // 4 and cache.is_contiguous()
+                and cache.get_device() == dev and table.dtype is i32 and per > 0 and table.is_contiguous()
+                and table.get_device() == dev and kv_lens.dtype is i32 and kv_lens.numel() == seqs
+                and kv_lens.is_contiguous() and kv_lens.get_device() == dev)
+        sp = None
+        if q_starts is None:
+            fine = fine and tq == seqs and max_q == 1
+        elif fine:
+            fine = (q_starts.dtype is i32 and q_starts.numel() == seqs + 1 and q_starts.is_contiguous()
+                    and q_starts.get_device() == dev)
+            sp = q_starts.data_ptr()
+        if fine and out is not None:
+            fine = (out.dtype is qt and out.numel() == tq * hq * dim and out.is_contiguous()
+                    and out.get_device() == dev)
+        if fine and ws is not None:
+            fine = ws.dtype is sv["u8"] and ws.is_contiguous() and ws.get_device() == dev
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, out, ws)
+        qts, qhs = qts if tq > 1 else 0, qhs if hq > 1 else 0
+    if out is None:
+        out = sv["empty"]((tq, hq, dim), dtype=qt, device=q.device)
     if ws is None:
-        ws = workspace(lib.gptq_kv4_attention_workspace_bytes(dim), dev)
-    _ws(ws, dev)
-    scale = dim ** -0.5 if scale is None else float(scale)
-    code = lib.gptq_kv4_attention(dt, _ptr(q), _step(qs, q.shape, 0), _step(qs, q.shape, 1), tq, _ptr(cache), pages,
-                                  heads, hq // heads, dim, page_size, _ptr(table), table.shape[1], _ptr(kv_lens),
-                                  _ptr(q_starts), seqs, int(max_q), scale, _ptr(out), _ptr(ws), ws.numel(),
-                                  _ptr(_serve_word(dev)), _stream(torch, stream))
-    _check("gptq_kv4_attention", code)
+        need = _attention_ws.get(dim)
+        if need is None:
+            need = _attention_ws[dim] = _lib.gptq_kv4_attention_workspace_bytes(dim)
+        ws = sv["empty"](need, dtype=sv["u8"], device=q.device)
+    code = _lib.gptq_kv4_attention(dt, q.data_ptr(), qts, qhs, tq, cache.data_ptr(), pages, heads, hq // heads, dim,
+                                   page_size, table.data_ptr(), per, kv_lens.data_ptr(), sp, seqs, int(max_q),
+                                   dim ** -0.5 if scale is None else float(scale), out.data_ptr(), ws.data_ptr(),
+                                   ws.numel(), (_serve_words.get(dev) or (0, _serve_word(dev)))[1],
+                                   _raw_stream(sv, stream, dev))
+    if code:
+        raise GptqError("gptq_kv4_attention", code)
     return out
