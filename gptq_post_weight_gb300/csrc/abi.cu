@@ -717,7 +717,7 @@ gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long lo
   if (ws_bytes < kv4_attention_ws_bytes(dim)) return GPTQ_ERR_NOMEM;
   const AttnArgs a{Q,     q_ts,         q_hs,    tq,       cache, pages, heads, group, page_size,
                    table, table_stride, kv_lens, q_starts, seqs,  max_q, scale * 1.4426950408889634f,
-                   out,   static_cast<float*>(ws), status};
+                   out,   static_cast<float*>(ws), dtype == GPTQ_BF16 ? 8u : 64u, status};
   return kv4_attention_run(dtype, dim, a, as_stream(stream));
 }
 

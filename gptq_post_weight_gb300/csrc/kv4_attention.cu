@@ -3,11 +3,11 @@
 // o = softmax(scale q K^T + causal mask) V per query head, in one pass over
 // the keys with a running maximum and sum; K and V become elements of T in
 // registers, one AND/OR and half a fused multiply-add a value, straight into
-// the B fragments of the tensor cores (16 x 8 x 16, f32 sums).
+// the A fragments of the tensor cores (16 x 8 x 16, f32 sums).
 //
 // Bytes bound it (5/8 byte a key or value channel), so the work is cut to
 // keep every SM loading: the (sequence, key head, row block) items and their
-// chunks of 64 tokens form one list, and each CTA takes an equal, contiguous
+// chunks of 128 tokens form one list, and each CTA takes an equal, contiguous
 // share of it.  An item inside one share is finished there; a cut one leaves
 // its running maximum, sum and unnormalised output (f32) in the workspace,
 // and k_kv4_join adds the pieces in the order of the list.  The cut depends
@@ -15,14 +15,20 @@
 //
 // Rows of a block are (query, head of the key head's group) pairs, so that a
 // key is decoded once for every head that shares it.  Each of a CTA's four
-// warps streams its own blocks of 16 tokens through a ring of bulk copies
-// and keeps its own maximum, sum and output; they meet at the item's end.
+// warps streams its own blocks of 16 tokens through a ring of bulk copies,
+// two at a time, and keeps its own maximum, sum and output; they meet at the
+// item's end.
 //
-// Fragments.  Within a block, key column n of the 16 x 8 products stands for
-// token n ^ (n >> 1 & 1) (which spreads the value rows over the banks), and
-// the channel order inside the products is the order in which the nibbles
-// come out: lane t of a quad owns whole words of a token's row, and q is
-// loaded to match.  For the values lane g owns channels g D/8 .. + D/8 - 1.
+// Fragments.  The products are transposed, S^T = K q^T and O^T = V^T P^T:
+// tokens (or value channels) are the 16 rows and the query rows the 8
+// columns, so that a group of up to 8 heads wastes nothing and a thread's
+// sums are half as many as with the query rows as rows of 16.  A tile of P
+// turns from S^T's sums to the B fragment by one movmatrix.  Row r of eight
+// stands for token r ^ (r >> 1 & 1) (which spreads the value rows over the
+// banks), and the channel order inside the products is the order in which
+// the nibbles come out: lane t of a quad owns whole words of a token's row,
+// and q is loaded to match.  For the values lane g owns channels g D/8 ..
+// + D/8 - 1, two a row tile.
 #include "serve.cuh"
 
 namespace gq {
@@ -30,7 +36,8 @@ namespace {
 
 constexpr int AW = 4;            // warps
 constexpr int ATHREADS = 32 * AW;
-constexpr int ACH = 16 * AW;     // tokens per chunk of the work list
+constexpr int ACH = 32 * AW;     // tokens per chunk of the work list
+constexpr int ASHARES = 8;       // resident CTAs a SM at most (sizes the workspace)
 constexpr int ASEQS = 1024;      // sequences per launch at most
 constexpr float kNone = -1e30f;  // running maximum of a row that has seen nothing
 
@@ -111,12 +118,22 @@ __device__ __forceinline__ int word_channel(int t, int w) {
   return D == 64 ? 16 * t + 8 * w : 128 * (w / 4) + 32 * t + 8 * (w % 4);
 }
 
-template <class T, int D, int MT, int ST>
+// The transposed 8 x 8 tile of 16-bit elements.
+__device__ __forceinline__ uint32_t turn8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// NQ: column tiles of eight query rows; ST: pairs of blocks in a warp's ring.
+template <class T, int D, int NQ, int ST>
 __global__ void __launch_bounds__(ATHREADS)
     k_kv4_attention(AttnArgs a, WaitCfg wc) {
   using T2 = typename Elem<T>::T2;
-  constexpr int MR = 16 * MT, NW = D / 32, BB = kv_block_bytes(D);
-  constexpr int DV = D / 8;  // value channels per lane and n-tiles
+  constexpr int MR = 8 * NQ, NW = D / 32, BB = kv_block_bytes(D), PB = 2 * BB;
+  constexpr int DV = D / 8;  // value channels per lane
+  constexpr int OS = D + 4;  // row stride of a warp's output in shared memory
+  static_assert(ST * PB >= MR * OS * 4, "a warp's output goes through its ring");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[AW * ST];
   __shared__ long long pref[ASEQS + 1];
@@ -125,9 +142,9 @@ __global__ void __launch_bounds__(ATHREADS)
   __shared__ int abort_sh;
   volatile int* abort = &abort_sh;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  uint8_t* ring = smem + warp * ST * BB;
-  float* osum = reinterpret_cast<float*>(smem + AW * ST * BB);  // [MR][D + 4]
+  uint8_t* ring = smem + warp * ST * PB;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_kv4_join may set itself up
   if (lane == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(&full[warp * ST + s], 1);
     if (warp == 0) abort_sh = 0;
@@ -140,7 +157,12 @@ __global__ void __launch_bounds__(ATHREADS)
   if (blockIdx.x >= shares) return;
   long long u = W * blockIdx.x / shares;
   const long long uend = W * (blockIdx.x + 1) / shares;
-  int cnt = 0;  // copies this warp has waited for (slot cnt % ST)
+  const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale: -q
+  const float sl = fabsf(a.scale_log2);
+  int slot = 0;  // of the ring: the next copy to wait for
+  uint32_t phase = 0u;
+  const int perm = g ^ ((g >> 1) & 1);                                // token of row g
+  const int ta = 2 * t + (t & 1), tb = 2 * t + 1 - (t & 1);           // tokens of rows 2t, 2t + 1
 
   while (u < uend) {
     // The item of chunk u.
@@ -157,233 +179,296 @@ __global__ void __launch_bounds__(ATHREADS)
     const int c1 = (int)min((long long)nch, c0 + (uend - u));
     const int head = item / nblk, r0 = (item % nblk) * MR;
     const int rows = min(MR, sq.nq * a.group - r0);
+    const int first_pos = sq.len - sq.nq + r0 / a.group;  // last key the block's first row sees
     const int vis = min(sq.len, sq.len - sq.nq + (r0 + rows - 1) / a.group + 1);  // keys the last row sees
     const int tok_end = min(c1 * ACH, vis);
-    // This warp's blocks: j0 + warp, + AW, ...
-    const int j0 = c0 * AW, nb_all = max(0, (tok_end + 15) / 16 - j0);
-    const int nb = max(0, (nb_all - warp + AW - 1) / AW);
-    const int* trow = a.table + (long long)b * a.table_stride;
+    // This warp's blocks: j0 + 2 warp, + 1, then + 2 AW, ...
+    const int j0 = c0 * (ACH / 16), nb_all = max(0, (tok_end + 15) / 16 - j0);
+    const int nb = 2 * (nb_all / (2 * AW)) + min(max(nb_all % (2 * AW) - 2 * warp, 0), 2);
+    // Copies: a pair of blocks at a time, one copy where they lie in one page.
     const int bpp = a.page_size / KV_BLOCK;
-    auto issue = [&](int i) {  // copy of this warp's i-th block into ring slot (cnt + i) % ST
-      const int j = j0 + warp + AW * i;
-      const int slot = (cnt + i) % ST;
-      // An entry outside the pool reads page 0: never outside the buffer.
-      const unsigned e = (unsigned)trow[j / bpp];
-      const long long page = e < (unsigned long long)a.pages ? (long long)e : 0;
-      mbar_expect_tx(&full[warp * ST + slot], BB);
-      bulk_load(smem_u32(ring + slot * BB), a.cache + ((page * a.heads + head) * bpp + j % bpp) * (long long)BB, BB,
-                &full[warp * ST + slot]);
+    const int* trow = a.table + (long long)b * a.table_stride;
+    const uint8_t* src0 = a.cache + (long long)head * bpp * BB;
+    const long long page_bytes = (long long)a.heads * bpp * BB;
+    const int jump = 2 * AW / bpp, jrest = 2 * AW % bpp;
+    int ip = (j0 + 2 * warp) / bpp, iin = (j0 + 2 * warp) % bpp, islot = slot, left = nb;
+    int entry = left > 0 ? trow[ip] : 0;  // of the next pair, loaded a round ahead
+    auto place = [&](int e, int in) {  // an entry outside the pool reads page 0: never outside the buffer
+      return src0 + ((unsigned)e < (unsigned long long)a.pages ? (long long)e : 0) * page_bytes + in * BB;
     };
-    if (lane == 0 && !wc.no_loads)
-      for (int i = 0; i < ST && i < nb; ++i) issue(i);
-
-    // q, in the order of the key words; rows g and g + 8 of each m-tile.
-    uint32_t qa[MT][NW][8];
-    int last[MT][2];  // last key the row sees (-1: none)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const T* qp[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = m * 16 + g + 8 * e, rr = r0 + min(r, rows - 1);
-        last[m][e] = r < rows ? sq.len - sq.nq + rr / a.group : -1;
-        qp[e] = static_cast<const T*>(a.q) + (long long)(sq.q0 + rr / a.group) * a.q_ts +
-                (long long)(head * a.group + rr % a.group) * a.q_hs;
+    auto issue = [&]() {
+      uint64_t* bar = &full[warp * ST + islot];
+      const uint32_t dst = smem_u32(ring + islot * PB);
+      if (lane == 0) {
+        if (left == 1 || iin + 1 < bpp) {
+          const uint32_t bytes = left == 1 ? BB : PB;
+          mbar_expect_tx(bar, bytes);
+          bulk_load(dst, place(entry, iin), bytes, bar);
+        } else {
+          mbar_expect_tx(bar, PB);
+          bulk_load(dst, place(entry, iin), BB, bar);
+          bulk_load(dst + BB, place(trow[ip + 1], 0), BB, bar);
+        }
       }
+      if (++islot == ST) islot = 0;
+      left -= 2;
+      ip += jump;
+      iin += jrest;
+      if (iin >= bpp) iin -= bpp, ++ip;
+      if (left > 0) entry = trow[ip];
+    };
+    if (!wc.no_loads)
+      for (int i = 0; i < ST && left > 0; ++i) issue();
+
+    // q, in the order of the key words: column g of each tile.
+    uint32_t qb[NQ][NW][4];
+    int last[NQ][2];  // last key that columns 2t, 2t + 1 see (-1: none)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int rr = r0 + min(8 * n + g, rows - 1);
+      const T* qp = static_cast<const T*>(a.q) + (long long)(sq.q0 + rr / a.group) * a.q_ts +
+                    (long long)(head * a.group + rr % a.group) * a.q_hs;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const int ch = word_channel<D>(t, w);
-        const uint4 x = pair_order(*reinterpret_cast<const uint4*>(qp[0] + ch));
-        const uint4 y = pair_order(*reinterpret_cast<const uint4*>(qp[1] + ch));
-        qa[m][w][0] = x.x; qa[m][w][1] = y.x; qa[m][w][2] = x.y; qa[m][w][3] = y.y;
-        qa[m][w][4] = x.z; qa[m][w][5] = y.z; qa[m][w][6] = x.w; qa[m][w][7] = y.w;
+        const uint4 x = pair_order(*reinterpret_cast<const uint4*>(qp + word_channel<D>(t, w)));
+        qb[n][w][0] = x.x ^ flip; qb[n][w][1] = x.y ^ flip; qb[n][w][2] = x.z ^ flip; qb[n][w][3] = x.w ^ flip;
       }
-    }
-    float o[MT][DV][4], mx[MT][2], sum[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      mx[m][0] = mx[m][1] = kNone;
-      sum[m][0] = sum[m][1] = 0.f;
-#pragma unroll
-      for (int j = 0; j < DV; ++j) o[m][j][0] = o[m][j][1] = o[m][j][2] = o[m][j][3] = 0.f;
-    }
-
-    for (int i = 0; i < nb; ++i) {
-      const int slot = (cnt + i) % ST;
-      if (!wait_bar_warp(&full[warp * ST + slot], (uint32_t)((cnt + i) / ST) & 1u, abort, wc.ns)) break;
-      const uint8_t* blk = ring + slot * BB;
-      const int tok0 = (j0 + warp + AW * i) * 16;
-
-      // Scores of 16 tokens.
-      float s[MT][2][4];
-#pragma unroll
-      for (int a2 = 0; a2 < 2; ++a2) {
-        const int kt = 8 * a2 + (g ^ ((g >> 1) & 1));
-#pragma unroll
-        for (int m = 0; m < MT; ++m) s[m][a2][0] = s[m][a2][1] = s[m][a2][2] = s[m][a2][3] = 0.f;
-        const uint8_t* kp = blk + kt * (D / 2);
-        const uint32_t* pp = reinterpret_cast<const uint32_t*>(blk + kv_param_off(D)) + kt * (D / 32);
-        uint32_t w[NW];
-        if (D == 64) {
-          const uint2 v = *reinterpret_cast<const uint2*>(kp + t * 8);
-          w[0] = v.x; w[1] = v.y;
-        } else {
-#pragma unroll
-          for (int c = 0; c < NW / 4; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4*>(kp + c * 64 + t * 16);
-            w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-          const uint32_t par = pp[word_channel<D>(t, k) / 32];
-          const T2 s2 = from_bits2<T2>(__byte_perm(par, par, 0x1010));
-          const T2 z2 = from_bits2<T2>(__byte_perm(par, par, 0x3232));
-          uint32_t v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = bits2(__hfma2(code16<T>(w[k], e), s2, z2));
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t a0[4] = {qa[m][k][0], qa[m][k][1], qa[m][k][2], qa[m][k][3]};
-            const uint32_t a1[4] = {qa[m][k][4], qa[m][k][5], qa[m][k][6], qa[m][k][7]};
-            mma16816<T>(s[m][a2], a0, v[0], v[1]);
-            mma16816<T>(s[m][a2], a1, v[2], v[3]);
-          }
-        }
-      }
-
-      // Mask, running maximum, exponentials.
-      const int ta = tok0 + 2 * t + (t & 1), tb = tok0 + 2 * t + 1 - (t & 1);  // tokens of columns 2t, 2t + 1
-      uint32_t pa[MT][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float nm[2] = {mx[m][0], mx[m][1]};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int a2 = 0; a2 < 2; ++a2) {
-            float& x = s[m][a2][2 * e];
-            float& y = s[m][a2][2 * e + 1];
-            x = ta + 8 * a2 <= last[m][e] ? x * a.scale_log2 : -INFINITY;
-            y = tb + 8 * a2 <= last[m][e] ? y * a.scale_log2 : -INFINITY;
-            nm[e] = fmaxf(nm[e], fmaxf(x, y));
-          }
-          nm[e] = fmaxf(nm[e], __shfl_xor_sync(0xffffffffu, nm[e], 1));
-          nm[e] = fmaxf(nm[e], __shfl_xor_sync(0xffffffffu, nm[e], 2));
-        }
-        if (__any_sync(0xffffffffu, nm[0] > mx[m][0] || nm[1] > mx[m][1])) {
-          const float f0 = ex2(mx[m][0] - nm[0]), f1 = ex2(mx[m][1] - nm[1]);
-          sum[m][0] *= f0;
-          sum[m][1] *= f1;
-#pragma unroll
-          for (int j = 0; j < DV; ++j) {
-            o[m][j][0] *= f0; o[m][j][1] *= f0;
-            o[m][j][2] *= f1; o[m][j][3] *= f1;
-          }
-          mx[m][0] = nm[0];
-          mx[m][1] = nm[1];
-        }
-#pragma unroll
-        for (int a2 = 0; a2 < 2; ++a2)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = ex2(s[m][a2][2 * e] - mx[m][e]), y = ex2(s[m][a2][2 * e + 1] - mx[m][e]);
-            sum[m][e] += x + y;
-            pa[m][2 * a2 + e] = bits2(Elem<T>::make2(x, y));
-          }
-      }
-
-      // Values: lane (g, t) takes channels g DV .. of the four tokens of its
-      // columns.  Tokens past the end count nothing, whatever the page holds.
-#pragma unroll
-      for (int wv = 0; wv < DV / 8; ++wv) {
-        uint32_t b0[8], b1[8];
-#pragma unroll
-        for (int a2 = 0; a2 < 2; ++a2) {
-          const int va = 8 * a2 + 2 * t + (t & 1), vb = 8 * a2 + 2 * t + 1 - (t & 1);
-          const uint8_t* vp = blk + kv_value_off(D) + (g * DV / 2 + wv * 4);
-          const uint32_t wa = *reinterpret_cast<const uint32_t*>(vp + va * (D / 2));
-          const uint32_t wb = *reinterpret_cast<const uint32_t*>(vp + vb * (D / 2));
-          const uint32_t* pp = reinterpret_cast<const uint32_t*>(blk + kv_value_off(D) + kv_param_off(D)) +
-                               (g * DV + wv * 8) / 32;
-          const uint32_t pA = tok0 + va < sq.len ? pp[va * (D / 32)] : 0u;
-          const uint32_t pB = tok0 + vb < sq.len ? pp[vb * (D / 32)] : 0u;
-          const T2 s2 = from_bits2<T2>(__byte_perm(pA, pB, 0x5410)), z2 = from_bits2<T2>(__byte_perm(pA, pB, 0x7632));
-          const uint32_t x = __byte_perm(wa, wb, 0x5410), y = __byte_perm(wa, wb, 0x7632);
-          uint32_t* dst = a2 == 0 ? b0 : b1;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            dst[e] = bits2(__hfma2(code16<T>(x, e), s2, z2));
-            dst[4 + e] = bits2(__hfma2(code16<T>(y, e), s2, z2));
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) mma16816<T>(o[m][wv * 8 + e], pa[m], b0[e], b1[e]);
-      }
-      __syncwarp();
-      if (lane == 0 && i + ST < nb) issue(i + ST);
-    }
-    cnt += nb;
-
-    // The four warps' maxima, sums and outputs meet.
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        sum[m][e] += __shfl_xor_sync(0xffffffffu, sum[m][e], 1);
-        sum[m][e] += __shfl_xor_sync(0xffffffffu, sum[m][e], 2);
-        if (t == 0) {
-          mls[warp][m * 16 + g + 8 * e][0] = mx[m][e];
-          mls[warp][m * 16 + g + 8 * e][1] = sum[m][e];
-        }
+        const int r = 8 * n + 2 * t + e;
+        last[n][e] = r < rows ? sq.len - sq.nq + (r0 + r) / a.group : -1;
       }
-    __syncthreads();
-    for (int w = 0; w < AW; ++w) {
-      if (warp == w) {
+    }
+    float o[NQ][DV / 2][4], mx[NQ][2], sum[NQ][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NQ; ++n) {
+      mx[n][0] = mx[n][1] = kNone;
+      sum[n][0] = sum[n][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < DV / 2; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+    }
+
+    int tok0 = (j0 + 2 * warp) * 16;
+#pragma unroll 1
+    for (int i = 0; i < nb; i += 2, tok0 += 32 * AW) {
+      const bool two = i + 1 < nb;
+      if (!wait_bar_warp(&full[warp * ST + slot], phase, abort, wc.ns)) break;
+      const uint8_t* pair = ring + slot * PB;
+      if (++slot == ST) slot = 0, phase ^= 1u;
+
+      // Scores of 32 tokens: sums (token g, columns 2t, 2t + 1), (token g + 8, ...).
+      float s[2][NQ][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) s[k][n][0] = s[k][n][1] = s[k][n][2] = s[k][n][3] = 0.f;
+        const uint8_t* kp = pair + k * BB + perm * (D / 2);
+        const uint32_t* pp = reinterpret_cast<const uint32_t*>(pair + k * BB + kv_param_off(D)) + perm * (D / 32);
+#pragma unroll
+        for (int c = 0; c < (NW + 3) / 4; ++c) {
+          uint32_t w[2][4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int r = m * 16 + g + 8 * e;
-            const float top = fmaxf(fmaxf(mls[0][r][0], mls[1][r][0]), fmaxf(mls[2][r][0], mls[3][r][0]));
-            const float f = ex2(mx[m][e] - top);
-            float* d0 = osum + r * (D + 4) + 2 * t * DV;
-#pragma unroll
-            for (int j = 0; j < DV; ++j) {
-              const float x = o[m][j][2 * e] * f, y = o[m][j][2 * e + 1] * f;
-              d0[j] = w == 0 ? x : d0[j] + x;
-              d0[DV + j] = w == 0 ? y : d0[DV + j] + y;
+            if (D == 64) {
+              const uint2 v = *reinterpret_cast<const uint2*>(kp + 8 * e * (D / 2) + t * 8);
+              w[e][0] = v.x; w[e][1] = v.y;
+            } else {
+              const uint4 v = *reinterpret_cast<const uint4*>(kp + 8 * e * (D / 2) + c * 64 + t * 16);
+              w[e][0] = v.x; w[e][1] = v.y; w[e][2] = v.z; w[e][3] = v.w;
             }
           }
-      }
-      __syncthreads();
-    }
-    const bool whole = c0 == 0 && c1 == nch;
-    float* slot = a.part + ((size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0)) * slot_floats<D>(MR);
-    for (int r = warp; r < rows; r += AW) {
-      const float top = fmaxf(fmaxf(mls[0][r][0], mls[1][r][0]), fmaxf(mls[2][r][0], mls[3][r][0]));
-      float den = 0.f;
+          // A lane's words of a token lie in one group.
+          const int grp = D == 64 ? t / 2 : 4 * c + t;
+          T2 s2[2], z2[2];
 #pragma unroll
-      for (int w = 0; w < AW; ++w) den += mls[w][r][1] * ex2(mls[w][r][0] - top);
-      const float* src = osum + r * (D + 4);
-      if (whole) {
-        const float inv = den != 0.f ? 1.f / den : 0.f;  // a row that sees nothing: zeros
-        T* dst = static_cast<T*>(a.out) +
-                 ((long long)(sq.q0 + (r0 + r) / a.group) * a.heads * a.group + head * a.group + (r0 + r) % a.group) * D;
-        for (int d = 2 * lane; d < D; d += 64)
-          *reinterpret_cast<T2*>(dst + d) = Elem<T>::make2(src[d] * inv, src[d + 1] * inv);
-      } else {
-        for (int d = lane; d < D; d += 32) slot[r * D + d] = src[d];
-        if (lane == 0) {
-          slot[MR * D + 2 * r] = top;
-          slot[MR * D + 2 * r + 1] = den;
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t par = pp[8 * e * (D / 32) + grp];
+            s2[e] = from_bits2<T2>(__byte_perm(par, par, 0x1010));
+            z2[e] = from_bits2<T2>(__byte_perm(par, par, 0x3232));
+          }
+#pragma unroll
+          for (int q = 0; q < (NW < 4 ? NW : 4); ++q) {
+            uint32_t v[2][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int p = 0; p < 4; ++p) v[e][p] = bits2(__hfma2(code16<T>(w[e][q], p, a.up), s2[e], z2[e]));
+            const uint32_t a0[4] = {v[0][0], v[1][0], v[0][1], v[1][1]};
+            const uint32_t a1[4] = {v[0][2], v[1][2], v[0][3], v[1][3]};
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+              mma16816<T>(s[k][n], a0, qb[n][4 * c + q][0], qb[n][4 * c + q][1]);
+              mma16816<T>(s[k][n], a1, qb[n][4 * c + q][2], qb[n][4 * c + q][3]);
+            }
+          }
         }
+      }
+
+      // Mask (only where a token of the two blocks is hidden from some row),
+      // running maximum, exponentials.
+      const bool hidden = tok0 + (two ? 31 : 15) > first_pos || !two;
+      uint32_t pb[2][NQ][2];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float nm[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (hidden) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (tok0 + 16 * k + 8 * h + perm > last[n][e] || (k == 1 && !two)) s[k][n][2 * h + e] = -INFINITY;
+          }
+          nm[e] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) nm[e] = fmaxf(nm[e], __shfl_xor_sync(0xffffffffu, nm[e], x));
+        }
+        if (__any_sync(0xffffffffu, nm[0] > mx[n][0] || nm[1] > mx[n][1])) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            nm[e] = fmaxf(nm[e], mx[n][e]);
+            f[e] = ex2(sl * (mx[n][e] - nm[e]));
+            sum[n][e] *= f[e];
+            mx[n][e] = nm[e];
+          }
+#pragma unroll
+          for (int i2 = 0; i2 < DV / 2; ++i2) {
+            o[n][i2][0] *= f[0]; o[n][i2][1] *= f[1];
+            o[n][i2][2] *= f[0]; o[n][i2][3] *= f[1];
+          }
+        }
+        const float m0 = sl * mx[n][0], m1 = sl * mx[n][1];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = ex2(fmaf(sl, s[k][n][2 * h], -m0)), y = ex2(fmaf(sl, s[k][n][2 * h + 1], -m1));
+            if (hidden) {  // (-inf times a scale of 0 is no number)
+              if (s[k][n][2 * h] == -INFINITY) x = 0.f;
+              if (s[k][n][2 * h + 1] == -INFINITY) y = 0.f;
+            }
+            sum[n][0] += x;
+            sum[n][1] += y;
+            pb[k][n][h] = turn8x8(bits2(Elem<T>::make2(x, y)));
+          }
+      }
+
+      // Values: lane (g, t) takes channels g DV .. of the tokens of rows 2t,
+      // 2t + 1 (and + 8).  Tokens past the end count nothing, whatever the
+      // page holds.
+      const bool tail = tok0 + 32 > sq.len || !two;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint8_t* vp = pair + k * BB + kv_value_off(D) + g * (DV / 2);
+        const uint32_t* pp = reinterpret_cast<const uint32_t*>(pair + k * BB + kv_value_off(D) + kv_param_off(D)) + g * DV / 32;
+        uint32_t w[4][DV / 8];  // tokens ta, tb, ta + 8, tb + 8
+        T2 s2[2], z2[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t par[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int tok = 8 * h + (e ? tb : ta);
+            const uint8_t* src = vp + tok * (D / 2);
+            if (DV / 8 == 1) {
+              w[2 * h + e][0] = *reinterpret_cast<const uint32_t*>(src);
+            } else if (DV / 8 == 2) {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              w[2 * h + e][0] = v.x; w[2 * h + e][DV / 8 - 1] = v.y;
+            } else {
+              const uint4 v = *reinterpret_cast<const uint4*>(src);
+              w[2 * h + e][0] = v.x; w[2 * h + e][(DV / 8) / 4] = v.y;
+              w[2 * h + e][(DV / 8) / 2] = v.z; w[2 * h + e][DV / 8 - 1] = v.w;
+            }
+            par[e] = pp[tok * (D / 32)];
+            if (tail && (tok0 + 16 * k + tok >= sq.len || (k == 1 && !two))) par[e] = 0u;
+          }
+          s2[h] = from_bits2<T2>(__byte_perm(par[0], par[1], 0x5410));
+          z2[h] = from_bits2<T2>(__byte_perm(par[0], par[1], 0x7632));
+        }
+#pragma unroll
+        for (int v = 0; v < DV / 8; ++v) {
+          uint32_t d[2][8];  // [tokens, tokens + 8][channel]
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = __byte_perm(w[2 * h][v], w[2 * h + 1][v], 0x5410),
+                           y = __byte_perm(w[2 * h][v], w[2 * h + 1][v], 0x7632);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              d[h][e] = bits2(__hfma2(code16<T>(x, e, a.up), s2[h], z2[h]));
+              d[h][4 + e] = bits2(__hfma2(code16<T>(y, e, a.up), s2[h], z2[h]));
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t av[4] = {d[0][2 * e], d[0][2 * e + 1], d[1][2 * e], d[1][2 * e + 1]};
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) mma16816<T>(o[n][4 * v + e], av, pb[k][n][0], pb[k][n][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (left > 0) issue();
+    }
+
+    // The four warps' maxima, sums and outputs meet; the outputs go through
+    // the rings, which are empty here.
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) sum[n][e] += __shfl_xor_sync(0xffffffffu, sum[n][e], x);
+        if (g == 0) {
+          mls[warp][8 * n + 2 * t + e][0] = mx[n][e];
+          mls[warp][8 * n + 2 * t + e][1] = sum[n][e];
+        }
+        float* dst = reinterpret_cast<float*>(ring) + (8 * n + 2 * t + e) * OS + g * DV;
+#pragma unroll
+        for (int i = 0; i < DV / 2; ++i)
+          *reinterpret_cast<float2*>(dst + 2 * i) = float2{o[n][i][e], o[n][i][2 + e]};
+      }
+    __syncthreads();
+    const bool whole = c0 == 0 && c1 == nch;
+    float* part = a.part + ((size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0)) * slot_floats<D>(MR);
+    for (int r = warp; r < rows; r += AW) {
+      float top = mls[0][r][0], f[AW], den = 0.f;
+#pragma unroll
+      for (int w = 1; w < AW; ++w) top = fmaxf(top, mls[w][r][0]);
+#pragma unroll
+      for (int w = 0; w < AW; ++w) {
+        f[w] = ex2(sl * (mls[w][r][0] - top));
+        den += mls[w][r][1] * f[w];
+      }
+      const float inv = den != 0.f ? 1.f / den : 0.f;  // a row that sees nothing: zeros
+      const int rr = r0 + r;
+      T* dst = static_cast<T*>(a.out) +
+               ((long long)(sq.q0 + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group) * D;
+#pragma unroll
+      for (int d = 2 * lane; d < D; d += 64) {
+        float2 v{0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < AW; ++w) {
+          const float2 x = *reinterpret_cast<const float2*>(smem + (size_t)w * ST * PB + (r * OS + d) * 4);
+          v.x = fmaf(x.x, f[w], v.x);
+          v.y = fmaf(x.y, f[w], v.y);
+        }
+        if (whole)
+          *reinterpret_cast<T2*>(dst + d) = Elem<T>::make2(v.x * inv, v.y * inv);
+        else
+          *reinterpret_cast<float2*>(part + r * D + d) = v;
+      }
+      if (!whole && lane == 0) {
+        part[MR * D + 2 * r] = top;
+        part[MR * D + 2 * r + 1] = den;
       }
     }
     u += c1 - c0;
     if (__syncthreads_or(abort_sh)) break;  // the whole CTA leaves together
+    fence_proxy_async_smem();               // the rings take copies again
+    __syncwarp();
   }
   __syncthreads();
   if (abort_sh) {
@@ -397,15 +482,16 @@ __global__ void __launch_bounds__(ATHREADS)
 
 // Adds the pieces of an item that more than one CTA shared.  One CTA per
 // (key head, row block) and sequence; a warp per row.
-template <class T, int D, int MT>
+template <class T, int D, int NQ>
 __global__ void __launch_bounds__(ATHREADS) k_kv4_join(AttnArgs a, int grid) {
-  constexpr int MR = 16 * MT;
+  constexpr int MR = 8 * NQ;
   __shared__ long long pref[ASEQS + 1];
   __shared__ long long scratch[AW];
   work_prefix<MR>(a, pref, scratch);
   const int b = (int)blockIdx.y, item = (int)blockIdx.x;
   const Seq sq = seq_of(a, b);
   const int nblk = blocks_of<MR>(a, sq), nch = chunks_of(sq);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are there
   if (item >= a.heads * nblk) return;
   const long long W = pref[a.seqs], u0 = pref[b] + (long long)item * nch;
   const long long shares = min(W, (long long)grid);
@@ -413,43 +499,50 @@ __global__ void __launch_bounds__(ATHREADS) k_kv4_join(AttnArgs a, int grid) {
   if (first == lastc) return;
   const int head = item / nblk, r0 = (item % nblk) * MR, rows = min(MR, sq.nq * a.group - r0);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const float sl = fabsf(a.scale_log2);
   auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == first ? 1 : 0)) * slot_floats<D>(MR); };
   for (int r = warp; r < rows; r += AW) {
-    float top = kNone;
-    for (int c = first; c <= lastc; ++c) top = fmaxf(top, slot(c)[MR * D + 2 * r]);
-    float den = 0.f, acc[D / 32];
+    // The running maximum and sum once more, over the pieces in order.
+    float top = kNone, den = 0.f, acc[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+#pragma unroll 4
     for (int c = first; c <= lastc; ++c) {
       const float* p = slot(c);
-      const float f = ex2(p[MR * D + 2 * r] - top);
-      den += p[MR * D + 2 * r + 1] * f;
+      const float m = p[MR * D + 2 * r], l = p[MR * D + 2 * r + 1];
+      const float nt = fmaxf(top, m), fo = ex2(sl * (top - nt)), fn = ex2(sl * (m - nt));
+      top = nt;
+      den = den * fo + l * fn;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) acc[i] += p[r * D + lane + 32 * i] * f;
+      for (int i = 0; i < D / 32; ++i) acc[i] = acc[i] * fo + p[r * D + lane + 32 * i] * fn;
     }
     const float inv = den != 0.f ? 1.f / den : 0.f;
+    const int rr = r0 + r;
     T* dst = static_cast<T*>(a.out) +
-             ((long long)(sq.q0 + (r0 + r) / a.group) * a.heads * a.group + head * a.group + (r0 + r) % a.group) * D;
+             ((long long)(sq.q0 + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group) * D;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = Elem<T>::from(acc[i] * inv);
   }
 }
 
-template <int D, int MT>
+// Pairs of blocks in a warp's ring: two keep the copies ahead; with four
+// column tiles the outputs need four.
+template <int NQ>
 constexpr int stages() {
-  return D == 64 ? 8 : (D == 128 ? 6 : 4);
+  return NQ == 4 ? 4 : 2;
 }
 
-// Shares of the work list: three CTAs a SM (two for dim 256).
-int shares_of(int dim) { return num_sms() * (dim == 256 ? 2 : 3); }
-
-template <class T, int D, int MT>
+template <class T, int D, int NQ>
 gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
-  constexpr int ST = stages<D, MT>();
-  constexpr int smem = AW * ST * kv_block_bytes(D) + 16 * MT * (D + 4) * 4;
+  constexpr int ST = stages<NQ>();
+  constexpr int smem = AW * ST * 2 * kv_block_bytes(D);
   static DeviceOnce attr;
+  static int per_sm = 1;  // resident CTAs a SM: one share each
   GQ_TRY(attr.run([](int) -> gptq_status {
-    GQ_CUDA(cudaFuncSetAttribute(k_kv4_attention<T, D, MT, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    GQ_CUDA(cudaFuncSetAttribute(k_kv4_attention<T, D, NQ, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    int n = 0;
+    GQ_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_kv4_attention<T, D, NQ, ST>, ATHREADS, smem));
+    per_sm = n < 1 ? 1 : (n > ASHARES ? ASHARES : n);
     return GPTQ_OK;
   }));
   const int seqs = a.seqs;
@@ -463,25 +556,40 @@ gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
     } else {
       p.q = static_cast<const T*>(a.q) + b0 * a.q_ts;
       p.out = static_cast<T*>(a.out) + (long long)b0 * a.heads * a.group * D;
+      p.tq = p.seqs;
     }
-    const int shares = shares_of(D);
+    // No more shares than the longest contexts the table allows have chunks.
+    const long long blocks = ((long long)a.max_q * a.group + 8 * NQ - 1) / (8 * NQ);
+    const long long most = (long long)p.seqs * a.heads * blocks *
+                           (((long long)a.table_stride * a.page_size + ACH - 1) / ACH);
+    long long shares = (long long)num_sms() * per_sm;
+    if (shares > most) shares = most;
     {
       GQ_PROF(K_KV4_ATTENTION, s);
-      k_kv4_attention<T, D, MT, ST><<<shares, ATHREADS, smem, s>>>(p, wait_cfg());
+      k_kv4_attention<T, D, NQ, ST><<<(unsigned)shares, ATHREADS, smem, s>>>(p, wait_cfg());
       GQ_LAUNCHED();
     }
-    const long long items = (long long)a.heads * (((long long)a.max_q * a.group + 16 * MT - 1) / (16 * MT));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.heads * blocks), (unsigned)p.seqs);
+    cfg.blockDim = dim3(ATHREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
     GQ_PROF(K_KV4_JOIN, s);
-    k_kv4_join<T, D, MT><<<dim3((unsigned)items, (unsigned)p.seqs), ATHREADS, 0, s>>>(p, shares);
-    GQ_LAUNCHED();
+    GQ_CUDA(cudaLaunchKernelEx(&cfg, k_kv4_join<T, D, NQ>, p, (int)shares));
   }
   return GPTQ_OK;
 }
 
 template <class T, int D>
 gptq_status attn_rows(const AttnArgs& a, cudaStream_t s) {
-  if (D <= 128 && (long long)a.max_q * a.group > 16) return attn_launch<T, D, D <= 128 ? 2 : 1>(a, s);
-  return attn_launch<T, D, 1>(a, s);
+  const long long rows = (long long)a.max_q * a.group;
+  if (rows <= 8) return attn_launch<T, D, 1>(a, s);
+  if (rows <= 16 || D == 256) return attn_launch<T, D, 2>(a, s);
+  return attn_launch<T, D, D == 256 ? 2 : 4>(a, s);
 }
 
 template <class T>
@@ -493,7 +601,7 @@ gptq_status attn_dim(int dim, const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t kv4_attention_ws_bytes(int dim) { return (size_t)shares_of(dim) * 2 * 32 * (dim + 2) * 4; }
+size_t kv4_attention_ws_bytes(int dim) { return (size_t)num_sms() * ASHARES * 2 * 32 * (dim + 2) * 4; }
 
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s) {
   if (a.seqs == 0 || a.tq == 0) return GPTQ_OK;

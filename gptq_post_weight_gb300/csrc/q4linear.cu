@@ -50,7 +50,7 @@ struct CodeNum<__half> {
 
 template <class T>
 __device__ __forceinline__ uint32_t code_num(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000F000Fu) | CodeNum<T>::kMagic;
+  return and_or<0x000F000Fu>(w >> (4 * i), CodeNum<T>::kMagic);
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -422,7 +422,7 @@ __device__ __forceinline__ void dequant32(uint4 v, uint32_t s, uint32_t (&o)[16]
                            __byte_perm(w[i], h, 0x7733)};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const T2 c = __hsub2(from_bits2<T2>((p[j] & 0x000F000Fu) | Code8<T>::kMagic), bias);
+      const T2 c = __hsub2(from_bits2<T2>(and_or<0x000F000Fu>(p[j], Code8<T>::kMagic)), bias);
       o[4 * i + j] = bits2(__hfma2(c, hi, __hmul2(c, lo)));
     }
   }

@@ -45,13 +45,29 @@ __device__ __forceinline__ T2 from_bits2(uint32_t v) {
   return *reinterpret_cast<T2*>(&v);
 }
 
+// (x & MASK) | magic as the one instruction it is (from the C expression the
+// compiler makes two, and the ALUs bound the kernels that decode).
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "n"(MASK), "r"(magic));
+  return r;
+}
+
 // (16 + nibble i of the low half, 16 + nibble i of the high half) as T2.
 template <class T>
 __device__ __forceinline__ typename Elem<T>::T2 code16(uint32_t w, int i) {
   constexpr int kPos = Elem<T>::kPos;
   const int sh = 4 * i - kPos;
-  const uint32_t x = sh >= 0 ? (w >> sh) : (w << -sh);
-  return from_bits2<typename Elem<T>::T2>((x & Elem<T>::kMask16) | Elem<T>::kMagic16);
+  return from_bits2<typename Elem<T>::T2>(and_or<Elem<T>::kMask16>(sh >= 0 ? (w >> sh) : (w << -sh), Elem<T>::kMagic16));
+}
+// The same with the shift of nibble 0 as a product with `up` = 2^kPos, of
+// which the compiler must not know that it is one: it then runs beside the
+// ALUs, on the multipliers.
+template <class T>
+__device__ __forceinline__ typename Elem<T>::T2 code16(uint32_t w, int i, uint32_t up) {
+  if (i != 0) return code16<T>(w, i);
+  return from_bits2<typename Elem<T>::T2>(and_or<Elem<T>::kMask16>(w * up, Elem<T>::kMagic16));
 }
 
 // 16 x 8 x 16 product with f32 accumulation.
@@ -170,6 +186,7 @@ struct AttnArgs {
   float scale_log2;  // scale * log2(e)
   void* out;         // [tq][heads * group][dim]
   float* part;       // workspace
+  uint32_t up;       // 2^kPos of T (see code16)
   unsigned* status;
 };
 
