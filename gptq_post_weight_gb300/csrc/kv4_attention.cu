@@ -32,6 +32,8 @@
 #include "serve.cuh"
 
 namespace gq {
+gptq_status kv4_chunk_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s);
+
 namespace {
 
 constexpr int AW = 4;            // warps
@@ -605,6 +607,8 @@ size_t kv4_attention_ws_bytes(int dim) { return (size_t)num_sms() * ASHARES * 2 
 
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s) {
   if (a.seqs == 0 || a.tq == 0) return GPTQ_OK;
+  const long long rows = (long long)a.max_q * a.group;
+  if (dim <= 128 && a.q_starts != nullptr && rows > 128 && rows <= 256ll * 65535) return kv4_chunk_run(dtype, dim, a, s);
   return dtype == GPTQ_BF16 ? attn_dim<__nv_bfloat16>(dim, a, s) : attn_dim<__half>(dim, a, s);
 }
 
