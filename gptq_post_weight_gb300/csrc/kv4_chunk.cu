@@ -9,11 +9,11 @@
 //   warps 0-3, 4-7  softmax of tile A, B: a row a thread.  S from tensor
 //                   memory (twice: maximum, then exponentials), P written
 //                   back over it in T, the operand A of the second product;
-//   warps 8-11      decode K and V of a step into shared memory in 128-byte
+//   warps 8-10, 11-13  decode K, V of a step into shared memory in 128-byte
 //                   swizzled rows of tokens (K is then a K-major operand, V
 //                   an N-major one: no transpose);
-//   warp 12         copies the step's cache blocks (untiled bulk copies);
-//   warp 13         issues the products: S_A, S_B of the next step between
+//   warp 14         copies the step's cache blocks (untiled bulk copies);
+//   warp 15         issues the products: S_A, S_B of the next step between
 //                   O_A += P_A V and O_B += P_B V, so that one tile's
 //                   softmax runs under the other's products.
 // Tensor memory: S_A, S_B (128 columns each, P over their first half), O_A,
@@ -30,7 +30,7 @@ namespace {
 
 constexpr int CK = 128;     // keys a step
 constexpr int CROWS = 256;  // query rows a CTA
-constexpr int CTHREADS = 448;
+constexpr int CTHREADS = 512;
 constexpr float kNone = -1e30f;
 
 template <class T>
@@ -48,6 +48,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
 }
 
 // For what is in tensor memory (ordered by the tcgen05 fences).
@@ -136,16 +142,16 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk_
   if (threadIdx.x == 0) {
     mbar_init(&qfull, 256);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&kfull[i], 128), mbar_init(&kempty[i], 1);
-      mbar_init(&rawfull[i], 1), mbar_init(&rawempty[i], 4);
+      mbar_init(&kfull[i], 96), mbar_init(&kempty[i], 1);
+      mbar_init(&rawfull[i], 1), mbar_init(&rawempty[i], 6);
       mbar_init(&sfull[i], 1), mbar_init(&pfull[i], 128);
     }
-    mbar_init(&vfull, 128), mbar_init(&vempty, 1);
+    mbar_init(&vfull, 96), mbar_init(&vempty, 1);
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == 13) {
+  if (warp == 15) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_sh)),
                  "r"(512u)
                  : "memory");
@@ -155,7 +161,10 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk_
   __syncthreads();
   tc_fence_after();
 
+  // Registers: 128 a thread at launch (512 threads); a softmax thread keeps a
+  // row of scores, 2 * 128 * 184 + 2 * 128 * 72 = 65536 in all.
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int x = warp / 4, rt = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = (uint32_t)(128 * x) + lanes, to = kO + (uint32_t)(D * x) + lanes;
@@ -183,7 +192,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk_
       fence_proxy_async_smem();
       mbar_arrive(&qfull);
     }
-    const float sl = fabsf(a.scale_log2);
+    // (Not 0: a hidden key is a score of -inf, and -inf times 0 is no number.)
+    const float sl = fmaxf(fabsf(a.scale_log2), 1e-30f);
     float m = kNone, l = 0.f;
     bool ok = true;
     if (x == 0 || two) {
@@ -191,24 +201,26 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk_
       for (int j = 0; j < steps && ok; ++j) {
         if (!(ok = wait_bar_warp(&sfull[x], (uint32_t)j & 1u, abort, wc.ns))) break;
         tc_fence_after();
+        uint32_t v[4][32];  // the row's scores, in registers from here on
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32u * (uint32_t)c, v[c]);
+        tmem_ld_wait();
         const int lim = last - j * CK;  // last visible column of the step
-        const bool masked = __any_sync(0xffffffffu, lim < CK - 1);
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < CK; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(ts + (uint32_t)c, v);
-          tmem_ld_wait();
-          if (masked) {
+        if (__any_sync(0xffffffffu, lim < CK - 1)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) top = c + i <= lim ? fmaxf(top, __uint_as_float(v[i])) : top;
-          } else {
-            float t4[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], __uint_as_float(v[i]));
-            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-          }
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i > lim) v[c][i] = 0xff800000u;  // -inf
         }
+        float t4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          t4[c] = max3(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]), -INFINITY);
+#pragma unroll
+          for (int i = 2; i < 32; i += 2) t4[c] = max3(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]), t4[c]);
+        }
+        const float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
         if (__any_sync(0xffffffffu, sl * (top - m) > 8.f)) {
           const float nm = fmaxf(m, top), f = ex2(sl * (m - nm));
           m = nm;
@@ -216,34 +228,29 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk_
           if (j > 0) {
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
-              uint32_t v[16];
-              tmem_ld16(to + (uint32_t)c, v);
+              uint32_t w[16];
+              tmem_ld16(to + (uint32_t)c, w);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              tmem_st16(to + (uint32_t)c, v);
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+              tmem_st16(to + (uint32_t)c, w);
             }
           }
         }
         const float ms = sl * m;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int c = 0; c < CK; c += 32) {
-          uint32_t v[32], p[16];
-          tmem_ld32(ts + (uint32_t)c, v);
-          tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float e0 = ex2(fmaf(sl, __uint_as_float(v[2 * i]), -ms)), e1 = ex2(fmaf(sl, __uint_as_float(v[2 * i + 1]), -ms));
-            if (masked) {
-              e0 = c + 2 * i <= lim ? e0 : 0.f;
-              e1 = c + 2 * i + 1 <= lim ? e1 : 0.f;
-            }
+            const float e0 = ex2(fmaf(sl, __uint_as_float(v[c][2 * i]), -ms)),
+                        e1 = ex2(fmaf(sl, __uint_as_float(v[c][2 * i + 1]), -ms));
             sum[2 * i & 3] += e0;
             sum[(2 * i + 1) & 3] += e1;
             p[i] = bits2(Elem<T>::make2(e0, e1));
           }
-          tmem_st16(ts + (uint32_t)(c / 2), p);
+          tmem_st16(ts + 16u * (uint32_t)c, p);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_st_wait();
@@ -279,53 +286,67 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk_
         tc_fence_before();
       }
     }
-  } else if (warp < 12) {
-    // A thread decodes 32 channels (one group) of a token at a time: 16 bytes
-    // of codes to 64 bytes.  Eight lanes take the four groups of two tokens,
-    // and the order of their four stores differs so that they meet no bank
-    // twice.
-    const int dt = threadIdx.x - 256;
-    constexpr int GR = D / 32;                 // groups a token
-    constexpr int ITER = CK * GR / 128;        // pieces a thread, K or V
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  }
+  if (warp >= 8 && warp < 14) {
+    // Three warps decode K, three V.  A thread takes 32 channels (one group)
+    // of a token at a time: 16 bytes of codes to 64 bytes; it stays with its
+    // group and its token's place among eight, so that its addresses advance
+    // by constants.  Lanes of the upper half of the channels store their
+    // pieces in another order: eight lanes then meet no bank twice.
+    const int dt = (threadIdx.x - 256) % 96;
+    const bool isv = warp >= 11;
+    constexpr int GR = D / 32, TSTEP = 96 / GR;  // groups a token; tokens between a thread's pieces
+    const int grp = dt % GR, tok0 = dt / GR;
+    const bool swap = GR == 4 && grp >= 2;
+    const int rot = swap ? 2 : 0;
+    uint32_t off[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      off[u] = (uint32_t)(grp / 2 * (CK * 128)) + swz(tok0, grp % 2 * 4 + (u ^ rot));
     bool ok = true;
 #pragma unroll 1
     for (int j = 0; j < steps && ok; ++j) {
       const int st = j & 1;
       if (!(ok = wait_bar_warp(&rawfull[st], (uint32_t)(j >> 1) & 1u, abort, wc.ns))) break;
-      const uint8_t* raw = smem + S::raw + st * S::kRaw;
-#pragma unroll 1
-      for (int kv = 0; kv < 2 && ok; ++kv) {
-        ok = kv == 0 ? wait_bar_warp(&kempty[st], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort, wc.ns)
-                     : wait_bar_warp(&vempty, ((uint32_t)j & 1u) ^ 1u, abort, wc.ns);
-        if (!ok) break;
-        uint8_t* tile = smem + (kv == 0 ? S::k + st * S::kTile : S::v);
-#pragma unroll 2
-        for (int it = 0; it < ITER; ++it) {
-          const int piece = dt + 128 * it, grp = piece % GR, tok = piece / GR;
-          const uint8_t* blk = raw + tok / KV_BLOCK * BB + (kv == 0 ? 0 : kv_value_off(D));
-          const uint4 codes = *reinterpret_cast<const uint4*>(blk + tok % KV_BLOCK * (D / 2) + grp * 16);
-          uint32_t par = *reinterpret_cast<const uint32_t*>(blk + kv_param_off(D) + tok % KV_BLOCK * (D / 8) + grp * 4);
-          if (j * CK + tok >= vis) par = 0u;  // past what any row sees: no value, whatever is there
-          const T2 s2 = from_bits2<T2>(__byte_perm(par, par, 0x1010)), z2 = from_bits2<T2>(__byte_perm(par, par, 0x3232));
-          const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-          uint8_t* dst = tile + grp / 2 * (CK * 128);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint4 o;
-            o.x = bits2(__hfma2(code16<T>(w[u], 0, a.up), s2, z2));
-            o.y = bits2(__hfma2(code16<T>(w[u], 1), s2, z2));
-            o.z = bits2(__hfma2(code16<T>(w[u], 2), s2, z2));
-            o.w = bits2(__hfma2(code16<T>(w[u], 3), s2, z2));
-            *reinterpret_cast<uint4*>(dst + swz(tok, grp % 2 * 4 + u)) = o;
-          }
+      ok = isv ? wait_bar_warp(&vempty, ((uint32_t)j & 1u) ^ 1u, abort, wc.ns)
+               : wait_bar_warp(&kempty[st], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort, wc.ns);
+      if (!ok) break;
+      const uint8_t* raw = smem + S::raw + st * S::kRaw + (isv ? kv_value_off(D) : 0);
+      uint8_t* tile = smem + (isv ? S::v : S::k + st * S::kTile);
+      const int seen = vis - j * CK;  // tokens of the step that some row sees
+#pragma unroll 3
+      for (int tok = tok0; tok < CK; tok += TSTEP) {
+        const uint8_t* blk = raw + tok / KV_BLOCK * BB;
+        uint4 codes = *reinterpret_cast<const uint4*>(blk + tok % KV_BLOCK * (D / 2) + grp * 16);
+        uint32_t par = *reinterpret_cast<const uint32_t*>(blk + kv_param_off(D) + tok % KV_BLOCK * (D / 8) + grp * 4);
+        if (tok >= seen) par = 0u;  // past what any row sees: no value, whatever is there
+        if (GR == 4) {
+          const uint4 c = codes;
+          codes.x = swap ? c.z : c.x, codes.y = swap ? c.w : c.y;
+          codes.z = swap ? c.x : c.z, codes.w = swap ? c.y : c.w;
         }
-        fence_proxy_async_smem();
-        mbar_arrive(kv == 0 ? &kfull[st] : &vfull);
+        const T2 s2 = from_bits2<T2>(__byte_perm(par, par, 0x1010)), z2 = from_bits2<T2>(__byte_perm(par, par, 0x3232));
+        const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+        uint8_t* dst = tile + (tok - tok0) * 128;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint4 o;
+          o.x = bits2(__hfma2(code16<T>(w[u], 0, a.up), s2, z2));
+          o.y = bits2(__hfma2(code16<T>(w[u], 1), s2, z2));
+          o.z = bits2(__hfma2(code16<T>(w[u], 2), s2, z2));
+          o.w = bits2(__hfma2(code16<T>(w[u], 3), s2, z2));
+          *reinterpret_cast<uint4*>(dst + off[u]) = o;
+        }
       }
+      fence_proxy_async_smem();
+      mbar_arrive(isv ? &vfull : &kfull[st]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&rawempty[st]);
     }
-  } else if (warp == 12) {
+  }
+  if (warp == 14) {
     if (!wc.no_loads) {
       const int bpp = a.page_size / KV_BLOCK, nb = (vis + KV_BLOCK - 1) / KV_BLOCK;
       const int* trow = a.table + (long long)b * a.table_stride;
@@ -343,7 +364,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk_
                     a.cache + ((page * a.heads + head) * bpp + blk % bpp) * (long long)BB, BB, &rawfull[st]);
       }
     }
-  } else {
+  } else if (warp == 15) {
     uint32_t one;
     asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(one));
     constexpr uint32_t fmt = MmaFormat<T>::k;
@@ -421,7 +442,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk_
     if (threadIdx.x == 0 && a.status != nullptr) atomicOr(a.status, 2u);
   }
   tc_fence_after();
-  if (warp == 13)
+  if (warp == 15)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base_sh), "r"(512u) : "memory");
 }
 
