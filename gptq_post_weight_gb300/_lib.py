@@ -49,7 +49,7 @@ SIGNATURES = {
     "gptq_q4tp_linear": (_I, [_I, _P, _L, _I, _P, _P, _P, _I, _I, _P, _I, _P, _L, _P, _L, _P, _P]),
     "gptq_kv4_write": (_I, [_I, _P, _L, _I, _I, _I, _P, _P, _L, _L, _L, _L, _P, _I, _P]),
     "gptq_kv4_read": (_I, [_I, _P, _L, _I, _I, _I, _P, _I, _P, _P, _P]),
-    "gptq_kv4_attention_workspace_bytes": (_S, [_I]),
+    "gptq_kv4_attention_workspace_bytes": (_S, [_I, _I, _I]),
     "gptq_kv4_attention": (_I, [_I, _P, _L, _L, _I, _P, _L, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _F, _P, _P,
                                 _S, _P, _P]),
     "gptq_launch_count": (ctypes.c_longlong, []),
@@ -592,7 +592,7 @@ def debias(bits, w, h_packed, codes, rungs, tab, lost, scales, ws=None, want_num
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _serve = {}  # torch, its dtypes and the raw-stream call, once the first wrapper ran
 _serve_words = {}  # device index -> the status word its serving calls set (tensor, address)
-_attention_ws = {}  # dim -> workspace bytes
+_attention_ws = {}  # (dim, group, max_q) -> workspace bytes
 
 
 def _serving():
@@ -951,9 +951,12 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
     if out is None:
         out = sv["empty"]((tq, hq, dim), dtype=qt, device=q.device)
     if ws is None:
-        need = _attention_ws.get(dim)
+        shape = (dim, hq // heads, max_q)
+        need = _attention_ws.get(shape)
         if need is None:
-            need = _attention_ws[dim] = _lib.gptq_kv4_attention_workspace_bytes(dim)
+            need = _lib.gptq_kv4_attention_workspace_bytes(*shape)
+            if len(_attention_ws) < 4096:
+                _attention_ws[shape] = need
         ws = sv["empty"](need, dtype=sv["u8"], device=q.device)
     code = _lib.gptq_kv4_attention(dt, q.data_ptr(), qts, qhs, tq, cache.data_ptr(), pages, heads, hq // heads, dim,
                                    page_size, table.data_ptr(), per, kv_lens.data_ptr(), sp, seqs, int(max_q),

@@ -68,7 +68,7 @@ gptq_status kv4_write_run(int dtype, uint8_t* cache, long long pages, int heads,
                           const long long* slots, int tokens, cudaStream_t s);
 gptq_status kv4_read_run(int dtype, const uint8_t* cache, long long pages, int heads, int dim, int page_size,
                          const long long* slots, int tokens, void* k, void* v, cudaStream_t s);
-size_t kv4_attention_ws_bytes(int dim);
+size_t kv4_attention_ws_bytes(int dim, int group, int max_q, bool single);
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s);
 }  // namespace gq
 
@@ -695,8 +695,10 @@ gptq_status gptq_kv4_read(int dtype, const uint8_t* cache, long long pages, int 
   return kv4_read_run(dtype, cache, pages, heads, dim, page_size, slots, tokens, K, V, as_stream(stream));
 }
 
-size_t gptq_kv4_attention_workspace_bytes(int dim) {
-  return (dim == 64 || dim == 128 || dim == 256) ? kv4_attention_ws_bytes(dim) : 0;
+size_t gptq_kv4_attention_workspace_bytes(int dim, int group, int max_q) {
+  if ((dim != 64 && dim != 128 && dim != 256) || group <= 0 || group > 1024 || max_q <= 0 || max_q > GPTQ_MAX_TOKENS)
+    return 0;
+  return kv4_attention_ws_bytes(dim, group, max_q, false);
 }
 
 gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
@@ -714,10 +716,11 @@ gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long lo
   if (bad_stride(q_ts) || bad_stride(q_hs)) return GPTQ_ERR_SHAPE;
   if (!ptr_ok(Q) || !ptr_ok(cache) || table == nullptr || kv_lens == nullptr || !ptr_ok(out) || !ptr_ok(ws))
     return GPTQ_ERR_ARG;
-  if (ws_bytes < kv4_attention_ws_bytes(dim)) return GPTQ_ERR_NOMEM;
+  if (ws_bytes < kv4_attention_ws_bytes(dim, group, max_q, q_starts == nullptr)) return GPTQ_ERR_NOMEM;
   const AttnArgs a{Q,     q_ts,         q_hs,    tq,       cache, pages, heads, group, page_size,
                    table, table_stride, kv_lens, q_starts, seqs,  max_q, scale * 1.4426950408889634f,
-                   out,   static_cast<float*>(ws), dtype == GPTQ_BF16 ? 8u : 64u, status};
+                   out,   static_cast<long long*>(ws), reinterpret_cast<float*>(static_cast<char*>(ws) + kListBytes),
+                   dtype == GPTQ_BF16 ? 8u : 64u, status};
   return kv4_attention_run(dtype, dim, a, as_stream(stream));
 }
 

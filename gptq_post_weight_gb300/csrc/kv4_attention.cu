@@ -33,6 +33,7 @@
 
 namespace gq {
 gptq_status kv4_chunk_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s);
+size_t kv4_chunk_ws_bytes(int dim);
 
 namespace {
 
@@ -156,6 +157,8 @@ __global__ void __launch_bounds__(ATHREADS)
   work_prefix<MR>(a, pref, scratch);
   const long long W = pref[a.seqs];
   const long long shares = min(W, (long long)gridDim.x);  // no share is empty
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= a.seqs; i += ATHREADS) a.list[i] = pref[i];  // for the join
   if (blockIdx.x >= shares) return;
   long long u = W * blockIdx.x / shares;
   const long long uend = W * (blockIdx.x + 1) / shares;
@@ -487,15 +490,12 @@ __global__ void __launch_bounds__(ATHREADS)
 template <class T, int D, int NQ>
 __global__ void __launch_bounds__(ATHREADS) k_kv4_join(AttnArgs a, int grid) {
   constexpr int MR = 8 * NQ;
-  __shared__ long long pref[ASEQS + 1];
-  __shared__ long long scratch[AW];
-  work_prefix<MR>(a, pref, scratch);
   const int b = (int)blockIdx.y, item = (int)blockIdx.x;
   const Seq sq = seq_of(a, b);
   const int nblk = blocks_of<MR>(a, sq), nch = chunks_of(sq);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are there
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list and the pieces are there
   if (item >= a.heads * nblk) return;
-  const long long W = pref[a.seqs], u0 = pref[b] + (long long)item * nch;
+  const long long W = a.list[a.seqs], u0 = a.list[b] + (long long)item * nch;
   const long long shares = min(W, (long long)grid);
   const int first = (int)(((u0 + 1) * shares - 1) / W), lastc = (int)(((u0 + nch) * shares - 1) / W);
   if (first == lastc) return;
@@ -603,12 +603,20 @@ gptq_status attn_dim(int dim, const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t kv4_attention_ws_bytes(int dim) { return (size_t)num_sms() * ASHARES * 2 * 32 * (dim + 2) * 4; }
+// Many rows a sequence go to the tcgen05 kernel (kv4_chunk.cu).
+bool kv4_is_chunk(int dim, int group, int max_q, bool single) {
+  const long long rows = (long long)max_q * group;
+  return dim <= 128 && !single && rows > 128 && rows <= (256ll << 11);
+}
+
+size_t kv4_attention_ws_bytes(int dim, int group, int max_q, bool single) {
+  if (kv4_is_chunk(dim, group, max_q, single)) return kv4_chunk_ws_bytes(dim);
+  return kListBytes + (size_t)num_sms() * ASHARES * 2 * 32 * (dim + 2) * 4;
+}
 
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s) {
   if (a.seqs == 0 || a.tq == 0) return GPTQ_OK;
-  const long long rows = (long long)a.max_q * a.group;
-  if (dim <= 128 && a.q_starts != nullptr && rows > 128 && rows <= 256ll * 65535) return kv4_chunk_run(dtype, dim, a, s);
+  if (kv4_is_chunk(dim, a.group, a.max_q, a.q_starts == nullptr)) return kv4_chunk_run(dtype, dim, a, s);
   return dtype == GPTQ_BF16 ? attn_dim<__nv_bfloat16>(dim, a, s) : attn_dim<__half>(dim, a, s);
 }
 

@@ -185,13 +185,17 @@ struct AttnArgs {
   int seqs, max_q;
   float scale_log2;  // scale * log2(e)
   void* out;         // [tq][heads * group][dim]
-  float* part;       // workspace
+  long long* list;   // workspace: the prefix of the work list, for the join
+  float* part;       // workspace: pieces of cut items
   uint32_t up;       // 2^kPos of T (see code16)
   unsigned* status;
 };
 
 // The driver's tensor-map encoder (null when it cannot be had).
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+
+// Bytes of the workspace's work list (before the pieces).
+constexpr size_t kListBytes = 2304 * 8;
 
 // Geometry of the cache: blocks of 16 tokens, each
 //   K codes [16][dim / 2], K (scale, offset) [16][dim / 32], V codes, V (scale, offset).

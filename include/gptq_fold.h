@@ -481,11 +481,11 @@ gptq_status gptq_kv4_read(int dtype, const uint8_t* cache, long long pages, int 
  *            sequence (tq == seqs).
  *   max_q    host bound on the queries of one sequence.
  *   out      out T [tq][heads*group][dim] (dense).
- *   ws       >= gptq_kv4_attention_workspace_bytes(dim).
+ *   ws       >= gptq_kv4_attention_workspace_bytes(dim, group, max_q).
  * The values of one sequence's keys must be finite where any of its queries
  * sees them; what the pages hold past kv_lens is never used.
  */
-size_t gptq_kv4_attention_workspace_bytes(int dim);
+size_t gptq_kv4_attention_workspace_bytes(int dim, int group, int max_q);
 gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
                                const uint8_t* cache, long long pages, int heads, int group, int dim,
                                int page_size, const int* table, int table_stride,

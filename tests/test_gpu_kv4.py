@@ -290,7 +290,7 @@ def test_strided_queries_given_buffers_and_stream(lib):
     wide = torch.full((2, 12, 136), float("nan"), dtype=torch.float16, device="cuda")
     wide[:, 2:10, :128] = dev(q, torch.float16)
     out = torch.empty(2, 8, 128, dtype=torch.float16, device="cuda")
-    ws = _lib.workspace(lib.gptq_kv4_attention_workspace_bytes(128), "cuda")
+    ws = _lib.workspace(lib.gptq_kv4_attention_workspace_bytes(128, 4, 1), "cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     got = attend(wide[:, 2:10, :128], cache, table, lens, 16, "f16", out=out, ws=ws, stream=side)

@@ -128,4 +128,5 @@ def test_c_entries(blib):
     assert attend(dt=3) == 1 and attend(scale=float("nan")) == 1 and attend(q=mis) == 1 and attend(lens=None) == 1
     assert attend(ws=16) == 3
     assert attend(tq=0, starts=ok) == 0
-    assert lib.gptq_kv4_attention_workspace_bytes(96) == 0
+    assert lib.gptq_kv4_attention_workspace_bytes(96, 4, 1) == 0
+    assert lib.gptq_kv4_attention_workspace_bytes(64, 0, 1) == 0
