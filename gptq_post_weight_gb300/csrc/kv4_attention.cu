@@ -606,7 +606,7 @@ gptq_status attn_dim(int dim, const AttnArgs& a, cudaStream_t s) {
 // Many rows a sequence go to the tcgen05 kernel (kv4_chunk.cu).
 bool kv4_is_chunk(int dim, int group, int max_q, bool single) {
   const long long rows = (long long)max_q * group;
-  return dim <= 128 && !single && rows > 128 && rows <= (256ll << 11);
+  return dim <= 128 && !single && rows > 128 && rows <= 256 * 512;
 }
 
 size_t kv4_attention_ws_bytes(int dim, int group, int max_q, bool single) {

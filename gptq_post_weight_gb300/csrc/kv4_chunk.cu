@@ -6,14 +6,14 @@
 // tokens.  With so many rows the products bound it (4 * 128 * D flop a row
 // and step), and the decoding of the codes, done once for both tiles, and the
 // exponentials run beside them:
-//   warps 0-3, 4-7  softmax of tile A, B: a row a thread.  S from tensor
-//                   memory (twice: maximum, then exponentials), P written
-//                   back over it in T, the operand A of the second product;
-//   warps 8-10, 11-13  decode K, V of a step into shared memory in 128-byte
+//   warps 0-7, 8-15 softmax of tile A, B: half a row (64 scores) a thread.  The
+//                   halves exchange their maxima through shared memory; P goes
+//                   back over S in T, the operand A of the second product;
+//   warps 16-19, 20-23  decode K, V of a step into shared memory in 128-byte
 //                   swizzled rows of tokens (K is then a K-major operand, V
 //                   an N-major one: no transpose);
-//   warp 14         copies the step's cache blocks (untiled bulk copies);
-//   warp 15         issues the products: S_A, S_B of the next step between
+//   warp 24         copies the step's cache blocks (untiled bulk copies);
+//   warp 25         issues the products: S_A, S_B of the next step between
 //                   O_A += P_A V and O_B += P_B V, so that one tile's
 //                   softmax runs under the other's products.
 // The (sequence, row block, key head) tiles and their steps form one list, of
@@ -21,8 +21,8 @@
 // inside one share is finished there, a cut one leaves its maximum, sum and
 // unnormalised output (f32) in the workspace, and k_kv4_chunk_join adds the
 // pieces in the order of the list.
-// Tensor memory: S_A, S_B (128 columns each, P over their first half), O_A,
-// O_B (D columns each).
+// Tensor memory: S_A, S_B (128 columns each; P of each half of the keys over
+// the first 32 columns of its scores), O_A, O_B (D columns each).
 // The running maximum is only raised (and O rescaled, by its rows' threads,
 // after the step's commit has shown the last product done) when it would
 // grow by more than 2^8; exponentials stay within that and nothing is lost.
@@ -35,8 +35,8 @@ namespace {
 
 constexpr int CK = 128;     // keys a step
 constexpr int CROWS = 256;  // query rows a CTA
-constexpr int CTHREADS = 512;
-constexpr int CLIST = 2048;  // (sequence, row block) pairs of one launch at most
+constexpr int CTHREADS = 896;
+constexpr int CLIST = 512;   // (sequence, row block) pairs of one launch at most
 constexpr int CSTART = 3;    // what a tile's start and end cost, in steps
 constexpr float kNone = -1e30f;
 
@@ -55,6 +55,48 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two f32 numbers as one operand.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
+// Scores past column `lim` count nothing.
+__device__ __forceinline__ void hide(uint32_t (&v)[32], int lim) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i > lim) v[i] = 0xff800000u;  // -inf
+}
+
+// Barrier of tile x's 256 softmax threads, AND-reducing: they go on or leave
+// together.
+__device__ __forceinline__ bool tile_all(int x, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.and.pred po, %2, 256, pi;\n"
+      " selp.u32 %0, 1, 0, po;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(1 + x)
+      : "memory");
+  return r != 0u;
 }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
@@ -111,12 +153,14 @@ __device__ __forceinline__ uint32_t swz(int r, int p) { return (uint32_t)(r * 12
 template <int D>
 struct ChunkSmem {  // byte offsets; 1024-byte aligned operands
   static constexpr int kTile = CK * D * 2;           // K, V, and a tile of Q
-  static constexpr int kRaw = (CK / KV_BLOCK) * kv_block_bytes(D);
+  // Codes come in units of 128 groups (of K and of V): a group a decoding thread.
+  static constexpr int kTokens = 128 / (D / 32), kUnits = CK / kTokens, kBlocks = kTokens / KV_BLOCK;
+  static constexpr int kRaw = kBlocks * kv_block_bytes(D);
   static constexpr int q = 0;                        // two tiles
   static constexpr int k = q + 2 * kTile;            // two steps
-  static constexpr int v = k + 2 * kTile;            // one
-  static constexpr int raw = v + kTile;              // two steps
-  static constexpr int bytes = raw + 2 * kRaw + 1024;
+  static constexpr int v = k + 2 * kTile;            // two steps
+  static constexpr int raw = v + 2 * kTile;          // the units of one step
+  static constexpr int bytes = raw + kUnits * kRaw + 1024;
 };
 
 // One (sequence, row block) pair.
@@ -211,27 +255,28 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
   constexpr uint32_t kO = 256;  // tensor memory: S_A 0, S_B 128, O_A 256, O_B 256 + D
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t qfull, kfull[2], kempty[2], vfull, vempty, rawfull[2], rawempty[2], sfull[2],
+  __shared__ __align__(8) uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], rawfull[4], rawempty[4], sfull[2],
       pfull[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ long long pref[CLIST + 1], scratch[CTHREADS / 32];
   __shared__ int abort_sh;
+  __shared__ float xmax[2][2][2][128];  // [turn][tile][half][row]: what a row's halves tell each other
   volatile int* abort = &abort_sh;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    mbar_init(&qfull, 256);
+    mbar_init(&qfull, 512);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&kfull[i], 96), mbar_init(&kempty[i], 1);
-      mbar_init(&rawfull[i], 1), mbar_init(&rawempty[i], 6);
-      mbar_init(&sfull[i], 1), mbar_init(&pfull[i], 128);
+      mbar_init(&kfull[i], 128), mbar_init(&kempty[i], 1);
+      mbar_init(&vfull[i], 128), mbar_init(&vempty[i], 1);
+      mbar_init(&sfull[i], 1), mbar_init(&pfull[i], 256);
     }
-    mbar_init(&vfull, 96), mbar_init(&vempty, 1);
+    for (int i = 0; i < S::kUnits; ++i) mbar_init(&rawfull[i], 1), mbar_init(&rawempty[i], 8);
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == 15) {
+  if (warp == 25) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_sh)),
                  "r"(512u)
                  : "memory");
@@ -248,20 +293,22 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
     for (int i = threadIdx.x; i <= a.seqs * nblk; i += CTHREADS) a.list[i] = pref[i];  // for the join
   const long long ubeg = has ? W * blockIdx.x / shares : 0, uend = has ? W * (blockIdx.x + 1) / shares : 0;
 
-  // Registers: 128 a thread at launch (512 threads); a softmax thread keeps a
-  // row of scores, 2 * 128 * 184 + 2 * 128 * 72 = 65536 in all.
-  if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    const int x = warp / 4, rt = threadIdx.x & 127;
+  // Registers: 72 a thread at launch, 896 * 72 = 64512; then the softmax warps
+  // 80, the decoding ones 72, the last four 40: 4 * 128 * 80 + 2 * 128 * 72 +
+  // 128 * 40 = 64512.
+  if (warp < 16) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
+    const int x = warp / 8, half = warp / 4 % 2, rt = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = (uint32_t)(128 * x) + lanes, to = kO + (uint32_t)(D * x) + lanes;
+    const uint32_t ts = (uint32_t)(128 * x) + lanes, to = kO + (uint32_t)(D * x + D / 2 * half) + lanes;
     // (Not 0: a hidden key is a score of -inf, and -inf times 0 is no number.)
     const float sl = fmaxf(fabsf(a.scale_log2), 1e-30f);
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale: -q
     uint32_t sph = 0u, qph = 0u;  // phases of sfull[x], qfull
+    uint32_t par = 0u;            // of the exchange buffer
     bool ok = true;
 #pragma unroll 1
-    for (long long u = ubeg; u < uend && ok;) {
+    for (long long u = ubeg; u < uend;) {
       // What the steps need of the piece; the rest is looked up again for the
       // output, to leave the registers to the scores.
       int last, j, j1;
@@ -275,65 +322,67 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
         const bool mine = 128 * x + rt < pc.t.rows;
         const int rr = pc.t.r0 + min(128 * x + rt, pc.t.rows - 1);
         const int qi = rr / a.group, hq = pc.head * a.group + rr % a.group;
-        last = mine ? pc.t.len - pc.t.nq + qi : -1;
+        last = mine ? pc.t.len - pc.t.nq + qi - 64 * half : -1 - 64 * half;  // among this thread's columns
         j = pc.j0;
         j1 = min(pc.j1, pc.t.steps);  // (a tile that sees nothing: no steps)
         active = x == 0 || pc.t.rows > 128;
-        // The row's q, in the nibbles' order of channels.
-        const T* qp = static_cast<const T*>(a.q) + (long long)(pc.t.q0 + qi) * a.q_ts + (long long)hq * a.q_hs;
+        // Half of the row's q, in the nibbles' order of channels.
+        const T* qp = static_cast<const T*>(a.q) + (long long)(pc.t.q0 + qi) * a.q_ts + (long long)hq * a.q_hs +
+                      D / 2 * half;
         uint8_t* tile = smem + S::q + x * S::kTile;
+        uint4 v[D / 16];
 #pragma unroll
-        for (int c0 = 0; c0 < D / 8; c0 += 8) {
-          uint4 v[8];
+        for (int c = 0; c < D / 16; ++c) v[c] = mine ? *reinterpret_cast<const uint4*>(qp + 8 * c) : uint4{};
 #pragma unroll
-          for (int c = 0; c < 8; ++c) v[c] = mine ? *reinterpret_cast<const uint4*>(qp + 8 * (c0 + c)) : uint4{};
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint4 o = pair_order(v[c]);
-            o.x ^= flip, o.y ^= flip, o.z ^= flip, o.w ^= flip;
-            *reinterpret_cast<uint4*>(tile + c0 / 8 * (CK * 128) + swz(rt, c)) = o;
-          }
+        for (int c = 0; c < D / 16; ++c) {
+          const int at = D / 16 * half + c;
+          uint4 o = pair_order(v[c]);
+          o.x ^= flip, o.y ^= flip, o.z ^= flip, o.w ^= flip;
+          *reinterpret_cast<uint4*>(tile + at / 8 * (CK * 128) + swz(rt, at % 8)) = o;
         }
         fence_proxy_async_smem();
         mbar_arrive(&qfull);
         // Nobody is a piece ahead of the others.
-        if (!(ok = wait_bar_warp(&qfull, qph, abort, wc.ns))) break;
+        ok = tile_all(x, wait_bar_warp(&qfull, qph, abort, wc.ns));
+        if (!ok) break;
         qph ^= 1u;
       }
       float m = kNone, l = 0.f;
       bool began = false;
 #pragma unroll 1
       for (; active && j < j1; ++j) {
-        if (!(ok = wait_bar_warp(&sfull[x], sph, abort, wc.ns))) break;
+        ok = wait_bar_warp(&sfull[x], sph, abort, wc.ns);
         sph ^= 1u;
-        tc_fence_after();
-        uint32_t v[4][32];  // the row's scores, in registers from here on
+        const int lim = last - j * CK;  // last visible column of this half
+        const bool masked = __any_sync(0xffffffffu, lim < 63);
+        float top = -INFINITY;
+        if (ok) {
+          tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32u * (uint32_t)c, v[c]);
-        tmem_ld_wait();
-        const int lim = last - j * CK;  // last visible column of the step
-        if (__any_sync(0xffffffffu, lim < CK - 1)) {
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[32];
+            tmem_ld32(ts + 64u * (uint32_t)half + 32u * (uint32_t)c, v);
+            tmem_ld_wait();
+            if (masked) hide(v, lim - 32 * c);
+            float t2[2] = {top, fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]))};
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i > lim) v[c][i] = 0xff800000u;  // -inf
+            for (int i = 2; i < 32; i += 2)
+              t2[i / 2 & 1] = max3(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), t2[i / 2 & 1]);
+            top = fmaxf(t2[0], t2[1]);
+          }
+          xmax[par][x][half][rt] = top;
         }
-        float t4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          t4[c] = max3(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]), -INFINITY);
-#pragma unroll
-          for (int i = 2; i < 32; i += 2) t4[c] = max3(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]), t4[c]);
-        }
-        const float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+        if (!(ok = tile_all(x, ok))) break;
+        top = fmaxf(top, xmax[par][x][half ^ 1][rt]);
+        par ^= 1u;
+        // Both halves of a row decide alike: they see the same numbers.
         if (__any_sync(0xffffffffu, sl * (top - m) > 8.f)) {
           const float nm = fmaxf(m, top), f = ex2(sl * (m - nm));
           m = nm;
           l *= f;
           if (began) {
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int c = 0; c < D / 2; c += 16) {
               uint32_t w[16];
               tmem_ld16(to + (uint32_t)c, w);
               tmem_ld_wait();
@@ -343,33 +392,44 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
             }
           }
         }
-        const float ms = sl * m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // Two at a time: p = 2^(sl s - sl m).
+        const float ms = -sl * m;
+        const uint64_t sl2 = pack2(sl, sl), ms2 = pack2(ms, ms);
+        uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t p[16];
+        for (int c = 0; c < 2; ++c) {
+          // (Read again: a row of 128 does not leave registers enough for the
+          // number of warps that hide these latencies.)
+          uint32_t v[32], p[16];
+          tmem_ld32(ts + 64u * (uint32_t)half + 32u * (uint32_t)c, v);
+          tmem_ld_wait();
+          if (masked) hide(v, lim - 32 * c);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float e0 = ex2(fmaf(sl, __uint_as_float(v[c][2 * i]), -ms)),
-                        e1 = ex2(fmaf(sl, __uint_as_float(v[c][2 * i + 1]), -ms));
-            sum[2 * i & 3] += e0;
-            sum[(2 * i + 1) & 3] += e1;
+            const float2 e = unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sl2, ms2));
+            const float e0 = ex2(e.x), e1 = ex2(e.y);
+            sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
             p[i] = bits2(Elem<T>::make2(e0, e1));
           }
-          tmem_st16(ts + 16u * (uint32_t)c, p);
+          tmem_st16(ts + 64u * (uint32_t)half + 16u * (uint32_t)c, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 s0 = unpack2(sum2[0]), s1 = unpack2(sum2[1]);
+        l += (s0.x + s0.y) + (s1.x + s1.y);
         tmem_st_wait();
         tc_fence_before();
         arrive_relaxed(&pfull[x]);
         began = true;
       }
-      // The output, once the last product is done.
-      if (ok && began) {
+      if (!ok) break;
+      // The output, once the last product is done; the halves' sums meet.
+      if (began) {
         ok = wait_bar_warp(&sfull[x], sph, abort, wc.ns);
         sph ^= 1u;
       }
-      if (!ok) break;
+      xmax[par][x][half][rt] = l;
+      if (!(ok = tile_all(x, ok))) break;
+      l += xmax[par][x][half ^ 1][rt];
+      par ^= 1u;
       tc_fence_after();
       const Piece pc = piece_at(a, nblk, pref, u, uend);
       u = pc.next;
@@ -378,10 +438,10 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       const int rr = pc.t.r0 + min(128 * x + rt, pc.t.rows - 1);
       const int qi = rr / a.group, hq = pc.head * a.group + rr % a.group;
       const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing: zeros
-      T* dst = static_cast<T*>(a.out) + ((long long)(pc.t.q0 + qi) * a.heads * a.group + hq) * D;
+      T* dst = static_cast<T*>(a.out) + ((long long)(pc.t.q0 + qi) * a.heads * a.group + hq) * D + D / 2 * half;
       float* part = a.part + ((size_t)blockIdx.x * 2 + (pc.j0 == 0 ? 1 : 0)) * piece_floats(D);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
+      for (int c = 0; c < D / 2; c += 16) {
         uint32_t v[16];
         if (began) {
           tmem_ld16(to + (uint32_t)c, v);
@@ -401,35 +461,35 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
             o.w = bits2(Elem<T>::make2(e[6] * inv, e[7] * inv));
             *reinterpret_cast<uint4*>(dst + c + 8 * h) = o;
           } else {
-            float4* o = reinterpret_cast<float4*>(part + (size_t)(128 * x + rt) * D + c + 8 * h);
+            float4* o = reinterpret_cast<float4*>(part + (size_t)(128 * x + rt) * D + D / 2 * half + c + 8 * h);
             o[0] = float4{e[0], e[1], e[2], e[3]};
             o[1] = float4{e[4], e[5], e[6], e[7]};
           }
         }
       }
-      if (!pc.whole && mine)
+      if (!pc.whole && mine && half == 0)
         *reinterpret_cast<float2*>(part + (size_t)CROWS * D + 2 * (128 * x + rt)) = float2{m, l};
       tc_fence_before();
     }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  }
-  if (warp >= 8 && warp < 14) {
-    // Three warps decode K, three V.  A thread takes 32 channels (one group)
-    // of a token at a time: 16 bytes of codes to 64 bytes; it stays with its
-    // group and its token's place among eight, so that its addresses advance
-    // by constants.  Lanes of the upper half of the channels store their
-    // pieces in another order: eight lanes then meet no bank twice.
-    const int dt = (threadIdx.x - 256) % 96;
-    const bool isv = warp >= 11;
-    constexpr int GR = D / 32, TSTEP = 96 / GR;  // groups a token; tokens between a thread's pieces
-    const int grp = dt % GR, tok0 = dt / GR;
+  } else if (warp < 24) {
+    // Four warps decode K, four V: a thread takes 32 channels (one group) of
+    // a token of each unit, 16 bytes of codes to 64 bytes.  Lanes of the upper
+    // half of the channels store their pieces in another order: eight lanes
+    // then meet no bank twice.
+    const int dt = threadIdx.x & 127;
+    const bool isv = warp >= 20;
+    constexpr int GR = D / 32;  // groups a token
+    const int grp = dt % GR, tok = dt / GR;
     const bool swap = GR == 4 && grp >= 2;
-    const int rot = swap ? 2 : 0;
     uint32_t off[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      off[u] = (uint32_t)(grp / 2 * (CK * 128)) + swz(tok0, grp % 2 * 4 + (u ^ rot));
+      off[u] = (uint32_t)(grp / 2 * (CK * 128)) + swz(tok, grp % 2 * 4 + (u ^ (swap ? 2 : 0)));
+    const uint8_t* from = smem + S::raw + tok / KV_BLOCK * BB + (isv ? kv_value_off(D) : 0);
+    const uint8_t* from_codes = from + tok % KV_BLOCK * (D / 2) + grp * 16;
+    const uint8_t* from_par = from + kv_param_off(D) + tok % KV_BLOCK * (D / 8) + grp * 4;
+    uint64_t* full = isv ? vfull : kfull;
+    uint64_t* empty = isv ? vempty : kempty;
     bool ok = true;
     int n = 0;  // steps so far
 #pragma unroll 1
@@ -439,19 +499,17 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
 #pragma unroll 1
       for (int j = pc.j0; j < min(pc.j1, pc.t.steps); ++j, ++n) {
         const int st = n & 1;
-        if (!(ok = wait_bar_warp(&rawfull[st], (uint32_t)(n >> 1) & 1u, abort, wc.ns))) break;
-        ok = isv ? wait_bar_warp(&vempty, ((uint32_t)n & 1u) ^ 1u, abort, wc.ns)
-                 : wait_bar_warp(&kempty[st], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort, wc.ns);
-        if (!ok) break;
-        const uint8_t* raw = smem + S::raw + st * S::kRaw + (isv ? kv_value_off(D) : 0);
-        uint8_t* tile = smem + (isv ? S::v : S::k + st * S::kTile);
-        const int seen = pc.t.vis - j * CK;  // tokens of the step that some row sees
-#pragma unroll 3
-        for (int tok = tok0; tok < CK; tok += TSTEP) {
-          const uint8_t* blk = raw + tok / KV_BLOCK * BB;
-          uint4 codes = *reinterpret_cast<const uint4*>(blk + tok % KV_BLOCK * (D / 2) + grp * 16);
-          uint32_t par = *reinterpret_cast<const uint32_t*>(blk + kv_param_off(D) + tok % KV_BLOCK * (D / 8) + grp * 4);
-          if (tok >= seen) par = 0u;  // past what any row sees: no value, whatever is there
+        if (!(ok = wait_bar_warp(&empty[st], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort, wc.ns))) break;
+        uint8_t* tile = smem + (isv ? S::v : S::k) + st * S::kTile;
+        const int seen = pc.t.vis - j * CK - tok;  // tokens from this thread's on that some row sees
+#pragma unroll 1
+        for (int q = 0; q < S::kUnits; ++q) {
+          if (!(ok = wait_bar_warp(&rawfull[q], (uint32_t)n & 1u, abort, wc.ns))) break;
+          uint4 codes = *reinterpret_cast<const uint4*>(from_codes + q * S::kRaw);
+          uint32_t par = *reinterpret_cast<const uint32_t*>(from_par + q * S::kRaw);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&rawempty[q]);
+          if (q * S::kTokens >= seen) par = 0u;  // past what any row sees: no value, whatever is there
           if (GR == 4) {
             const uint4 c = codes;
             codes.x = swap ? c.z : c.x, codes.y = swap ? c.w : c.y;
@@ -459,25 +517,26 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
           }
           const T2 s2 = from_bits2<T2>(__byte_perm(par, par, 0x1010)), z2 = from_bits2<T2>(__byte_perm(par, par, 0x3232));
           const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-          uint8_t* dst = tile + (tok - tok0) * 128;
+          uint8_t* dst = tile + q * S::kTokens * 128;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int e = 0; e < 4; ++e) {
             uint4 o;
-            o.x = bits2(__hfma2(code16<T>(w[u], 0, a.up), s2, z2));
-            o.y = bits2(__hfma2(code16<T>(w[u], 1), s2, z2));
-            o.z = bits2(__hfma2(code16<T>(w[u], 2), s2, z2));
-            o.w = bits2(__hfma2(code16<T>(w[u], 3), s2, z2));
-            *reinterpret_cast<uint4*>(dst + off[u]) = o;
+            o.x = bits2(__hfma2(code16<T>(w[e], 0, a.up), s2, z2));
+            o.y = bits2(__hfma2(code16<T>(w[e], 1), s2, z2));
+            o.z = bits2(__hfma2(code16<T>(w[e], 2), s2, z2));
+            o.w = bits2(__hfma2(code16<T>(w[e], 3), s2, z2));
+            *reinterpret_cast<uint4*>(dst + off[e]) = o;
           }
         }
+        if (!ok) break;
         fence_proxy_async_smem();
-        mbar_arrive(isv ? &vfull : &kfull[st]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&rawempty[st]);
+        mbar_arrive(&full[st]);
       }
     }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   }
-  if (warp == 14) {
+  if (warp == 24) {
     if (!wc.no_loads) {
       const int bpp = a.page_size / KV_BLOCK;
       bool ok = true;
@@ -490,27 +549,37 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
         const int* trow = a.table + (long long)pc.b * a.table_stride;
 #pragma unroll 1
         for (int j = pc.j0; j < min(pc.j1, pc.t.steps); ++j, ++n) {
-          const int st = n & 1, blk = j * (CK / KV_BLOCK) + lane;
+          const int blk = j * (CK / KV_BLOCK) + lane;
           const bool in = lane < CK / KV_BLOCK && blk < nb;
           const unsigned e = in ? (unsigned)trow[blk / bpp] : 0u;  // an entry outside the pool reads page 0
           const long long page = e < (unsigned long long)a.pages ? (long long)e : 0;
-          if (!(ok = wait_bar_warp(&rawempty[st], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort, wc.ns))) break;
-          if (lane == 0) mbar_expect_tx(&rawfull[st], (uint32_t)(min(CK / KV_BLOCK, nb - j * (CK / KV_BLOCK)) * BB));
-          __syncwarp();
-          if (in)
-            bulk_load(smem_u32(smem + S::raw + st * S::kRaw + lane * BB),
-                      a.cache + ((page * a.heads + pc.head) * bpp + blk % bpp) * (long long)BB, BB, &rawfull[st]);
+          const uint8_t* src = a.cache + ((page * a.heads + pc.head) * bpp + blk % bpp) * (long long)BB;
+#pragma unroll 1
+          for (int q = 0; q < S::kUnits; ++q) {
+            if (!(ok = wait_bar_warp(&rawempty[q], ((uint32_t)n & 1u) ^ 1u, abort, wc.ns))) break;
+            const int have = min(max(nb - j * (CK / KV_BLOCK) - q * S::kBlocks, 0), S::kBlocks);
+            if (lane == 0) {
+              if (have > 0)
+                mbar_expect_tx(&rawfull[q], (uint32_t)(have * BB));
+              else
+                mbar_arrive(&rawfull[q]);  // nothing of the unit is seen
+            }
+            __syncwarp();
+            if (in && lane / S::kBlocks == q)
+              bulk_load(smem_u32(smem + S::raw + lane * BB), src, BB, &rawfull[q]);
+          }
+          if (!ok) break;
         }
       }
     }
-  } else if (warp == 15) {
+  } else if (warp == 25) {
     uint32_t one;
     asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(one));
     constexpr uint32_t fmt = MmaFormat<T>::k;
     constexpr uint32_t ids = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(CK >> 3) << 17) | (8u << 24);
     constexpr uint32_t idp = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
     const uint64_t qd = sdesc(smem_u32(smem + S::q)), kd = sdesc(smem_u32(smem + S::k));
-    const uint64_t vd = ndesc(smem_u32(smem + S::v), CK * 128);
+    const uint64_t vd0 = ndesc(smem_u32(smem + S::v), CK * 128);
     auto score = [&](int x, int st) {  // S_x = Q_x K^T
 #pragma unroll
       for (int h = 0; h < HALVES; ++h)
@@ -519,10 +588,11 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
           mma_ss((uint32_t)(128 * x), qd + (uint64_t)((x * S::kTile + h * CK * 128 + 32 * k) >> 4),
                  kd + (uint64_t)((st * S::kTile + h * CK * 128 + 32 * k) >> 4), ids, (h || k) ? 1u : 0u);
     };
-    auto value = [&](int x, int j) {  // O_x += P_x V
+    auto value = [&](int x, int st, int j) {  // O_x += P_x V
+      const uint64_t vd = vd0 + (uint64_t)((st * S::kTile) >> 4);
 #pragma unroll
       for (int k = 0; k < CK / 16; ++k)
-        mma_ts(kO + (uint32_t)(D * x), (uint32_t)(128 * x + 8 * k), vd + (uint64_t)((2048 * k) >> 4), idp,
+        mma_ts(kO + (uint32_t)(D * x), (uint32_t)(128 * x + k / 4 * 64 + k % 4 * 8), vd + (uint64_t)((2048 * k) >> 4), idp,
                (j || k) ? 1u : 0u);
     };
     bool ok = true;
@@ -554,13 +624,13 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
         const int nx = (n + 1) & 1;
         const bool more = j + 1 < count;
         if (more && !(ok = wait_bar_warp(&kfull[nx], (uint32_t)((n + 1) >> 1) & 1u, abort, wc.ns))) break;
-        if (!(ok = wait_bar_warp(&vfull, (uint32_t)n & 1u, abort, wc.ns))) break;
+        if (!(ok = wait_bar_warp(&vfull[n & 1], (uint32_t)(n >> 1) & 1u, abort, wc.ns))) break;
         if (!(ok = wait_bar_warp(&pfull[0], pph[0], abort, wc.ns))) break;
         pph[0] ^= 1u;
         tc_fence_after();
         if (one) {
-          value(0, j);
-          if (!two) mma_commit(&vempty);
+          value(0, n & 1, j);
+          if (!two) mma_commit(&vempty[n & 1]);
           if (more) score(0, nx);
           mma_commit(&sfull[0]);
           if (!two && more) mma_commit(&kempty[nx]);
@@ -570,8 +640,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
           pph[1] ^= 1u;
           tc_fence_after();
           if (one) {
-            value(1, j);
-            mma_commit(&vempty);
+            value(1, n & 1, j);
+            mma_commit(&vempty[n & 1]);
             if (more) score(1, nx);
             mma_commit(&sfull[1]);
             if (more) mma_commit(&kempty[nx]);
@@ -595,25 +665,33 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
     if (threadIdx.x == 0 && a.status != nullptr) atomicOr(a.status, 2u);
   }
   tc_fence_after();
-  if (warp == 15)
+  if (warp == 25)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base_sh), "r"(512u) : "memory");
 }
 
-// Adds the pieces of a tile that more than one CTA shared: a CTA takes 32
-// rows of a (pair, head) tile, a warp a row at a time.
+// Adds the pieces of the tiles that more than one CTA shared.  Block (c, i)
+// looks at the cut between shares c and c + 1: if it is the first one inside
+// a tile's steps, the block takes 32 of the tile's rows, a warp a row.
 template <class T, int D>
 __global__ void __launch_bounds__(256) k_kv4_chunk_join(AttnArgs a, int nblk, int grid) {
-  const int p = (int)blockIdx.x / a.heads, head = (int)blockIdx.x % a.heads;
-  const Pair t = pair_of(a, p / nblk, p % nblk);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the list and the pieces are there
+  const long long W = a.list[a.seqs * nblk] * a.heads;
+  const long long shares = min(W, (long long)grid);
+  if ((long long)blockIdx.x + 1 >= shares) return;
+  const long long cut = W * (blockIdx.x + 1) / shares;
+  int lo = 0, hi = a.seqs * nblk - 1;  // the tile that holds unit cut - 1
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (a.list[mid] * a.heads <= cut - 1) lo = mid; else hi = mid - 1;
+  }
+  const Pair t = pair_of(a, lo / nblk, lo % nblk);
   const int r1 = min(t.rows, ((int)blockIdx.y + 1) * 32);
   if ((int)blockIdx.y * 32 >= r1) return;
+  const int n = units_of(t), head = (int)((cut - 1 - a.list[lo] * a.heads) / n);
+  const long long u0 = a.list[lo] * a.heads + (long long)head * n;
   // The shares of the first and the last step.
-  const int n = units_of(t);
-  const long long W = a.list[a.seqs * nblk] * a.heads, u0 = a.list[p] * a.heads + (long long)head * n;
-  const long long shares = min(W, (long long)grid);
   const int first = (int)(((u0 + CSTART + 1) * shares - 1) / W), lastc = (int)(((u0 + n) * shares - 1) / W);
-  if (first == lastc) return;
+  if (first == lastc || first != (int)blockIdx.x) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const float sl = fmaxf(fabsf(a.scale_log2), 1e-30f);
   for (int r = (int)blockIdx.y * 32 + warp; r < r1; r += 8) {
@@ -661,7 +739,7 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
       GQ_LAUNCHED();
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.seqs * nblk * a.heads), CROWS / 32);
+    cfg.gridDim = dim3((unsigned)grid, CROWS / 32);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
