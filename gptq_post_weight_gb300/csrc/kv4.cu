@@ -14,8 +14,10 @@
 // back as NaN.
 //
 // Both kernels move each byte once: four lanes share a group (16 bytes of T
-// a lane), a thread does the key and the value of its place, so that the
-// slot is looked up once and two loads are in flight.
+// a lane), a thread does the key and the value of its place, so that two
+// loads are in flight for each.  A block looks its tokens' slots up once, into
+// shared memory: the divisions of a 64-bit slot would otherwise be most of
+// what a place costs.
 #include "serve.cuh"
 
 namespace gq {
@@ -27,14 +29,33 @@ struct CacheShape {
   int heads, dim, page_size;
 };
 
-// Byte address of the block that holds `slot` for `head`; null when the slot
+constexpr int MAXTOK = 128;  // tokens of one CTA at most: a token has at least eight places
+
+// Byte address of the block that holds `slot` for head 0; null when the slot
 // is not in the pool (negative slots mark padding).
-__device__ __forceinline__ uint8_t* block_of(const CacheShape& c, long long slot, int head) {
-  const long long page = slot < 0 ? -1 : slot / c.page_size;
-  if (page < 0 || page >= c.pages) return nullptr;
-  const int off = (int)(slot - page * c.page_size);
+__device__ __forceinline__ uint8_t* block_of(const CacheShape& c, long long slot) {
+  if (slot < 0) return nullptr;
   const int bpp = c.page_size / KV_BLOCK;
-  return c.base + ((page * c.heads + head) * bpp + off / KV_BLOCK) * (long long)kv_block_bytes(c.dim);
+  const long long blk = slot / KV_BLOCK;
+  // (A 32-bit division is a quarter of a 64-bit one.)
+  const long long page = blk >> 32 ? blk / bpp : (long long)((uint32_t)blk / (uint32_t)bpp);
+  if (page >= c.pages) return nullptr;
+  return c.base + (page * c.heads * bpp + (blk - page * bpp)) * (long long)kv_block_bytes(c.dim);
+}
+
+// What a CTA knows of its tokens.
+struct Tokens {
+  uint8_t* blk[MAXTOK];
+  int row[MAXTOK];
+};
+
+__device__ __forceinline__ void look_up(Tokens& t, const CacheShape& c, const long long* slots, long long tok0, int n) {
+  if ((int)threadIdx.x < n) {
+    const long long slot = slots[tok0 + threadIdx.x];
+    t.blk[threadIdx.x] = block_of(c, slot);
+    t.row[threadIdx.x] = (int)(slot & (KV_BLOCK - 1));  // page_size is a multiple of the block
+  }
+  __syncthreads();
 }
 
 // Quantises the eight elements of one lane (four lanes a group): the word of
@@ -43,18 +64,15 @@ template <class T>
 __device__ __forceinline__ uint32_t quantise8(uint4 raw, uint32_t& par) {
   using T2 = typename Elem<T>::T2;
   const T2 a = from_bits2<T2>(raw.x), b = from_bits2<T2>(raw.y), c = from_bits2<T2>(raw.z), d = from_bits2<T2>(raw.w);
-  const float2 mn2 = Elem<T>::to2(__hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d)));
-  const float2 mx2 = Elem<T>::to2(__hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d)));
-  // A NaN on either side must survive: x + 0 * y keeps it where fminf drops it.
-  float lo = fminf(mn2.x, mn2.y), hi = fmaxf(mx2.x, mx2.y);
-  if (mn2.x != mn2.x || mn2.y != mn2.y) lo = hi = __int_as_float(0x7fffffff);
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    const float l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
-    const bool nan = l2 != l2 || lo != lo;
-    lo = nan ? __int_as_float(0x7fffffff) : fminf(lo, l2);
-    hi = nan ? __int_as_float(0x7fffffff) : fmaxf(hi, h2);
-  }
+  T2 mn = __hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d));
+  T2 mx = __hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d));
+  // Both ends in one pair, (lo, -hi), for the steps across the lanes.
+  const uint32_t n = bits2(mn), x = bits2(mx) ^ 0x80008000u;
+  T2 e = __hmin2_nan(from_bits2<T2>(__byte_perm(n, x, 0x5410)), from_bits2<T2>(__byte_perm(n, x, 0x7632)));
+  e = __hmin2_nan(e, from_bits2<T2>(__shfl_xor_sync(0xffffffffu, bits2(e), 1)));
+  e = __hmin2_nan(e, from_bits2<T2>(__shfl_xor_sync(0xffffffffu, bits2(e), 2)));
+  const float2 ends = Elem<T>::to2(e);
+  const float lo = ends.x, hi = -ends.y;
   T st = Elem<T>::from(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f));
   float s = Elem<T>::to(st);
   T zt = Elem<T>::from(__fsub_rn(lo, __fmul_rn(16.0f, s)));
@@ -63,13 +81,20 @@ __device__ __forceinline__ uint32_t quantise8(uint4 raw, uint32_t& par) {
   if (isfinite(s) && isfinite(z)) {
     const float r = s > 0.f ? __frcp_rn(s) : 0.f;
     const float2 f[4] = {Elem<T>::to2(a), Elem<T>::to2(b), Elem<T>::to2(c), Elem<T>::to2(d)};
+    // The clamp's ends are integers, so that it may come before the rounding;
+    // adding 3 * 2^22 then rounds to the nearest even and leaves the integer
+    // in the low bits.
+    uint32_t q[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float q0 = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(f[i].x, z), r)), 16.f), 31.f);
-      const float q1 = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(f[i].y, z), r)), 16.f), 31.f);
-      w |= ((uint32_t)q0 - 16u) << (8 * i);
-      w |= ((uint32_t)q1 - 16u) << (8 * i + 4);
+      const float q0 = fminf(fmaxf(__fmul_rn(__fsub_rn(f[i].x, z), r), 16.f), 31.f);
+      const float q1 = fminf(fmaxf(__fmul_rn(__fsub_rn(f[i].y, z), r), 16.f), 31.f);
+      q[2 * i] = __float_as_uint(__fadd_rn(q0, 12582912.f));
+      q[2 * i + 1] = __float_as_uint(__fadd_rn(q1, 12582912.f));
     }
+    const uint32_t even = __byte_perm(__byte_perm(q[0], q[2], 0x0040), __byte_perm(q[4], q[6], 0x0040), 0x5410);
+    const uint32_t odd = __byte_perm(__byte_perm(q[1], q[3], 0x0040), __byte_perm(q[5], q[7], 0x0040), 0x5410);
+    w = (even & 0x0f0f0f0fu) | ((odd << 4) & 0xf0f0f0f0u);
     par = (uint32_t)*reinterpret_cast<uint16_t*>(&st) | ((uint32_t)*reinterpret_cast<uint16_t*>(&zt) << 16);
   } else {
     par = 0x7fff7fffu;  // NaN in both types
@@ -97,63 +122,100 @@ struct Strides {
   long long kt, kh, vt, vh;  // elements between tokens and between heads
 };
 
-// A place: (token, head, eight channels).  per = heads * dim / 8 a token.
+// A place: (token, head, eight channels).  per = heads * dim / 8 a token; a CTA
+// has `take` tokens, place i of them is token i / per (per_inv = ceil(2^32 /
+// per): exact for the places of a CTA, which are less than 2^16 or one token's).
 template <class T>
 __global__ void __launch_bounds__(256)
     k_kv4_write(CacheShape c, const T* __restrict__ k, const T* __restrict__ v, Strides st,
-                const long long* __restrict__ slots, int tokens, int per) {
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long total = (long long)tokens * per;
-  const long long tok = id / per;
-  const bool in = id < total;
-  const int at = (int)(id - tok * per), cpr = c.dim / 8;
-  const int head = at / cpr, ch = at % cpr;
-  uint8_t* blk = in ? block_of(c, slots[tok], head) : nullptr;
-  uint4 rk{}, rv{};
-  if (blk != nullptr) {
-    rk = *reinterpret_cast<const uint4*>(k + tok * st.kt + head * st.kh + ch * 8);
-    rv = *reinterpret_cast<const uint4*>(v + tok * st.vt + head * st.vh + ch * 8);
-  }
-  // The four lanes of a group are always active together (dim % 32 == 0).
-  uint32_t pk, pv;
-  const uint32_t wk = quantise8<T>(rk, pk), wv = quantise8<T>(rv, pv);
-  if (blk == nullptr) return;
-  const int row = (int)(slots[tok] % KV_BLOCK);  // page_size is a multiple of the block
-  uint8_t* kb = blk + row * (c.dim / 2) + ch * 4;
-  *reinterpret_cast<uint32_t*>(kb) = wk;
-  *reinterpret_cast<uint32_t*>(kb + kv_value_off(c.dim)) = wv;
-  if ((ch & 3) == 0) {
-    uint8_t* pb = blk + kv_param_off(c.dim) + row * (c.dim / 8) + ch;
-    *reinterpret_cast<uint32_t*>(pb) = pk;
-    *reinterpret_cast<uint32_t*>(pb + kv_value_off(c.dim)) = pv;
+                const long long* __restrict__ slots, int tokens, int per, uint32_t per_inv, int take) {
+  __shared__ Tokens ts;
+  const long long tok0 = (long long)blockIdx.x * take;
+  const int n = (int)min((long long)take, tokens - tok0);
+  look_up(ts, c, slots, tok0, n);
+  const int cl = c.dim == 256 ? 5 : c.dim == 128 ? 4 : 3;  // log2(dim / 8)
+  const long long head_bytes = (long long)(c.page_size / KV_BLOCK) * kv_block_bytes(c.dim);
+  const int total = n * per;
+#pragma unroll 2
+  for (int i = threadIdx.x; (i & ~31) < total; i += 256) {
+    const bool in = i < total;
+    const int tok = take == 1 || !in ? 0 : (int)__umulhi((uint32_t)i, per_inv);
+    const int at = i - tok * per, head = at >> cl, ch = at & ((1 << cl) - 1);
+    uint8_t* blk = in ? ts.blk[tok] : nullptr;
+    uint4 rk{}, rv{};
+    if (blk != nullptr) {
+      rk = *reinterpret_cast<const uint4*>(k + (tok0 + tok) * st.kt + head * st.kh + ch * 8);
+      rv = *reinterpret_cast<const uint4*>(v + (tok0 + tok) * st.vt + head * st.vh + ch * 8);
+    }
+    // The four lanes of a group always come together (dim % 32 == 0).
+    uint32_t pk, pv;
+    const uint32_t wk = quantise8<T>(rk, pk), wv = quantise8<T>(rv, pv);
+    if (blk != nullptr) {
+      blk += head * head_bytes;
+      const int row = ts.row[tok];
+      uint8_t* kb = blk + row * (c.dim / 2) + ch * 4;
+      *reinterpret_cast<uint32_t*>(kb) = wk;
+      *reinterpret_cast<uint32_t*>(kb + kv_value_off(c.dim)) = wv;
+      if ((ch & 3) == 0) {
+        uint8_t* pb = blk + kv_param_off(c.dim) + row * (c.dim / 8) + ch;
+        *reinterpret_cast<uint32_t*>(pb) = pk;
+        *reinterpret_cast<uint32_t*>(pb + kv_value_off(c.dim)) = pv;
+      }
+    }
   }
 }
 
 template <class T>
 __global__ void __launch_bounds__(256)
-    k_kv4_read(CacheShape c, const long long* __restrict__ slots, int tokens, int per, T* __restrict__ k,
-               T* __restrict__ v) {
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (id >= (long long)tokens * per) return;
-  const long long tok = id / per;
-  const int at = (int)(id - tok * per), cpr = c.dim / 8;
-  const int head = at / cpr, ch = at % cpr;
-  const long long slot = slots[tok];
-  const uint8_t* blk = block_of(c, slot, head);
-  uint4 ok{}, ov{};
-  if (blk != nullptr) {
-    const int row = (int)(slot % KV_BLOCK);
-    const uint8_t* kb = blk + row * (c.dim / 2) + ch * 4;
-    const uint8_t* pb = blk + kv_param_off(c.dim) + row * (c.dim / 8) + (ch & ~3);
-    const uint32_t wk = *reinterpret_cast<const uint32_t*>(kb);
-    const uint32_t wv = *reinterpret_cast<const uint32_t*>(kb + kv_value_off(c.dim));
-    const uint32_t pk = *reinterpret_cast<const uint32_t*>(pb);
-    const uint32_t pv = *reinterpret_cast<const uint32_t*>(pb + kv_value_off(c.dim));
-    ok = values8<T>(wk, pk);
-    ov = values8<T>(wv, pv);
+    k_kv4_read(CacheShape c, const long long* __restrict__ slots, int tokens, int per, uint32_t per_inv, int take,
+               T* __restrict__ k, T* __restrict__ v) {
+  __shared__ Tokens ts;
+  const long long tok0 = (long long)blockIdx.x * take;
+  const int n = (int)min((long long)take, tokens - tok0);
+  look_up(ts, c, slots, tok0, n);
+  const int cl = c.dim == 256 ? 5 : c.dim == 128 ? 4 : 3;  // log2(dim / 8)
+  const long long head_bytes = (long long)(c.page_size / KV_BLOCK) * kv_block_bytes(c.dim);
+  const int total = n * per;
+  uint4* ko = reinterpret_cast<uint4*>(k) + tok0 * per;
+  uint4* vo = reinterpret_cast<uint4*>(v) + tok0 * per;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < total; i += 256) {
+    const int tok = take == 1 ? 0 : (int)__umulhi((uint32_t)i, per_inv);
+    const int at = i - tok * per, head = at >> cl, ch = at & ((1 << cl) - 1);
+    const uint8_t* blk = ts.blk[tok];
+    uint4 ok{}, ov{};
+    if (blk != nullptr) {
+      blk += head * head_bytes;
+      const int row = ts.row[tok];
+      const uint8_t* kb = blk + row * (c.dim / 2) + ch * 4;
+      const uint8_t* pb = blk + kv_param_off(c.dim) + row * (c.dim / 8) + (ch & ~3);
+      const uint32_t wk = *reinterpret_cast<const uint32_t*>(kb);
+      const uint32_t wv = *reinterpret_cast<const uint32_t*>(kb + kv_value_off(c.dim));
+      const uint32_t pk = *reinterpret_cast<const uint32_t*>(pb);
+      const uint32_t pv = *reinterpret_cast<const uint32_t*>(pb + kv_value_off(c.dim));
+      ok = values8<T>(wk, pk);
+      ov = values8<T>(wv, pv);
+    }
+    __stcs(ko + i, ok);
+    __stcs(vo + i, ov);
   }
-  reinterpret_cast<uint4*>(k)[id] = ok;
-  reinterpret_cast<uint4*>(v)[id] = ov;
+}
+
+// Tokens a CTA: PLACES a thread when that still fills the GPU, else one.
+struct Split {
+  int take;
+  unsigned grid;
+  uint32_t per_inv;
+};
+
+Split split_of(int tokens, int per) {
+  const long long places = (long long)tokens * per;
+  const int want = places >= 152ll * 8 * 1024 ? 1024 : 256;
+  Split s;
+  s.take = std::min(std::max(want / per, 1), MAXTOK);
+  s.grid = (unsigned)((tokens + s.take - 1) / s.take);
+  s.per_inv = (uint32_t)(((1ull << 32) + per - 1) / per);
+  return s;
 }
 
 }  // namespace
@@ -165,12 +227,12 @@ gptq_status kv4_write_run(int dtype, uint8_t* cache, long long pages, int heads,
   const CacheShape c{cache, pages, heads, dim, page_size};
   const Strides st{kt, kh, vt, vh};
   const int per = heads * (dim / 8);
-  const unsigned grid = (unsigned)(((long long)tokens * per + 255) / 256);
+  const Split p = split_of(tokens, per);
   GQ_PROF(K_KV4_WRITE, s);
   if (dtype == GPTQ_BF16)
-    k_kv4_write<<<grid, 256, 0, s>>>(c, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, st, slots, tokens, per);
+    k_kv4_write<<<p.grid, 256, 0, s>>>(c, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, st, slots, tokens, per, p.per_inv, p.take);
   else
-    k_kv4_write<<<grid, 256, 0, s>>>(c, (const __half*)k, (const __half*)v, st, slots, tokens, per);
+    k_kv4_write<<<p.grid, 256, 0, s>>>(c, (const __half*)k, (const __half*)v, st, slots, tokens, per, p.per_inv, p.take);
   GQ_LAUNCHED();
   return GPTQ_OK;
 }
@@ -180,12 +242,12 @@ gptq_status kv4_read_run(int dtype, const uint8_t* cache, long long pages, int h
   if (tokens == 0) return GPTQ_OK;
   const CacheShape c{const_cast<uint8_t*>(cache), pages, heads, dim, page_size};
   const int per = heads * (dim / 8);
-  const unsigned grid = (unsigned)(((long long)tokens * per + 255) / 256);
+  const Split p = split_of(tokens, per);
   GQ_PROF(K_KV4_READ, s);
   if (dtype == GPTQ_BF16)
-    k_kv4_read<<<grid, 256, 0, s>>>(c, slots, tokens, per, (__nv_bfloat16*)k, (__nv_bfloat16*)v);
+    k_kv4_read<<<p.grid, 256, 0, s>>>(c, slots, tokens, per, p.per_inv, p.take, (__nv_bfloat16*)k, (__nv_bfloat16*)v);
   else
-    k_kv4_read<<<grid, 256, 0, s>>>(c, slots, tokens, per, (__half*)k, (__half*)v);
+    k_kv4_read<<<p.grid, 256, 0, s>>>(c, slots, tokens, per, p.per_inv, p.take, (__half*)k, (__half*)v);
   GQ_LAUNCHED();
   return GPTQ_OK;
 }
