@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(ATHREADS)
     const long long page_bytes = (long long)a.heads * bpp * BB;
     const int jump = 2 * AW / bpp, jrest = 2 * AW % bpp;
     int ip = (j0 + 2 * warp) / bpp, iin = (j0 + 2 * warp) % bpp, islot = slot, left = nb;
-    int entry = left > 0 ? trow[ip] : 0;  // of the next pair, loaded a round ahead
+    // Of the next pair, loaded a round ahead; `entry2` where it crosses pages.
+    int entry = left > 0 ? trow[ip] : 0, entry2 = left > 1 && iin + 1 >= bpp ? trow[ip + 1] : 0;
     auto place = [&](int e, int in) {  // an entry outside the pool reads page 0: never outside the buffer
       return src0 + ((unsigned)e < (unsigned long long)a.pages ? (long long)e : 0) * page_bytes + in * BB;
     };
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(ATHREADS)
         } else {
           mbar_expect_tx(bar, PB);
           bulk_load(dst, place(entry, iin), BB, bar);
-          bulk_load(dst + BB, place(trow[ip + 1], 0), BB, bar);
+          bulk_load(dst + BB, place(entry2, 0), BB, bar);
         }
       }
       if (++islot == ST) islot = 0;
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(ATHREADS)
       iin += jrest;
       if (iin >= bpp) iin -= bpp, ++ip;
       if (left > 0) entry = trow[ip];
+      if (left > 1 && iin + 1 >= bpp) entry2 = trow[ip + 1];
     };
     if (!wc.no_loads)
       for (int i = 0; i < ST && left > 0; ++i) issue();
@@ -485,12 +487,12 @@ __global__ void __launch_bounds__(ATHREADS)
   }
 }
 
-// Adds the pieces of an item that more than one CTA shared.  One CTA per
-// (key head, row block) and sequence; a warp per row.
+// Adds the pieces of an item that more than one CTA shared.  blockIdx: (key
+// head, row block), four of its rows, sequence; a warp a row.
 template <class T, int D, int NQ>
 __global__ void __launch_bounds__(ATHREADS) k_kv4_join(AttnArgs a, int grid) {
   constexpr int MR = 8 * NQ;
-  const int b = (int)blockIdx.y, item = (int)blockIdx.x;
+  const int b = (int)blockIdx.z, item = (int)blockIdx.x;
   const Seq sq = seq_of(a, b);
   const int nblk = blocks_of<MR>(a, sq), nch = chunks_of(sq);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the list and the pieces are there
@@ -500,38 +502,37 @@ __global__ void __launch_bounds__(ATHREADS) k_kv4_join(AttnArgs a, int grid) {
   const int first = (int)(((u0 + 1) * shares - 1) / W), lastc = (int)(((u0 + nch) * shares - 1) / W);
   if (first == lastc) return;
   const int head = item / nblk, r0 = (item % nblk) * MR, rows = min(MR, sq.nq * a.group - r0);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int r = (int)blockIdx.y * AW + threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (r >= rows) return;
   const float sl = fabsf(a.scale_log2);
   auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == first ? 1 : 0)) * slot_floats<D>(MR); };
-  for (int r = warp; r < rows; r += AW) {
-    // The running maximum and sum once more, over the pieces in order.
-    float top = kNone, den = 0.f, acc[D / 32];
+  // The running maximum and sum once more, over the pieces in order.
+  float top = kNone, den = 0.f, acc[D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
 #pragma unroll 4
-    for (int c = first; c <= lastc; ++c) {
-      const float* p = slot(c);
-      const float m = p[MR * D + 2 * r], l = p[MR * D + 2 * r + 1];
-      const float nt = fmaxf(top, m), fo = ex2(sl * (top - nt)), fn = ex2(sl * (m - nt));
-      top = nt;
-      den = den * fo + l * fn;
+  for (int c = first; c <= lastc; ++c) {
+    const float* p = slot(c);
+    const float m = p[MR * D + 2 * r], l = p[MR * D + 2 * r + 1];
+    const float nt = fmaxf(top, m), fo = ex2(sl * (top - nt)), fn = ex2(sl * (m - nt));
+    top = nt;
+    den = den * fo + l * fn;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) acc[i] = acc[i] * fo + p[r * D + lane + 32 * i] * fn;
-    }
-    const float inv = den != 0.f ? 1.f / den : 0.f;
-    const int rr = r0 + r;
-    T* dst = static_cast<T*>(a.out) +
-             ((long long)(sq.q0 + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group) * D;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = Elem<T>::from(acc[i] * inv);
+    for (int i = 0; i < D / 32; ++i) acc[i] = acc[i] * fo + p[r * D + lane + 32 * i] * fn;
   }
+  const float inv = den != 0.f ? 1.f / den : 0.f;
+  const int rr = r0 + r;
+  T* dst = static_cast<T*>(a.out) +
+           ((long long)(sq.q0 + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group) * D;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = Elem<T>::from(acc[i] * inv);
 }
 
 // Pairs of blocks in a warp's ring: two keep the copies ahead; with four
 // column tiles the outputs need four.
 template <int NQ>
 constexpr int stages() {
-  return NQ == 4 ? 4 : 2;
+  return NQ > 2 ? NQ : 2;
 }
 
 template <class T, int D, int NQ>
@@ -572,7 +573,7 @@ gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
       GQ_LAUNCHED();
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.heads * blocks), (unsigned)p.seqs);
+    cfg.gridDim = dim3((unsigned)(a.heads * blocks), 2 * NQ, (unsigned)p.seqs);
     cfg.blockDim = dim3(ATHREADS);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -591,6 +592,7 @@ gptq_status attn_rows(const AttnArgs& a, cudaStream_t s) {
   const long long rows = (long long)a.max_q * a.group;
   if (rows <= 8) return attn_launch<T, D, 1>(a, s);
   if (rows <= 16 || D == 256) return attn_launch<T, D, 2>(a, s);
+  if (rows <= 24) return attn_launch<T, D, D == 256 ? 2 : 3>(a, s);
   return attn_launch<T, D, D == 256 ? 2 : 4>(a, s);
 }
 
