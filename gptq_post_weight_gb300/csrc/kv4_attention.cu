@@ -13,6 +13,13 @@
 // and k_kv4_join adds the pieces in the order of the list.  The cut depends
 // on the lengths alone: results do not change from run to run.
 //
+// Measured: 48 sequences of up to 16384 tokens, 8 key heads of 128 with 8
+// query heads each, one new token: 127 us, 4.3 TB/s of cache; the vector ALU
+// (codes to values: two instructions a pair, at half rate) is then 62 % busy
+// and the memory 64 %.  16 sequences of 5 drafted tokens over up to 4001
+// tokens, 20 rows of 64: 26.5 us, three CTAs an SM waiting on their own
+// chains of products and shuffles.  One token over 1000: 5.4 us.
+//
 // Rows of a block are (query, head of the key head's group) pairs, so that a
 // key is decoded once for every head that shares it.  Each of a CTA's four
 // warps streams its own blocks of 16 tokens through a ring of bulk copies,
@@ -128,9 +135,25 @@ __device__ __forceinline__ uint32_t turn8x8(uint32_t v) {
   return r;
 }
 
+// Two floats at this CTA's address `at`, read in the cluster's CTA `rank`.
+__device__ __forceinline__ float2 peer2(uint32_t at, uint32_t rank) {
+  float2 v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %2, %3;\n ld.shared::cluster.v2.f32 {%0, %1}, [a];\n}\n"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// CTAs an SM that the registers are cut to.
+constexpr int resident(int dim, int nq) { return dim * nq <= 128 ? 4 : dim * nq <= 192 ? 3 : 2; }
+
 // NQ: column tiles of eight query rows; ST: pairs of blocks in a warp's ring.
-template <class T, int D, int NQ, int ST>
-__global__ void __launch_bounds__(ATHREADS)
+// CL = 0: equal shares of the list.  CL > 0: blockIdx.y is the sequence, and
+// CL CTAs of a cluster share each item of it and join its pieces themselves.
+template <class T, int D, int NQ, int ST, int CL>
+__global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
     k_kv4_attention(AttnArgs a, WaitCfg wc) {
   using T2 = typename Elem<T>::T2;
   constexpr int MR = 8 * NQ, NW = D / 32, BB = kv_block_bytes(D), PB = 2 * BB;
@@ -154,14 +177,19 @@ __global__ void __launch_bounds__(ATHREADS)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  work_prefix<MR>(a, pref, scratch);
-  const long long W = pref[a.seqs];
-  const long long shares = min(W, (long long)gridDim.x);  // no share is empty
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= a.seqs; i += ATHREADS) a.list[i] = pref[i];  // for the join
-  if (blockIdx.x >= shares) return;
-  long long u = W * blockIdx.x / shares;
-  const long long uend = W * (blockIdx.x + 1) / shares;
+  long long u = 0, uend = 1;
+  if (CL == 0) {
+    work_prefix<MR>(a, pref, scratch);
+    const long long W = pref[a.seqs];
+    const long long shares = min(W, (long long)gridDim.x);  // no share is empty
+    if (threadIdx.x == 0) reinterpret_cast<int4*>(a.list)[blockIdx.x] = int4{0, 0, 0, -1};  // no rows to join
+    if (blockIdx.x >= shares) return;
+    u = W * blockIdx.x / shares;
+    uend = W * (blockIdx.x + 1) / shares;
+  } else {
+    __syncthreads();
+  }
+  const uint32_t rank = CL ? blockIdx.x % max(CL, 1) : 0u;
   const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale: -q
   const float sl = fabsf(a.scale_log2);
   int slot = 0;  // of the ring: the next copy to wait for
@@ -171,18 +199,30 @@ __global__ void __launch_bounds__(ATHREADS)
 
   while (u < uend) {
     // The item of chunk u.
-    int lo = 0, hi = a.seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (pref[mid] <= u) lo = mid; else hi = mid - 1;
+    int b = (int)blockIdx.y;
+    if (CL == 0) {
+      int lo = 0, hi = a.seqs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (pref[mid] <= u) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
     }
-    const int b = lo;
     const Seq sq = seq_of(a, b);
-    const int nblk = blocks_of<MR>(a, sq), nch = chunks_of(sq);
-    const long long rem = u - pref[b];
-    const int item = (int)(rem / nch), c0 = (int)(rem % nch);
-    const int c1 = (int)min((long long)nch, c0 + (uend - u));
-    const int head = item / nblk, r0 = (item % nblk) * MR;
+    const int nch = chunks_of(sq);
+    int c0, c1, head, r0;
+    if (CL == 0) {
+      const int nblk = blocks_of<MR>(a, sq);
+      const long long rem = u - pref[b];
+      const int item = (int)(rem / nch);
+      c0 = (int)(rem % nch);
+      c1 = (int)min((long long)nch, c0 + (uend - u));
+      head = item / nblk, r0 = (item % nblk) * MR;
+    } else {
+      if (sq.nq == 0) return;  // the whole cluster
+      c0 = (int)(nch * rank / max(CL, 1)), c1 = (int)(nch * (rank + 1) / max(CL, 1));
+      head = (int)blockIdx.x / max(CL, 1), r0 = 0;  // one row block
+    }
     const int rows = min(MR, sq.nq * a.group - r0);
     const int first_pos = sq.len - sq.nq + r0 / a.group;  // last key the block's first row sees
     const int vis = min(sq.len, sq.len - sq.nq + (r0 + rows - 1) / a.group + 1);  // keys the last row sees
@@ -438,8 +478,8 @@ __global__ void __launch_bounds__(ATHREADS)
           *reinterpret_cast<float2*>(dst + 2 * i) = float2{o[n][i][e], o[n][i][2 + e]};
       }
     __syncthreads();
-    const bool whole = c0 == 0 && c1 == nch;
-    float* part = a.part + ((size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0)) * slot_floats<D>(MR);
+    const bool whole = CL == 0 && c0 == 0 && c1 == nch;
+    float* part = CL ? nullptr : a.part + ((size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0)) * slot_floats<D>(MR);
     for (int r = warp; r < rows; r += AW) {
       float top = mls[0][r][0], f[AW], den = 0.f;
 #pragma unroll
@@ -462,17 +502,61 @@ __global__ void __launch_bounds__(ATHREADS)
           v.x = fmaf(x.x, f[w], v.x);
           v.y = fmaf(x.y, f[w], v.y);
         }
-        if (whole)
+        if (CL)  // over warp 0's, which only this thread reads
+          *reinterpret_cast<float2*>(smem + (r * OS + d) * 4) = v;
+        else if (whole)
           *reinterpret_cast<T2*>(dst + d) = Elem<T>::make2(v.x * inv, v.y * inv);
         else
           *reinterpret_cast<float2*>(part + r * D + d) = v;
       }
-      if (!whole && lane == 0) {
+      __syncwarp();
+      if (CL && lane == 0) {
+        mls[0][r][0] = top;
+        mls[0][r][1] = den;
+      } else if (!whole && lane == 0) {
         part[MR * D + 2 * r] = top;
         part[MR * D + 2 * r + 1] = den;
       }
     }
+    if (CL) {
+      // The pieces of the cluster's CTAs, in the order of the ranks.
+      cluster_sync_all();
+      for (int r = (int)rank * AW + warp; r < rows; r += CL * AW) {
+        float f[CL ? CL : 1], den = 0.f, top = kNone;
+        float2 ml[CL ? CL : 1];
+#pragma unroll
+        for (int c = 0; c < CL; ++c) ml[c] = peer2(smem_u32(&mls[0][r][0]), (uint32_t)c);
+#pragma unroll
+        for (int c = 0; c < CL; ++c) top = fmaxf(top, ml[c].x);
+#pragma unroll
+        for (int c = 0; c < CL; ++c) {
+          f[c] = ex2(sl * (ml[c].x - top));
+          den += ml[c].y * f[c];
+        }
+        const float inv = den != 0.f ? 1.f / den : 0.f;  // a row that sees nothing: zeros
+        T* dst = static_cast<T*>(a.out) +
+                 ((long long)(sq.q0 + r / a.group) * a.heads * a.group + head * a.group + r % a.group) * D;
+#pragma unroll
+        for (int d = 2 * lane; d < D; d += 64) {
+          float2 v{0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < CL; ++c) {
+            const float2 x = peer2(smem_u32(smem + (r * OS + d) * 4), (uint32_t)c);
+            v.x = fmaf(x.x, f[c], v.x);
+            v.y = fmaf(x.y, f[c], v.y);
+          }
+          *reinterpret_cast<T2*>(dst + d) = Elem<T>::make2(v.x * inv, v.y * inv);
+        }
+      }
+      cluster_sync_all();  // nobody leaves while its pieces are read
+      break;
+    }
     u += c1 - c0;
+    if (c0 == 0 && c1 < nch && threadIdx.x == 0) {  // the cut's first piece: the join's work
+      const long long W = pref[a.seqs], shares = min(W, (long long)gridDim.x);
+      const int lastc = (int)(((u + nch - c1) * shares - 1) / W);  // the share of the last chunk
+      reinterpret_cast<int4*>(a.list)[blockIdx.x] = int4{sq.q0, r0, head * 64 + rows, lastc};
+    }
     if (__syncthreads_or(abort_sh)) break;  // the whole CTA leaves together
     fence_proxy_async_smem();               // the rings take copies again
     __syncwarp();
@@ -487,43 +571,58 @@ __global__ void __launch_bounds__(ATHREADS)
   }
 }
 
-// Adds the pieces of an item that more than one CTA shared.  blockIdx: (key
-// head, row block), four of its rows, sequence; a warp a row.
+// Adds the pieces of the items that more than one CTA shared: block (c, y)
+// those of the item whose first piece share c ends with, rows 4 y .. 4 y + 3,
+// a warp a row.  A row's pieces come through shared memory, a batch of JB at a
+// time: one latency a batch (loaded one after the other into registers they
+// took 0.25 us each, 16 us of a context of 8000 tokens in 63 pieces).
 template <class T, int D, int NQ>
-__global__ void __launch_bounds__(ATHREADS) k_kv4_join(AttnArgs a, int grid) {
-  constexpr int MR = 8 * NQ;
-  const int b = (int)blockIdx.z, item = (int)blockIdx.x;
-  const Seq sq = seq_of(a, b);
-  const int nblk = blocks_of<MR>(a, sq), nch = chunks_of(sq);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list and the pieces are there
-  if (item >= a.heads * nblk) return;
-  const long long W = a.list[a.seqs], u0 = a.list[b] + (long long)item * nch;
-  const long long shares = min(W, (long long)grid);
-  const int first = (int)(((u0 + 1) * shares - 1) / W), lastc = (int)(((u0 + nch) * shares - 1) / W);
-  if (first == lastc) return;
-  const int head = item / nblk, r0 = (item % nblk) * MR, rows = min(MR, sq.nq * a.group - r0);
-  const int r = (int)blockIdx.y * AW + threadIdx.x / 32, lane = threadIdx.x % 32;
+__global__ void __launch_bounds__(ATHREADS) k_kv4_join(AttnArgs a) {
+  constexpr int MR = 8 * NQ, JB = D == 256 ? 8 : 16;
+  __shared__ __align__(16) float batch[AW][JB][D];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int r = (int)blockIdx.y * AW + warp, first = (int)blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the cuts and the pieces are there
+  const int4 cut = reinterpret_cast<const int4*>(a.list)[first];
+  const int head = cut.z / 64, rows = cut.z % 64, lastc = cut.w;
   if (r >= rows) return;
   const float sl = fabsf(a.scale_log2);
   auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == first ? 1 : 0)) * slot_floats<D>(MR); };
-  // The running maximum and sum once more, over the pieces in order.
   float top = kNone, den = 0.f, acc[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int c = first; c <= lastc; ++c) {
-    const float* p = slot(c);
-    const float m = p[MR * D + 2 * r], l = p[MR * D + 2 * r + 1];
-    const float nt = fmaxf(top, m), fo = ex2(sl * (top - nt)), fn = ex2(sl * (m - nt));
-    top = nt;
-    den = den * fo + l * fn;
+#pragma unroll 1
+  for (int c0 = first; c0 <= lastc; c0 += JB) {
+    const int n = min(JB, lastc + 1 - c0);
+    for (int i = lane; i < n * (D / 4); i += 32)
+      cp_async16(&batch[warp][i / (D / 4)][i % (D / 4) * 4], slot(c0 + i / (D / 4)) + r * D + i % (D / 4) * 4);
+    float2 ml{kNone, 0.f};
+    if (lane < n) ml = *reinterpret_cast<const float2*>(slot(c0 + lane) + MR * D + 2 * r);
+    float nt = ml.x;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = acc[i] * fo + p[r * D + lane + 32 * i] * fn;
+    for (int x = 1; x < 32; x <<= 1) nt = fmaxf(nt, __shfl_xor_sync(0xffffffffu, nt, x));
+    nt = fmaxf(nt, top);
+    const float f = ex2(sl * (ml.x - nt)), fo = ex2(sl * (top - nt));
+    float l = ml.y * f;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    top = nt;
+    den = fmaf(den, fo, l);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] *= fo;
+    cp_async_wait_all();
+    __syncwarp();
+    for (int k = 0; k < n; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(batch[warp][k][lane + 32 * i], fk, acc[i]);
+    }
+    __syncwarp();  // the batch is read
   }
-  const float inv = den != 0.f ? 1.f / den : 0.f;
-  const int rr = r0 + r;
+  const float inv = den != 0.f ? 1.f / den : 0.f;  // a row that sees nothing: zeros
+  const int rr = cut.y + r;
   T* dst = static_cast<T*>(a.out) +
-           ((long long)(sq.q0 + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group) * D;
+           ((long long)(cut.x + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group) * D;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = Elem<T>::from(acc[i] * inv);
 }
@@ -535,19 +634,59 @@ constexpr int stages() {
   return NQ > 2 ? NQ : 2;
 }
 
+// Few rows, few items and short contexts: a cluster of ACL CTAs an item joins
+// its own pieces, in one launch.  Measured, one new token, 8 key heads of 128,
+// clusters against shares and a join: 1 sequence of 1000 tokens 5.4 and 7.5 us,
+// of 8000 tokens 12.3 and 13.6, of 16000 tokens 19.6 and 17.7; 8 sequences of
+// 1000 tokens 7.5 and 9.6, of 8000 17.4 and 20.4, of 16000 39.5 and 37.0.  The
+// lengths are on the device, so the table's width is what is looked at.
+constexpr int ACL = 8;
+constexpr int kClusterTokens = 8192;
+
+template <class T, int D, int NQ, int CL>
+struct Kernel {
+  static constexpr int ST = stages<NQ>(), smem = AW * ST * 2 * kv_block_bytes(D);
+  static constexpr auto fn = k_kv4_attention<T, D, NQ, ST, CL>;
+  // Resident CTAs a SM.
+  static gptq_status per_sm(int* out) {
+    static DeviceOnce attr;
+    static int n = 1;
+    GQ_TRY(attr.run([](int) -> gptq_status {
+      GQ_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+      int m = 0;
+      GQ_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&m, fn, ATHREADS, smem));
+      n = m < 1 ? 1 : (m > ASHARES ? ASHARES : m);
+      return GPTQ_OK;
+    }));
+    *out = n;
+    return GPTQ_OK;
+  }
+};
+
+template <class T, int D>
+gptq_status attn_cluster(const AttnArgs& a, cudaStream_t s) {
+  using K = Kernel<T, D, 1, ACL>;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.heads * ACL), (unsigned)a.seqs);
+  cfg.blockDim = dim3(ATHREADS);
+  cfg.dynamicSmemBytes = K::smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ACL;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  GQ_PROF(K_KV4_ATTENTION, s);
+  GQ_CUDA(cudaLaunchKernelEx(&cfg, K::fn, a, wait_cfg()));
+  return GPTQ_OK;
+}
+
 template <class T, int D, int NQ>
 gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
-  constexpr int ST = stages<NQ>();
-  constexpr int smem = AW * ST * 2 * kv_block_bytes(D);
-  static DeviceOnce attr;
-  static int per_sm = 1;  // resident CTAs a SM: one share each
-  GQ_TRY(attr.run([](int) -> gptq_status {
-    GQ_CUDA(cudaFuncSetAttribute(k_kv4_attention<T, D, NQ, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    int n = 0;
-    GQ_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_kv4_attention<T, D, NQ, ST>, ATHREADS, smem));
-    per_sm = n < 1 ? 1 : (n > ASHARES ? ASHARES : n);
-    return GPTQ_OK;
-  }));
+  using K = Kernel<T, D, NQ, 0>;
+  int per_sm = 1;  // one share each
+  GQ_TRY(K::per_sm(&per_sm));
   const int seqs = a.seqs;
   for (int b0 = 0; b0 < seqs; b0 += ASEQS) {
     AttnArgs p = a;
@@ -565,15 +704,15 @@ gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
     const long long blocks = ((long long)a.max_q * a.group + 8 * NQ - 1) / (8 * NQ);
     const long long most = (long long)p.seqs * a.heads * blocks *
                            (((long long)a.table_stride * a.page_size + ACH - 1) / ACH);
-    long long shares = (long long)num_sms() * per_sm;
+    long long shares = std::min((long long)num_sms() * per_sm, (long long)(kListBytes / 16));
     if (shares > most) shares = most;
     {
       GQ_PROF(K_KV4_ATTENTION, s);
-      k_kv4_attention<T, D, NQ, ST><<<(unsigned)shares, ATHREADS, smem, s>>>(p, wait_cfg());
+      K::fn<<<(unsigned)shares, ATHREADS, K::smem, s>>>(p, wait_cfg());
       GQ_LAUNCHED();
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.heads * blocks), 2 * NQ, (unsigned)p.seqs);
+    cfg.gridDim = dim3((unsigned)shares, 2 * NQ);
     cfg.blockDim = dim3(ATHREADS);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -582,7 +721,7 @@ gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     GQ_PROF(K_KV4_JOIN, s);
-    GQ_CUDA(cudaLaunchKernelEx(&cfg, k_kv4_join<T, D, NQ>, p, (int)shares));
+    GQ_CUDA(cudaLaunchKernelEx(&cfg, k_kv4_join<T, D, NQ>, p));
   }
   return GPTQ_OK;
 }
@@ -590,6 +729,11 @@ gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
 template <class T, int D>
 gptq_status attn_rows(const AttnArgs& a, cudaStream_t s) {
   const long long rows = (long long)a.max_q * a.group;
+  if (rows <= 8 && (long long)a.table_stride * a.page_size <= kClusterTokens) {
+    int per_sm = 1;
+    GQ_TRY((Kernel<T, D, 1, ACL>::per_sm(&per_sm)));
+    if ((long long)a.seqs * a.heads * ACL <= (long long)num_sms() * per_sm) return attn_cluster<T, D>(a, s);
+  }
   if (rows <= 8) return attn_launch<T, D, 1>(a, s);
   if (rows <= 16 || D == 256) return attn_launch<T, D, 2>(a, s);
   if (rows <= 24) return attn_launch<T, D, D == 256 ? 2 : 3>(a, s);

@@ -185,7 +185,7 @@ struct AttnArgs {
   int seqs, max_q;
   float scale_log2;  // scale * log2(e)
   void* out;         // [tq][heads * group][dim]
-  long long* list;   // workspace: the prefix of the work list, for the join
+  long long* list;   // workspace: the work list's prefix, or its cuts, for the join
   float* part;       // workspace: pieces of cut items
   uint32_t up;       // 2^kPos of T (see code16)
   unsigned* status;
@@ -194,8 +194,9 @@ struct AttnArgs {
 // The driver's tensor-map encoder (null when it cannot be had).
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
-// Bytes of the workspace's work list (before the pieces).
-constexpr size_t kListBytes = 2304 * 8;
+// Bytes of the workspace before the pieces: the prompt-chunk kernel's work list
+// (2305 sums at most) or the decode kernel's cuts (16 bytes a share).
+constexpr size_t kListBytes = 2560 * 16;
 
 // Geometry of the cache: blocks of 16 tokens, each
 //   K codes [16][dim / 2], K (scale, offset) [16][dim / 32], V codes, V (scale, offset).
