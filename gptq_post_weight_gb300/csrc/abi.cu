@@ -719,7 +719,7 @@ gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long lo
   if (ws_bytes < kv4_attention_ws_bytes(dim, group, max_q, q_starts == nullptr)) return GPTQ_ERR_NOMEM;
   const AttnArgs a{Q,     q_ts,         q_hs,    tq,       cache, pages, heads, group, page_size,
                    table, table_stride, kv_lens, q_starts, seqs,  max_q, scale * 1.4426950408889634f,
-                   out,   static_cast<long long*>(ws), reinterpret_cast<float*>(static_cast<char*>(ws) + kListBytes),
+                   out,   static_cast<int4*>(ws), reinterpret_cast<float*>(static_cast<char*>(ws) + kCutBytes),
                    dtype == GPTQ_BF16 ? 8u : 64u, status};
   return kv4_attention_run(dtype, dim, a, as_stream(stream));
 }

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
     work_prefix<MR>(a, pref, scratch);
     const long long W = pref[a.seqs];
     const long long shares = min(W, (long long)gridDim.x);  // no share is empty
-    if (threadIdx.x == 0) reinterpret_cast<int4*>(a.list)[blockIdx.x] = int4{0, 0, 0, -1};  // no rows to join
+    if (threadIdx.x == 0) a.cuts[blockIdx.x] = int4{};  // nothing to join
     if (blockIdx.x >= shares) return;
     u = W * blockIdx.x / shares;
     uend = W * (blockIdx.x + 1) / shares;
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
     if (c0 == 0 && c1 < nch && threadIdx.x == 0) {  // the cut's first piece: the join's work
       const long long W = pref[a.seqs], shares = min(W, (long long)gridDim.x);
       const int lastc = (int)(((u + nch - c1) * shares - 1) / W);  // the share of the last chunk
-      reinterpret_cast<int4*>(a.list)[blockIdx.x] = int4{sq.q0, r0, head * 64 + rows, lastc};
+      a.cuts[blockIdx.x] = int4{sq.q0, r0, head << 9 | rows, lastc};
     }
     if (__syncthreads_or(abort_sh)) break;  // the whole CTA leaves together
     fence_proxy_async_smem();               // the rings take copies again
@@ -583,8 +583,8 @@ __global__ void __launch_bounds__(ATHREADS) k_kv4_join(AttnArgs a) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int r = (int)blockIdx.y * AW + warp, first = (int)blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the cuts and the pieces are there
-  const int4 cut = reinterpret_cast<const int4*>(a.list)[first];
-  const int head = cut.z / 64, rows = cut.z % 64, lastc = cut.w;
+  const int4 cut = a.cuts[first];
+  const int head = cut.z >> 9, rows = cut.z & 511, lastc = cut.w;
   if (r >= rows) return;
   const float sl = fabsf(a.scale_log2);
   auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == first ? 1 : 0)) * slot_floats<D>(MR); };
@@ -704,7 +704,7 @@ gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
     const long long blocks = ((long long)a.max_q * a.group + 8 * NQ - 1) / (8 * NQ);
     const long long most = (long long)p.seqs * a.heads * blocks *
                            (((long long)a.table_stride * a.page_size + ACH - 1) / ACH);
-    long long shares = std::min((long long)num_sms() * per_sm, (long long)(kListBytes / 16));
+    long long shares = std::min((long long)num_sms() * per_sm, (long long)kShares);
     if (shares > most) shares = most;
     {
       GQ_PROF(K_KV4_ATTENTION, s);
@@ -757,7 +757,7 @@ bool kv4_is_chunk(int dim, int group, int max_q, bool single) {
 
 size_t kv4_attention_ws_bytes(int dim, int group, int max_q, bool single) {
   if (kv4_is_chunk(dim, group, max_q, single)) return kv4_chunk_ws_bytes(dim);
-  return kListBytes + (size_t)num_sms() * ASHARES * 2 * 32 * (dim + 2) * 4;
+  return kCutBytes + (size_t)num_sms() * ASHARES * 2 * 32 * (dim + 2) * 4;
 }
 
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s) {

@@ -289,8 +289,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
   const long long W = pref[a.seqs * nblk] * a.heads;
   const long long shares = min(W, (long long)gridDim.x);  // no share is empty
   const bool has = blockIdx.x < shares;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= a.seqs * nblk; i += CTHREADS) a.list[i] = pref[i];  // for the join
+  if (threadIdx.x == 0) a.cuts[blockIdx.x] = int4{};  // nothing to join
   const long long ubeg = has ? W * blockIdx.x / shares : 0, uend = has ? W * (blockIdx.x + 1) / shares : 0;
 
   // Registers: 72 a thread at launch, 896 * 72 = 64512; then the softmax warps
@@ -433,6 +432,11 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       tc_fence_after();
       const Piece pc = piece_at(a, nblk, pref, u, uend);
       u = pc.next;
+      if (threadIdx.x == 0 && pc.j0 == 0 && !pc.whole) {  // a cut tile's first piece: the join's work
+        const long long w = pref[a.seqs * nblk] * a.heads, n = min(w, (long long)gridDim.x);
+        const int lastc = (int)(((u + units_of(pc.t) - CSTART - pc.j1) * n - 1) / w);  // its last unit's share
+        a.cuts[blockIdx.x] = int4{pc.t.q0, pc.t.r0, pc.head << 9 | pc.t.rows, lastc};
+      }
       if (!active) continue;
       const bool mine = 128 * x + rt < pc.t.rows;
       const int rr = pc.t.r0 + min(128 * x + rt, pc.t.rows - 1);
@@ -669,51 +673,70 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base_sh), "r"(512u) : "memory");
 }
 
-// Adds the pieces of the tiles that more than one CTA shared.  Block (c, i)
-// looks at the cut between shares c and c + 1: if it is the first one inside
-// a tile's steps, the block takes 32 of the tile's rows, a warp a row.
+// Adds the pieces of the tiles that more than one CTA shared: block (c, i)
+// those of the tile whose first piece share c ends with, sixteen rows of it,
+// a warp four, whose pieces come through shared memory four at a time.
 template <class T, int D>
-__global__ void __launch_bounds__(256) k_kv4_chunk_join(AttnArgs a, int nblk, int grid) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list and the pieces are there
-  const long long W = a.list[a.seqs * nblk] * a.heads;
-  const long long shares = min(W, (long long)grid);
-  if ((long long)blockIdx.x + 1 >= shares) return;
-  const long long cut = W * (blockIdx.x + 1) / shares;
-  int lo = 0, hi = a.seqs * nblk - 1;  // the tile that holds unit cut - 1
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (a.list[mid] * a.heads <= cut - 1) lo = mid; else hi = mid - 1;
-  }
-  const Pair t = pair_of(a, lo / nblk, lo % nblk);
-  const int r1 = min(t.rows, ((int)blockIdx.y + 1) * 32);
-  if ((int)blockIdx.y * 32 >= r1) return;
-  const int n = units_of(t), head = (int)((cut - 1 - a.list[lo] * a.heads) / n);
-  const long long u0 = a.list[lo] * a.heads + (long long)head * n;
-  // The shares of the first and the last step.
-  const int first = (int)(((u0 + CSTART + 1) * shares - 1) / W), lastc = (int)(((u0 + n) * shares - 1) / W);
-  if (first == lastc || first != (int)blockIdx.x) return;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+__global__ void __launch_bounds__(128) k_kv4_chunk_join(AttnArgs a) {
+  __shared__ __align__(16) float batch[4][16][D];  // [warp][piece, row]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, first = (int)blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the cuts and the pieces are there
+  const int4 cut = a.cuts[first];
+  const int head = cut.z >> 9, rows = cut.z & 511, lastc = cut.w;
+  const int r0 = (int)blockIdx.y * 16 + 4 * warp;
+  if (r0 >= rows) return;
   const float sl = fmaxf(fabsf(a.scale_log2), 1e-30f);
-  for (int r = (int)blockIdx.y * 32 + warp; r < r1; r += 8) {
-    float top = kNone, den = 0.f, acc[D / 32];
+  auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == first ? 1 : 0)) * piece_floats(D); };
+  float top = kNone, den = 0.f;  // of row r0 + lane % 4
+  float acc[4][D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int c = first; c <= lastc; ++c) {
-      const float* s = a.part + ((size_t)c * 2 + (c == first ? 1 : 0)) * piece_floats(D);
-      const float2 ml = *reinterpret_cast<const float2*>(s + (size_t)CROWS * D + 2 * r);
-      const float nt = fmaxf(top, ml.x), fo = ex2(sl * (top - nt)), fn = ex2(sl * (ml.x - nt));
-      top = nt;
-      den = den * fo + ml.y * fn;
+  for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) acc[i] = acc[i] * fo + s[(size_t)r * D + lane + 32 * i] * fn;
+    for (int i = 0; i < D / 32; ++i) acc[k][i] = 0.f;
+#pragma unroll 1
+  for (int c0 = first; c0 <= lastc; c0 += 4) {
+    const int pieces = min(4, lastc + 1 - c0);  // (rows past the tile's are the workspace's all the same)
+    for (int i = lane; i < pieces * D; i += 32)
+      cp_async16(&batch[warp][i / (D / 4)][i % (D / 4) * 4],
+                 slot(c0 + i / D) + (size_t)(r0 + i / (D / 4) % 4) * D + i % (D / 4) * 4);
+    float2 ml{kNone, 0.f};
+    if (lane < 4 * pieces) ml = *reinterpret_cast<const float2*>(slot(c0 + lane / 4) + (size_t)CROWS * D + 2 * (r0 + lane % 4));
+    float nt = fmaxf(ml.x, top);
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) nt = fmaxf(nt, __shfl_xor_sync(0xffffffffu, nt, x));
+    const float f = ex2(sl * (ml.x - nt)), fo = ex2(sl * (top - nt));
+    float l = ml.y * f;
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    top = nt;
+    den = fmaf(den, fo, l);
+    cp_async_wait_all();
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, fo, k);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) acc[k][i] *= fk;
     }
-    const float inv = den != 0.f ? 1.f / den : 0.f;
-    const int rr = t.r0 + r;
-    T* dst = static_cast<T*>(a.out) +
-             ((long long)(t.q0 + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group) * D;
+    for (int c = 0; c < pieces; ++c)
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = Elem<T>::from(acc[i] * inv);
+      for (int k = 0; k < 4; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, 4 * c + k);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[k][i] = fmaf(batch[warp][4 * c + k][lane + 32 * i], fk, acc[k][i]);
+      }
+    __syncwarp();  // the batch is read
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float dk = __shfl_sync(0xffffffffu, den, k);
+    if (r0 + k >= rows) continue;
+    const float inv = dk != 0.f ? 1.f / dk : 0.f;  // a row that sees nothing: zeros
+    const int rr = cut.y + r0 + k;
+    T* dst = static_cast<T*>(a.out) +
+             ((long long)(cut.x + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group) * D;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = Elem<T>::from(acc[k][i] * inv);
   }
 }
 
@@ -739,8 +762,8 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
       GQ_LAUNCHED();
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, CROWS / 32);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)grid, CROWS / 16);
+    cfg.blockDim = dim3(128);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -748,14 +771,14 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     GQ_PROF(K_KV4_JOIN, s);
-    GQ_CUDA(cudaLaunchKernelEx(&cfg, k_kv4_chunk_join<T, D>, p, nblk, grid));
+    GQ_CUDA(cudaLaunchKernelEx(&cfg, k_kv4_chunk_join<T, D>, p));
   }
   return GPTQ_OK;
 }
 
 }  // namespace
 
-size_t kv4_chunk_ws_bytes(int dim) { return kListBytes + (size_t)num_sms() * 2 * piece_floats(dim) * 4; }
+size_t kv4_chunk_ws_bytes(int dim) { return kCutBytes + (size_t)num_sms() * 2 * piece_floats(dim) * 4; }
 
 gptq_status kv4_chunk_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s) {
   if (dim == 64)

@@ -185,7 +185,8 @@ struct AttnArgs {
   int seqs, max_q;
   float scale_log2;  // scale * log2(e)
   void* out;         // [tq][heads * group][dim]
-  long long* list;   // workspace: the work list's prefix, or its cuts, for the join
+  int4* cuts;        // workspace: a share's cut item for the join: (first query row, first row of the
+                     // block, head << 9 | rows, share of its last piece); no rows: nothing to join
   float* part;       // workspace: pieces of cut items
   uint32_t up;       // 2^kPos of T (see code16)
   unsigned* status;
@@ -194,9 +195,9 @@ struct AttnArgs {
 // The driver's tensor-map encoder (null when it cannot be had).
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
-// Bytes of the workspace before the pieces: the prompt-chunk kernel's work list
-// (2305 sums at most) or the decode kernel's cuts (16 bytes a share).
-constexpr size_t kListBytes = 2560 * 16;
+// Shares of a launch at most, and bytes of the workspace before the pieces.
+constexpr int kShares = 2560;
+constexpr size_t kCutBytes = kShares * sizeof(int4);
 
 // Geometry of the cache: blocks of 16 tokens, each
 //   K codes [16][dim / 2], K (scale, offset) [16][dim / 32], V codes, V (scale, offset).
