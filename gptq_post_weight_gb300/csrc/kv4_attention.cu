@@ -749,10 +749,15 @@ gptq_status attn_dim(int dim, const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Many rows a sequence go to the tcgen05 kernel (kv4_chunk.cu).
+// More rows a sequence than a CTA of this file takes go to the tcgen05 kernel
+// (kv4_chunk.cu).  Measured, 8 key heads of 128, tcgen05 kernel and this one:
+// 16 sequences of up to 8000 tokens, 32 rows 86 and 88 us, 48 rows 87 and 141,
+// 128 rows 80 and 263; one sequence of 8000, 32 rows 27 and 23, 48 rows 28 and
+// 28, 128 rows 30 and 44; of 1000, 48 rows 17 and 13 (its start costs more).
+// Heads of 256 have no room in tensor memory there.
 bool kv4_is_chunk(int dim, int group, int max_q, bool single) {
   const long long rows = (long long)max_q * group;
-  return dim <= 128 && !single && rows > 128 && rows <= 256 * 512;
+  return dim <= 128 && !single && rows > 32 && rows <= 256 * 512;
 }
 
 size_t kv4_attention_ws_bytes(int dim, int group, int max_q, bool single) {
