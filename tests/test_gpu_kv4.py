@@ -252,6 +252,20 @@ def test_long_contexts(lib):
     one([9001], 2, 4, 128, 16, "f16", [5], seed=7)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,q_lens,lens", [
+    (2, None, [9001, 700]),      # one row block cut into scores of pieces
+    (3, [4, 1], [5000, 130]),    # 12 rows
+    (4, [5, 5], [3000, 2000]),   # 20 rows
+    (4, [7, 8], [3000, 2000]),   # 32 rows
+    (4, [9, 2], [3000, 2000]),   # 36 rows
+    (4, [40], [12000]),          # one tile shared by every CTA
+])
+def test_cut_items(lib, group, q_lens, lens, dim, dtype):
+    one(lens, 1, group, dim, 16, dtype, q_lens, seed=8)
+
+
 def test_many_sequences(lib):
     r = np.random.default_rng(9)
     one([int(n) for n in r.integers(0, 40, 1500)], 1, 2, 64, 16, "bf16", seed=9)

@@ -3,7 +3,7 @@
 Tolerance, per output: one rounding to T of the result (u |y|, u = 2^-8 or
 2^-11 taken as a whole ulp), plus the product's own error times the
 activation's largest slope (1.13): every weight rounded once to T (u / 2 of
-sum |x w|, only above 16 tokens) and f32 sums.  For these, a group's 32
+sum |x w|, only above 8 tokens) and f32 sums.  For these, a group's 32
 products of x and a code of at most 143 (bf16: 128 + 15; the f16 codes are
 smaller) are added with at most 2^-22 of error each to their running total,
 so 34 * 143 * 2^-22 of s sum |x|, and the n / 32 groups add 2^-23 of
