@@ -50,6 +50,7 @@ SIGNATURES = {
     "gptq_kv4_write": (_I, [_I, _P, _L, _I, _I, _I, _P, _P, _L, _L, _L, _L, _P, _I, _P]),
     "gptq_kv4_read": (_I, [_I, _P, _L, _I, _I, _I, _P, _I, _P, _P, _P]),
     "gptq_kv4_attention_workspace_bytes": (_S, [_I, _I, _I]),
+    "gptq_kv4_attention_call_bytes": (_S, [_I, _I, _I, _I, _I, _I, _L]),
     "gptq_kv4_attention": (_I, [_I, _P, _L, _L, _I, _P, _L, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _F, _P, _P,
                                 _S, _P, _P]),
     "gptq_launch_count": (ctypes.c_longlong, []),
@@ -592,7 +593,7 @@ def debias(bits, w, h_packed, codes, rungs, tab, lost, scales, ws=None, want_num
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _serve = {}  # torch, its dtypes and the raw-stream call, once the first wrapper ran
 _serve_words = {}  # device index -> the status word its serving calls set (tensor, address)
-_attention_ws = {}  # (dim, group, max_q) -> workspace bytes
+_attention_ws = {}  # shape of a kv4_attention call -> its workspace bytes
 
 
 def _serving():
@@ -950,18 +951,22 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
         qts, qhs = qts if tq > 1 else 0, qhs if hq > 1 else 0
     if out is None:
         out = sv["empty"]((tq, hq, dim), dtype=qt, device=q.device)
+    wp = wn = 0
     if ws is None:
-        shape = (dim, hq // heads, max_q)
-        need = _attention_ws.get(shape)
-        if need is None:
-            need = _lib.gptq_kv4_attention_workspace_bytes(*shape)
+        shape = (dim, heads, hq, max_q, seqs, sp is None, per * page_size)
+        wn = _attention_ws.get(shape)
+        if wn is None:
+            wn = _lib.gptq_kv4_attention_call_bytes(dim, heads, hq // heads, max_q, seqs, sp is None, per * page_size)
             if len(_attention_ws) < 4096:
-                _attention_ws[shape] = need
-        ws = sv["empty"](need, dtype=sv["u8"], device=q.device)
+                _attention_ws[shape] = wn
+        if wn:
+            ws = sv["empty"](wn, dtype=sv["u8"], device=q.device)
+    if ws is not None:
+        wp, wn = ws.data_ptr(), ws.numel()
     code = _lib.gptq_kv4_attention(dt, q.data_ptr(), qts, qhs, tq, cache.data_ptr(), pages, heads, hq // heads, dim,
                                    page_size, table.data_ptr(), per, kv_lens.data_ptr(), sp, seqs, int(max_q),
-                                   dim ** -0.5 if scale is None else float(scale), out.data_ptr(), ws.data_ptr(),
-                                   ws.numel(), (_serve_words.get(dev) or (0, _serve_word(dev)))[1],
+                                   dim ** -0.5 if scale is None else float(scale), out.data_ptr(), wp, wn,
+                                   (_serve_words.get(dev) or (0, _serve_word(dev)))[1],
                                    _raw_stream(sv, stream, dev))
     if code:
         raise GptqError("gptq_kv4_attention", code)

@@ -68,7 +68,7 @@ gptq_status kv4_write_run(int dtype, uint8_t* cache, long long pages, int heads,
                           const long long* slots, int tokens, cudaStream_t s);
 gptq_status kv4_read_run(int dtype, const uint8_t* cache, long long pages, int heads, int dim, int page_size,
                          const long long* slots, int tokens, void* k, void* v, cudaStream_t s);
-size_t kv4_attention_ws_bytes(int dim, int group, int max_q, bool single);
+size_t kv4_attention_ws_bytes(int dim, int heads, int group, int max_q, int seqs, bool single, long long max_len);
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s);
 }  // namespace gq
 
@@ -695,10 +695,25 @@ gptq_status gptq_kv4_read(int dtype, const uint8_t* cache, long long pages, int 
   return kv4_read_run(dtype, cache, pages, heads, dim, page_size, slots, tokens, K, V, as_stream(stream));
 }
 
+static bool bad_attention(int dim, int group, int max_q) {
+  return (dim != 64 && dim != 128 && dim != 256) || group <= 0 || group > 1024 || max_q <= 0 ||
+         max_q > GPTQ_MAX_TOKENS;
+}
+
 size_t gptq_kv4_attention_workspace_bytes(int dim, int group, int max_q) {
-  if ((dim != 64 && dim != 128 && dim != 256) || group <= 0 || group > 1024 || max_q <= 0 || max_q > GPTQ_MAX_TOKENS)
+  if (bad_attention(dim, group, max_q)) return 0;
+  // More sequences and longer contexts than any split is cut for.
+  const size_t one = kv4_attention_ws_bytes(dim, 1024, group, max_q, 1024, true, 1ll << 30);
+  const size_t several = kv4_attention_ws_bytes(dim, 1024, group, max_q, 1024, false, 1ll << 30);
+  return one > several ? one : several;
+}
+
+size_t gptq_kv4_attention_call_bytes(int dim, int heads, int group, int max_q, int seqs, int single,
+                                     long long max_len) {
+  if (bad_attention(dim, group, max_q) || heads <= 0 || heads > 1024 || seqs <= 0 || seqs > GPTQ_MAX_TOKENS ||
+      max_len <= 0 || max_len > (1ll << 30))
     return 0;
-  return kv4_attention_ws_bytes(dim, group, max_q, false);
+  return kv4_attention_ws_bytes(dim, heads, group, max_q, seqs, single != 0, max_len);
 }
 
 gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
@@ -714,9 +729,11 @@ gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long lo
   if (q_starts == nullptr && (tq != seqs || max_q != 1)) return GPTQ_ERR_SHAPE;
   if (tq == 0 || seqs == 0) return GPTQ_OK;
   if (bad_stride(q_ts) || bad_stride(q_hs)) return GPTQ_ERR_SHAPE;
-  if (!ptr_ok(Q) || !ptr_ok(cache) || table == nullptr || kv_lens == nullptr || !ptr_ok(out) || !ptr_ok(ws))
+  if (!ptr_ok(Q) || !ptr_ok(cache) || table == nullptr || kv_lens == nullptr || !ptr_ok(out) || !opt_ok(ws))
     return GPTQ_ERR_ARG;
-  if (ws_bytes < kv4_attention_ws_bytes(dim, group, max_q, q_starts == nullptr)) return GPTQ_ERR_NOMEM;
+  const size_t need = kv4_attention_ws_bytes(dim, heads, group, max_q, seqs, q_starts == nullptr,
+                                             (long long)table_stride * page_size);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return GPTQ_ERR_NOMEM;
   const AttnArgs a{Q,     q_ts,         q_hs,    tq,       cache, pages, heads, group, page_size,
                    table, table_stride, kv_lens, q_starts, seqs,  max_q, scale * 1.4426950408889634f,
                    out,   static_cast<int4*>(ws), reinterpret_cast<float*>(static_cast<char*>(ws) + kCutBytes),

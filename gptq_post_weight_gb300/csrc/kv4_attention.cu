@@ -47,7 +47,6 @@ namespace {
 constexpr int AW = 4;            // warps
 constexpr int ATHREADS = 32 * AW;
 constexpr int ACH = 32 * AW;     // tokens per chunk of the work list
-constexpr int ASHARES = 8;       // resident CTAs a SM at most (sizes the workspace)
 constexpr int ASEQS = 1024;      // sequences per launch at most
 constexpr float kNone = -1e30f;  // running maximum of a row that has seen nothing
 
@@ -643,29 +642,62 @@ constexpr int stages() {
 constexpr int ACL = 8;
 constexpr int kClusterTokens = 8192;
 
+// More rows a sequence than a CTA of this file takes go to the tcgen05 kernel
+// (kv4_chunk.cu).  Measured, 8 key heads of 128, tcgen05 kernel and this one:
+// 16 sequences of up to 8000 tokens, 32 rows 86 and 88 us, 48 rows 87 and 141,
+// 128 rows 80 and 263; one sequence of 8000, 32 rows 27 and 23, 48 rows 28 and
+// 28, 128 rows 30 and 44; of 1000, 48 rows 17 and 13 (its start costs more).
+// Heads of 256 have no room in tensor memory there.
+bool kv4_is_chunk(int dim, int group, int max_q, bool single) {
+  const long long rows = (long long)max_q * group;
+  return dim <= 128 && !single && rows > 32 && rows <= 256 * 512;
+}
+
+// What a call launches and what it needs for that.
+struct Plan {
+  bool chunk, cluster;
+  int nq;            // column tiles
+  long long shares;  // of the largest launch
+  size_t ws;
+};
+Plan plan_of(int dim, int heads, int group, int max_q, int seqs, bool single, long long max_len) {
+  Plan p{};
+  const long long rows = (long long)max_q * group;
+  p.chunk = kv4_is_chunk(dim, group, max_q, single);
+  if (p.chunk) {
+    p.ws = kv4_chunk_ws_bytes(dim);
+    return p;
+  }
+  p.nq = rows <= 8 ? 1 : rows <= 16 || dim == 256 ? 2 : rows <= 24 ? 3 : 4;
+  const long long resident_ctas = (long long)num_sms() * resident(dim, p.nq);
+  p.cluster = rows <= 8 && max_len <= kClusterTokens && (long long)seqs * heads * ACL <= resident_ctas;
+  if (p.cluster) return p;
+  // No more shares than the longest contexts the table allows have chunks.
+  const long long blocks = (rows + 8 * p.nq - 1) / (8 * p.nq);
+  const long long most = (long long)std::min(seqs, ASEQS) * heads * blocks * ((max_len + ACH - 1) / ACH);
+  p.shares = std::min(std::min(resident_ctas, (long long)kShares), most);
+  p.ws = kCutBytes + (size_t)p.shares * 2 * 8 * p.nq * (dim + 2) * 4;
+  return p;
+}
+
 template <class T, int D, int NQ, int CL>
 struct Kernel {
   static constexpr int ST = stages<NQ>(), smem = AW * ST * 2 * kv_block_bytes(D);
   static constexpr auto fn = k_kv4_attention<T, D, NQ, ST, CL>;
-  // Resident CTAs a SM.
-  static gptq_status per_sm(int* out) {
+  static_assert(resident(D, NQ) * (smem + 12288) <= 233472, "the CTAs that the registers leave room for fit");
+  static gptq_status ready() {
     static DeviceOnce attr;
-    static int n = 1;
-    GQ_TRY(attr.run([](int) -> gptq_status {
+    return attr.run([](int) -> gptq_status {
       GQ_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-      int m = 0;
-      GQ_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&m, fn, ATHREADS, smem));
-      n = m < 1 ? 1 : (m > ASHARES ? ASHARES : m);
       return GPTQ_OK;
-    }));
-    *out = n;
-    return GPTQ_OK;
+    });
   }
 };
 
 template <class T, int D>
 gptq_status attn_cluster(const AttnArgs& a, cudaStream_t s) {
   using K = Kernel<T, D, 1, ACL>;
+  GQ_TRY(K::ready());
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.heads * ACL), (unsigned)a.seqs);
   cfg.blockDim = dim3(ATHREADS);
@@ -683,10 +715,9 @@ gptq_status attn_cluster(const AttnArgs& a, cudaStream_t s) {
 }
 
 template <class T, int D, int NQ>
-gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
+gptq_status attn_launch(const AttnArgs& a, long long shares, cudaStream_t s) {
   using K = Kernel<T, D, NQ, 0>;
-  int per_sm = 1;  // one share each
-  GQ_TRY(K::per_sm(&per_sm));
+  GQ_TRY(K::ready());
   const int seqs = a.seqs;
   for (int b0 = 0; b0 < seqs; b0 += ASEQS) {
     AttnArgs p = a;
@@ -700,12 +731,6 @@ gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
       p.out = static_cast<T*>(a.out) + (long long)b0 * a.heads * a.group * D;
       p.tq = p.seqs;
     }
-    // No more shares than the longest contexts the table allows have chunks.
-    const long long blocks = ((long long)a.max_q * a.group + 8 * NQ - 1) / (8 * NQ);
-    const long long most = (long long)p.seqs * a.heads * blocks *
-                           (((long long)a.table_stride * a.page_size + ACH - 1) / ACH);
-    long long shares = std::min((long long)num_sms() * per_sm, (long long)kShares);
-    if (shares > most) shares = most;
     {
       GQ_PROF(K_KV4_ATTENTION, s);
       K::fn<<<(unsigned)shares, ATHREADS, K::smem, s>>>(p, wait_cfg());
@@ -727,48 +752,33 @@ gptq_status attn_launch(AttnArgs a, cudaStream_t s) {
 }
 
 template <class T, int D>
-gptq_status attn_rows(const AttnArgs& a, cudaStream_t s) {
-  const long long rows = (long long)a.max_q * a.group;
-  if (rows <= 8 && (long long)a.table_stride * a.page_size <= kClusterTokens) {
-    int per_sm = 1;
-    GQ_TRY((Kernel<T, D, 1, ACL>::per_sm(&per_sm)));
-    if ((long long)a.seqs * a.heads * ACL <= (long long)num_sms() * per_sm) return attn_cluster<T, D>(a, s);
-  }
-  if (rows <= 8) return attn_launch<T, D, 1>(a, s);
-  if (rows <= 16 || D == 256) return attn_launch<T, D, 2>(a, s);
-  if (rows <= 24) return attn_launch<T, D, D == 256 ? 2 : 3>(a, s);
-  return attn_launch<T, D, D == 256 ? 2 : 4>(a, s);
+gptq_status attn_rows(const AttnArgs& a, const Plan& p, cudaStream_t s) {
+  if (p.cluster) return attn_cluster<T, D>(a, s);
+  if (p.nq == 1) return attn_launch<T, D, 1>(a, p.shares, s);
+  if (p.nq == 2) return attn_launch<T, D, 2>(a, p.shares, s);
+  if (p.nq == 3) return attn_launch<T, D, D == 256 ? 2 : 3>(a, p.shares, s);
+  return attn_launch<T, D, D == 256 ? 2 : 4>(a, p.shares, s);
 }
 
 template <class T>
-gptq_status attn_dim(int dim, const AttnArgs& a, cudaStream_t s) {
-  if (dim == 64) return attn_rows<T, 64>(a, s);
-  if (dim == 128) return attn_rows<T, 128>(a, s);
-  return attn_rows<T, 256>(a, s);
+gptq_status attn_dim(int dim, const AttnArgs& a, const Plan& p, cudaStream_t s) {
+  if (dim == 64) return attn_rows<T, 64>(a, p, s);
+  if (dim == 128) return attn_rows<T, 128>(a, p, s);
+  return attn_rows<T, 256>(a, p, s);
 }
 
 }  // namespace
 
-// More rows a sequence than a CTA of this file takes go to the tcgen05 kernel
-// (kv4_chunk.cu).  Measured, 8 key heads of 128, tcgen05 kernel and this one:
-// 16 sequences of up to 8000 tokens, 32 rows 86 and 88 us, 48 rows 87 and 141,
-// 128 rows 80 and 263; one sequence of 8000, 32 rows 27 and 23, 48 rows 28 and
-// 28, 128 rows 30 and 44; of 1000, 48 rows 17 and 13 (its start costs more).
-// Heads of 256 have no room in tensor memory there.
-bool kv4_is_chunk(int dim, int group, int max_q, bool single) {
-  const long long rows = (long long)max_q * group;
-  return dim <= 128 && !single && rows > 32 && rows <= 256 * 512;
-}
-
-size_t kv4_attention_ws_bytes(int dim, int group, int max_q, bool single) {
-  if (kv4_is_chunk(dim, group, max_q, single)) return kv4_chunk_ws_bytes(dim);
-  return kCutBytes + (size_t)num_sms() * ASHARES * 2 * 32 * (dim + 2) * 4;
+size_t kv4_attention_ws_bytes(int dim, int heads, int group, int max_q, int seqs, bool single, long long max_len) {
+  return plan_of(dim, heads, group, max_q, seqs, single, max_len).ws;
 }
 
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s) {
   if (a.seqs == 0 || a.tq == 0) return GPTQ_OK;
-  if (kv4_is_chunk(dim, a.group, a.max_q, a.q_starts == nullptr)) return kv4_chunk_run(dtype, dim, a, s);
-  return dtype == GPTQ_BF16 ? attn_dim<__nv_bfloat16>(dim, a, s) : attn_dim<__half>(dim, a, s);
+  const Plan p = plan_of(dim, a.heads, a.group, a.max_q, a.seqs, a.q_starts == nullptr,
+                         (long long)a.table_stride * a.page_size);
+  if (p.chunk) return kv4_chunk_run(dtype, dim, a, s);
+  return dtype == GPTQ_BF16 ? attn_dim<__nv_bfloat16>(dim, a, p, s) : attn_dim<__half>(dim, a, p, s);
 }
 
 }  // namespace gq

@@ -481,11 +481,16 @@ gptq_status gptq_kv4_read(int dtype, const uint8_t* cache, long long pages, int 
  *            sequence (tq == seqs).
  *   max_q    host bound on the queries of one sequence.
  *   out      out T [tq][heads*group][dim] (dense).
- *   ws       >= gptq_kv4_attention_workspace_bytes(dim, group, max_q).
+ *   ws       >= gptq_kv4_attention_call_bytes(...) of this call (single: q_starts
+ *            is NULL; max_len: table_stride * page_size), which is 0 where the
+ *            call needs none (ws may then be NULL) and never more than
+ *            gptq_kv4_attention_workspace_bytes(dim, group, max_q).
  * The values of one sequence's keys must be finite where any of its queries
  * sees them; what the pages hold past kv_lens is never used.
  */
 size_t gptq_kv4_attention_workspace_bytes(int dim, int group, int max_q);
+size_t gptq_kv4_attention_call_bytes(int dim, int heads, int group, int max_q, int seqs, int single,
+                                     long long max_len);
 gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
                                const uint8_t* cache, long long pages, int heads, int group, int dim,
                                int page_size, const int* table, int table_stride,

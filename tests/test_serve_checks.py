@@ -126,7 +126,17 @@ def test_c_entries(blib):
     assert attend(group=0) == 2 and attend(stride=0) == 2 and attend(tq=4) == 2 and attend(max_q=2) == 2
     assert attend(qt=4) == 2 and attend(seqs=-1) == 2 and attend(starts=ok, max_q=0) == 2
     assert attend(dt=3) == 1 and attend(scale=float("nan")) == 1 and attend(q=mis) == 1 and attend(lens=None) == 1
-    assert attend(ws=16) == 3
+    assert attend(ws=16, stride=1000) == 3 and attend(ws=0, starts=ok, max_q=100) == 3
     assert attend(tq=0, starts=ok) == 0
     assert lib.gptq_kv4_attention_workspace_bytes(96, 4, 1) == 0
     assert lib.gptq_kv4_attention_workspace_bytes(64, 0, 1) == 0
+    # What one call needs: nothing for few rows over a short table, never more
+    # than the bound that does not know the call.
+    assert lib.gptq_kv4_attention_call_bytes(96, 8, 4, 1, 1, 1, 1024) == 0
+    for dim in (64, 128, 256):
+        for group, max_q in ((1, 1), (8, 1), (16, 1), (4, 5), (4, 8), (8, 9), (4, 512)):
+            bound = lib.gptq_kv4_attention_workspace_bytes(dim, group, max_q)
+            for heads, seqs, length in ((1, 1, 16), (8, 1, 8192), (8, 64, 1024), (1024, 5000, 1 << 30)):
+                need = lib.gptq_kv4_attention_call_bytes(dim, heads, group, max_q, seqs, max_q == 1, length)
+                assert need <= bound
+                assert (need == 0) == (group * max_q <= 8 and seqs * heads <= 8)
