@@ -184,7 +184,23 @@ __device__ __forceinline__ uint2 box_rungs(const LinearArgs& a, int row, int b, 
   return r;
 }
 
+// Floats of shared memory a group for its starting sums, and a warp for the
+// scales that its lanes look up for one another.
+template <int TT>
+constexpr int kInitFloats = TT <= 2 ? TT : 16;
+template <int TT>
+constexpr int kScaleFloats = TT <= 2 ? 0 : 128;
+
 // TT: tokens of a block (1, 2, 4 or 8); FW warps.
+//
+// With one or two tokens the eight columns of a product would be six or seven
+// empty ones.  There a column is (token, group mod 4) instead: lane t of a
+// quad puts group t's codes into its own four of the sixteen places of K, the
+// column of group c holds x in the places of lane c and zeros elsewhere, and
+// one accumulator collects the sums of four groups.  Their scales are then
+// two factors a lane and half a box, looked up by the lane that needs them,
+// where one column takes 32 multiply-adds and an exchange through shared
+// memory.  Measured, one token, 5120 x 17408: 16.9 us against 17.8.
 template <class T, int TT, int FW>
 __global__ void __launch_bounds__(32 * FW)
     k_q4_few(const __grid_constant__ CUtensorMap wmap, LinearArgs a, int boxes, WaitCfg wc) {
@@ -210,9 +226,10 @@ __global__ void __launch_bounds__(32 * FW)
   uint8_t* ring = smem + warp * FST * FBOX;
   uint4* xs = reinterpret_cast<uint4*>(smem + FW * FST * FBOX);               // [group][TT][4]
   float4* init = reinterpret_cast<float4*>(xs + (size_t)boxes * 8 * TT * 4);  // [group][4]: tokens 2t, 2t+1, twice
-  float* tabs = reinterpret_cast<float*>(init + (size_t)boxes * 8 * 4);
-  float* sc = tabs + FROWS * FTAB + warp * 128;  // [16][8]
-  uint2* rung = reinterpret_cast<uint2*>(tabs + FROWS * FTAB + FW * 128);  // [boxes][row]
+  float* init1 = reinterpret_cast<float*>(init);                              // (to two tokens: [token][group])
+  float* tabs = init1 + (size_t)boxes * 8 * kInitFloats<TT>;
+  float* sc = tabs + FROWS * FTAB + warp * kScaleFloats<TT>;                             // [16][8]
+  uint2* rung = reinterpret_cast<uint2*>(tabs + FROWS * FTAB + FW * kScaleFloats<TT>);  // [boxes][row]
 
   if (lane == 0) {
     for (int s = 0; s < FST; ++s) mbar_init(&full[warp * FST + s], 1);
@@ -242,7 +259,8 @@ __global__ void __launch_bounds__(32 * FW)
       for (int i = 0; i < 4; ++i) v[i] = b0 + 2 * i < nbox ? box_rungs(a, row0 + r, box0 + b0 + 2 * i, gpr) : uint2{};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (b0 + 2 * i < nbox) rung[(b0 + 2 * i) * FROWS + r] = v[i];
+        if (b0 + 2 * i < nbox)  // a rung above 31 is entry 32 of its ladder: 0
+          rung[(b0 + 2 * i) * FROWS + r] = uint2{__vminu4(v[i].x, 0x20202020u), __vminu4(v[i].y, 0x20202020u)};
     }
   }
   const T* x = static_cast<const T*>(a.x);
@@ -269,8 +287,12 @@ __global__ void __launch_bounds__(32 * FW)
       if (at < chunks) {
         xs[at] = pair_order(v[i]);
         if (at % 4 == 0) {
-          float* d = reinterpret_cast<float*>(init + grp * 4 + tok / 2) + tok % 2;
-          d[0] = d[2] = s * CodeNum<T>::kInit;
+          if (TT <= 2) {
+            init1[tok * boxes * 8 + grp] = s * CodeNum<T>::kInit;
+          } else {
+            float* d = reinterpret_cast<float*>(init + grp * 4 + tok / 2) + tok % 2;
+            d[0] = d[2] = s * CodeNum<T>::kInit;
+          }
         }
       }
     }
@@ -285,68 +307,133 @@ __global__ void __launch_bounds__(32 * FW)
   __syncthreads();
 
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-
-  // Scales: lane l looks up groups 4 (l % 2) .. + 3 of row l / 2 of each box.
-  const int srow = lane / 2;
-  const uint32_t* rp = reinterpret_cast<const uint32_t*>(rung + warp * 16 + srow) + lane % 2;
-  const float* tp = tabs + (warp * 16 + srow) * FTAB;
-  float4* sp = reinterpret_cast<float4*>(sc) + lane;
-  const float4* sa = reinterpret_cast<const float4*>(sc) + g * 2;
-  // Column g of a token tile: columns past the block's tokens repeat it, and
-  // their sums are not used.
-  const uint4* xp = xs + (TT < 8 ? g % TT : g) * 4 + t;
-  const float4* ip = init + t;
-  // ldmatrix: (rows 0-7, group c), (rows 8-15, group c), the same for c + 1.
-  const int mrow = (lane & 7) + (lane & 8);
-  uint32_t moff[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) moff[c] = (uint32_t)(mrow * 128 + (((2 * c + (lane >> 4)) ^ (mrow & 7)) * 16));
-  int st = 0;
-  uint32_t ph = 0u;
-#pragma unroll 1
-  for (int b = 0; b < nbox; ++b) {
-    const uint32_t rg = *rp;
-    rp += FROWS * 2;
-    __syncwarp();
-    *sp = float4{tp[min(rg & 0xffu, 32u)], tp[min((rg >> 8) & 0xffu, 32u)], tp[min((rg >> 16) & 0xffu, 32u)],
-                 tp[min(rg >> 24, 32u)]};
-    if (!wait_bar_warp(&full[warp * FST + st], ph, abort, wc.ns)) break;
-    const uint32_t base = smem_u32(ring + st * FBOX);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 s_lo = sa[h], s_hi = sa[16 + h];
-      const float lo4[4] = {s_lo.x, s_lo.y, s_lo.z, s_lo.w}, hi4[4] = {s_hi.x, s_hi.y, s_hi.z, s_hi.w};
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        uint32_t w[4];
-        ldmatrix4(w, base + moff[2 * h + p]);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int c = 4 * h + 2 * p + u;
-          const uint32_t a0[4] = {code_num<T>(w[2 * u], 0), code_num<T>(w[2 * u + 1], 0), code_num<T>(w[2 * u], 1),
-                                  code_num<T>(w[2 * u + 1], 1)};
-          const uint32_t a1[4] = {code_num<T>(w[2 * u], 2), code_num<T>(w[2 * u + 1], 2), code_num<T>(w[2 * u], 3),
-                                  code_num<T>(w[2 * u + 1], 3)};
-          const float4 i4 = ip[c * 4];
-          const uint4 xb = xp[c * TT * 4];
-          float d[4] = {i4.x, i4.y, i4.z, i4.w};
-          mma16816<T>(d, a0, xb.x, xb.y);
-          mma16816<T>(d, a1, xb.z, xb.w);
-          acc[0] = fmaf(lo4[2 * p + u], d[0], acc[0]);
-          acc[1] = fmaf(lo4[2 * p + u], d[1], acc[1]);
-          acc[2] = fmaf(hi4[2 * p + u], d[2], acc[2]);
-          acc[3] = fmaf(hi4[2 * p + u], d[3], acc[3]);
-        }
-      }
-    }
-    ip += 8 * 4;
-    xp += 8 * TT * 4;
+  auto refill = [&](int b, int st) {  // the stage that box b has left
     __syncwarp();
     if (lane == 0 && b + FST < nbox) {
       mbar_expect_tx(&full[warp * FST + st], FBOX);
-      tma_load_2d(base, &wmap, (box0 + b + FST) * 128, row0 + warp * 16, &full[warp * FST + st]);
+      tma_load_2d(smem_u32(ring + st * FBOX), &wmap, (box0 + b + FST) * 128, row0 + warp * 16, &full[warp * FST + st]);
     }
-    if (++st == FST) st = 0, ph ^= 1u;
+  };
+  // Row of the box that lane g's first half of a fragment is (the other one
+  // is 8 below): eight lanes' pieces of four groups then meet no bank twice.
+  const int row = TT <= 2 ? (g >> 1) | ((g & 1) << 2) : g;
+
+  if constexpr (TT <= 2) {
+    const bool act = t == g % 4 && g / 4 < TT;  // this lane's places of its column hold x
+    const uint4* xp = xs + (t * TT + (act ? g / 4 : 0)) * 4;
+    const float2* ip = reinterpret_cast<const float2*>(init1 + (t / 2 < TT ? t / 2 : 0) * boxes * 8) + t % 2;
+    const uint2* rp = rung + warp * 16 + row;
+    const float* tl = tabs + (warp * 16 + row) * FTAB;
+    const float* th = tl + 8 * FTAB;
+    const uint32_t off = (uint32_t)(row * 128 + ((t ^ row) * 16));
+    const int shift = 16 * (t % 2);
+    uint4 xb[2][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) xb[i / 4][i % 4] = uint4{};
+    int st = 0;
+    uint32_t ph = 0u;
+#pragma unroll 1
+    for (int b = 0; b < nbox; ++b) {
+      const uint2 rl = rp[0], rh = rp[8];
+      rp += FROWS;
+      const uint32_t wl[2] = {rl.x >> shift, rl.y >> shift}, wh[2] = {rh.x >> shift, rh.y >> shift};
+      float sl[2][2], sh[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sl[h][0] = tl[wl[h] & 0xffu], sl[h][1] = tl[(wl[h] >> 8) & 0xffu];
+        sh[h][0] = th[wh[h] & 0xffu], sh[h][1] = th[(wh[h] >> 8) & 0xffu];
+      }
+      if (act) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xb[i / 4][i % 4] = xp[i / 4 * 4 * TT * 4 + i % 4];
+      }
+      if (!wait_bar_warp(&full[warp * FST + st], ph, abort, wc.ns)) break;
+      const uint8_t* box = ring + st * FBOX;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 c0 = *reinterpret_cast<const uint4*>(box + (off ^ (64u * h)));
+        const uint4 c1 = *reinterpret_cast<const uint4*>(box + (off ^ (64u * h)) + 1024);
+        const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+        const float2 i2 = ip[2 * h];
+        float d[4] = {i2.x, i2.y, i2.x, i2.y};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t a0[4] = {code_num<T>(w0[u], 0), code_num<T>(w1[u], 0), code_num<T>(w0[u], 1),
+                                  code_num<T>(w1[u], 1)};
+          const uint32_t a1[4] = {code_num<T>(w0[u], 2), code_num<T>(w1[u], 2), code_num<T>(w0[u], 3),
+                                  code_num<T>(w1[u], 3)};
+          mma16816<T>(d, a0, xb[h][u].x, xb[h][u].y);
+          mma16816<T>(d, a1, xb[h][u].z, xb[h][u].w);
+        }
+        acc[0] = fmaf(sl[h][1], d[1], fmaf(sl[h][0], d[0], acc[0]));
+        acc[2] = fmaf(sh[h][1], d[3], fmaf(sh[h][0], d[2], acc[2]));
+      }
+      xp += 8 * TT * 4;
+      ip += 4;
+      refill(b, st);
+      if (++st == FST) st = 0, ph ^= 1u;
+    }
+    // Columns 2t, 2t + 1 are two of the four groups of token t / 2.
+    acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
+    acc[2] += __shfl_xor_sync(0xffffffffu, acc[2], 1);
+  } else {
+    // Scales: lane l looks up groups 4 (l % 2) .. + 3 of row l / 2 of each box.
+    const int srow = lane / 2;
+    const uint32_t* rp = reinterpret_cast<const uint32_t*>(rung + warp * 16 + srow) + lane % 2;
+    const float* tp = tabs + (warp * 16 + srow) * FTAB;
+    float4* sp = reinterpret_cast<float4*>(sc) + lane;
+    const float4* sa = reinterpret_cast<const float4*>(sc) + g * 2;
+    // Column g of a token tile: columns past the block's tokens repeat it, and
+    // their sums are not used.
+    const uint4* xp = xs + (TT < 8 ? g % TT : g) * 4 + t;
+    const float4* ip = init + t;
+    // ldmatrix: (rows 0-7, group c), (rows 8-15, group c), the same for c + 1.
+    const int mrow = (lane & 7) + (lane & 8);
+    uint32_t moff[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) moff[c] = (uint32_t)(mrow * 128 + (((2 * c + (lane >> 4)) ^ (mrow & 7)) * 16));
+    int st = 0;
+    uint32_t ph = 0u;
+#pragma unroll 1
+    for (int b = 0; b < nbox; ++b) {
+      const uint32_t rg = *rp;
+      rp += FROWS * 2;
+      __syncwarp();
+      *sp = float4{tp[rg & 0xffu], tp[(rg >> 8) & 0xffu], tp[(rg >> 16) & 0xffu], tp[rg >> 24]};
+      if (!wait_bar_warp(&full[warp * FST + st], ph, abort, wc.ns)) break;
+      const uint32_t base = smem_u32(ring + st * FBOX);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 s_lo = sa[h], s_hi = sa[16 + h];
+        const float lo4[4] = {s_lo.x, s_lo.y, s_lo.z, s_lo.w}, hi4[4] = {s_hi.x, s_hi.y, s_hi.z, s_hi.w};
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t w[4];
+          ldmatrix4(w, base + moff[2 * h + p]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int c = 4 * h + 2 * p + u;
+            const uint32_t a0[4] = {code_num<T>(w[2 * u], 0), code_num<T>(w[2 * u + 1], 0), code_num<T>(w[2 * u], 1),
+                                    code_num<T>(w[2 * u + 1], 1)};
+            const uint32_t a1[4] = {code_num<T>(w[2 * u], 2), code_num<T>(w[2 * u + 1], 2), code_num<T>(w[2 * u], 3),
+                                    code_num<T>(w[2 * u + 1], 3)};
+            const float4 i4 = ip[c * 4];
+            const uint4 xb = xp[c * TT * 4];
+            float d[4] = {i4.x, i4.y, i4.z, i4.w};
+            mma16816<T>(d, a0, xb.x, xb.y);
+            mma16816<T>(d, a1, xb.z, xb.w);
+            acc[0] = fmaf(lo4[2 * p + u], d[0], acc[0]);
+            acc[1] = fmaf(lo4[2 * p + u], d[1], acc[1]);
+            acc[2] = fmaf(hi4[2 * p + u], d[2], acc[2]);
+            acc[3] = fmaf(hi4[2 * p + u], d[3], acc[3]);
+          }
+        }
+      }
+      ip += 8 * 4;
+      xp += 8 * TT * 4;
+      refill(b, st);
+      if (++st == FST) st = 0, ph ^= 1u;
+    }
   }
   __syncthreads();
   if (abort_sh) {
@@ -362,8 +449,8 @@ __global__ void __launch_bounds__(32 * FW)
   float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int tok = 2 * t + (e & 1);
-    if (tok < TT) part[tok * FROWS + warp * 16 + g + (e >> 1) * 8] = acc[e];
+    const int tok = TT <= 2 ? t / 2 : 2 * t + (e & 1);
+    if (tok < TT && (TT > 2 || (e | t) % 2 == 0)) part[tok * FROWS + warp * 16 + row + (e >> 1) * 8] = acc[e];
   }
   namespace cg = cooperative_groups;
   if (nrank > 1)
@@ -986,8 +1073,8 @@ gptq_status make_code_map(CUtensorMap* m, const uint8_t* nib, int rows, int n, i
 template <int TT, int FW>
 size_t few_smem(int boxes) {
   constexpr int FROWS = 16 * FW;
-  return 1024 + (size_t)FW * FST * FBOX + (size_t)boxes * 8 * 64 * (TT + 1) +
-         (size_t)(FROWS * FTAB + FW * 128) * 4 + (size_t)FROWS * boxes * 8;
+  return 1024 + (size_t)FW * FST * FBOX + (size_t)boxes * 8 * (64 * TT + 4 * kInitFloats<TT>) +
+         (size_t)(FROWS * FTAB + FW * kScaleFloats<TT>) * 4 + (size_t)FROWS * boxes * 8;
 }
 
 template <class T, int TT, int FW>
@@ -1002,8 +1089,10 @@ gptq_status few_launch(const LinearArgs& a, cudaStream_t s) {
   GQ_TRY(make_code_map(&m, a.nibbles, a.rows, a.n, 16));
   const int nbox = (a.n / GROUP + 7) / 8;
   const int rb = (a.rows + FROWS - 1) / FROWS, tz = (a.tokens + TT - 1) / TT;
-  // The split of the columns that takes the fewest boxes in a row, a CTA's
-  // start and end counted as four, among those whose slices fit.
+  // The split of the columns with the least time, among those whose slices
+  // fit.  In units of the 500 cycles that a box costs the SM's quarter that
+  // decodes it: no warp takes a box in less than two, and a CTA's start and
+  // end (ladders, rungs, x; the sum over the cluster) take twenty.
   int split = 8, boxes = 0;
   long long least = -1;
   for (int k = 8; k >= 1; --k) {
@@ -1011,8 +1100,9 @@ gptq_status few_launch(const LinearArgs& a, cudaStream_t s) {
     if (few_smem<TT, FW>(bx) > kFewSmem) break;
     long long slots = (long long)(233472 / (few_smem<TT, FW>(bx) + 1024 + 512));
     if (slots > 32 / FW) slots = 32 / FW;  // registers
-    const long long ctas = (long long)rb * tz * ((nbox + bx - 1) / bx);
-    const long long cost = ((ctas + slots * num_sms() - 1) / (slots * num_sms())) * (bx + 4) * slots;
+    const long long ctas = (long long)rb * tz * ((nbox + bx - 1) / bx), sms = num_sms();
+    const long long at_once = std::min(slots, (ctas + sms - 1) / sms) * FW / 4;
+    const long long cost = ((ctas + slots * sms - 1) / (slots * sms)) * (bx * std::max(2ll, at_once) + 20);
     if (least < 0 || cost < least) least = cost, split = (nbox + bx - 1) / bx, boxes = bx;
   }
   cudaLaunchConfig_t cfg{};
@@ -1149,7 +1239,7 @@ gptq_status many_launch(const LinearArgs& a, cudaStream_t s) {
 
 template <class T>
 gptq_status linear_t(const LinearArgs& a, cudaStream_t s) {
-  // Up to 8 tokens the few-token kernel is the faster (5120 x 17408: 20 / 27
+  // Up to 8 tokens the few-token kernel is the faster (5120 x 17408: 17 / 26
   // us for 1 / 8 tokens against 28); at 16 its blocks of x leave one CTA a SM
   // (58 us against 29).
   if (a.tokens <= 8) return few_tokens<T>(a, s);
