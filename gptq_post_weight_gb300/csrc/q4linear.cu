@@ -70,7 +70,8 @@ __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
     case GPTQ_ACT_RELU: return v > 0.f ? v : (v != v ? v : 0.f);
     case GPTQ_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    case GPTQ_ACT_GELU_TANH: return 0.5f * v * (1.f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
+    case GPTQ_ACT_GELU_TANH:  // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+      return v / (1.f + expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
     case GPTQ_ACT_SILU: return v / (1.f + expf(-v));
     default: return v;
   }
@@ -105,11 +106,12 @@ __device__ __forceinline__ void finish8(const LinearArgs& a, int tok, int r, boo
     if (a.bias != nullptr) add8<T>(v, *reinterpret_cast<const uint4*>(static_cast<const T*>(a.bias) + r));
     if (a.act != GPTQ_ACT_NONE) {
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {  // one copy of the activations' code
-        const float x = activate(v[0], a.act);
+      for (int i = 0; i < 2; ++i) {  // (one at a time 20.5 us for the case of k_q4_mid, eight 20.1, four 19.9)
+        float x[4];
 #pragma unroll
-        for (int k = 0; k < 7; ++k) v[k] = v[k + 1];
-        v[7] = x;
+        for (int k = 0; k < 4; ++k) x[k] = activate(v[k], a.act);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = v[k + 4], v[k + 4] = x[k];
       }
     }
     if (a.residual != nullptr) add8<T>(v, raw);
