@@ -1167,31 +1167,66 @@ gptq_status make_x_map(CUtensorMap* m, const LinearArgs& a, bool bf16, int box_r
 }
 
 // Shape of a launch of k_q4_mid: token tiles, tokens a tile, boxes a CTA,
-// CTAs of a cluster.
+// CTAs of a cluster; and the cycles it takes.
 struct MidShape {
   int nt, tn, boxes, split;
+  double cycles;
 };
-MidShape mid_shape(const LinearArgs& a) {
-  MidShape m;
+
+// Clusters of one to eight CTAs of k_q4_mid that run at once (a CTA fills an
+// SM; clusters stay within a part of the GPU, so that 152 SMs hold 36 clusters
+// of four, 23 of six and 15 of eight: 2048 x 4096, 45 tokens, in sixteen of
+// eight took 25.2 us, in sixteen of six it takes 12.7).
+template <class T>
+gptq_status mid_clusters(const int** out) {
+  static DeviceOnce attr;
+  static int active[9];
+  GQ_TRY(attr.run([](int) -> gptq_status {
+    constexpr int most = 1024 + MNS * QBOX + 128 * 1024 + QROWS * QTAB * 4;
+    GQ_CUDA(cudaFuncSetAttribute(k_q4_mid<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    for (int k = 1; k <= 8; ++k) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(1, 1, (unsigned)k);
+      cfg.blockDim = dim3(640);
+      cfg.dynamicSmemBytes = most;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = at[0].val.clusterDim.y = 1;
+      at[0].val.clusterDim.z = (unsigned)k;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      GQ_CUDA(cudaOccupancyMaxActiveClusters(&n, k_q4_mid<T>, &cfg));
+      active[k] = n < 1 ? 1 : n;
+    }
+    return GPTQ_OK;
+  }));
+  *out = active;
+  return GPTQ_OK;
+}
+
+// The split of the columns with the least time.  A stage takes 575 cycles,
+// more above 128 tokens a tile (x then streams through half the ring), a
+// CTA's start and end 9000.
+MidShape mid_shape(const LinearArgs& a, const int* active) {
+  MidShape best{};
   const int nbox = (a.n / GROUP + 7) / 8, rb = (a.rows + QROWS - 1) / QROWS;
-  m.nt = (a.tokens + MTN - 1) / MTN;
-  m.tn = ((a.tokens + m.nt - 1) / m.nt + 15) / 16 * 16;
-  m.split = num_sms() / (rb * m.nt);
-  m.split = m.split < 1 ? 1 : (m.split > 8 ? 8 : m.split);
-  m.boxes = (nbox + m.split - 1) / m.split;
-  m.split = (nbox + m.boxes - 1) / m.boxes;
-  return m;
+  const int nt = (a.tokens + MTN - 1) / MTN, tn = ((a.tokens + nt - 1) / nt + 15) / 16 * 16;
+  const double stage = 575.0 + 3.3 * (tn > 128 ? tn - 128 : 0);
+  for (int k = 1; k <= 8 && k <= nbox; ++k) {
+    const int boxes = (nbox + k - 1) / k, split = (nbox + boxes - 1) / boxes;
+    const long long rounds = ((long long)rb * nt + active[split] - 1) / active[split];
+    // (In several rounds clusters wait for one another's places: 14336 x 4096,
+    // 300 tokens in three rounds of pairs 60 us, in two of single CTAs 46.)
+    if (split > 1 && rounds > 1) continue;
+    const double cycles = (double)rounds * (boxes * 4 * stage + 9000.0);
+    if (best.split == 0 || cycles < best.cycles) best = MidShape{nt, tn, boxes, split, cycles};
+  }
+  return best;
 }
 
 template <class T>
-gptq_status mid_launch(const LinearArgs& a, cudaStream_t s) {
-  static DeviceOnce attr;
-  GQ_TRY(attr.run([](int) -> gptq_status {
-    GQ_CUDA(cudaFuncSetAttribute(k_q4_mid<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 1024 + MNS * QBOX + 128 * 1024 + QROWS * QTAB * 4));
-    return GPTQ_OK;
-  }));
-  const MidShape ms = mid_shape(a);
+gptq_status mid_launch(const LinearArgs& a, const MidShape& ms, cudaStream_t s) {
   const int rb = (a.rows + QROWS - 1) / QROWS, nt = ms.nt, tn = ms.tn, boxes = ms.boxes, split = ms.split;
   const int nx = tn > 128 ? MXS / 2 : MXS;
   CUtensorMap wm, xm;
@@ -1260,17 +1295,15 @@ gptq_status linear_t(const LinearArgs& a, cudaStream_t s) {
   // (58 us against 29).
   if (a.tokens <= 8) return few_tokens<T>(a, s);
   // Cycles of the two kernels as measured over 17 .. 4096 tokens (4096 x
-  // 4096, 5120 x 17408, 14336 x 4096): a stage takes 575 on one SM, more
-  // above 128 tokens a tile (x then streams through half the ring), and 540
-  // on a pair of SMs, which spends 13000 more on a tile.
-  const MidShape ms = mid_shape(a);
-  const long long sms = num_sms(), rb = (a.rows + QROWS - 1) / QROWS;
-  const double stage = 575.0 + 3.3 * (ms.tn > 128 ? ms.tn - 128 : 0);
-  const double mid = (double)((rb * ms.nt * ms.split + sms - 1) / sms) * (ms.boxes * 4 * stage + 9000.0);
+  // 4096, 5120 x 17408, 14336 x 4096): mid_shape has the first's; a stage takes
+  // 540 on a pair of SMs, which spends 13000 more on a tile.
+  const int* active = nullptr;
+  GQ_TRY(mid_clusters<T>(&active));
+  const MidShape ms = mid_shape(a, active);
   long long rounds;
-  many_tile(a.tokens, (a.rows + 2 * QROWS - 1) / (2 * QROWS), (int)(sms / 2), rounds);
+  many_tile(a.tokens, (a.rows + 2 * QROWS - 1) / (2 * QROWS), num_sms() / 2, rounds);
   const double many = (double)rounds * ((a.n / GROUP + 7) / 8 * 4 * 540.0 + 13000.0);
-  return mid <= many ? mid_launch<T>(a, s) : many_launch<T>(a, s);
+  return ms.cycles <= many ? mid_launch<T>(a, ms, s) : many_launch<T>(a, s);
 }
 
 }  // namespace
