@@ -1093,12 +1093,38 @@ size_t few_smem(int boxes) {
          (size_t)(FROWS * FTAB + FW * kScaleFloats<TT>) * 4 + (size_t)FROWS * boxes * 8;
 }
 
+// A launch of k_q4_few with clusters of k CTAs.
+template <class T, int TT, int FW>
+struct FewLaunch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  FewLaunch(unsigned rb, unsigned k, unsigned tz, size_t smem) {
+    cfg.gridDim = dim3(rb, k, tz);
+    cfg.blockDim = dim3(32 * FW);
+    cfg.dynamicSmemBytes = smem;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = at[0].val.clusterDim.z = 1;
+    at[0].val.clusterDim.y = k;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+};
+
+constexpr int kFewSlots = 8;  // CTAs an SM at most
+constexpr size_t few_slot_smem(int slots) { return 233472 / slots - 1536; }
+
 template <class T, int TT, int FW>
 gptq_status few_launch(const LinearArgs& a, cudaStream_t s) {
   constexpr int FROWS = 16 * FW;
   static DeviceOnce attr;
+  static int active[9][kFewSlots + 1];  // clusters of k that run at once, by CTAs an SM
   GQ_TRY(attr.run([](int) -> gptq_status {
     GQ_CUDA(cudaFuncSetAttribute(k_q4_few<T, TT, FW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem));
+    for (int k = 1; k <= 8; ++k)
+      for (int n = 1; n <= kFewSlots; ++n) {
+        FewLaunch<T, TT, FW> l(1, (unsigned)k, 1, std::min(few_slot_smem(n), kFewSmem));
+        GQ_CUDA(cudaOccupancyMaxActiveClusters(&active[k][n], k_q4_few<T, TT, FW>, &l.cfg));
+      }
     return GPTQ_OK;
   }));
   CUtensorMap m;
@@ -1108,33 +1134,28 @@ gptq_status few_launch(const LinearArgs& a, cudaStream_t s) {
   // The split of the columns with the least time, among those whose slices
   // fit.  In units of the 500 cycles that a box costs the SM's quarter that
   // decodes it: no warp takes a box in less than two, and a CTA's start and
-  // end (ladders, rungs, x; the sum over the cluster) take twenty.
-  int split = 8, boxes = 0;
+  // end (ladders, rungs, x; the sum over the cluster) take twenty.  Clusters
+  // stay within a part of the GPU, so that fewer CTAs of large ones run at
+  // once (6000 x 4096, one token: 94 clusters of eight 12.2 us, of four 8.9).
+  int split = 0, boxes = 0;
   long long least = -1;
   for (int k = 8; k >= 1; --k) {
-    const int bx = (nbox + k - 1) / k;
-    if (few_smem<TT, FW>(bx) > kFewSmem) break;
-    long long slots = (long long)(233472 / (few_smem<TT, FW>(bx) + 1024 + 512));
-    if (slots > 32 / FW) slots = 32 / FW;  // registers
-    const long long ctas = (long long)rb * tz * ((nbox + bx - 1) / bx), sms = num_sms();
-    const long long at_once = std::min(slots, (ctas + sms - 1) / sms) * FW / 4;
-    const long long cost = ((ctas + slots * sms - 1) / (slots * sms)) * (bx * std::max(2ll, at_once) + 20);
-    if (least < 0 || cost < least) least = cost, split = (nbox + bx - 1) / bx, boxes = bx;
+    const int bx = (nbox + k - 1) / k, sp = (nbox + bx - 1) / bx;
+    const size_t smem = few_smem<TT, FW>(bx);
+    if (smem > kFewSmem) break;
+    int slots = kFewSlots;
+    while (slots > 1 && smem > few_slot_smem(slots)) --slots;
+    const long long clusters = (long long)rb * tz, sms = num_sms(), room = active[sp][slots];
+    if (room < 1) continue;
+    const long long at_once = std::min((long long)slots, (clusters * sp + sms - 1) / sms) * FW / 4;
+    const long long cost = ((clusters + room - 1) / room) * (bx * std::max(2ll, at_once) + 20);
+    if (least < 0 || cost < least) least = cost, split = sp, boxes = bx;
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)rb, (unsigned)split, (unsigned)tz);
-  cfg.blockDim = dim3(32 * FW);
-  cfg.dynamicSmemBytes = few_smem<TT, FW>(boxes);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 1;
-  at[0].val.clusterDim.y = (unsigned)split;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  if (split == 0) return GPTQ_ERR_SHAPE;
+  FewLaunch<T, TT, FW> l((unsigned)rb, (unsigned)split, (unsigned)tz, few_smem<TT, FW>(boxes));
+  l.cfg.stream = s;
   GQ_PROF(K_Q4_LINEAR, s);
-  GQ_CUDA(cudaLaunchKernelEx(&cfg, k_q4_few<T, TT, FW>, m, a, boxes, wait_cfg()));
+  GQ_CUDA(cudaLaunchKernelEx(&l.cfg, k_q4_few<T, TT, FW>, m, a, boxes, wait_cfg()));
   return GPTQ_OK;
 }
 
