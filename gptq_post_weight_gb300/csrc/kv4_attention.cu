@@ -647,10 +647,11 @@ constexpr int kClusterTokens = 8192;
 // 16 sequences of up to 8000 tokens, 32 rows 86 and 88 us, 48 rows 87 and 141,
 // 128 rows 80 and 263; one sequence of 8000, 32 rows 27 and 23, 48 rows 28 and
 // 28, 128 rows 30 and 44; of 1000, 48 rows 17 and 13 (its start costs more).
-// Heads of 256 have no room in tensor memory there.
+// Heads of 256, 112 rows: 48 sequences to 4000, 217 and 633; one of 4000, 33
+// and 34.
 bool kv4_is_chunk(int dim, int group, int max_q, bool single) {
   const long long rows = (long long)max_q * group;
-  return dim <= 128 && !single && rows > 32 && rows <= 256 * 512;
+  return !single && rows > 32 && rows <= (dim == 256 ? 128 : 256) * 512;
 }
 
 // What a call launches and what it needs for that.

@@ -22,10 +22,14 @@
 // unnormalised output (f32) in the workspace, and k_kv4_chunk_join adds the
 // pieces in the order of the list.
 // Measured: 2 sequences of 2048 queries of 32 heads (8 key heads of 128),
-// contexts to 8192: 327 us, 0.92 PFLOP/s, the tensor cores 46 % busy.  A step of a tile is a
-// chain of 3650 cycles (maximum 440, exchange 180, exponentials 1400, products
-// 1250 and their waits), of which two tiles overlap; tensor memory has no room
-// for a third.
+// contexts to 8192: 327 us, 0.92 PFLOP/s, the tensor cores 46 % busy.  A step
+// of a tile is a chain of 3650 cycles (maximum 440, exchange 180, exponentials
+// 1400, products 1250 and their waits), of which two tiles overlap; tensor
+// memory has no room for a third.
+// Heads of 256 have one tile of 128 rows and steps of 64 keys: their outputs
+// take half of tensor memory, and K and V of a step are as large as with 128
+// keys of 128 (48 sequences of 7 queries of 8 x 16 heads, contexts to 4000: 217
+// us, three times as fast as sixteen rows at a time on mma.sync).
 // Tensor memory: S_A, S_B (128 columns each; P of each half of the keys over
 // the first 32 columns of its scores), O_A, O_B (D columns each).
 // The running maximum is only raised (and O rescaled, by its rows' threads,
@@ -38,8 +42,12 @@
 namespace gq {
 namespace {
 
-constexpr int CK = 128;     // keys a step
-constexpr int CROWS = 256;  // query rows a CTA
+// Keys a step, and query rows a CTA: heads of 256 leave tensor and shared
+// memory for half of both.
+template <int D>
+constexpr int kKeys = D == 256 ? 64 : 128;
+template <int D>
+constexpr int kRows = D == 256 ? 128 : 256;
 constexpr int CTHREADS = 896;
 constexpr int CLIST = 512;   // (sequence, row block) pairs of one launch at most
 constexpr int CSTART = 3;    // what a tile's start and end cost, in steps
@@ -157,12 +165,13 @@ __device__ __forceinline__ uint32_t swz(int r, int p) { return (uint32_t)(r * 12
 
 template <int D>
 struct ChunkSmem {  // byte offsets; 1024-byte aligned operands
-  static constexpr int kTile = CK * D * 2;           // K, V, and a tile of Q
+  static constexpr int CK = kKeys<D>;
+  static constexpr int kQTile = 128 * D * 2, kTile = CK * D * 2;  // a tile of Q; K or V of a step
   // Codes come in units of 128 groups (of K and of V): a group a decoding thread.
   static constexpr int kTokens = 128 / (D / 32), kUnits = CK / kTokens, kBlocks = kTokens / KV_BLOCK;
   static constexpr int kRaw = kBlocks * kv_block_bytes(D);
-  static constexpr int q = 0;                        // two tiles
-  static constexpr int k = q + 2 * kTile;            // two steps
+  static constexpr int q = 0;                                // its tiles
+  static constexpr int k = q + kRows<D> / 128 * kQTile;      // two steps
   static constexpr int v = k + 2 * kTile;            // two steps
   static constexpr int raw = v + 2 * kTile;          // the units of one step
   static constexpr int bytes = raw + kUnits * kRaw + 1024;
@@ -172,15 +181,16 @@ struct ChunkSmem {  // byte offsets; 1024-byte aligned operands
 struct Pair {
   int q0, nq, len, r0, rows, vis, steps;
 };
+template <int D>
 __device__ __forceinline__ Pair pair_of(const AttnArgs& a, int b, int rb) {
   Pair t;
   t.q0 = min(max(a.q_starts[b], 0), a.tq);
   t.nq = min(min(max(a.q_starts[b + 1], t.q0), a.tq) - t.q0, a.max_q);
   t.len = (int)min((long long)max(a.kv_lens[b], 0), (long long)a.table_stride * a.page_size);
-  t.r0 = rb * CROWS;
-  t.rows = max(0, min(CROWS, t.nq * a.group - t.r0));
+  t.r0 = rb * kRows<D>;
+  t.rows = max(0, min(kRows<D>, t.nq * a.group - t.r0));
   t.vis = t.rows > 0 ? max(0, min(t.len, t.len - t.nq + (t.r0 + t.rows - 1) / a.group + 1)) : 0;
-  t.steps = (t.vis + CK - 1) / CK;
+  t.steps = (t.vis + kKeys<D> - 1) / kKeys<D>;
   return t;
 }
 // Units of a tile in the list: its steps (one that writes zeros if its rows
@@ -189,12 +199,13 @@ __device__ __forceinline__ int units_of(const Pair& t) { return t.rows > 0 ? max
 
 // pref[i] = units of one head before pair i = (sequence i / nblk, row block
 // i % nblk); pref[pairs] = all.  By every thread of the CTA.
+template <int D>
 __device__ void pair_prefix(const AttnArgs& a, int nblk, long long* pref, long long* scratch) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, pairs = a.seqs * nblk;
   long long before = 0;
   for (int p0 = 0; p0 < pairs; p0 += CTHREADS) {
     const int p = p0 + tid;
-    const long long mine = p < pairs ? units_of(pair_of(a, p / nblk, p % nblk)) : 0;
+    const long long mine = p < pairs ? units_of(pair_of<D>(a, p / nblk, p % nblk)) : 0;
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -223,6 +234,7 @@ struct Piece {
   bool whole;
   long long next;
 };
+template <int D>
 __device__ __forceinline__ Piece piece_at(const AttnArgs& a, int nblk, const long long* pref, long long u, long long uend) {
   int lo = 0, hi = a.seqs * nblk - 1;  // the last pair that starts at or before u
   while (lo < hi) {
@@ -231,7 +243,7 @@ __device__ __forceinline__ Piece piece_at(const AttnArgs& a, int nblk, const lon
   }
   Piece p;
   p.b = lo / nblk;
-  p.t = pair_of(a, p.b, lo % nblk);
+  p.t = pair_of<D>(a, p.b, lo % nblk);
   const int n = units_of(p.t);
   const long long rem = u - pref[lo] * a.heads;
   int at;
@@ -250,13 +262,14 @@ __device__ __forceinline__ Piece piece_at(const AttnArgs& a, int nblk, const lon
   return p;
 }
 
-constexpr size_t piece_floats(int dim) { return (size_t)CROWS * (dim + 2); }
+constexpr int rows_of(int dim) { return dim == 256 ? kRows<256> : kRows<128>; }
+constexpr size_t piece_floats(int dim) { return (size_t)rows_of(dim) * (dim + 2); }
 
 template <class T, int D>
 __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk, WaitCfg wc) {
   using T2 = typename Elem<T>::T2;
   using S = ChunkSmem<D>;
-  constexpr int BB = kv_block_bytes(D), HALVES = D / 64;
+  constexpr int BB = kv_block_bytes(D), HALVES = D / 64, CK = kKeys<D>;
   constexpr uint32_t kO = 256;  // tensor memory: S_A 0, S_B 128, O_A 256, O_B 256 + D
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -288,7 +301,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
-  pair_prefix(a, nblk, pref, scratch);
+  pair_prefix<D>(a, nblk, pref, scratch);
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_kv4_chunk_join may set itself up
   const long long W = pref[a.seqs * nblk] * a.heads;
@@ -318,7 +331,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       int last, j, j1;
       bool active;
       {
-        const Piece pc = piece_at(a, nblk, pref, u, uend);
+        const Piece pc = piece_at<D>(a, nblk, pref, u, uend);
         if (pc.j1 == 0) {  // no steps of the tile in this share
           u = pc.next;
           continue;
@@ -326,23 +339,27 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
         const bool mine = 128 * x + rt < pc.t.rows;
         const int rr = pc.t.r0 + min(128 * x + rt, pc.t.rows - 1);
         const int qi = rr / a.group, hq = pc.head * a.group + rr % a.group;
-        last = mine ? pc.t.len - pc.t.nq + qi - 64 * half : -1 - 64 * half;  // among this thread's columns
+        last = mine ? pc.t.len - pc.t.nq + qi - CK / 2 * half : -1 - CK / 2 * half;  // among this thread's columns
         j = pc.j0;
         j1 = min(pc.j1, pc.t.steps);  // (a tile that sees nothing: no steps)
         active = x == 0 || pc.t.rows > 128;
         // Half of the row's q, in the nibbles' order of channels.
         const T* qp = static_cast<const T*>(a.q) + (long long)(pc.t.q0 + qi) * a.q_ts + (long long)hq * a.q_hs +
                       D / 2 * half;
-        uint8_t* tile = smem + S::q + x * S::kTile;
-        uint4 v[D / 16];
+        uint8_t* tile = smem + S::q + x * S::kQTile;
+        constexpr int QC = D / 16 < 8 ? D / 16 : 8;  // pieces at a time
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 16 && x < kRows<D> / 128; c0 += QC) {
+          uint4 v[QC];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) v[c] = mine ? *reinterpret_cast<const uint4*>(qp + 8 * c) : uint4{};
+          for (int c = 0; c < QC; ++c) v[c] = mine ? *reinterpret_cast<const uint4*>(qp + 8 * (c0 + c)) : uint4{};
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const int at = D / 16 * half + c;
-          uint4 o = pair_order(v[c]);
-          o.x ^= flip, o.y ^= flip, o.z ^= flip, o.w ^= flip;
-          *reinterpret_cast<uint4*>(tile + at / 8 * (CK * 128) + swz(rt, at % 8)) = o;
+          for (int c = 0; c < QC; ++c) {
+            const int at = D / 16 * half + c0 + c;
+            uint4 o = pair_order(v[c]);
+            o.x ^= flip, o.y ^= flip, o.z ^= flip, o.w ^= flip;
+            *reinterpret_cast<uint4*>(tile + at / 8 * (128 * 128) + swz(rt, at % 8)) = o;
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(&qfull);
@@ -358,14 +375,14 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
         ok = wait_bar_warp(&sfull[x], sph, abort, wc.ns);
         sph ^= 1u;
         const int lim = last - j * CK;  // last visible column of this half
-        const bool masked = __any_sync(0xffffffffu, lim < 63);
+        const bool masked = __any_sync(0xffffffffu, lim < CK / 2 - 1);
         float top = -INFINITY;
         if (ok) {
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < CK / 64; ++c) {
             uint32_t v[32];
-            tmem_ld32(ts + 64u * (uint32_t)half + 32u * (uint32_t)c, v);
+            tmem_ld32(ts + (uint32_t)(CK / 2 * half) + 32u * (uint32_t)c, v);
             tmem_ld_wait();
             if (masked) hide(v, lim - 32 * c);
             float t2[2] = {top, fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]))};
@@ -401,11 +418,11 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
         const uint64_t sl2 = pack2(sl, sl), ms2 = pack2(ms, ms);
         uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < CK / 64; ++c) {
           // (Read again: a row of 128 does not leave registers enough for the
           // number of warps that hide these latencies.)
           uint32_t v[32], p[16];
-          tmem_ld32(ts + 64u * (uint32_t)half + 32u * (uint32_t)c, v);
+          tmem_ld32(ts + (uint32_t)(CK / 2 * half) + 32u * (uint32_t)c, v);
           tmem_ld_wait();
           if (masked) hide(v, lim - 32 * c);
 #pragma unroll
@@ -415,7 +432,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
             sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
             p[i] = bits2(Elem<T>::make2(e0, e1));
           }
-          tmem_st16(ts + 64u * (uint32_t)half + 16u * (uint32_t)c, p);
+          tmem_st16(ts + (uint32_t)(CK / 2 * half) + 16u * (uint32_t)c, p);
         }
         const float2 s0 = unpack2(sum2[0]), s1 = unpack2(sum2[1]);
         l += (s0.x + s0.y) + (s1.x + s1.y);
@@ -435,7 +452,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       l += xmax[par][x][half ^ 1][rt];
       par ^= 1u;
       tc_fence_after();
-      const Piece pc = piece_at(a, nblk, pref, u, uend);
+      const Piece pc = piece_at<D>(a, nblk, pref, u, uend);
       u = pc.next;
       if (threadIdx.x == 0 && pc.j0 == 0 && !pc.whole) {  // a cut tile's first piece: the join's work
         const long long w = pref[a.seqs * nblk] * a.heads, n = min(w, (long long)gridDim.x);
@@ -477,7 +494,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
         }
       }
       if (!pc.whole && mine && half == 0)
-        *reinterpret_cast<float2*>(part + (size_t)CROWS * D + 2 * (128 * x + rt)) = float2{m, l};
+        *reinterpret_cast<float2*>(part + (size_t)kRows<D> * D + 2 * (128 * x + rt)) = float2{m, l};
       tc_fence_before();
     }
   } else if (warp < 24) {
@@ -489,11 +506,11 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
     const bool isv = warp >= 20;
     constexpr int GR = D / 32;  // groups a token
     const int grp = dt % GR, tok = dt / GR;
-    const bool swap = GR == 4 && grp >= 2;
+    const int turn = GR == 8 ? grp / 2 : GR == 4 ? grp / 2 * 2 : 0;
     uint32_t off[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      off[u] = (uint32_t)(grp / 2 * (CK * 128)) + swz(tok, grp % 2 * 4 + (u ^ (swap ? 2 : 0)));
+      off[u] = (uint32_t)(grp / 2 * (CK * 128)) + swz(tok, grp % 2 * 4 + (u ^ turn));
     const uint8_t* from = smem + S::raw + tok / KV_BLOCK * BB + (isv ? kv_value_off(D) : 0);
     const uint8_t* from_codes = from + tok % KV_BLOCK * (D / 2) + grp * 16;
     const uint8_t* from_par = from + kv_param_off(D) + tok % KV_BLOCK * (D / 8) + grp * 4;
@@ -503,7 +520,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
     int n = 0;  // steps so far
 #pragma unroll 1
     for (long long u = ubeg; u < uend && ok;) {
-      const Piece pc = piece_at(a, nblk, pref, u, uend);
+      const Piece pc = piece_at<D>(a, nblk, pref, u, uend);
       u = pc.next;
 #pragma unroll 1
       for (int j = pc.j0; j < min(pc.j1, pc.t.steps); ++j, ++n) {
@@ -519,10 +536,17 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
           __syncwarp();
           if (lane == 0) mbar_arrive(&rawempty[q]);
           if (q * S::kTokens >= seen) par = 0u;  // past what any row sees: no value, whatever is there
-          if (GR == 4) {
+          if (GR >= 4) {
+            const bool two = (turn & 2) != 0;
             const uint4 c = codes;
-            codes.x = swap ? c.z : c.x, codes.y = swap ? c.w : c.y;
-            codes.z = swap ? c.x : c.z, codes.w = swap ? c.y : c.w;
+            codes.x = two ? c.z : c.x, codes.y = two ? c.w : c.y;
+            codes.z = two ? c.x : c.z, codes.w = two ? c.y : c.w;
+          }
+          if (GR == 8) {
+            const bool one = (turn & 1) != 0;
+            const uint4 c = codes;
+            codes.x = one ? c.y : c.x, codes.y = one ? c.x : c.y;
+            codes.z = one ? c.w : c.z, codes.w = one ? c.z : c.w;
           }
           const T2 s2 = from_bits2<T2>(__byte_perm(par, par, 0x1010)), z2 = from_bits2<T2>(__byte_perm(par, par, 0x3232));
           const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
@@ -552,7 +576,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       int n = 0;
 #pragma unroll 1
       for (long long u = ubeg; u < uend && ok;) {
-        const Piece pc = piece_at(a, nblk, pref, u, uend);
+        const Piece pc = piece_at<D>(a, nblk, pref, u, uend);
         u = pc.next;
         const int nb = (pc.t.vis + KV_BLOCK - 1) / KV_BLOCK;
         const int* trow = a.table + (long long)pc.b * a.table_stride;
@@ -594,14 +618,14 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       for (int h = 0; h < HALVES; ++h)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_ss((uint32_t)(128 * x), qd + (uint64_t)((x * S::kTile + h * CK * 128 + 32 * k) >> 4),
+          mma_ss((uint32_t)(128 * x), qd + (uint64_t)((x * S::kQTile + h * 128 * 128 + 32 * k) >> 4),
                  kd + (uint64_t)((st * S::kTile + h * CK * 128 + 32 * k) >> 4), ids, (h || k) ? 1u : 0u);
     };
     auto value = [&](int x, int st, int j) {  // O_x += P_x V
       const uint64_t vd = vd0 + (uint64_t)((st * S::kTile) >> 4);
 #pragma unroll
       for (int k = 0; k < CK / 16; ++k)
-        mma_ts(kO + (uint32_t)(D * x), (uint32_t)(128 * x + k / 4 * 64 + k % 4 * 8), vd + (uint64_t)((2048 * k) >> 4), idp,
+        mma_ts(kO + (uint32_t)(D * x), (uint32_t)(128 * x + k / (CK / 32) * (CK / 2) + k % (CK / 32) * 8), vd + (uint64_t)((2048 * k) >> 4), idp,
                (j || k) ? 1u : 0u);
     };
     bool ok = true;
@@ -609,7 +633,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
     uint32_t qph = 0u, pph[2] = {0u, 0u};    // phases of qfull, pfull
 #pragma unroll 1
     for (long long u = ubeg; u < uend && ok;) {
-      const Piece pc = piece_at(a, nblk, pref, u, uend);
+      const Piece pc = piece_at<D>(a, nblk, pref, u, uend);
       u = pc.next;
       if (pc.j1 == 0) continue;
       const int count = min(pc.j1, pc.t.steps) - pc.j0;
@@ -679,61 +703,64 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
 }
 
 // Adds the pieces of the tiles that more than one CTA shared: block (c, i)
-// those of the tile whose first piece share c ends with, sixteen rows of it,
-// a warp four, whose pieces come through shared memory four at a time.
+// those of the tile whose first piece share c ends with, sixteen rows of it
+// (heads of 256: eight), a warp RW, whose pieces come through shared memory
+// four at a time.
 template <class T, int D>
 __global__ void __launch_bounds__(128) k_kv4_chunk_join(AttnArgs a) {
-  __shared__ __align__(16) float batch[4][16][D];  // [warp][piece, row]
+  constexpr int RW = D == 256 ? 2 : 4;
+  __shared__ __align__(16) float batch[4][4 * RW][D];  // [warp][piece, row]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, first = (int)blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the cuts and the pieces are there
   const int4 cut = a.cuts[first];
   const int head = cut.z >> 9, rows = cut.z & 511, lastc = cut.w;
-  const int r0 = (int)blockIdx.y * 16 + 4 * warp;
+  const int r0 = ((int)blockIdx.y * 4 + warp) * RW;
   if (r0 >= rows) return;
   const float sl = fmaxf(fabsf(a.scale_log2), 1e-30f);
   auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == first ? 1 : 0)) * piece_floats(D); };
-  float top = kNone, den = 0.f;  // of row r0 + lane % 4
-  float acc[4][D / 32];
+  float top = kNone, den = 0.f;  // of row r0 + lane % RW
+  float acc[RW][D / 32];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < RW; ++k)
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) acc[k][i] = 0.f;
 #pragma unroll 1
   for (int c0 = first; c0 <= lastc; c0 += 4) {
     const int pieces = min(4, lastc + 1 - c0);  // (rows past the tile's are the workspace's all the same)
-    for (int i = lane; i < pieces * D; i += 32)
+    for (int i = lane; i < pieces * RW * (D / 4); i += 32)
       cp_async16(&batch[warp][i / (D / 4)][i % (D / 4) * 4],
-                 slot(c0 + i / D) + (size_t)(r0 + i / (D / 4) % 4) * D + i % (D / 4) * 4);
+                 slot(c0 + i / (RW * (D / 4))) + (size_t)(r0 + i / (D / 4) % RW) * D + i % (D / 4) * 4);
     float2 ml{kNone, 0.f};
-    if (lane < 4 * pieces) ml = *reinterpret_cast<const float2*>(slot(c0 + lane / 4) + (size_t)CROWS * D + 2 * (r0 + lane % 4));
+    if (lane < RW * pieces)
+      ml = *reinterpret_cast<const float2*>(slot(c0 + lane / RW) + (size_t)kRows<D> * D + 2 * (r0 + lane % RW));
     float nt = fmaxf(ml.x, top);
 #pragma unroll
-    for (int x = 4; x < 32; x <<= 1) nt = fmaxf(nt, __shfl_xor_sync(0xffffffffu, nt, x));
+    for (int x = RW; x < 32; x <<= 1) nt = fmaxf(nt, __shfl_xor_sync(0xffffffffu, nt, x));
     const float f = ex2(sl * (ml.x - nt)), fo = ex2(sl * (top - nt));
     float l = ml.y * f;
 #pragma unroll
-    for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    for (int x = RW; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     top = nt;
     den = fmaf(den, fo, l);
     cp_async_wait_all();
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < RW; ++k) {
       const float fk = __shfl_sync(0xffffffffu, fo, k);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) acc[k][i] *= fk;
     }
     for (int c = 0; c < pieces; ++c)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, 4 * c + k);
+      for (int k = 0; k < RW; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, RW * c + k);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[k][i] = fmaf(batch[warp][4 * c + k][lane + 32 * i], fk, acc[k][i]);
+        for (int i = 0; i < D / 32; ++i) acc[k][i] = fmaf(batch[warp][RW * c + k][lane + 32 * i], fk, acc[k][i]);
       }
     __syncwarp();  // the batch is read
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < RW; ++k) {
     const float dk = __shfl_sync(0xffffffffu, den, k);
     if (r0 + k >= rows) continue;
     const float inv = dk != 0.f ? 1.f / dk : 0.f;  // a row that sees nothing: zeros
@@ -752,7 +779,7 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
     GQ_CUDA(cudaFuncSetAttribute(k_kv4_chunk<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<D>::bytes));
     return GPTQ_OK;
   }));
-  const int nblk = (int)(((long long)a.max_q * a.group + CROWS - 1) / CROWS);
+  const int nblk = (int)(((long long)a.max_q * a.group + kRows<D> - 1) / kRows<D>);
   const int per = CLIST / nblk;  // sequences of a launch
   for (int b0 = 0; b0 < a.seqs; b0 += per) {
     AttnArgs p = a;
@@ -767,7 +794,7 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
       GQ_LAUNCHED();
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, CROWS / 16);
+    cfg.gridDim = dim3((unsigned)grid, 16);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -788,6 +815,8 @@ size_t kv4_chunk_ws_bytes(int dim) { return kCutBytes + (size_t)num_sms() * 2 * 
 gptq_status kv4_chunk_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s) {
   if (dim == 64)
     return dtype == GPTQ_BF16 ? chunk_launch<__nv_bfloat16, 64>(a, s) : chunk_launch<__half, 64>(a, s);
+  if (dim == 256)
+    return dtype == GPTQ_BF16 ? chunk_launch<__nv_bfloat16, 256>(a, s) : chunk_launch<__half, 256>(a, s);
   return dtype == GPTQ_BF16 ? chunk_launch<__nv_bfloat16, 128>(a, s) : chunk_launch<__half, 128>(a, s);
 }
 
