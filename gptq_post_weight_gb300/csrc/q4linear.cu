@@ -1139,13 +1139,14 @@ gptq_status few_launch(const LinearArgs& a, cudaStream_t s) {
   // once (6000 x 4096, one token: 94 clusters of eight 12.2 us, of four 8.9).
   int split = 0, boxes = 0;
   long long least = -1;
+  const long long sms = num_sms(), clusters = (long long)rb * tz;
   for (int k = 8; k >= 1; --k) {
     const int bx = (nbox + k - 1) / k, sp = (nbox + bx - 1) / bx;
     const size_t smem = few_smem<TT, FW>(bx);
     if (smem > kFewSmem) break;
     int slots = kFewSlots;
     while (slots > 1 && smem > few_slot_smem(slots)) --slots;
-    const long long clusters = (long long)rb * tz, sms = num_sms(), room = active[sp][slots];
+    const long long room = active[sp][slots];
     if (room < 1) continue;
     const long long at_once = std::min((long long)slots, (clusters * sp + sms - 1) / sms) * FW / 4;
     const long long cost = ((clusters + room - 1) / room) * (bx * std::max(2ll, at_once) + 20);
