@@ -265,7 +265,11 @@ __device__ __forceinline__ Piece piece_at(const AttnArgs& a, int nblk, const lon
 constexpr int rows_of(int dim) { return dim == 256 ? kRows<256> : kRows<128>; }
 constexpr size_t piece_floats(int dim) { return (size_t)rows_of(dim) * (dim + 2); }
 
-template <class T, int D>
+// TURNS: no sequence has more than 128 rows; the two tiles hold the same rows
+// and take turns at the steps, so that two chains run for them too, and join
+// at the end of a piece (112 rows of 128, 8 sequences to 32000: 168 -> 144 us;
+// of 64, 48 sequences: 674 -> 525; decoding is then the longer part).
+template <class T, int D, bool TURNS>
 __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk, WaitCfg wc) {
   using T2 = typename Elem<T>::T2;
   using S = ChunkSmem<D>;
@@ -274,16 +278,17 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], rawfull[4], rawempty[4], sfull[2],
-      pfull[2];
+      pfull[2], mfull;
   __shared__ uint32_t tmem_base_sh;
   __shared__ long long pref[CLIST + 1], scratch[CTHREADS / 32];
   __shared__ int abort_sh;
+  __shared__ float2 other[128];  // maximum and sum of tile B's half of the steps
   __shared__ float xmax[2][2][2][128];  // [turn][tile][half][row]: what a row's halves tell each other
   volatile int* abort = &abort_sh;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    mbar_init(&qfull, 512);
+    mbar_init(&qfull, 512), mbar_init(&mfull, 128);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], 128), mbar_init(&kempty[i], 1);
       mbar_init(&vfull[i], 128), mbar_init(&vempty[i], 1);
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
     // (Not 0: a hidden key is a score of -inf, and -inf times 0 is no number.)
     const float sl = fmaxf(fabsf(a.scale_log2), 1e-30f);
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale: -q
-    uint32_t sph = 0u, qph = 0u;  // phases of sfull[x], qfull
+    uint32_t sph = 0u, qph = 0u, mph = 0u;  // phases of sfull[x], qfull, mfull
     uint32_t par = 0u;            // of the exchange buffer
     bool ok = true;
 #pragma unroll 1
@@ -329,20 +334,20 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       // What the steps need of the piece; the rest is looked up again for the
       // output, to leave the registers to the scores.
       int last, j, j1;
-      bool active;
       {
         const Piece pc = piece_at<D>(a, nblk, pref, u, uend);
         if (pc.j1 == 0) {  // no steps of the tile in this share
           u = pc.next;
           continue;
         }
-        const bool mine = 128 * x + rt < pc.t.rows;
-        const int rr = pc.t.r0 + min(128 * x + rt, pc.t.rows - 1);
+        const int row = (TURNS ? 0 : 128 * x) + rt;
+        const bool mine = row < pc.t.rows;
+        const int rr = pc.t.r0 + min(row, pc.t.rows - 1);
         const int qi = rr / a.group, hq = pc.head * a.group + rr % a.group;
         last = mine ? pc.t.len - pc.t.nq + qi - CK / 2 * half : -1 - CK / 2 * half;  // among this thread's columns
-        j = pc.j0;
+        j = pc.j0 + (TURNS ? x : 0);
         j1 = min(pc.j1, pc.t.steps);  // (a tile that sees nothing: no steps)
-        active = x == 0 || pc.t.rows > 128;
+        if (!TURNS && 128 * x >= pc.t.rows && x > 0) j = j1;  // nothing for tile B
         // Half of the row's q, in the nibbles' order of channels.
         const T* qp = static_cast<const T*>(a.q) + (long long)(pc.t.q0 + qi) * a.q_ts + (long long)hq * a.q_hs +
                       D / 2 * half;
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       float m = kNone, l = 0.f;
       bool began = false;
 #pragma unroll 1
-      for (; active && j < j1; ++j) {
+      for (; j < j1; j += TURNS ? 2 : 1) {
         ok = wait_bar_warp(&sfull[x], sph, abort, wc.ns);
         sph ^= 1u;
         const int lim = last - j * CK;  // last visible column of this half
@@ -451,15 +456,34 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       if (!(ok = tile_all(x, ok))) break;
       l += xmax[par][x][half ^ 1][rt];
       par ^= 1u;
-      tc_fence_after();
+      float fa = 1.f, fb = 0.f;  // weights of the tiles' outputs
       const Piece pc = piece_at<D>(a, nblk, pref, u, uend);
       u = pc.next;
+      if (TURNS) {
+        if (x == 1) {
+          if (half == 0) {
+            other[rt] = float2{m, l};
+            tc_fence_before();
+            mbar_arrive(&mfull);
+          }
+          continue;  // (the next piece's q waits for tile A's threads)
+        }
+        ok = tile_all(x, wait_bar_warp(&mfull, mph, abort, wc.ns));
+        if (!ok) break;
+        mph ^= 1u;
+        const float2 ml = other[rt];
+        const float nm = fmaxf(m, ml.x);
+        fa = ex2(sl * (m - nm)), fb = ex2(sl * (ml.x - nm));
+        l = l * fa + ml.y * fb;
+        m = nm;
+      }
+      tc_fence_after();
       if (threadIdx.x == 0 && pc.j0 == 0 && !pc.whole) {  // a cut tile's first piece: the join's work
         const long long w = pref[a.seqs * nblk] * a.heads, n = min(w, (long long)gridDim.x);
         const int lastc = (int)(((u + units_of(pc.t) - CSTART - pc.j1) * n - 1) / w);  // its last unit's share
         a.cuts[blockIdx.x] = int4{pc.t.q0, pc.t.r0, pc.head << 9 | pc.t.rows, lastc};
       }
-      if (!active) continue;
+      if (x > 0 && pc.t.rows <= 128) continue;
       const bool mine = 128 * x + rt < pc.t.rows;
       const int rr = pc.t.r0 + min(128 * x + rt, pc.t.rows - 1);
       const int qi = rr / a.group, hq = pc.head * a.group + rr % a.group;
@@ -472,6 +496,14 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
         if (began) {
           tmem_ld16(to + (uint32_t)c, v);
           tmem_ld_wait();
+        }
+        if (TURNS && min(pc.j1, pc.t.steps) - pc.j0 > 1) {  // tile B had a step: so had this one
+          uint32_t w[16];
+          tmem_ld16(to + (uint32_t)(D + c), w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            v[i] = __float_as_uint(__uint_as_float(v[i]) * fa + __uint_as_float(w[i]) * fb);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -643,6 +675,43 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       if (count <= 0) continue;
       if (!(ok = wait_bar_warp(&kfull[n & 1], (uint32_t)(n >> 1) & 1u, abort, wc.ns))) break;
       tc_fence_after();
+      if (TURNS) {
+        // Steps in turn: the next but one's scores behind a step's output.
+        auto begin = [&](int x, int st) {
+          score(x, st);
+          mma_commit(&sfull[x]);
+          mma_commit(&kempty[st]);
+        };
+        if (one) begin(0, n & 1);
+        __syncwarp();
+        if (count > 1) {
+          if (!(ok = wait_bar_warp(&kfull[(n + 1) & 1], (uint32_t)((n + 1) >> 1) & 1u, abort, wc.ns))) break;
+          tc_fence_after();
+          if (one) begin(1, (n + 1) & 1);
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int j = 0; j < count; ++j, ++n) {
+          const int x = j & 1, st = n & 1;
+          if (!(ok = wait_bar_warp(&vfull[st], (uint32_t)(n >> 1) & 1u, abort, wc.ns))) break;
+          if (!(ok = wait_bar_warp(&pfull[x], pph[x], abort, wc.ns))) break;
+          pph[x] ^= 1u;
+          tc_fence_after();
+          if (one) {
+            value(x, st, j > 1);
+            mma_commit(&vempty[st]);
+            if (j + 2 >= count) mma_commit(&sfull[x]);
+          }
+          __syncwarp();
+          if (j + 2 < count) {
+            if (!(ok = wait_bar_warp(&kfull[st], (uint32_t)((n + 2) >> 1) & 1u, abort, wc.ns))) break;
+            tc_fence_after();
+            if (one) begin(x, st);
+            __syncwarp();
+          }
+        }
+        continue;
+      }
       if (one) {
         score(0, n & 1);
         mma_commit(&sfull[0]);
@@ -772,11 +841,11 @@ __global__ void __launch_bounds__(128) k_kv4_chunk_join(AttnArgs a) {
   }
 }
 
-template <class T, int D>
+template <class T, int D, bool TURNS>
 gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
   static DeviceOnce attr;
   GQ_TRY(attr.run([](int) -> gptq_status {
-    GQ_CUDA(cudaFuncSetAttribute(k_kv4_chunk<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<D>::bytes));
+    GQ_CUDA(cudaFuncSetAttribute(k_kv4_chunk<T, D, TURNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<D>::bytes));
     return GPTQ_OK;
   }));
   const int nblk = (int)(((long long)a.max_q * a.group + kRows<D> - 1) / kRows<D>);
@@ -790,7 +859,7 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
     const int grid = num_sms();
     {
       GQ_PROF(K_KV4_CHUNK, s);
-      k_kv4_chunk<T, D><<<grid, CTHREADS, ChunkSmem<D>::bytes, s>>>(p, nblk, wait_cfg());
+      k_kv4_chunk<T, D, TURNS><<<grid, CTHREADS, ChunkSmem<D>::bytes, s>>>(p, nblk, wait_cfg());
       GQ_LAUNCHED();
     }
     cudaLaunchConfig_t cfg{};
@@ -812,12 +881,16 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
 
 size_t kv4_chunk_ws_bytes(int dim) { return kCutBytes + (size_t)num_sms() * 2 * piece_floats(dim) * 4; }
 
+template <class T>
+static gptq_status chunk_dim(int dim, const AttnArgs& a, cudaStream_t s) {
+  const bool turns = (long long)a.max_q * a.group <= 128;
+  if (dim == 64) return turns ? chunk_launch<T, 64, true>(a, s) : chunk_launch<T, 64, false>(a, s);
+  if (dim == 128) return turns ? chunk_launch<T, 128, true>(a, s) : chunk_launch<T, 128, false>(a, s);
+  return chunk_launch<T, 256, false>(a, s);
+}
+
 gptq_status kv4_chunk_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s) {
-  if (dim == 64)
-    return dtype == GPTQ_BF16 ? chunk_launch<__nv_bfloat16, 64>(a, s) : chunk_launch<__half, 64>(a, s);
-  if (dim == 256)
-    return dtype == GPTQ_BF16 ? chunk_launch<__nv_bfloat16, 256>(a, s) : chunk_launch<__half, 256>(a, s);
-  return dtype == GPTQ_BF16 ? chunk_launch<__nv_bfloat16, 128>(a, s) : chunk_launch<__half, 128>(a, s);
+  return dtype == GPTQ_BF16 ? chunk_dim<__nv_bfloat16>(dim, a, s) : chunk_dim<__half>(dim, a, s);
 }
 
 }  // namespace gq

@@ -260,6 +260,7 @@ def test_long_contexts(lib):
     (4, [5, 5], [3000, 2000]),   # 20 rows
     (4, [7, 8], [3000, 2000]),   # 32 rows
     (4, [9, 2], [3000, 2000]),   # 36 rows
+    (4, [20], [12000]),          # 80 rows, the tiles take turns
     (4, [40], [12000]),          # one tile shared by every CTA
 ])
 def test_cut_items(lib, group, q_lens, lens, dim, dtype):
