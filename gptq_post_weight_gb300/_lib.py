@@ -614,6 +614,18 @@ def _raw_stream(sv, stream, index):
     return raw(index) if raw is not None else sv["torch"].cuda.current_stream(index).cuda_stream
 
 
+def _empty(sv, stream):
+    """torch.empty for what a call on the given `stream` writes: memory of that
+    stream, so that neither an earlier use of it nor its next one overlaps the
+    call."""
+
+    def empty(*size, **kw):
+        with sv["torch"].cuda.stream(stream):
+            return sv["empty"](*size, **kw)
+
+    return empty
+
+
 def _serve_word(index):
     w = _serve_words.get(index)
     if w is None:
@@ -761,7 +773,7 @@ def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, ou
         _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out)
         ldx = max(n, -(-n // 8) * 8)  # a dense x without elements, or of one row
     if out is None:
-        out = sv["empty"]((tokens, rows), dtype=xt, device=x.device)
+        out = (sv["empty"] if stream is None else _empty(sv, stream))((tokens, rows), dtype=xt, device=x.device)
     code = _lib.gptq_q4tp_linear(dt, x.data_ptr(), ldx, tokens, nibbles.data_ptr(), rungs.data_ptr(), tab.data_ptr(),
                                  rows, n, bp, code, rp, ldr, out.data_ptr(), ldy,
                                  (_serve_words.get(dev) or (0, _serve_word(dev)))[1], _raw_stream(sv, stream, dev))
@@ -869,8 +881,9 @@ def kv4_read(cache, slots, dim, page_size, dtype, stream=None):
         fine = False
     if not fine:
         _refuse_read(cache, slots, dim, page_size, dtype)
-    k = sv["empty"]((tokens, heads, dim), dtype=dtype, device=cache.device)
-    v = sv["empty"]((tokens, heads, dim), dtype=dtype, device=cache.device)
+    empty = sv["empty"] if stream is None else _empty(sv, stream)
+    k = empty((tokens, heads, dim), dtype=dtype, device=cache.device)
+    v = empty((tokens, heads, dim), dtype=dtype, device=cache.device)
     code = _lib.gptq_kv4_read(dt, cache.data_ptr(), pages, heads, dim, page_size, slots.data_ptr(), tokens,
                               k.data_ptr(), v.data_ptr(), _raw_stream(sv, stream, dev))
     if code:
@@ -950,7 +963,7 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
         _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, out, ws)
         qts, qhs = qts if tq > 1 else 0, qhs if hq > 1 else 0
     if out is None:
-        out = sv["empty"]((tq, hq, dim), dtype=qt, device=q.device)
+        out = (sv["empty"] if stream is None else _empty(sv, stream))((tq, hq, dim), dtype=qt, device=q.device)
     wp = wn = 0
     if ws is None:
         shape = (dim, heads, hq, max_q, seqs, sp is None, per * page_size)
@@ -960,7 +973,7 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
             if len(_attention_ws) < 4096:
                 _attention_ws[shape] = wn
         if wn:
-            ws = sv["empty"](wn, dtype=sv["u8"], device=q.device)
+            ws = (sv["empty"] if stream is None else _empty(sv, stream))(wn, dtype=sv["u8"], device=q.device)
     if ws is not None:
         wp, wn = ws.data_ptr(), ws.numel()
     code = _lib.gptq_kv4_attention(dt, q.data_ptr(), qts, qhs, tq, cache.data_ptr(), pages, heads, hq // heads, dim,

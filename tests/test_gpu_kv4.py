@@ -376,3 +376,37 @@ def test_nothing_to_do(lib):
     o = _lib.kv4_attention(e, cache, torch.empty(0, 1, dtype=torch.int32, device="cuda"),
                            torch.empty(0, dtype=torch.int32, device="cuda"), 16)
     assert o.shape == (0, 2, 64)
+
+
+def test_buffers_belong_to_the_call_s_stream(lib):
+    # What a call on a given stream allocates is that stream's memory: given
+    # back, it goes to that stream's next allocation, never to one of the
+    # current stream's, which would not wait for the call.
+    from gptq_post_weight_gb300 import _lib
+
+    r = np.random.default_rng(17)
+    cache, table, lens, ks, vs = context(r, [9000, 40], 2, 128, 16, "bf16")
+    q = dev(serve.round_to(r.standard_normal((2, 8, 128)), "bf16"), torch.bfloat16)
+    slots = torch.arange(3, device="cuda")
+    x = torch.ones(3, 64, dtype=torch.bfloat16, device="cuda")
+    nib, rungs = torch.zeros(64 * 32, dtype=torch.uint8, device="cuda"), torch.zeros(64 * 2, dtype=torch.uint8, device="cuda")
+    tab = torch.ones(64, 32, device="cuda")
+    side = torch.cuda.Stream()
+    calls = [lambda: _lib.kv4_attention(q, cache, table, lens, 16, stream=side),
+             lambda: _lib.kv4_read(cache, slots, 128, 16, torch.bfloat16, stream=side)[1],
+             lambda: _lib.q4tp_linear(x, nib, rungs, tab, stream=side)]
+    torch.cuda.synchronize()
+    for call in calls:
+        y = call()
+        at, shape = y.data_ptr(), y.shape
+        del y
+        mine = [torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+        assert at not in [t.data_ptr() for t in mine]
+        with torch.cuda.stream(side):
+            theirs = [torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+        assert at in [t.data_ptr() for t in theirs]
+        side.synchronize()
+    # The workspace of cut items, too: the same bits as on the current stream.
+    a, b = _lib.kv4_attention(q, cache, table, lens, 16), calls[0]()
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
