@@ -588,7 +588,9 @@ def debias(bits, w, h_packed, codes, rungs, tab, lost, scales, ws=None, want_num
 #
 # These calls are short, so the host's part of them counts: each wrapper first
 # looks at its arguments in one expression of cheap attributes, and only where
-# that does not hold goes through the checks that name the argument.
+# that does not hold goes through the checks that name the argument.  What the
+# library gets of an argument is taken whether or not the expression holds,
+# since the long checks let through some calls that it does not know.
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _serve = {}  # torch, its dtypes and the raw-stream call, once the first wrapper ran
@@ -712,6 +714,8 @@ def _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out):
         raise ValueError(f"x must have a multiple of 32 columns, got {n}")
     dev = x.device
     _strided(x, "x", x.shape, x)
+    if tokens > 1 and x.stride(0) < n:
+        raise ValueError(f"x must have rows that do not overlap, got strides {x.stride()}")
     _need(tab, "tab", device=dev)
     if tab.dim() != 2 or tab.shape[1] != 32:
         raise ValueError(f"tab must be [rows, 32], got shape {tuple(tab.shape)}")
@@ -732,8 +736,8 @@ def _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out):
 def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, out=None, stream=None):
     """act(x W^T + bias) + residual with W [rows, n] in q4tp form (nibbles,
     rungs, tab as quantize_group returns them).  x [tokens, n] bf16 or f16
-    (rows may be strided), bias [rows], residual [tokens, rows] and the result
-    [tokens, rows] of x's dtype.  act: a key of ACTIVATIONS."""
+    (rows may be strided, not overlap), bias [rows], residual [tokens, rows] and
+    the result [tokens, rows] of x's dtype.  act: a key of ACTIVATIONS."""
     sv = _serve or _serving()
     try:
         xt, xs, u8 = x.dtype, x.shape, sv["u8"]
@@ -752,26 +756,26 @@ def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, ou
                 and rungs.get_device() == dev)
         bp = rp = None
         ldr = 0
-        if fine and bias is not None:
-            fine = bias.dtype is xt and bias.numel() == rows and bias.is_contiguous() and bias.get_device() == dev
+        if bias is not None:
+            fine = (fine and bias.dtype is xt and bias.numel() == rows and bias.is_contiguous()
+                    and bias.get_device() == dev)
             bp = bias.data_ptr()
-        if fine and residual is not None:
+        if residual is not None:
             st = residual.stride()
             ldr = st[0] if tokens > 1 else rows
-            fine = (residual.dtype is xt and residual.shape == (tokens, rows) and (rows == 1 or st[1] == 1)
+            fine = (fine and residual.dtype is xt and residual.shape == (tokens, rows) and (rows == 1 or st[1] == 1)
                     and ldr >= rows and residual.get_device() == dev)
             rp = residual.data_ptr()
         ldy = rows
-        if fine and out is not None:
+        if out is not None:
             st = out.stride()
             ldy = st[0] if tokens > 1 else rows
-            fine = (out.dtype is xt and out.shape == (tokens, rows) and (rows == 1 or st[1] == 1) and ldy >= rows
-                    and out.get_device() == dev)
+            fine = (fine and out.dtype is xt and out.shape == (tokens, rows) and (rows == 1 or st[1] == 1)
+                    and ldy >= rows and out.get_device() == dev)
     except (AttributeError, KeyError, TypeError, ValueError, IndexError):
         fine = False
     if not fine:
         _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out)
-        ldx = max(n, -(-n // 8) * 8)  # a dense x without elements, or of one row
     if out is None:
         out = (sv["empty"] if stream is None else _empty(sv, stream))((tokens, rows), dtype=xt, device=x.device)
     code = _lib.gptq_q4tp_linear(dt, x.data_ptr(), ldx, tokens, nibbles.data_ptr(), rungs.data_ptr(), tab.data_ptr(),

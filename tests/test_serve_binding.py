@@ -1,0 +1,94 @@
+"""What the serving wrappers hand to the library (CPU only).
+
+The library is replaced by a recorder, and the tensors say that they live on
+a GPU, so that a call goes through its checks and to its end without one."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class Gpu(torch.Tensor):
+    """A host tensor whose checks see one of device `index`."""
+
+    index = 0
+    is_cuda = True
+
+    def get_device(self):
+        return self.index
+
+
+def gpu(t):
+    return t.as_subclass(Gpu)
+
+
+class Stream:
+    cuda_stream = 0x51
+
+
+class Recorder:
+    """Stands for the library: notes the last call's arguments."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+
+        return call
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    from gptq_post_weight_gb300 import _lib
+
+    r = Recorder()
+    monkeypatch.setattr(_lib, "_lib", r)
+    monkeypatch.setattr(_lib, "_attention_ws", {})
+    monkeypatch.setitem(_lib._serve_words, 0, (None, 0x77))
+    _lib._serving()
+    return r
+
+
+def weights(rows, n):
+    return (gpu(torch.zeros(rows * n // 2, dtype=torch.uint8)), gpu(torch.zeros(rows * n // 32, dtype=torch.uint8)),
+            gpu(torch.zeros(rows, 32)))
+
+
+def b16(*shape):
+    return gpu(torch.zeros(*shape, dtype=torch.bfloat16))
+
+
+# q4tp_linear's arguments at the library
+X, LDX, TOKENS, BIAS, RESIDUAL, LDR, Y, LDY = 1, 2, 3, 9, 11, 12, 13, 14
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_linear_refuses_rows_of_x_that_overlap(rec, bias):
+    from gptq_post_weight_gb300 import _lib
+
+    t, rows, n = 4, 6, 64
+    b = b16(rows) if bias else None
+    out = b16(t, rows + 2)[:, :rows]
+    flat = b16(n + 8 * (t - 1))
+    for x in (b16(1, n).expand(t, n), torch.as_strided(flat, (t, n), (8, 1))):
+        with pytest.raises(ValueError, match="x must have rows that do not overlap"):
+            _lib.q4tp_linear(x, *weights(rows, n), bias=b, out=out, stream=Stream)
+    assert not rec.calls
+
+
+def test_linear_hands_on_every_argument(rec):
+    from gptq_post_weight_gb300 import _lib
+
+    t, rows, n = 4, 6, 64
+    x, b, r, out = b16(t, n + 8)[:, :n], b16(rows), b16(t, rows + 3)[:, :rows], b16(t, rows + 2)[:, :rows]
+    _lib.q4tp_linear(x, *weights(rows, n), bias=b, act="silu", residual=r, out=out, stream=Stream)
+    # No rows, in strides that the quick look at the arguments does not know.
+    none = torch.as_strided(b16(2 * n), (0, n), (n, 2))
+    _lib.q4tp_linear(none, *weights(rows, n), bias=b, residual=r[:0], out=out[:0], stream=Stream)
+    (name, a), (_, e) = rec.calls
+    assert name == "gptq_q4tp_linear"
+    assert (a[X], a[LDX], a[TOKENS]) == (x.data_ptr(), n + 8, t)
+    assert (a[BIAS], a[RESIDUAL], a[LDR], a[Y], a[LDY]) == (b.data_ptr(), r.data_ptr(), rows + 3, out.data_ptr(), rows + 2)
+    assert e[TOKENS] == 0 and e[BIAS] == b.data_ptr() and e[RESIDUAL] is not None and e[LDY] >= rows
