@@ -952,8 +952,8 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
         sp = None
         if q_starts is None:
             fine = fine and tq == seqs and max_q == 1
-        elif fine:
-            fine = (q_starts.dtype is i32 and q_starts.numel() == seqs + 1 and q_starts.is_contiguous()
+        else:
+            fine = (fine and q_starts.dtype is i32 and q_starts.numel() == seqs + 1 and q_starts.is_contiguous()
                     and q_starts.get_device() == dev)
             sp = q_starts.data_ptr()
         if fine and out is not None:

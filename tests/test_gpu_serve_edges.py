@@ -1,0 +1,43 @@
+"""Uses of the serving operators beside the sizes of test_gpu_linear.py and
+test_gpu_kv4.py, whose tolerances these tests use."""
+import numpy as np
+import pytest
+
+from oracle import serve
+import test_gpu_kv4 as kv
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,lens", [([3, 0, 1], [70, 5, 1]), ([1, 1, 2], [17, 0, 300]), ([40, 2, 9], [50, 33, 4]),
+                                         ([300, 1, 140], [700, 64, 140])])
+def test_one_query_head_with_several_queries(lib, q_lens, lens, dim, dtype):
+    kv.one(lens, 1, 1, dim, 16, dtype, q_lens, seed=20)
+
+
+@pytest.mark.parametrize("seqs", [0, 2])
+def test_no_queries_with_starts(lib, seqs):
+    from gptq_post_weight_gb300 import _lib
+
+    cache = _lib.kv4_cache(2, 2, 64, 16)
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    o = _lib.kv4_attention(q, cache, torch.zeros(seqs, 1, **i32), torch.ones(seqs, **i32), 16,
+                           q_starts=torch.zeros(seqs + 1, **i32), max_q=3)
+    assert o.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("heads,group", [(1, 1), (2, 4)])
+def test_one_token_of_any_token_stride(lib, heads, group):
+    r = np.random.default_rng(21)
+    cache, table, lens, ks, vs = kv.context(r, [40], heads, 64, 16, "bf16")
+    q = serve.round_to(r.standard_normal((1, heads * group, 64)), "bf16")
+    plain = kv.attend(q, cache, table, lens, 16, "bf16")
+    wide = torch.zeros(heads * group * 64 + 3, dtype=torch.bfloat16, device="cuda")
+    wide[:-3] = kv.dev(q, torch.bfloat16).flatten()
+    odd = torch.as_strided(wide, (1, heads * group, 64), (heads * group * 64 + 3, 64, 1))
+    assert torch.equal(plain, kv.attend(odd, cache, table, lens, 16, "bf16"))
+    assert torch.equal(plain, kv.attend(odd, cache, table, lens, 16, "bf16", [1]))

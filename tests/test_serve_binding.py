@@ -92,3 +92,27 @@ def test_linear_hands_on_every_argument(rec):
     assert (a[X], a[LDX], a[TOKENS]) == (x.data_ptr(), n + 8, t)
     assert (a[BIAS], a[RESIDUAL], a[LDR], a[Y], a[LDY]) == (b.data_ptr(), r.data_ptr(), rows + 3, out.data_ptr(), rows + 2)
     assert e[TOKENS] == 0 and e[BIAS] == b.data_ptr() and e[RESIDUAL] is not None and e[LDY] >= rows
+
+
+# kv4_attention's arguments at the library, and those of its workspace's size
+Q_TS, TQ, Q_STARTS, SEQS, MAX_Q, SINGLE = 2, 4, 14, 15, 16, 5
+
+
+@pytest.mark.parametrize("tq,heads,group,ts", [(9, 1, 1, 64), (0, 2, 2, 256), (0, 1, 1, 64), (1, 2, 2, 259),
+                                               (1, 1, 1, 67), (9, 2, 2, 256)])
+def test_attention_hands_on_q_starts(rec, tq, heads, group, ts):
+    # One query head, no rows, a token stride that one token does not use.
+    from gptq_post_weight_gb300 import _lib
+
+    dim, page = 64, 16
+    hq = heads * group
+    q = torch.as_strided(b16(max(1, tq) * ts + hq * dim), (tq, hq, dim), (ts, dim, 1))
+    cache = gpu(torch.zeros(4, heads, page * dim * 5 // 4, dtype=torch.uint8))
+    table, lens = gpu(torch.zeros(2, 3, dtype=torch.int32)), gpu(torch.ones(2, dtype=torch.int32))
+    starts = gpu(torch.tensor([0, 0, tq], dtype=torch.int32))
+    _lib.kv4_attention(q, cache, table, lens, page, q_starts=starts, max_q=9, out=b16(tq, hq, dim), stream=Stream)
+    (size, s), (name, a) = rec.calls
+    assert (size, name) == ("gptq_kv4_attention_call_bytes", "gptq_kv4_attention")
+    assert not s[SINGLE]
+    assert (a[TQ], a[Q_STARTS], a[SEQS], a[MAX_Q]) == (tq, starts.data_ptr(), 2, 9)
+    assert a[Q_TS] % 8 == 0 and (tq <= 1 or a[Q_TS] == ts)
