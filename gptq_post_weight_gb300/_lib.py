@@ -595,7 +595,7 @@ def debias(bits, w, h_packed, codes, rungs, tab, lost, scales, ws=None, want_num
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _serve = {}  # torch, its dtypes and the raw-stream call, once the first wrapper ran
 _serve_words = {}  # device index -> the status word its serving calls set (tensor, address)
-_attention_ws = {}  # shape of a kv4_attention call -> its workspace bytes
+_attention_ws = {}  # device index and shape of a kv4_attention call -> its workspace bytes
 
 
 def _serving():
@@ -603,7 +603,8 @@ def _serving():
 
     _serve.update(torch=torch, empty=torch.empty, f32=torch.float32, u8=torch.uint8, i32=torch.int32, i64=torch.int64,
                   dtypes={torch.bfloat16: 0, torch.float16: 1},
-                  raw=getattr(torch._C, "_cuda_getCurrentRawStream", None))
+                  raw=getattr(torch._C, "_cuda_getCurrentRawStream", None),
+                  current=getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
     load()
     return _serve
 
@@ -611,6 +612,9 @@ def _serving():
 def _raw_stream(sv, stream, index):
     """The call's stream as an integer: the given one, or the device's current one."""
     if stream is not None:
+        at = getattr(stream, "device", None)
+        if at is not None and at.index != index:
+            raise ValueError(f"the stream is on {at}, the call's data on cuda:{index}")
         return stream.cuda_stream
     raw = sv["raw"]
     return raw(index) if raw is not None else sv["torch"].cuda.current_stream(index).cuda_stream
@@ -653,6 +657,16 @@ def serve_check(device=None):
         if int(w[0][0]) != 0:
             w[0].zero_()
             raise GptqError("serving call", 6)
+
+
+def _here(t, name):
+    """Raise ValueError unless ``t`` is on the current device.  The library
+    launches there, and the default stream has one handle on every device, so
+    nothing else would notice."""
+    _ptr(t)
+    at, current = t.get_device(), _serve["current"]()
+    if at != current:
+        raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{current}")
 
 
 def _dtype16(t, name):
@@ -730,7 +744,7 @@ def _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out):
         _rows_of(residual, "residual", tokens, rows, x)
     if out is not None:
         _rows_of(out, "out", tokens, rows, x)
-    _ptr(x)
+    _here(x, "x")
 
 
 def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, out=None, stream=None):
@@ -747,7 +761,8 @@ def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, ou
         code = ACTIVATIONS[act]
         st = x.stride()
         ldx = st[0] if tokens > 1 else n
-        fine = (dev >= 0 and n > 0 and n % 32 == 0 and st[1] == 1 and ldx % 8 == 0 and ldx >= n
+        fine = (dev >= 0 and dev == sv["current"]() and n > 0 and n % 32 == 0 and st[1] == 1 and ldx % 8 == 0
+                and ldx >= n
                 and tab.dtype is sv["f32"] and tab.shape == (rows, 32) and tab.is_contiguous()
                 and tab.get_device() == dev
                 and nibbles.dtype is u8 and nibbles.numel() == rows * n // 2 and nibbles.is_contiguous()
@@ -825,7 +840,7 @@ def _refuse_write(cache, k, v, slots, page_size):
     _strided(k, "k", k.shape, k)
     _strided(v, "v", k.shape, k)
     _need(slots, "slots", dtype=torch.int64, numel=tokens, device=k.device)
-    _ptr(k)
+    _here(k, "k")
 
 
 def kv4_write(cache, k, v, slots, page_size, stream=None):
@@ -840,7 +855,8 @@ def kv4_write(cache, k, v, slots, page_size, stream=None):
         pages = cache.shape[0]
         kts, khs, k1 = k.stride()
         vts, vhs, v1 = v.stride()
-        fine = (dev >= 0 and dim in (64, 128, 256) and tokens > 1 and heads > 1 and v.dtype is kt and v.shape == shape
+        fine = (dev >= 0 and dev == sv["current"]() and dim in (64, 128, 256) and tokens > 1 and heads > 1
+                and v.dtype is kt and v.shape == shape
                 and k1 == 1 and v1 == 1 and (kts | khs | vts | vhs) % 8 == 0 and v.get_device() == dev
                 and 0 < page_size <= 4096 and page_size % 16 == 0 and cache.dtype is sv["u8"]
                 and cache.shape == (pages, heads, page_size * dim * 5 // 4) and cache.is_contiguous()
@@ -867,7 +883,7 @@ def _refuse_read(cache, slots, dim, page_size, dtype):
     _need(slots, "slots", dtype=torch.int64, device=cache.device)
     if dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
-    _ptr(cache)
+    _here(cache, "cache")
 
 
 def kv4_read(cache, slots, dim, page_size, dtype, stream=None):
@@ -878,7 +894,8 @@ def kv4_read(cache, slots, dim, page_size, dtype, stream=None):
         dt, dev = sv["dtypes"][dtype], cache.get_device()
         pages, heads, size = cache.shape
         tokens = slots.numel()
-        fine = (dev >= 0 and dim in (64, 128, 256) and 0 < page_size <= 4096 and page_size % 16 == 0
+        fine = (dev >= 0 and dev == sv["current"]() and dim in (64, 128, 256) and 0 < page_size <= 4096
+                and page_size % 16 == 0
                 and cache.dtype is sv["u8"] and size == page_size * dim * 5 // 4 and cache.is_contiguous()
                 and slots.dtype is sv["i64"] and slots.is_contiguous() and slots.get_device() == dev)
     except (AttributeError, KeyError, TypeError, ValueError, IndexError):
@@ -924,7 +941,7 @@ def _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, out,
         _need(out, "out", dtype=q.dtype, numel=q.numel(), device=dev)
     if ws is not None:
         _ws(ws, dev)
-    _ptr(q)
+    _here(q, "q")
 
 
 def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, scale=None, out=None, ws=None,
@@ -943,7 +960,8 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
         pages, heads, size = cache.shape
         seqs, per = table.shape
         qts, qhs, q1 = q.stride()
-        fine = (dev >= 0 and dim in (64, 128, 256) and tq > 0 and hq > 1 and hq % heads == 0 and q1 == 1
+        fine = (dev >= 0 and dev == sv["current"]() and dim in (64, 128, 256) and tq > 0 and hq > 1
+                and hq % heads == 0 and q1 == 1
                 and (qts | qhs) % 8 == 0 and 0 < page_size <= 4096 and page_size % 16 == 0 and max_q > 0
                 and cache.dtype is sv["u8"] and size == page_size * dim * 5 // 4 and cache.is_contiguous()
                 and cache.get_device() == dev and table.dtype is i32 and per > 0 and table.is_contiguous()
@@ -970,7 +988,7 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
         out = (sv["empty"] if stream is None else _empty(sv, stream))((tq, hq, dim), dtype=qt, device=q.device)
     wp = wn = 0
     if ws is None:
-        shape = (dim, heads, hq, max_q, seqs, sp is None, per * page_size)
+        shape = (dev, dim, heads, hq, max_q, seqs, sp is None, per * page_size)
         wn = _attention_ws.get(shape)
         if wn is None:
             wn = _lib.gptq_kv4_attention_call_bytes(dim, heads, hq // heads, max_q, seqs, sp is None, per * page_size)

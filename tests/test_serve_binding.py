@@ -48,6 +48,7 @@ def rec(monkeypatch):
     monkeypatch.setattr(_lib, "_attention_ws", {})
     monkeypatch.setitem(_lib._serve_words, 0, (None, 0x77))
     _lib._serving()
+    monkeypatch.setitem(_lib._serve, "current", lambda: 0)
     return r
 
 
@@ -116,3 +117,62 @@ def test_attention_hands_on_q_starts(rec, tq, heads, group, ts):
     assert not s[SINGLE]
     assert (a[TQ], a[Q_STARTS], a[SEQS], a[MAX_Q]) == (tq, starts.data_ptr(), 2, 9)
     assert a[Q_TS] % 8 == 0 and (tq <= 1 or a[Q_TS] == ts)
+
+
+def calls(stream=Stream):
+    """One good call of each wrapper, its buffers given."""
+    from gptq_post_weight_gb300 import _lib
+
+    cache = gpu(torch.zeros(4, 2, 16 * 64 * 5 // 4, dtype=torch.uint8))
+    k, slots = b16(3, 2, 64), gpu(torch.zeros(3, dtype=torch.int64))
+    table, lens = gpu(torch.zeros(3, 1, dtype=torch.int32)), gpu(torch.ones(3, dtype=torch.int32))
+    return {
+        "x": lambda: _lib.q4tp_linear(b16(3, 64), *weights(6, 64), out=b16(3, 6), stream=stream),
+        "k": lambda: _lib.kv4_write(cache, k, k, slots, 16, stream=stream),
+        "cache": lambda: _lib.kv4_read(cache, slots, 64, 16, torch.bfloat16, stream=stream),
+        "q": lambda: _lib.kv4_attention(b16(3, 4, 64), cache, table, lens, 16, out=b16(3, 4, 64), stream=stream),
+    }
+
+
+@pytest.fixture
+def no_streams(monkeypatch):
+    """torch.cuda.stream takes any object (kv4_read allocates under the call's)."""
+    import contextlib
+
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+
+
+@pytest.mark.parametrize("name", ["x", "k", "cache", "q"])
+def test_tensors_of_another_device_than_the_current_one_are_refused(rec, no_streams, monkeypatch, name):
+    # The default stream has the same handle on every device: the launch would
+    # run on the current one with the other one's addresses.
+    from gptq_post_weight_gb300 import _lib
+
+    calls()[name]()
+    assert rec.calls
+    monkeypatch.setitem(_lib._serve, "current", lambda: 1)
+    rec.calls.clear()
+    with pytest.raises(ValueError, match=f"{name} is on cuda:0, the current device is cuda:1"):
+        calls()[name]()
+    assert not rec.calls
+
+
+@pytest.mark.parametrize("name", ["x", "k", "cache", "q"])
+def test_streams_of_another_device_are_refused(rec, no_streams, name):
+    class Other(Stream):
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="the stream is on cuda:1, the call's data on cuda:0"):
+        calls(Other)[name]()
+    assert not [c for c in rec.calls if not c[0].endswith("_bytes")]
+
+
+def test_the_workspace_of_a_shape_is_the_device_s_own(rec, monkeypatch):
+    from gptq_post_weight_gb300 import _lib
+
+    calls()["q"]()
+    monkeypatch.setattr(Gpu, "index", 1)
+    monkeypatch.setitem(_lib._serve, "current", lambda: 1)
+    monkeypatch.setitem(_lib._serve_words, 1, (None, 0x78))
+    calls()["q"]()
+    assert [c[0] for c in rec.calls].count("gptq_kv4_attention_call_bytes") == 2
