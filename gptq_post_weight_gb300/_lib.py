@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgptqfold.so")
@@ -595,17 +596,18 @@ def debias(bits, w, h_packed, codes, rungs, tab, lost, scales, ws=None, want_num
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _serve = {}  # torch, its dtypes and the raw-stream call, once the first wrapper ran
 _serve_words = {}  # device index -> the status word its serving calls set (tensor, address)
+_serve_lock = threading.Lock()
 _attention_ws = {}  # device index and shape of a kv4_attention call -> its workspace bytes
 
 
 def _serving():
     import torch
 
+    load()  # first: another thread's call goes ahead as soon as _serve holds anything
     _serve.update(torch=torch, empty=torch.empty, f32=torch.float32, u8=torch.uint8, i32=torch.int32, i64=torch.int64,
                   dtypes={torch.bfloat16: 0, torch.float16: 1},
                   raw=getattr(torch._C, "_cuda_getCurrentRawStream", None),
                   current=getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
-    load()
     return _serve
 
 
@@ -633,13 +635,14 @@ def _empty(sv, stream):
 
 
 def _serve_word(index):
-    w = _serve_words.get(index)
-    if w is None:
-        import torch
+    with _serve_lock:  # one word a device, whoever is first: calls in flight keep its address
+        w = _serve_words.get(index)
+        if w is None:
+            import torch
 
-        t = torch.zeros(4, dtype=torch.int32, device=torch.device("cuda", index))
-        torch.cuda.current_stream(index).synchronize()  # before a call on any stream may set it
-        w = _serve_words[index] = (t, t.data_ptr())
+            t = torch.zeros(4, dtype=torch.int32, device=torch.device("cuda", index))
+            torch.cuda.current_stream(index).synchronize()  # before a call on any stream may set it
+            w = _serve_words[index] = (t, t.data_ptr())
     return w[1]
 
 

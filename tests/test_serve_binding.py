@@ -176,3 +176,43 @@ def test_the_workspace_of_a_shape_is_the_device_s_own(rec, monkeypatch):
     monkeypatch.setitem(_lib._serve_words, 1, (None, 0x78))
     calls()["q"]()
     assert [c[0] for c in rec.calls].count("gptq_kv4_attention_call_bytes") == 2
+
+
+def test_the_library_is_loaded_before_a_wrapper_finds_what_it_needs(monkeypatch):
+    # Another thread's first call goes past `_serve or _serving()` as soon as
+    # _serve holds anything, and then uses the library.
+    from gptq_post_weight_gb300 import _lib
+
+    seen = []
+    monkeypatch.setattr(_lib, "_serve", {})
+    monkeypatch.setattr(_lib, "load", lambda: seen.append(dict(_lib._serve)))
+    assert _lib._serving() is _lib._serve and seen == [{}]
+
+
+def test_threads_share_one_status_word(monkeypatch):
+    import threading
+    import time
+
+    from gptq_post_weight_gb300 import _lib
+
+    zeros = torch.zeros
+
+    def slow(*a, **k):
+        time.sleep(0.05)
+        return zeros(4, dtype=torch.int32)
+
+    monkeypatch.setattr(_lib, "_serve_words", {})
+    monkeypatch.setattr(torch, "zeros", slow)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda i: type("S", (), {"synchronize": lambda self: None})())
+    got, start = [], threading.Barrier(4)
+
+    def first():
+        start.wait()
+        got.append(_lib._serve_word(0))
+
+    threads = [threading.Thread(target=first) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert set(got) == {_lib._serve_words[0][1]} and len(got) == 4
