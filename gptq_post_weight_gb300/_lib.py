@@ -849,7 +849,8 @@ def _refuse_write(cache, k, v, slots, page_size):
 def kv4_write(cache, k, v, slots, page_size, stream=None):
     """Quantise k, v [tokens, heads, dim] (bf16 or f16, strided views allowed)
     into the cache at slots [tokens] i64 (page * page_size + place; negative:
-    left out).  Returns the cache."""
+    left out).  The slots of a call have to differ: one given twice ends as a mix
+    of its tokens.  Returns the cache."""
     sv = _serve or _serving()
     try:
         kt, shape, dev = k.dtype, k.shape, k.get_device()

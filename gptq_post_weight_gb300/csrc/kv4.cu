@@ -15,7 +15,8 @@
 //
 // Both kernels move each byte once: four lanes share a group (16 bytes of T
 // a lane), a thread does the key and the value of its place, so that two
-// loads are in flight for each.  A block looks its tokens' slots up once, into
+// loads are in flight for each.  Nothing orders the stores of one place
+// against another's: the slots of a write have to differ.  A block looks its tokens' slots up once, into
 // shared memory: the divisions of a 64-bit slot would otherwise be most of
 // what a place costs.  They are bound by the memory: 131072 tokens of 8 heads
 // of 128 read back in 122 us, 5.78 TB/s of codes and values together, and

@@ -448,8 +448,10 @@ gptq_status gptq_q4tp_linear(int dtype, const void* X, long long ldx, int tokens
  * gptq_kv4_write -- quantise tokens into the cache.  K, V in T
  * [tokens][heads][dim] with strides in elements (kt, vt between tokens, kh,
  * vh between heads; multiples of 8), slots in i64 [tokens].  A slot outside
- * the pool (a negative one: padding) is left out; one slot twice in a call
- * keeps either token.
+ * the pool (a negative one: padding) is left out.  The slots of one call have
+ * to differ: tokens are stored in 4-byte words in no order, so that a slot
+ * given twice ends with words of both tokens (codes of one may meet the scale
+ * of the other) and holds neither; the other slots are as they should be.
  */
 gptq_status gptq_kv4_write(int dtype, uint8_t* cache, long long pages, int heads, int dim,
                            int page_size, const void* K, const void* V, long long kt, long long kh,

@@ -41,3 +41,31 @@ def test_one_token_of_any_token_stride(lib, heads, group):
     odd = torch.as_strided(wide, (1, heads * group, 64), (heads * group * 64 + 3, 64, 1))
     assert torch.equal(plain, kv.attend(odd, cache, table, lens, 16, "bf16"))
     assert torch.equal(plain, kv.attend(odd, cache, table, lens, 16, "bf16", [1]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_slot_given_twice_mixes_its_tokens_and_leaves_the_others(lib, dtype):
+    # What the header says of it: each word is one of the tokens', the other
+    # slots hold what they should.
+    from gptq_post_weight_gb300 import _lib
+
+    r = np.random.default_rng(22)
+    tokens, heads, dim, page = 300, 2, 128, 16
+    k, v = kv.keys(r, (tokens, heads, dim), dtype), kv.keys(r, (tokens, heads, dim), dtype)
+    slots = r.permutation(400)[:tokens].astype(np.int64)
+    pairs = [(0, 1), (5, 299), (40, 200)]
+    for i, j in pairs:
+        slots[j] = slots[i]
+    last = [b for _, b in pairs]
+    first = [a for a, _ in pairs]
+
+    def written(keep):
+        cache = _lib.kv4_cache(25, heads, dim, page)
+        _lib.kv4_write(cache, kv.dev(k[keep], kv.DT[dtype]), kv.dev(v[keep], kv.DT[dtype]), kv.dev(slots[keep]), page)
+        return cache.view(torch.int32)
+
+    everyone = np.arange(tokens)
+    both = written(everyone)
+    one, two = written(np.setdiff1d(everyone, last)), written(np.setdiff1d(everyone, first))
+    assert (one != two).any()
+    assert ((both == one) | (both == two)).all()
