@@ -902,9 +902,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t nfull[PNS], nempty[PNS], xfull[PXS], xempty[PXS], afull[4], aempty[4],
-      tfull, tempty, drain;
+      tfull, tempty, drain, scaled[4];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
+  // A tile's row scales, in turns of four: the ladders are at most three tiles
+  // ahead of the sums (one box a tile: two in tensor memory, one waiting), and
+  // `scaled` shows the warps that write out that a turn's have been stored.
   __shared__ float rowscale[4][QROWS], rowmax[4 * QROWS];
   volatile int* abort = &abort_sh;
   const uint32_t rank = cluster_rank();
@@ -922,6 +925,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&afull[i], QDEQ / 2), mbar_init(&aempty[i], 1);
     mbar_init(&tfull, 1), mbar_init(&tempty, 512);
     mbar_init(&drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&scaled[i], 1);
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -1003,6 +1007,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
     for (int t = pair; t < tiles; t += npairs, ++k) {
       const int row0 = (t % mt) * 2 * QROWS + (int)rank * QROWS;
       load_ladders<T>(a, row0, tab, rowscale[k & 3], rowmax);
+      if (threadIdx.x == 128) mbar_arrive(&scaled[k & 3]);  // (behind load_ladders' last barrier)
       // After a wait has run out the warps only keep meeting at the ladders' barriers.
       if (ok) ok = dq.tile(a, row0, 0, nbox, k * nbox, nring, tab, nfull, nempty, afull, aempty, abort, wc.ns);
     }
@@ -1029,7 +1034,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
       };
       fetch(c);
       // One thread looks; the others wait in the barrier.
-      if (!epi8_all(threadIdx.x % 256 != 128 || wait_bar_idle(&tfull, (uint32_t)k & 1u, abort, wc.ns))) break;
+      if (!epi8_all(threadIdx.x % 256 != 128 || (wait_bar_idle(&tfull, (uint32_t)k & 1u, abort, wc.ns) &&
+                                                 wait_bar(&scaled[k & 3], (uint32_t)(k >> 2) & 1u, abort, wc.ns))))
+        break;
       tc_fence_after();
       const float sc = rowscale[k & 3][r];
       for (; c < c1; c += 16) {
