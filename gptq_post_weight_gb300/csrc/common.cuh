@@ -48,7 +48,7 @@ enum Kind : int {
   K_DIAG = 0, K_BUILD, K_POTRF, K_TRSM, K_FOLD_GEMM, K_LADDER, K_SWEEP_BLOCK, K_PREP_UT,
   K_SWEEP_GEMM, K_GROUP, K_COPY, K_GRAM_PREP, K_GRAM_GEMM, K_PLACE, K_DEBIAS, K_DEBIAS_GEMM, K_FOLD_STRIP,
   K_Q4_LINEAR, K_KV4_WRITE, K_KV4_READ, K_KV4_ATTENTION, K_KV4_JOIN,
-  K_KV4_CHUNK, K_NKINDS
+  K_KV4_CHUNK, K_Q4_MID, K_Q4_MANY, K_NKINDS
 };
 
 // Every launch site calls prof_begin/prof_end around its <<<>>>: they count

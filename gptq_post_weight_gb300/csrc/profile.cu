@@ -28,7 +28,7 @@ const char* kNames[K_NKINDS] = {"diag", "build", "potrf", "trsm", "fold_gemm", "
                                 "sweep_block", "prep_ut", "sweep_gemm", "group", "copy",
                                 "gram_prep", "gram_gemm", "place", "debias",
                                 "debias_gemm", "fold_strip", "q4_linear", "kv4_write", "kv4_read",
-                                "kv4_attention", "kv4_join", "kv4_chunk"};
+                                "kv4_attention", "kv4_join", "kv4_chunk", "q4_linear_mid", "q4_linear_many"};
 
 }  // namespace
 

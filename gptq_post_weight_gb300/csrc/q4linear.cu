@@ -1274,7 +1274,7 @@ gptq_status mid_launch(const LinearArgs& a, const MidShape& ms, cudaStream_t s) 
   at[0].val.clusterDim.z = (unsigned)split;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  GQ_PROF(K_Q4_LINEAR, s);
+  GQ_PROF(K_Q4_MID, s);
   GQ_CUDA(cudaLaunchKernelEx(&cfg, k_q4_mid<T>, wm, xm, a, tn, boxes, nx, wait_cfg()));
   return GPTQ_OK;
 }
@@ -1311,7 +1311,7 @@ gptq_status many_launch(const LinearArgs& a, cudaStream_t s) {
   const int np = tiles < pairs ? (int)tiles : pairs;
   const size_t smem = 1024 + (size_t)PNS * QBOX + (size_t)2 * PXS * (tn / 2) * 128 + (size_t)QROWS * QTAB * 4 +
                       8 * 16 * 36 * 4;
-  GQ_PROF(K_Q4_LINEAR, s);
+  GQ_PROF(K_Q4_MANY, s);
   k_q4_many<T><<<2 * np, 896, smem, s>>>(wm, xm, a, tn, mt, (int)tiles, wait_cfg());
   GQ_LAUNCHED();
   return GPTQ_OK;
