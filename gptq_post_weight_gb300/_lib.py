@@ -954,8 +954,9 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
     4-bit cache: softmax(scale q k^T) v per sequence and head, scale default
     1 / sqrt(dim).  table [seqs, pages per sequence] i32, kv_lens [seqs] i32
     (the queries' own keys included).  The queries of sequence b are its last
-    tokens, rows q_starts[b] .. q_starts[b + 1] - 1 of q (i32 [seqs + 1], at
-    most max_q each); without q_starts, one a sequence."""
+    tokens, rows q_starts[b] .. q_starts[b + 1] - 1 of q (i32 [seqs + 1], the
+    first max_q of each); without q_starts, one a sequence.  Outputs of rows
+    that are no sequence's are zero."""
     sv = _serve or _serving()
     try:
         qt, dev, i32 = q.dtype, q.get_device(), sv["i32"]

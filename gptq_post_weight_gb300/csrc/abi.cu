@@ -727,7 +727,12 @@ gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long lo
     return GPTQ_ERR_SHAPE;
   if (bad_dtype(dtype) || !isfinite(scale)) return GPTQ_ERR_ARG;
   if (q_starts == nullptr && (tq != seqs || max_q != 1)) return GPTQ_ERR_SHAPE;
-  if (tq == 0 || seqs == 0) return GPTQ_OK;
+  if (tq == 0) return GPTQ_OK;
+  if (seqs == 0) {  // every row is no sequence's
+    if (!ptr_ok(out)) return GPTQ_ERR_ARG;
+    GQ_CUDA(cudaMemsetAsync(out, 0, (size_t)tq * heads * group * dim * 2, as_stream(stream)));
+    return GPTQ_OK;
+  }
   if (bad_stride(q_ts) || bad_stride(q_hs)) return GPTQ_ERR_SHAPE;
   if (!ptr_ok(Q) || !ptr_ok(cache) || table == nullptr || kv_lens == nullptr || !ptr_ok(out) || !opt_ok(ws))
     return GPTQ_ERR_ARG;

@@ -218,7 +218,10 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
       c1 = (int)min((long long)nch, c0 + (uend - u));
       head = item / nblk, r0 = (item % nblk) * MR;
     } else {
-      if (sq.nq == 0) return;  // the whole cluster
+      if (a.q_starts != nullptr && sq.nq == 0) {  // the whole cluster
+        zero_other_rows<T, D>(a, (int)(blockIdx.y * gridDim.x + blockIdx.x), (int)(gridDim.x * gridDim.y));
+        return;
+      }
       c0 = (int)(nch * rank / max(CL, 1)), c1 = (int)(nch * (rank + 1) / max(CL, 1));
       head = (int)blockIdx.x / max(CL, 1), r0 = 0;  // one row block
     }
@@ -265,6 +268,8 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
     };
     if (!wc.no_loads)
       for (int i = 0; i < ST && left > 0; ++i) issue();
+    if (CL && a.q_starts != nullptr)  // (elsewhere the join's, before it waits)
+      zero_other_rows<T, D>(a, (int)(blockIdx.y * gridDim.x + blockIdx.x), (int)(gridDim.x * gridDim.y));
 
     // q, in the order of the key words: column g of each tile.
     uint32_t qb[NQ][NW][4];
@@ -581,6 +586,8 @@ __global__ void __launch_bounds__(ATHREADS) k_kv4_join(AttnArgs a) {
   __shared__ __align__(16) float batch[AW][JB][D];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int r = (int)blockIdx.y * AW + warp, first = (int)blockIdx.x;
+  if (a.q_starts != nullptr)
+    zero_other_rows<T, D>(a, (int)(blockIdx.y * gridDim.x + blockIdx.x), (int)(gridDim.x * gridDim.y));
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the cuts and the pieces are there
   const int4 cut = a.cuts[first];
   const int head = cut.z >> 9, rows = cut.z & 511, lastc = cut.w;
@@ -725,6 +732,7 @@ gptq_status attn_launch(const AttnArgs& a, long long shares, cudaStream_t s) {
     p.seqs = seqs - b0 < ASEQS ? seqs - b0 : ASEQS;
     p.table += (long long)b0 * a.table_stride;
     p.kv_lens += b0;
+    p.first = b0 == 0, p.last = b0 + p.seqs == seqs;
     if (a.q_starts != nullptr) {
       p.q_starts += b0;
     } else {

@@ -780,6 +780,7 @@ __global__ void __launch_bounds__(128) k_kv4_chunk_join(AttnArgs a) {
   constexpr int RW = D == 256 ? 2 : 4;
   __shared__ __align__(16) float batch[4][4 * RW][D];  // [warp][piece, row]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, first = (int)blockIdx.x;
+  zero_other_rows<T, D>(a, (int)(blockIdx.y * gridDim.x + blockIdx.x), (int)(gridDim.x * gridDim.y));
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the cuts and the pieces are there
   const int4 cut = a.cuts[first];
   const int head = cut.z >> 9, rows = cut.z & 511, lastc = cut.w;
@@ -856,6 +857,7 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
     p.table += (long long)b0 * a.table_stride;
     p.kv_lens += b0;
     p.q_starts += b0;
+    p.first = b0 == 0, p.last = b0 + p.seqs == a.seqs;
     const int grid = num_sms();
     {
       GQ_PROF(K_KV4_CHUNK, s);

@@ -190,7 +190,27 @@ struct AttnArgs {
   float* part;       // workspace: pieces of cut items
   uint32_t up;       // 2^kPos of T (see code16)
   unsigned* status;
+  bool first = true, last = true;  // the launch has the call's first, last sequence
 };
+
+// Zeros for the output rows that are no sequence's: before the first one's,
+// after the last one's and past max_q of their own.  By `ctas` CTAs of a
+// launch, this one number `cta`; a.q_starts is given.
+template <class T, int D>
+__device__ __forceinline__ void zero_other_rows(const AttnArgs& a, int cta, int ctas) {
+  auto start = [&](int i) { return min(max(a.q_starts[i], 0), a.tq); };
+  auto zero = [&](int row) {
+    const int n = a.heads * a.group * (D / 8);  // 16 bytes each
+    uint4* dst = static_cast<uint4*>(a.out) + (long long)row * n;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) dst[i] = uint4{};
+  };
+  if (a.first)
+    for (int r = cta, end = start(0); r < end; r += ctas) zero(r);
+  if (a.last)
+    for (int r = start(a.seqs) + cta; r < a.tq; r += ctas) zero(r);
+  for (int b = cta; b < a.seqs; b += ctas)
+    for (int r = start(b), end = start(b + 1), i = a.max_q; i < end - r; ++i) zero(r + i);
+}
 
 // The driver's tensor-map encoder (null when it cannot be had).
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();

@@ -478,9 +478,11 @@ gptq_status gptq_kv4_read(int dtype, const uint8_t* cache, long long pages, int 
  *            of each sequence.  An entry outside the pool reads page 0.
  *   kv_lens  in  i32 [seqs], the queries' own keys included; at most
  *            table_stride * page_size counts.
- *   q_starts in  i32 [seqs + 1]: the queries of b are rows q_starts[b] ..
- *            q_starts[b + 1] - 1 of Q (at most max_q count); NULL: one query a
- *            sequence (tq == seqs).
+ *   q_starts in  i32 [seqs + 1], not decreasing: the queries of b are rows
+ *            q_starts[b] .. q_starts[b + 1] - 1 of Q, the first max_q of them;
+ *            NULL: one query a sequence (tq == seqs).  The outputs of rows that
+ *            are no sequence's (before the first one's, after the last one's,
+ *            past max_q) are zero.
  *   max_q    host bound on the queries of one sequence.
  *   out      out T [tq][heads*group][dim] (dense).
  *   ws       >= gptq_kv4_attention_call_bytes(...) of this call (single: q_starts

@@ -69,3 +69,49 @@ def test_a_slot_given_twice_mixes_its_tokens_and_leaves_the_others(lib, dtype):
     one, two = written(np.setdiff1d(everyone, last)), written(np.setdiff1d(everyone, first))
     assert (one != two).any()
     assert ((both == one) | (both == two)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("group,max_q,lens,q_lens,extra", [
+    (2, 1, [30, 40], [1, 1], [0, 3]),        # clusters; two sequences have rows past max_q
+    (2, 3, [30, 40, 9], [3, 0, 2], [0, 0, 0]),
+    (4, 5, [300, 7000, 12], [5, 4, 5], [2, 0, 1]),  # shares and a join
+    (4, 60, [100, 3000, 70], [60, 0, 31], [0, 0, 0]),  # tcgen05, the tiles in turns
+    (4, 150, [200, 900], [150, 7], [70, 0]),   # tcgen05
+    (2, 2, [20] * 1100, [2, 1] * 550, [0, 1] * 550),  # more sequences than one launch takes
+])
+def test_rows_that_no_sequence_has_are_zero(lib, group, max_q, lens, q_lens, extra, dtype):
+    # Rows before the first sequence's, after the last one's and past max_q of
+    # their own: zeros in `out`, and the others as without them.
+    r = np.random.default_rng(23)
+    heads, dim, page, before, after = 2, 64, 16, 3, 70
+    counts = [n if e == 0 else max_q + e for n, e in zip(q_lens, extra)]
+    q_lens = [min(c, max_q) for c in counts]
+    cache, table, lens_d, ks, vs = kv.context(r, lens, heads, dim, page, dtype)
+    starts = before + np.concatenate([[0], np.cumsum(counts)])
+    tq = int(starts[-1]) + after
+    q = serve.round_to(r.standard_normal((tq, heads * group, dim)), dtype)
+    out = torch.full((tq, heads * group, dim), float("nan"), dtype=kv.DT[dtype], device="cuda")
+    from gptq_post_weight_gb300 import _lib
+
+    got = kv.host(_lib.kv4_attention(kv.dev(q, kv.DT[dtype]), cache, table, lens_d, page,
+                                     q_starts=kv.dev(starts.astype(np.int32)), max_q=max_q, out=out))
+    _lib.serve_check()
+    seen = np.concatenate([np.arange(s, s + n) for s, n in zip(starts, q_lens)])
+    rest = np.setdiff1d(np.arange(tq), seen)
+    assert not got[rest].any()  # (a NaN counts as any)
+    want = serve.attention(q[seen], ks, vs, lens, group, dim ** -0.5, q_lens)
+    tol = kv.tolerance(q[seen], ks, vs, lens, group, dim ** -0.5, q_lens, dtype, want)
+    assert (np.abs(got[seen] - want) <= tol).all()
+
+
+def test_no_sequences_leave_every_row_zero(lib):
+    from gptq_post_weight_gb300 import _lib
+
+    cache = _lib.kv4_cache(2, 2, 64, 16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.ones(5, 4, 64, dtype=torch.float16, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    _lib.kv4_attention(q, cache, torch.zeros(0, 1, **i32), torch.zeros(0, **i32), 16,
+                       q_starts=torch.zeros(1, **i32), max_q=3, out=out)
+    assert not out.any()
