@@ -672,6 +672,16 @@ def _here(t, name):
         raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{current}")
 
 
+def _no_gradient(**tensors):
+    """Raise ValueError if one of them would need the operator's gradient."""
+    import torch
+
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} requires a gradient, and the call has none: make it under torch.no_grad()")
+
+
 def _dtype16(t, name):
     import torch
 
@@ -747,6 +757,7 @@ def _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out):
         _rows_of(residual, "residual", tokens, rows, x)
     if out is not None:
         _rows_of(out, "out", tokens, rows, x)
+    _no_gradient(x=x, bias=bias, residual=residual)
     _here(x, "x")
 
 
@@ -765,7 +776,7 @@ def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, ou
         st = x.stride()
         ldx = st[0] if tokens > 1 else n
         fine = (dev >= 0 and dev == sv["current"]() and n > 0 and n % 32 == 0 and st[1] == 1 and ldx % 8 == 0
-                and ldx >= n
+                and ldx >= n and not x.requires_grad
                 and tab.dtype is sv["f32"] and tab.shape == (rows, 32) and tab.is_contiguous()
                 and tab.get_device() == dev
                 and nibbles.dtype is u8 and nibbles.numel() == rows * n // 2 and nibbles.is_contiguous()
@@ -776,13 +787,13 @@ def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, ou
         ldr = 0
         if bias is not None:
             fine = (fine and bias.dtype is xt and bias.numel() == rows and bias.is_contiguous()
-                    and bias.get_device() == dev)
+                    and bias.get_device() == dev and not bias.requires_grad)
             bp = bias.data_ptr()
         if residual is not None:
             st = residual.stride()
             ldr = st[0] if tokens > 1 else rows
             fine = (fine and residual.dtype is xt and residual.shape == (tokens, rows) and (rows == 1 or st[1] == 1)
-                    and ldr >= rows and residual.get_device() == dev)
+                    and ldr >= rows and residual.get_device() == dev and not residual.requires_grad)
             rp = residual.data_ptr()
         ldy = rows
         if out is not None:
@@ -945,6 +956,7 @@ def _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, out,
         _need(out, "out", dtype=q.dtype, numel=q.numel(), device=dev)
     if ws is not None:
         _ws(ws, dev)
+    _no_gradient(q=q)
     _here(q, "q")
 
 
@@ -966,7 +978,7 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
         seqs, per = table.shape
         qts, qhs, q1 = q.stride()
         fine = (dev >= 0 and dev == sv["current"]() and dim in (64, 128, 256) and tq > 0 and hq > 1
-                and hq % heads == 0 and q1 == 1
+                and hq % heads == 0 and q1 == 1 and not q.requires_grad
                 and (qts | qhs) % 8 == 0 and 0 < page_size <= 4096 and page_size % 16 == 0 and max_q > 0
                 and cache.dtype is sv["u8"] and size == page_size * dim * 5 // 4 and cache.is_contiguous()
                 and cache.get_device() == dev and table.dtype is i32 and per > 0 and table.is_contiguous()

@@ -216,3 +216,28 @@ def test_threads_share_one_status_word(monkeypatch):
     for t in threads:
         t.join()
     assert set(got) == {_lib._serve_words[0][1]} and len(got) == 4
+
+
+@pytest.mark.parametrize("which", ["x", "bias", "residual", "q"])
+def test_inputs_that_want_a_gradient_are_refused(rec, which):
+    # The operators have no backward pass: the result would have no history,
+    # and training would go on without that gradient.
+    from gptq_post_weight_gb300 import _lib
+
+    x, bias, residual, q = b16(3, 64), b16(6), b16(3, 6), b16(3, 4, 64)
+    cache = gpu(torch.zeros(4, 2, 16 * 64 * 5 // 4, dtype=torch.uint8))
+    table, lens = gpu(torch.zeros(3, 1, dtype=torch.int32)), gpu(torch.ones(3, dtype=torch.int32))
+    dict(x=x, bias=bias, residual=residual, q=q)[which].requires_grad_()
+
+    def call():
+        if which == "q":
+            _lib.kv4_attention(q, cache, table, lens, 16, out=b16(3, 4, 64), stream=Stream)
+        else:
+            _lib.q4tp_linear(x, *weights(6, 64), bias=bias, residual=residual, out=b16(3, 6), stream=Stream)
+
+    with pytest.raises(ValueError, match=f"{which} requires a gradient"):
+        call()
+    assert not rec.calls
+    with torch.no_grad():
+        call()
+    assert rec.calls
