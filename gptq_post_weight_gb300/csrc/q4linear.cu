@@ -12,7 +12,8 @@
 //   f16:  code c is the subnormal c 2^-24, its scale 2^24 s.
 // The sum starts at -(128 + 8) sum(x) (bf16; -8 2^-24 sum(x) for f16), which
 // takes the offset of the nibble off again (f32: the cancellation costs some
-// 2^-18 of the result).
+// 2^-18 of the result; sums that are no finite number are taken again without
+// it, see sum_again).
 //
 // A CTA is four or eight warps of 16 rows and a slice of the columns; the CTAs of a
 // cluster share the rows and split the columns, and add their sums over
@@ -188,6 +189,42 @@ __device__ __forceinline__ uint2 box_rungs(const LinearArgs& a, int row, int b, 
     r.y |= (g0 + 4 + i < gpr ? (uint32_t)p[4 + i] : 0xffu) << (8 * i);
   }
   return r;
+}
+
+// The lane's sums in `part` that are no finite number, again from the slice of
+// x and the weights, weight by weight.  (Where it is comes from the special
+// registers once more, opaque to the compiler: kept from the kernel's start,
+// it cost two tokens a tenth of their time.)
+template <class T, int TT, int FROWS>
+__device__ __forceinline__ void sum_again(const LinearArgs& a, int boxes, float* part) {
+  uint32_t tid, bx, by, bz;
+  asm volatile("mov.u32 %0, %%tid.x;\n mov.u32 %1, %%ctaid.x;\n mov.u32 %2, %%ctaid.y;\n mov.u32 %3, %%ctaid.z;"
+               : "=r"(tid), "=r"(bx), "=r"(by), "=r"(bz));
+  const int g = tid % 32 / 4, t = tid % 4, gpr = a.n / GROUP;
+  const int row = tid / 32 * 16 + (TT <= 2 ? (g >> 1) | ((g & 1) << 2) : g);  // as in k_q4_few
+  const int grp0 = (int)by * boxes * 8, groups = min(boxes * 8, gpr - grp0);
+#pragma unroll 1
+  for (int e = 0; e < 4; ++e) {
+    const int tok = TT <= 2 ? t / 2 : 2 * t + (e & 1), r = row + (e >> 1) * 8;
+    if (tok >= TT || (TT <= 2 && (e | t) % 2 != 0)) continue;  // not this lane's
+    const int token = (int)bz * TT + tok, rr = (int)bx * FROWS + r;
+    if (token >= a.tokens || rr >= a.rows || fabsf(part[tok * FROWS + r]) < INFINITY) continue;
+    const T* x = static_cast<const T*>(a.x) + (size_t)token * a.ldx + (size_t)grp0 * 32;
+    const uint8_t* nibbles = a.nibbles + ((size_t)rr * gpr + grp0) * 16;
+    const uint8_t* rungs = a.rungs + (size_t)rr * gpr + grp0;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < groups; ++k) {
+      const float s = rungs[k] < 32 ? a.tab[(size_t)rr * 32 + rungs[k]] : 0.f;
+#pragma unroll 1
+      for (int i = 0; i < 16; ++i) {
+        const int b = nibbles[k * 16 + i];
+        sum = fmaf((float)((b & 15) - 8) * s, Elem<T>::to(x[k * 32 + 2 * i]), sum);
+        sum = fmaf((float)((b >> 4) - 8) * s, Elem<T>::to(x[k * 32 + 2 * i + 1]), sum);
+      }
+    }
+    part[tok * FROWS + r] = sum;
+  }
 }
 
 // Floats of shared memory a group for its starting sums, and a warp for the
@@ -453,11 +490,18 @@ __global__ void __launch_bounds__(32 * FW)
 
   // Sums to shared memory [token][row], added over the cluster's ranks in order.
   float* part = reinterpret_cast<float*>(smem);
+  bool finite = true;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int tok = TT <= 2 ? t / 2 : 2 * t + (e & 1);
-    if (tok < TT && (TT > 2 || (e | t) % 2 == 0)) part[tok * FROWS + warp * 16 + row + (e >> 1) * 8] = acc[e];
+    if (tok < TT && (TT > 2 || (e | t) % 2 == 0)) {
+      part[tok * FROWS + warp * 16 + row + (e >> 1) * 8] = acc[e];
+      finite = finite && fabsf(acc[e]) < INFINITY;
+    }
   }
+  // An infinite x has an infinite offset, so that its sums are infinity minus
+  // infinity (and the offsets of numbers near bf16's end leave f32's range).
+  if (!finite) sum_again<T, TT, FROWS>(a, boxes, part);
   namespace cg = cooperative_groups;
   if (nrank > 1)
     cg::this_cluster().sync();

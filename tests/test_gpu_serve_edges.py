@@ -115,3 +115,71 @@ def test_no_sequences_leave_every_row_zero(lib):
     _lib.kv4_attention(q, cache, torch.zeros(0, 1, **i32), torch.zeros(0, **i32), 16,
                        q_starts=torch.zeros(1, **i32), max_q=3, out=out)
     assert not out.any()
+
+
+def product_of(p, dtype, x):
+    """(result, what it has to be, how far off a finite one may be)."""
+    import test_gpu_linear as lin
+
+    q = dict(p, x=x)
+    with np.errstate(invalid="ignore"):
+        want = serve.linear(x, p["nib"], p["rungs"], p["tab"])
+        # Past T's range a result is an infinity.
+        want = np.where(np.abs(want) > serve.TYPES[dtype][2], np.copysign(np.inf, want), want)
+    w = np.abs(serve.weights(p["nib"], p["rungs"], p["tab"]))
+    sc = np.abs(serve.weights(np.full_like(p["nib"], 0x99), p["rungs"], p["tab"]))
+    ax = np.where(np.isfinite(x), np.abs(x), 0)
+    u = 2.0 ** (1 - serve.TYPES[dtype][0])
+    # As in test_gpu_linear.py; plain sums in f32 instead of a group's at a time
+    # are n 2^-23 of sum |x w|.
+    err = 34 * 143 * 2.0 ** -22 * (ax @ sc.T) + x.shape[1] * 2.0 ** -23 * (ax @ w.T)
+    if len(x) > 8:
+        err = err + 0.5 * u * (ax @ w.T)
+    tol = np.where(np.isfinite(want), u * np.abs(want) + err + 2.0 ** -24, 0)
+    return lin.run(q, dtype, "none").float().cpu().numpy().astype(np.float64), want, tol
+
+
+def same_numbers(got, want, tol):
+    with np.errstate(invalid="ignore"):
+        near = np.abs(got - want) <= tol
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+    assert (near | np.isnan(want) | (got == want)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens", [1, 2, 3, 4, 6, 8, 12, 40, 300])
+def test_infinite_activations(lib, tokens, dtype):
+    # A row has an infinity in columns of every sign of code, one of a zero
+    # code gives NaN, opposite ones give NaN; the other rows do not notice.
+    import test_gpu_linear as lin
+
+    rows, n = 300, 2080
+    p = lin.problem(tokens, rows, n, dtype, 41)
+    r = np.random.default_rng(42)
+    x = p["x"].copy()
+    x[0, 7] = np.inf
+    if tokens > 2:
+        x[1, [40, 2079]] = -np.inf, np.inf
+        x[2, 1000] = np.nan
+    got, want, tol = product_of(p, dtype, x)
+    assert np.isinf(want[0]).any() and np.isnan(want[0]).any()
+    same_numbers(got, want, tol)
+    plain = lin.run(p, dtype, "none").float().cpu().numpy()
+    clean = np.isfinite(x).all(1)
+    np.testing.assert_array_equal(got[clean], plain[clean])
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 4, 8])
+def test_activations_near_the_end_of_bf16(lib, tokens):
+    # 2^112 and more times an offset of 136 would leave f32's range.
+    import test_gpu_linear as lin
+
+    p = lin.problem(tokens, 70, 544, "bf16", 43)
+    p["tab"] = (p["tab"] / 64).astype(np.float32)
+    x = p["x"].copy()
+    x[0, ::50] = serve.round_to(np.float64(3e38) * np.sign(x[0, ::50]), "bf16")
+    if tokens > 1:
+        x[1] = serve.round_to(x[1] * 2.0 ** 111, "bf16")
+    got, want, tol = product_of(p, "bf16", x)
+    assert np.isfinite(want).all()
+    same_numbers(got, want, tol)
