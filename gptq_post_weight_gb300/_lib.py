@@ -765,7 +765,8 @@ def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, ou
     """act(x W^T + bias) + residual with W [rows, n] in q4tp form (nibbles,
     rungs, tab as quantize_group returns them).  x [tokens, n] bf16 or f16
     (rows may be strided, not overlap), bias [rows], residual [tokens, rows] and
-    the result [tokens, rows] of x's dtype.  act: a key of ACTIVATIONS."""
+    the result [tokens, rows] of x's dtype.  act: a key of ACTIVATIONS.  `out` may
+    be the residual itself, and overlaps no other input."""
     sv = _serve or _serving()
     try:
         xt, xs, u8 = x.dtype, x.shape, sv["u8"]
@@ -968,7 +969,9 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
     (the queries' own keys included).  The queries of sequence b are its last
     tokens, rows q_starts[b] .. q_starts[b + 1] - 1 of q (i32 [seqs + 1], the
     first max_q of each); without q_starts, one a sequence.  Outputs of rows
-    that are no sequence's are zero."""
+    that are no sequence's are zero.  A value that is NaN (a group that was not
+    finite, or past f16's range) reaches every query of its sequence whose rows
+    share a tile with one that sees it.  `out` overlaps no input."""
     sv = _serve or _serving()
     try:
         qt, dev, i32 = q.dtype, q.get_device(), sv["i32"]

@@ -483,14 +483,19 @@ gptq_status gptq_kv4_read(int dtype, const uint8_t* cache, long long pages, int 
  *            NULL: one query a sequence (tq == seqs).  The outputs of rows that
  *            are no sequence's (before the first one's, after the last one's,
  *            past max_q) are zero.
- *   max_q    host bound on the queries of one sequence.
+ *   max_q    host bound on the queries of one sequence.  It chooses the kernel
+ *            and the number of row blocks, so a tight one is faster; above 131072
+ *            query rows a sequence and key head (max_q * group; 65536 for heads of
+ *            256) the kernel for few rows takes the call, several times slower.
  *   out      out T [tq][heads*group][dim] (dense).
  *   ws       >= gptq_kv4_attention_call_bytes(...) of this call (single: q_starts
  *            is NULL; max_len: table_stride * page_size), which is 0 where the
  *            call needs none (ws may then be NULL) and never more than
  *            gptq_kv4_attention_workspace_bytes(dim, group, max_q).
- * The values of one sequence's keys must be finite where any of its queries
- * sees them; what the pages hold past kv_lens is never used.
+ * The values (V) of one sequence's keys must be finite where any of its queries
+ * sees them: one that is NaN also reaches queries before it whose rows share a
+ * tile with one that sees it.  Keys (K) may hold anything where a query does
+ * not see them, and what the pages hold past kv_lens is never used.
  */
 size_t gptq_kv4_attention_workspace_bytes(int dim, int group, int max_q);
 size_t gptq_kv4_attention_call_bytes(int dim, int heads, int group, int max_q, int seqs, int single,

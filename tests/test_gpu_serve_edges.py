@@ -183,3 +183,44 @@ def test_activations_near_the_end_of_bf16(lib, tokens):
     got, want, tol = product_of(p, "bf16", x)
     assert np.isfinite(want).all()
     same_numbers(got, want, tol)
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 33])
+@pytest.mark.parametrize("how", ["debias", "act order"])
+def test_product_with_weights_of_the_other_quantizers(lib, how, tokens):
+    # What debias leaves of the ladder, and act order's scales put back into one
+    # (it returns a scale a group, and every scale is its rung's entry).
+    import synth
+    import test_gpu_linear as lin
+    from gptq_post_weight_gb300 import _lib
+
+    cfg = synth.config("tiny")
+    hp, w = (t.cuda() for t in synth.make_problem(cfg, "cpu"))
+    if how == "debias":
+        q = _lib.quantize_group(hp, cfg.n, w, cfg.lam)
+        before = q["tab"].clone()
+        _lib.debias(4, w, hp, q["nibbles"], q["rungs"], q["tab"], q["lost"], q["scales"])
+        tab = q["tab"]
+        assert (tab != before).any()
+        at = q["rungs"].view(len(w), -1).long()
+        assert torch.equal(torch.gather(tab, 1, at).flatten(), q["scales"].flatten())
+    else:
+        q = _lib.quantize_group_act_order(hp, cfg.n, w, cfg.lam)
+        at = q["rungs"].view(len(w), -1).long()
+        tab = torch.zeros(len(w), 32, device="cuda").scatter_(1, at, q["scales"].view(len(w), -1))
+    r = np.random.default_rng(51)
+    p = dict(x=serve.round_to(r.standard_normal((tokens, cfg.n)), "bf16"), bias=None, residual=None,
+             nib=q["nibbles"].cpu().numpy(), rungs=q["rungs"].cpu().numpy(), tab=tab.cpu().numpy())
+    lin.check(lin.run(p, "bf16", "none"), p, "bf16", "none")
+    # The oracle's weights are the quantizer's: close to what it was given.
+    wq = serve.weights(p["nib"], p["rungs"], p["tab"])
+    alive = torch.diagonal(full(hp, cfg.n)).cpu().numpy() > 0
+    w0 = w.cpu().numpy()[:, alive]
+    assert np.linalg.norm(wq[:, alive] - w0) < 0.3 * np.linalg.norm(w0)
+
+
+def full(hp, n):
+    h = torch.zeros(n, n, device=hp.device)
+    i = torch.triu_indices(n, n, device=hp.device)
+    h[i[0], i[1]] = hp
+    return h
