@@ -115,12 +115,6 @@ constexpr size_t slot_floats(int mr) {
   return (size_t)mr * (D + 2);
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // First channel of word w of quad lane t (keys): lanes own 16-byte pieces.
 template <int D>
 __device__ __forceinline__ int word_channel(int t, int w) {

@@ -64,12 +64,6 @@ struct MmaFormat<__half> {
   static constexpr uint32_t k = 0u;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two f32 numbers as one operand.
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
   uint64_t r;
@@ -118,11 +112,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
-// For what is in tensor memory (ordered by the tcgen05 fences).
-__device__ __forceinline__ void arrive_relaxed(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // Descriptor of an N-major operand, 128-byte swizzle: rows of 64 elements
 // (one a token), 8 rows in 1024 bytes; `lead` bytes between the 64-element
 // halves of N.
@@ -149,16 +138,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Byte offset of 16-byte piece p (0 .. 7) of row r in a swizzled tile.
 __device__ __forceinline__ uint32_t swz(int r, int p) { return (uint32_t)(r * 128 + ((p ^ (r & 7)) * 16)); }
@@ -443,7 +422,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
         l += (s0.x + s0.y) + (s1.x + s1.y);
         tmem_st_wait();
         tc_fence_before();
-        arrive_relaxed(&pfull[x]);
+        mbar_arrive_relaxed(&pfull[x]);
         began = true;
       }
       if (!ok) break;
@@ -638,8 +617,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       }
     }
   } else if (warp == 25) {
-    uint32_t one;
-    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(one));
+    const bool one = elect_one();
     constexpr uint32_t fmt = MmaFormat<T>::k;
     constexpr uint32_t ids = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(CK >> 3) << 17) | (8u << 24);
     constexpr uint32_t idp = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);

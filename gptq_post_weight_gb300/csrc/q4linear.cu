@@ -565,25 +565,12 @@ __device__ __forceinline__ void dequant32(uint4 v, uint32_t s, uint32_t (&o)[16]
   }
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Arrivals without release semantics, on this CTA's barrier and on the pair
-// leader's.  What they announce (stores to tensor memory, finished reads of
-// shared memory) is ordered by tcgen05.wait::st and the tcgen05 fences on
-// both sides, or has been consumed; a releasing arrival waits for the
-// thread's own loads from global memory as well, and those are the rungs of
-// boxes to come (measured: 1400 cycles from arrival to completed phase).
-__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
+// mbar_arrive_relaxed on the pair leader's barrier.  What these arrivals
+// announce (stores to tensor memory, finished reads of shared memory) is
+// ordered by tcgen05.wait::st and the tcgen05 fences on both sides, or has been
+// consumed; a releasing arrival waits for the thread's own loads from global
+// memory as well, and those are the rungs of boxes to come (measured: 1400
+// cycles from arrival to completed phase).
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_u32(smem_u32(bar), 0))
                : "memory");
@@ -611,12 +598,6 @@ __device__ __forceinline__ bool epi8_all(bool p) {
       : "r"((uint32_t)p)
       : "memory");
   return r != 0u;
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
-  return p != 0u;
 }
 
 // The eight products of two stages: A at tensor-memory column a (8 columns

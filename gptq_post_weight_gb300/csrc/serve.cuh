@@ -100,6 +100,13 @@ __device__ __forceinline__ uint4 pair_order(uint4 v) {
   return o;
 }
 
+// 2^x.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // mbar_wait for waits that are short and many: the clock is looked at once in
 // 64 tries, since reading it costs more than such a wait.  CTA scope also on
 // barriers that a cluster's peer arrives on: what those announce is in shared
