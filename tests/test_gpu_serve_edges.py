@@ -224,3 +224,30 @@ def full(hp, n):
     i = torch.triu_indices(n, n, device=hp.device)
     h[i[0], i[1]] = hp
     return h
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,nq,ln", [(1, 5, 40), (4, 6, 300), (4, 20, 200), (2, 150, 400)])
+def test_keys_that_are_no_numbers_reach_only_queries_that_see_them(lib, group, nq, ln, dim, dtype):
+    # Keys of NaN and of infinities (which the cache holds as NaN) a few places
+    # before the end: the queries before them are as ever, the others NaN.
+    from gptq_post_weight_gb300 import _lib
+
+    r = np.random.default_rng(61)
+    heads, page = 2, 16
+    cache, table, lens, ks, vs = kv.context(r, [ln], heads, dim, page, dtype)
+    bad = [ln - 3, ln - 2]
+    k = kv.keys(r, (2, heads, dim), dtype)
+    k[0, :, 5], k[1, :, dim - 1] = np.nan, -np.inf
+    slots = torch.tensor([int(table[0, p // page]) * page + p % page for p in bad], device="cuda")
+    _lib.kv4_write(cache, kv.dev(k, kv.DT[dtype]), kv.dev(vs[0][bad], kv.DT[dtype]), slots, page)
+    v = vs[0].copy()
+    v[bad] = serve.round_trip(vs[0][bad], dtype)
+    q = serve.round_to(r.standard_normal((nq, heads * group, dim)), dtype)
+    got = kv.host(kv.attend(q, cache, table, lens, page, dtype, [nq]))
+    n = nq - 3  # queries before the first of them
+    want = serve.attention(q[:n], [ks[0][:ln - 3]], [v[:ln - 3]], [ln - 3], group, dim ** -0.5, [n])
+    tol = kv.tolerance(q[:n], [ks[0][:ln - 3]], [v[:ln - 3]], [ln - 3], group, dim ** -0.5, [n], dtype, want)
+    assert (np.abs(got[:n] - want) <= tol).all()
+    assert np.isnan(got[n:]).all()
