@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    mbar_init(&qfull, 512), mbar_init(&mfull, 128);
+    mbar_init(&qfull, 513), mbar_init(&mfull, 128);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], 128), mbar_init(&kempty[i], 1);
       mbar_init(&vfull[i], 128), mbar_init(&vempty[i], 1);
@@ -648,6 +648,9 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       if (pc.j1 == 0) continue;
       const int count = min(pc.j1, pc.t.steps) - pc.j0;
       const bool two = pc.t.rows > 128;
+      // This warp takes part: pieces without steps wait for nothing of it, and
+      // two of them ahead the phase's parity would be the old one again.
+      if (lane == 0) mbar_arrive(&qfull);
       if (!(ok = wait_bar_warp(&qfull, qph, abort, wc.ns))) break;
       qph ^= 1u;
       if (count <= 0) continue;

@@ -251,3 +251,32 @@ def test_keys_that_are_no_numbers_reach_only_queries_that_see_them(lib, group, n
     tol = kv.tolerance(q[:n], [ks[0][:ln - 3]], [v[:ln - 3]], [ln - 3], group, dim ** -0.5, [n], dtype, want)
     assert (np.abs(got[:n] - want) <= tol).all()
     assert np.isnan(got[n:]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,nq", [(2, 20), (1, 150), (1, 300)])
+def test_prompt_chunks_of_many_sequences_that_see_nothing(lib, group, nq, dim):
+    # Tiles without steps one after the other, which the roles of a CTA pass at
+    # their own speed, before and between tiles with steps.
+    from gptq_post_weight_gb300 import _lib
+
+    r = np.random.default_rng(24)
+    heads, page, seqs = 8, 16, 400
+    lens = [0] * seqs
+    lens[seqs // 2], lens[-1] = 90, 33
+    cache, table, _, kk, vv = kv.context(r, [90, 33], heads, dim, page, "bf16")
+    wide = torch.zeros(seqs, table.shape[1], dtype=torch.int32, device="cuda")
+    wide[seqs // 2], wide[-1] = table[0], table[1]
+    q = serve.round_to(r.standard_normal((2 * nq, heads * group, dim)), "bf16")
+    qd = torch.ones(seqs * nq, heads * group, dim, dtype=torch.bfloat16, device="cuda")
+    qd.view(seqs, nq, -1)[[seqs // 2, seqs - 1]] = kv.dev(q, torch.bfloat16).view(2, nq, -1)
+    starts = torch.arange(0, seqs * nq + 1, nq, dtype=torch.int32, device="cuda")
+    out = torch.full_like(qd, float("nan"))
+    _lib.kv4_attention(qd, cache, wide, torch.tensor(lens, dtype=torch.int32, device="cuda"), page, q_starts=starts,
+                       max_q=nq, out=out)
+    _lib.serve_check()
+    got = kv.host(out).reshape(seqs, nq, heads * group, dim)
+    assert not np.delete(got, [seqs // 2, seqs - 1], 0).any()
+    want = serve.attention(q, kk, vv, [90, 33], group, dim ** -0.5, [nq, nq])
+    tol = kv.tolerance(q, kk, vv, [90, 33], group, dim ** -0.5, [nq, nq], "bf16", want)
+    assert (np.abs(got[[seqs // 2, seqs - 1]].reshape(want.shape) - want) <= tol).all()
