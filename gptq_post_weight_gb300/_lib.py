@@ -969,9 +969,7 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
     (the queries' own keys included).  The queries of sequence b are its last
     tokens, rows q_starts[b] .. q_starts[b + 1] - 1 of q (i32 [seqs + 1], the
     first max_q of each); without q_starts, one a sequence.  Outputs of rows
-    that are no sequence's are zero.  A value that is NaN (a group that was not
-    finite, or past f16's range) reaches every query of its sequence whose rows
-    share a tile with one that sees it.  `out` overlaps no input."""
+    that are no sequence's are zero.  `out` overlaps no input."""
     sv = _serve or _serving()
     try:
         qt, dev, i32 = q.dtype, q.get_device(), sv["i32"]

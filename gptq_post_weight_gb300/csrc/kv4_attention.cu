@@ -115,6 +115,80 @@ constexpr size_t slot_floats(int mr) {
   return (size_t)mr * (D + 2);
 }
 
+// The sequence of chunk u of the list.
+__device__ __forceinline__ int seq_at(const AttnArgs& a, const long long* pref, long long u) {
+  int lo = 0, hi = a.seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (pref[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A piece of an item: chunks c0 .. c1 - 1 of nch of a row block.
+struct Item {
+  int b, head, r0, rows, c0, c1, nch;
+};
+
+// A value that is no number must not meet the probability of 0 of a row that
+// does not see its token: it counted nothing, and the rows that do see it get
+// their NaN here, over the sums of row r at row(r), or over its output where row(r)
+// is null.  By the whole CTA.
+template <class T, int D, class Row>
+__device__ __forceinline__ void spoil_item(const AttnArgs& a, const Seq& sq, const Item& it, int* first, Row row) {
+  if (threadIdx.x < D / 32) first[threadIdx.x] = INT_MAX;
+  __syncthreads();
+  const int open = max(0, sq.len - sq.nq + it.r0 / a.group + 1);  // the first token that some row does not see
+  const int end = min(it.c1 * ACH, min(sq.len, sq.len - sq.nq + (it.r0 + it.rows - 1) / a.group + 1));
+#pragma unroll 1
+  for (int t = max(open, it.c0 * ACH) + (int)threadIdx.x; t < end; t += ATHREADS) {
+    const uint32_t* par = value_params<D>(a, it.b, it.head, t);
+#pragma unroll 1
+    for (int i = 0; i < D / 32; ++i)
+      if (no_numbers<T>(par[i])) atomicMin(&first[i], t);
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = threadIdx.x; i < it.rows * (D / 2); i += ATHREADS) {
+    const int r = i / (D / 2), d = i % (D / 2) * 2, rr = it.r0 + r, qi = rr / a.group;
+    if (sq.len - sq.nq + qi < first[d / 32]) continue;
+    float* sums = row(r);
+    if (sums != nullptr)
+      *reinterpret_cast<float2*>(sums + d) = float2{NAN, NAN};
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + ((long long)(sq.q0 + qi) * a.heads * a.group +
+                                                             it.head * a.group + rr % a.group) * D + d) = 0x7fff7fffu;
+  }
+  __syncthreads();
+}
+
+// The same for every item of a CTA's share, after its steps.  (The share is
+// worked out again, from what the compiler does not see through, so that no
+// register is kept for this, which no call with numbers in its cache comes to.)
+template <class T, int D, int NQ>
+__device__ __forceinline__ void spoil_items(const AttnArgs& a, const volatile long long* prefix, int* first) {
+  constexpr int MR = 8 * NQ;
+  uint32_t cta, ctas;
+  asm volatile("mov.u32 %0, %%ctaid.x;\n mov.u32 %1, %%nctaid.x;" : "=r"(cta), "=r"(ctas));
+  const long long* pref = const_cast<const long long*>(prefix);
+  const long long W = prefix[a.seqs], shares = min(W, (long long)ctas), uend = W * (cta + 1) / shares;
+#pragma unroll 1
+  for (long long u = W * cta / shares; u < uend;) {
+    const int b = seq_at(a, pref, u);
+    const Seq sq = seq_of(a, b);
+    const int nch = chunks_of(sq), nblk = blocks_of<MR>(a, sq);
+    const long long rem = u - pref[b];
+    const int item = (int)(rem / nch), c0 = (int)(rem % nch);
+    const Item it{b, item / nblk, item % nblk * MR, min(MR, sq.nq * a.group - item % nblk * MR), c0,
+                  (int)min((long long)nch, c0 + (uend - u)), nch};
+    float* part = a.part + ((size_t)cta * 2 + (c0 == 0 ? 1 : 0)) * slot_floats<D>(MR);
+    spoil_item<T, D>(a, sq, it, first, [&](int r) {
+      return it.c0 == 0 && it.c1 == it.nch ? nullptr : part + r * D;
+    });
+    u += it.c1 - it.c0;
+  }
+}
+
 // First channel of word w of quad lane t (keys): lanes own 16-byte pieces.
 template <int D>
 __device__ __forceinline__ int word_channel(int t, int w) {
@@ -145,7 +219,10 @@ constexpr int resident(int dim, int nq) { return dim * nq <= 128 ? 4 : dim * nq 
 // NQ: column tiles of eight query rows; ST: pairs of blocks in a warp's ring.
 // CL = 0: equal shares of the list.  CL > 0: blockIdx.y is the sequence, and
 // CL CTAs of a cluster share each item of it and join its pieces themselves.
-template <class T, int D, int NQ, int ST, int CL>
+// SEV: a sequence may have several queries, of which one sees a key that
+// another does not (one query a sequence keeps the kernel without what that
+// takes, which was 2 % of the time of 48 sequences to 16384 tokens).
+template <class T, int D, int NQ, int ST, int CL, bool SEV>
 __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
     k_kv4_attention(AttnArgs a, WaitCfg wc) {
   using T2 = typename Elem<T>::T2;
@@ -158,6 +235,7 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
   __shared__ long long pref[ASEQS + 1];
   __shared__ long long scratch[AW];
   __shared__ float mls[AW][MR][2];
+  __shared__ int spoiled, spoiled_at[D / 32];  // SEV: see spoil_item
   __shared__ int abort_sh;
   volatile int* abort = &abort_sh;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -166,7 +244,7 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_kv4_join may set itself up
   if (lane == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(&full[warp * ST + s], 1);
-    if (warp == 0) abort_sh = 0;
+    if (warp == 0) abort_sh = 0, spoiled = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -192,15 +270,7 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
 
   while (u < uend) {
     // The item of chunk u.
-    int b = (int)blockIdx.y;
-    if (CL == 0) {
-      int lo = 0, hi = a.seqs - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (pref[mid] <= u) lo = mid; else hi = mid - 1;
-      }
-      b = lo;
-    }
+    const int b = CL == 0 ? seq_at(a, pref, u) : (int)blockIdx.y;
     const Seq sq = seq_of(a, b);
     const int nch = chunks_of(sq);
     int c0, c1, head, r0;
@@ -400,6 +470,34 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
           }
       }
 
+      // A group without numbers of a token that some row does not see must not meet
+      // that row's probability of 0: it counts nothing, and the rows that see the
+      // first such token get their NaN at the item's end.  (A warp has one such
+      // pair of blocks an item, its last: the rows of a block are at most 32 tokens
+      // apart and a warp's pairs 128.  The fence for the copies into this ring is
+      // the one at the item's end.)
+      if (SEV && hidden) {
+        uint2* at = reinterpret_cast<uint2*>(const_cast<uint8_t*>(pair) + lane / 16 * BB + kv_value_off(D) + kv_param_off(D) +
+                                             lane % 16 * (D / 8));
+        uint2 par[D / 64];
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          par[i] = at[i];
+          nan = nan || no_numbers<T>(par[i].x) || no_numbers<T>(par[i].y);
+        }
+        nan = nan && tok0 + lane > first_pos && tok0 + lane < sq.len;
+        if (__builtin_expect(__any_sync(0xffffffffu, nan), 0)) {
+#pragma unroll 1
+          for (int i = 0; i < D / 32 && nan; ++i) {
+            uint32_t* p = reinterpret_cast<uint32_t*>(at) + i;
+            if (no_numbers<T>(*p)) *p = 0u;
+          }
+          if (lane == 0) spoiled = 1;
+          __syncwarp();
+        }
+      }
+
       // Values: lane (g, t) takes channels g DV .. of the tokens of rows 2t,
       // 2t + 1 (and + 8).  Tokens past the end count nothing, whatever the
       // page holds.
@@ -516,6 +614,12 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
         part[MR * D + 2 * r + 1] = den;
       }
     }
+    if (SEV && CL && __builtin_expect(spoiled != 0, 0)) {
+      __syncthreads();
+      const Item it{b, head, r0, rows, c0, c1, nch};
+      spoil_item<T, D>(a, sq, it, spoiled_at, [&](int r) { return reinterpret_cast<float*>(smem) + r * OS; });
+      __syncthreads();
+    }
     if (CL) {
       // The pieces of the cluster's CTAs, in the order of the ranks.
       cluster_sync_all();
@@ -560,6 +664,7 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
     __syncwarp();
   }
   __syncthreads();
+  if (SEV && CL == 0 && __builtin_expect(spoiled != 0, 0)) spoil_items<T, D, NQ>(a, pref, spoiled_at);
   if (abort_sh) {
     // Copies in flight land in this CTA's ring: give them time.
     const uint64_t t0 = globaltimer();
@@ -682,10 +787,10 @@ Plan plan_of(int dim, int heads, int group, int max_q, int seqs, bool single, lo
   return p;
 }
 
-template <class T, int D, int NQ, int CL>
+template <class T, int D, int NQ, int CL, bool SEV>
 struct Kernel {
   static constexpr int ST = stages<NQ>(), smem = AW * ST * 2 * kv_block_bytes(D);
-  static constexpr auto fn = k_kv4_attention<T, D, NQ, ST, CL>;
+  static constexpr auto fn = k_kv4_attention<T, D, NQ, ST, CL, SEV>;
   static_assert(resident(D, NQ) * (smem + 12288) <= 233472, "the CTAs that the registers leave room for fit");
   static gptq_status ready() {
     static DeviceOnce attr;
@@ -696,9 +801,9 @@ struct Kernel {
   }
 };
 
-template <class T, int D>
+template <class T, int D, bool SEV>
 gptq_status attn_cluster(const AttnArgs& a, cudaStream_t s) {
-  using K = Kernel<T, D, 1, ACL>;
+  using K = Kernel<T, D, 1, ACL, SEV>;
   GQ_TRY(K::ready());
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.heads * ACL), (unsigned)a.seqs);
@@ -716,9 +821,9 @@ gptq_status attn_cluster(const AttnArgs& a, cudaStream_t s) {
   return GPTQ_OK;
 }
 
-template <class T, int D, int NQ>
+template <class T, int D, int NQ, bool SEV>
 gptq_status attn_launch(const AttnArgs& a, long long shares, cudaStream_t s) {
-  using K = Kernel<T, D, NQ, 0>;
+  using K = Kernel<T, D, NQ, 0, SEV>;
   GQ_TRY(K::ready());
   const int seqs = a.seqs;
   for (int b0 = 0; b0 < seqs; b0 += ASEQS) {
@@ -754,20 +859,24 @@ gptq_status attn_launch(const AttnArgs& a, long long shares, cudaStream_t s) {
   return GPTQ_OK;
 }
 
-template <class T, int D>
+template <class T, int D, bool SEV>
 gptq_status attn_rows(const AttnArgs& a, const Plan& p, cudaStream_t s) {
-  if (p.cluster) return attn_cluster<T, D>(a, s);
-  if (p.nq == 1) return attn_launch<T, D, 1>(a, p.shares, s);
-  if (p.nq == 2) return attn_launch<T, D, 2>(a, p.shares, s);
-  if (p.nq == 3) return attn_launch<T, D, D == 256 ? 2 : 3>(a, p.shares, s);
-  return attn_launch<T, D, D == 256 ? 2 : 4>(a, p.shares, s);
+  if (p.cluster) return attn_cluster<T, D, SEV>(a, s);
+  if (p.nq == 1) return attn_launch<T, D, 1, SEV>(a, p.shares, s);
+  if (p.nq == 2) return attn_launch<T, D, 2, SEV>(a, p.shares, s);
+  if (p.nq == 3) return attn_launch<T, D, D == 256 ? 2 : 3, SEV>(a, p.shares, s);
+  return attn_launch<T, D, D == 256 ? 2 : 4, SEV>(a, p.shares, s);
 }
 
-template <class T>
+template <class T, bool SEV>
 gptq_status attn_dim(int dim, const AttnArgs& a, const Plan& p, cudaStream_t s) {
-  if (dim == 64) return attn_rows<T, 64>(a, p, s);
-  if (dim == 128) return attn_rows<T, 128>(a, p, s);
-  return attn_rows<T, 256>(a, p, s);
+  if (dim == 64) return attn_rows<T, 64, SEV>(a, p, s);
+  if (dim == 128) return attn_rows<T, 128, SEV>(a, p, s);
+  return attn_rows<T, 256, SEV>(a, p, s);
+}
+template <class T>
+gptq_status attn_queries(int dim, const AttnArgs& a, const Plan& p, cudaStream_t s) {
+  return a.max_q > 1 ? attn_dim<T, true>(dim, a, p, s) : attn_dim<T, false>(dim, a, p, s);
 }
 
 }  // namespace
@@ -781,7 +890,7 @@ gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_
   const Plan p = plan_of(dim, a.heads, a.group, a.max_q, a.seqs, a.q_starts == nullptr,
                          (long long)a.table_stride * a.page_size);
   if (p.chunk) return kv4_chunk_run(dtype, dim, a, s);
-  return dtype == GPTQ_BF16 ? attn_dim<__nv_bfloat16>(dim, a, p, s) : attn_dim<__half>(dim, a, p, s);
+  return dtype == GPTQ_BF16 ? attn_queries<__nv_bfloat16>(dim, a, p, s) : attn_queries<__half>(dim, a, p, s);
 }
 
 }  // namespace gq

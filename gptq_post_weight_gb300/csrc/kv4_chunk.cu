@@ -172,6 +172,8 @@ __device__ __forceinline__ Pair pair_of(const AttnArgs& a, int b, int rb) {
   t.steps = (t.vis + kKeys<D> - 1) / kKeys<D>;
   return t;
 }
+// The first token that some of the rows does not see.
+__device__ __forceinline__ int open_end(const AttnArgs& a, const Pair& t) { return max(0, t.len - t.nq + t.r0 / a.group + 1); }
 // Units of a tile in the list: its steps (one that writes zeros if its rows
 // see nothing), and CSTART for its start and end.
 __device__ __forceinline__ int units_of(const Pair& t) { return t.rows > 0 ? max(t.steps, 1) + CSTART : 0; }
@@ -241,6 +243,54 @@ __device__ __forceinline__ Piece piece_at(const AttnArgs& a, int nblk, const lon
   return p;
 }
 
+constexpr size_t piece_floats(int dim);
+
+// A value that is no number must not meet the probability of 0 of a row that
+// does not see its token: it was decoded as 0, and the rows that do see it get
+// their NaN here, over what the CTA has written of each of its pieces.  By the
+// softmax warps (the others have given registers away), after the steps.  (The
+// share is worked out again, from what the compiler does not see through: kept
+// in registers for this, which no call with numbers in its cache comes to, it
+// cost the steps 2 % of their time.)
+template <class T, int D>
+__device__ __forceinline__ void spoil_pieces(const AttnArgs& a, int nblk, const volatile long long* prefix, int* first) {
+  uint32_t cta, ctas;
+  asm volatile("mov.u32 %0, %%ctaid.x;\n mov.u32 %1, %%nctaid.x;" : "=r"(cta), "=r"(ctas));
+  const long long* pref = const_cast<const long long*>(prefix);
+  const long long W = prefix[a.seqs * nblk] * a.heads, shares = min(W, (long long)ctas), uend = W * (cta + 1) / shares;
+#pragma unroll 1
+  for (long long u = W * cta / shares; u < uend;) {
+    const Piece pc = piece_at<D>(a, nblk, pref, u, uend);
+    u = pc.next;
+    if (pc.j1 == 0) continue;
+    if (threadIdx.x < D / 32) first[threadIdx.x] = INT_MAX;
+    asm volatile("bar.sync 3, 512;" ::: "memory");
+    const int end = min(pc.t.vis, pc.j1 * kKeys<D>);
+#pragma unroll 1
+    for (int t = max(open_end(a, pc.t), pc.j0 * kKeys<D>) + (int)threadIdx.x; t < end; t += 512) {
+      const uint32_t* par = value_params<D>(a, pc.b, pc.head, t);
+#pragma unroll 1
+      for (int i = 0; i < D / 32; ++i)
+        if (no_numbers<T>(par[i])) atomicMin(&first[i], t);
+    }
+    asm volatile("bar.sync 3, 512;" ::: "memory");
+    float* part = a.part + ((size_t)cta * 2 + (pc.j0 == 0 ? 1 : 0)) * piece_floats(D);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < pc.t.rows * (D / 8); i += 512) {
+      const int row = i / (D / 8), c = i % (D / 8) * 8, rr = pc.t.r0 + row, qi = rr / a.group;
+      if (pc.t.len - pc.t.nq + qi < first[c / 32]) continue;
+      if (pc.whole) {
+        T* dst = static_cast<T*>(a.out) + ((long long)(pc.t.q0 + qi) * a.heads * a.group + pc.head * a.group + rr % a.group) * D;
+        *reinterpret_cast<uint4*>(dst + c) = uint4{0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu};
+      } else {
+        float4* o = reinterpret_cast<float4*>(part + (size_t)row * D + c);
+        o[0] = o[1] = float4{NAN, NAN, NAN, NAN};
+      }
+    }
+    asm volatile("bar.sync 3, 512;" ::: "memory");
+  }
+}
+
 constexpr int rows_of(int dim) { return dim == 256 ? kRows<256> : kRows<128>; }
 constexpr size_t piece_floats(int dim) { return (size_t)rows_of(dim) * (dim + 2); }
 
@@ -261,6 +311,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
   __shared__ uint32_t tmem_base_sh;
   __shared__ long long pref[CLIST + 1], scratch[CTHREADS / 32];
   __shared__ int abort_sh;
+  __shared__ int spoiled, spoiled_at[D / 32];  // see spoil_pieces
   __shared__ float2 other[128];  // maximum and sum of tile B's half of the steps
   __shared__ float xmax[2][2][2][128];  // [turn][tile][half][row]: what a row's halves tell each other
   volatile int* abort = &abort_sh;
@@ -274,7 +325,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
       mbar_init(&sfull[i], 1), mbar_init(&pfull[i], 256);
     }
     for (int i = 0; i < S::kUnits; ++i) mbar_init(&rawfull[i], 1), mbar_init(&rawempty[i], 8);
-    abort_sh = 0;
+    abort_sh = 0, spoiled = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -533,6 +584,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
     for (long long u = ubeg; u < uend && ok;) {
       const Piece pc = piece_at<D>(a, nblk, pref, u, uend);
       u = pc.next;
+      const int open = open_end(a, pc.t) - tok;  // tokens from this thread's on that every row sees
 #pragma unroll 1
       for (int j = pc.j0; j < min(pc.j1, pc.t.steps); ++j, ++n) {
         const int st = n & 1;
@@ -546,7 +598,14 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
           uint32_t par = *reinterpret_cast<const uint32_t*>(from_par + q * S::kRaw);
           __syncwarp();
           if (lane == 0) mbar_arrive(&rawempty[q]);
-          if (q * S::kTokens >= seen) par = 0u;  // past what any row sees: no value, whatever is there
+          if (j * CK + q * S::kTokens >= open) {
+            if (q * S::kTokens >= seen) {
+              par = 0u;  // past what any row sees: no value, whatever is there
+            } else if (isv && no_numbers<T>(par)) {
+              par = 0u;
+              spoiled = 1;
+            }
+          }
           if (GR >= 4) {
             const bool two = (turn & 2) != 0;
             const uint4 c = codes;
@@ -747,6 +806,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
     }
     if (threadIdx.x == 0 && a.status != nullptr) atomicOr(a.status, 2u);
   }
+  if (__builtin_expect(spoiled != 0, 0) && warp < 16) spoil_pieces<T, D>(a, nblk, pref, spoiled_at);
   tc_fence_after();
   if (warp == 25)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base_sh), "r"(512u) : "memory");

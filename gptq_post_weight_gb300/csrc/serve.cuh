@@ -20,6 +20,7 @@ struct Elem<__nv_bfloat16> {
   using T2 = __nv_bfloat162;
   static constexpr uint32_t kMagic16 = 0x41804180u, kMask16 = 0x00780078u;
   static constexpr int kPos = 3;  // lowest of the top four mantissa bits
+  static constexpr uint32_t kExp = 0x7F80u;
   static __device__ __forceinline__ T2 make2(float a, float b) { return __floats2bfloat162_rn(a, b); }
   static __device__ __forceinline__ float2 to2(T2 v) { return __bfloat1622float2(v); }
   static __device__ __forceinline__ __nv_bfloat16 from(float a) { return __float2bfloat16_rn(a); }
@@ -30,6 +31,7 @@ struct Elem<__half> {
   using T2 = __half2;
   static constexpr uint32_t kMagic16 = 0x4C004C00u, kMask16 = 0x03C003C0u;
   static constexpr int kPos = 6;
+  static constexpr uint32_t kExp = 0x7C00u;
   static __device__ __forceinline__ T2 make2(float a, float b) { return __floats2half2_rn(a, b); }
   static __device__ __forceinline__ float2 to2(T2 v) { return __half22float2(v); }
   static __device__ __forceinline__ __half from(float a) { return __float2half_rn(a); }
@@ -68,6 +70,12 @@ template <class T>
 __device__ __forceinline__ typename Elem<T>::T2 code16(uint32_t w, int i, uint32_t up) {
   if (i != 0) return code16<T>(w, i);
   return from_bits2<typename Elem<T>::T2>(and_or<Elem<T>::kMask16>(w * up, Elem<T>::kMagic16));
+}
+
+// Whether a group of the cache (s and z as a pair) holds no numbers.
+template <class T>
+__device__ __forceinline__ bool no_numbers(uint32_t par) {
+  return (~par & Elem<T>::kExp) == 0u || (~par & (Elem<T>::kExp << 16)) == 0u;
 }
 
 // 16 x 8 x 16 product with f32 accumulation.
@@ -232,5 +240,16 @@ constexpr int KV_BLOCK = 16;
 __host__ __device__ constexpr int kv_block_bytes(int dim) { return 20 * dim; }
 __host__ __device__ constexpr int kv_param_off(int dim) { return 8 * dim; }
 __host__ __device__ constexpr int kv_value_off(int dim) { return 10 * dim; }
+
+// (s, z) pairs of the value of token t of sequence b: what the copies of the
+// attention kernels read (an entry of the table outside the pool: page 0).
+template <int D>
+__device__ __forceinline__ const uint32_t* value_params(const AttnArgs& a, int b, int head, int t) {
+  const unsigned e = (unsigned)a.table[(long long)b * a.table_stride + t / a.page_size];
+  const long long page = e < (unsigned long long)a.pages ? (long long)e : 0;
+  const int bpp = a.page_size / KV_BLOCK;
+  const uint8_t* blk = a.cache + ((page * a.heads + head) * bpp + t / KV_BLOCK % bpp) * (long long)kv_block_bytes(D);
+  return reinterpret_cast<const uint32_t*>(blk + kv_value_off(D) + kv_param_off(D) + t % KV_BLOCK * (D / 8));
+}
 
 }  // namespace gq

@@ -492,10 +492,9 @@ gptq_status gptq_kv4_read(int dtype, const uint8_t* cache, long long pages, int 
  *            is NULL; max_len: table_stride * page_size), which is 0 where the
  *            call needs none (ws may then be NULL) and never more than
  *            gptq_kv4_attention_workspace_bytes(dim, group, max_q).
- * The values (V) of one sequence's keys must be finite where any of its queries
- * sees them: one that is NaN also reaches queries before it whose rows share a
- * tile with one that sees it.  Keys (K) may hold anything where a query does
- * not see them, and what the pages hold past kv_lens is never used.
+ * What a query does not see may hold anything: keys or values that are NaN reach
+ * the queries that see them only (a value's group of 32 channels), and what the
+ * pages hold past kv_lens is never used.
  */
 size_t gptq_kv4_attention_workspace_bytes(int dim, int group, int max_q);
 size_t gptq_kv4_attention_call_bytes(int dim, int heads, int group, int max_q, int seqs, int single,

@@ -280,3 +280,61 @@ def test_prompt_chunks_of_many_sequences_that_see_nothing(lib, group, nq, dim):
     want = serve.attention(q, kk, vv, [90, 33], group, dim ** -0.5, [nq, nq])
     tol = kv.tolerance(q, kk, vv, [90, 33], group, dim ** -0.5, [nq, nq], "bf16", want)
     assert (np.abs(got[[seqs // 2, seqs - 1]].reshape(want.shape) - want) <= tol).all()
+
+
+def spoil(r, cache, table, ks, vs, lens, page, dtype, places):
+    """Writes a NaN or an infinity into one group of a value at each (sequence,
+    token) of `places`; the oracle's copy of the values follows."""
+    from gptq_post_weight_gb300 import _lib
+
+    heads, dim = vs[0].shape[1:]
+    slots, k, v = [], [], []
+    for i, (b, p) in enumerate(places):
+        x = vs[b][p].copy()
+        x[np.isnan(x)] = 1.0
+        x[r.integers(heads), r.integers(dim)] = [np.nan, np.inf, -np.inf][i % 3]
+        slots.append(int(table[b, p // page]) * page + p % page)
+        k.append(ks[b][p])
+        v.append(x)
+    k, v = np.stack(k), np.stack(v)
+    _lib.kv4_write(cache, kv.dev(k, kv.DT[dtype]), kv.dev(v, kv.DT[dtype]), torch.tensor(slots, device="cuda"), page)
+    k, v = serve.round_trip(k, dtype), serve.round_trip(v, dtype)
+    for (b, p), kk, x in zip(places, k, v):
+        ks[b][p], vs[b][p] = kk, x
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("heads,group,q_lens,lens", [
+    (1, 1, [6], [40]),                                  # clusters
+    (2, 2, [4, 1], [70, 33]),                           # clusters, two sequences
+    (2, 4, [5, 3, 1, 2] * 5, [300, 40, 7, 129] * 5),    # shares, several items each
+    (1, 4, [8], [9000]),                                # an item cut into pieces
+    (2, 4, [20, 9, 1] * 4, [200, 60, 30] * 4),          # tcgen05, the tiles in turns
+    (1, 2, [60], [12000]),                              # the same, cut
+    (2, 2, [150, 3, 128] * 3, [400, 20, 128] * 3),      # tcgen05
+    (1, 4, [130], [9000]),                              # the same, cut
+])
+def test_values_that_are_no_numbers_reach_only_queries_that_see_them(lib, heads, group, q_lens, lens, dim, dtype):
+    # Values spoiled at places that the last queries of every other sequence see
+    # and its first ones do not, at one that all see, and at its very last.
+    r = np.random.default_rng(62)
+    page = 16
+    cache, table, lens_d, ks, vs = kv.context(r, lens, heads, dim, page, dtype)
+    places = []
+    for b in range(0, len(lens), 2):
+        first = lens[b] - q_lens[b]  # the first token that not every query sees
+        some = {lens[b] - 1, first + int(r.integers(q_lens[b])), first + int(r.integers(q_lens[b]))}
+        if b % 4 == 2 and first > 0:
+            some.add(int(r.integers(first)))
+        places += [(b, p) for p in sorted(some)]
+    spoil(r, cache, table.cpu(), ks, vs, lens, page, dtype, places)
+    q = serve.round_to(r.standard_normal((sum(q_lens), heads * group, dim)), dtype)
+    got = kv.host(kv.attend(q, cache, table, lens_d, page, dtype, q_lens))
+    with np.errstate(invalid="ignore"):
+        want = serve.attention(q, ks, vs, lens, group, dim ** -0.5, q_lens)
+    clean = [np.where(np.isnan(v), 0, v) for v in vs]
+    tol = kv.tolerance(q, ks, clean, lens, group, dim ** -0.5, q_lens, dtype, np.nan_to_num(want))
+    assert np.isnan(want).any() and np.isfinite(want).any()
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+    assert (np.abs(got - want) <= tol)[np.isfinite(want)].all()
