@@ -14,11 +14,11 @@
 // on the lengths alone: results do not change from run to run.
 //
 // Measured: 48 sequences of up to 16384 tokens, 8 key heads of 128 with 8
-// query heads each, one new token: 127 us, 4.3 TB/s of cache; the vector ALU
+// query heads each, one new token: 129 us, 4.2 TB/s of cache; the vector ALU
 // (codes to values: two instructions a pair, at half rate) is then 62 % busy
 // and the memory 64 %.  16 sequences of 5 drafted tokens over up to 4001
-// tokens, 20 rows of 64: 26.5 us, three CTAs an SM waiting on their own
-// chains of products and shuffles.  One token over 1000: 5.4 us.
+// tokens, 20 rows of 64: 27.3 us, three CTAs an SM waiting on their own
+// chains of products and shuffles.  One token over 1000: 5.2 us.
 //
 // Rows of a block are (query, head of the key head's group) pairs, so that a
 // key is decoded once for every head that shares it.  Each of a CTA's four
@@ -754,7 +754,8 @@ constexpr int kClusterTokens = 8192;
 // 128 rows 80 and 263; one sequence of 8000, 32 rows 27 and 23, 48 rows 28 and
 // 28, 128 rows 30 and 44; of 1000, 48 rows 17 and 13 (its start costs more).
 // Heads of 256, 112 rows: 48 sequences to 4000, 217 and 633; one of 4000, 33
-// and 34.
+// and 34.  (The rows alone decide: for one short sequence of 33 to 48 rows this
+// kernel would be the faster by those 4 us.)
 bool kv4_is_chunk(int dim, int group, int max_q, bool single) {
   const long long rows = (long long)max_q * group;
   return !single && rows > 32 && rows <= (dim == 256 ? 128 : 256) * 512;

@@ -22,7 +22,7 @@
 // unnormalised output (f32) in the workspace, and k_kv4_chunk_join adds the
 // pieces in the order of the list.
 // Measured: 2 sequences of 2048 queries of 32 heads (8 key heads of 128),
-// contexts to 8192: 330 us, 0.91 PFLOP/s, the tensor cores 46 % busy.  A step
+// contexts to 8192: 331 us, 0.91 PFLOP/s, the tensor cores 46 % busy.  A step
 // of a tile is a chain of 3650 cycles (maximum 440, exchange 180, exponentials
 // 1400, products 1250 and their waits), of which two tiles overlap; tensor
 // memory has no room for a third.
@@ -297,7 +297,7 @@ constexpr size_t piece_floats(int dim) { return (size_t)rows_of(dim) * (dim + 2)
 // TURNS: no sequence has more than 128 rows; the two tiles hold the same rows
 // and take turns at the steps, so that two chains run for them too, and join
 // at the end of a piece (112 rows of 128, 8 sequences to 32000: 168 -> 144 us;
-// of 64, 48 sequences: 674 -> 525; decoding is then the longer part).
+// of 64, 48 sequences: 674 -> 523; decoding is then the longer part).
 template <class T, int D, bool TURNS>
 __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk, WaitCfg wc) {
   using T2 = typename Elem<T>::T2;

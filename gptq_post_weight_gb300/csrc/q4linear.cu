@@ -22,7 +22,7 @@
 // ldmatrix: its 8 x 16-byte matrices are eight rows of one group's codes,
 // and hand lane (row, t) word t of it (one and two tokens: see k_q4_few).
 // The slice of x sits in shared memory in the order in which the nibbles come
-// out.  Measured: one token, 4096 x 4096 6.7 us, 5120 x 17408 17.0 us (2.8
+// out.  Measured: one token, 4096 x 4096 8.0 us, 5120 x 17408 18.4 us (2.6
 // TB/s of codes and rungs; 6 000 of 30 000 cycles load ladders, rungs and x,
 // 4 000 join the cluster, and a box takes a warp 1400, shared by the ALU's
 // shifts and masks, the products and the shared-memory reads of twelve warps).
@@ -107,7 +107,7 @@ __device__ __forceinline__ void finish8(const LinearArgs& a, int tok, int r, boo
     if (a.bias != nullptr) add8<T>(v, *reinterpret_cast<const uint4*>(static_cast<const T*>(a.bias) + r));
     if (a.act != GPTQ_ACT_NONE) {
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i) {  // (one at a time 20.5 us for the case of k_q4_mid, eight 20.1, four 19.9)
+      for (int i = 0; i < 2; ++i) {  // (the case of k_q4_mid on one box: one at a time 20.5 us, eight 20.1, four 19.9)
         float x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] = activate(v[k], a.act);
@@ -762,7 +762,7 @@ struct Dequant {
 
 // ---- up to some hundreds of tokens: one SM a tile, the columns split over a cluster
 
-// Measured: 45 tokens, 14336 x 4096, GELU: 22.8 us, 112 tiles on 152 SMs.  A
+// Measured: 45 tokens, 14336 x 4096, GELU: 22.5 us, 112 tiles on 152 SMs.  A
 // stage of 64 columns takes 575 cycles, all of them decoding (the vector ALU
 // and the multiply-add pipe half busy each, 0.7 instructions a cycle); the
 // tensor cores are 15 % busy.
@@ -904,9 +904,9 @@ __global__ void __launch_bounds__(640, 1)
 
 // ---- many tokens: pairs of SMs, persistent
 
-// Measured: 3840 tokens, 5120 x 17408: 366 us, 1.87 PFLOP/s (95 % of the plain
-// library product's burst rate); 4096 tokens: 429, as the fifth round of tiles
-// is a fifth full (470 when the power limit is reached).  A stage of 64
+// Measured: 3840 tokens, 5120 x 17408: 371 us, 1.84 PFLOP/s (94 % of the plain
+// library product's burst rate); 4096 tokens: 423, as the fifth round of tiles
+// is a fifth full (486 when the power limit is reached).  A stage of 64
 // columns takes 540 cycles, its products 512.
 
 constexpr int PNS = 3;  // boxes of codes
@@ -1344,7 +1344,7 @@ gptq_status many_launch(const LinearArgs& a, cudaStream_t s) {
 
 template <class T>
 gptq_status linear_t(const LinearArgs& a, cudaStream_t s) {
-  // Up to 8 tokens the few-token kernel is the faster (5120 x 17408: 17 / 26
+  // Up to 8 tokens the few-token kernel is the faster (5120 x 17408: 18 / 27
   // us for 1 / 8 tokens against 28); at 16 its blocks of x leave one CTA a SM
   // (58 us against 29).
   if (a.tokens <= 8) return few_tokens<T>(a, s);
