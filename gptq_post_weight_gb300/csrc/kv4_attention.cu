@@ -782,8 +782,11 @@ Plan plan_of(int dim, int heads, int group, int max_q, int seqs, bool single, lo
   if (p.cluster) return p;
   // No more shares than the longest contexts the table allows have chunks.
   const long long blocks = (rows + 8 * p.nq - 1) / (8 * p.nq);
-  const long long most = (long long)std::min(seqs, ASEQS) * heads * blocks * ((max_len + ACH - 1) / ACH);
-  p.shares = std::min(std::min(resident_ctas, (long long)kShares), most);
+  // (A step at a time: at the arguments' limits the product passes 64 bits.)
+  p.shares = std::min(resident_ctas, (long long)kShares);
+  long long most = std::min((long long)std::min(seqs, ASEQS) * heads, p.shares);
+  most = std::min(most * blocks, p.shares);
+  p.shares = std::min(most * ((max_len + ACH - 1) / ACH), p.shares);
   p.ws = kCutBytes + (size_t)p.shares * 2 * 8 * p.nq * (dim + 2) * 4;
   return p;
 }
