@@ -107,7 +107,7 @@ __device__ __forceinline__ void finish8(const LinearArgs& a, int tok, int r, boo
     if (a.bias != nullptr) add8<T>(v, *reinterpret_cast<const uint4*>(static_cast<const T*>(a.bias) + r));
     if (a.act != GPTQ_ACT_NONE) {
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i) {  // (the case of k_q4_mid on one box: one at a time 20.5 us, eight 20.1, four 19.9)
+      for (int i = 0; i < 2; ++i) {  // (the case of k_q4_mid, side by side: one at a time 20.5 us, eight 20.1, four 19.9)
         float x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] = activate(v[k], a.act);

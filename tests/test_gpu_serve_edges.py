@@ -338,3 +338,24 @@ def test_values_that_are_no_numbers_reach_only_queries_that_see_them(lib, heads,
     assert np.isnan(want).any() and np.isfinite(want).any()
     np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
     assert (np.abs(got - want) <= tol)[np.isfinite(want)].all()
+
+
+@pytest.mark.parametrize("page", [48, 80, 4096])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,lens", [(None, [47, 48, 49, 500, 1]), ([3, 1, 5], [50, 161, 300]),
+                                         ([40, 9], [400, 97]), ([200, 1, 70], [700, 33, 81])])
+def test_pages_that_are_no_power_of_two_or_large(lib, q_lens, lens, dim, page):
+    kv.one(lens, 2, 2, dim, page, "bf16", q_lens, seed=71)
+
+
+@pytest.mark.parametrize("nq", [1, 4, 30, 150])
+def test_queries_in_strided_and_transposed_layouts(lib, nq):
+    # A slice of a wider projection, and heads outermost.
+    r = np.random.default_rng(72)
+    cache, table, lens, ks, vs = kv.context(r, [400, 160], 2, 128, 32, "f16")
+    q = kv.dev(serve.round_to(r.standard_normal((2 * nq, 8, 128)), "f16"), torch.float16)
+    plain = kv.attend(q, cache, table, lens, 32, "f16", [nq, nq])
+    wide = torch.full((2 * nq, 13, 136), float("nan"), dtype=torch.float16, device="cuda")
+    wide[:, 3:11, :128] = q
+    for view in (wide[:, 3:11, :128], q.transpose(0, 1).contiguous().transpose(0, 1)):
+        assert torch.equal(plain, kv.attend(view, cache, table, lens, 32, "f16", [nq, nq]))
