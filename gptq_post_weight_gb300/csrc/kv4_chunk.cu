@@ -139,6 +139,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
+// 16 bytes of shared memory in one load.
+__device__ __forceinline__ uint4 load128(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem_u32(p))
+               : "memory");
+  return v;
+}
+
 // Byte offset of 16-byte piece p (0 .. 7) of row r in a swizzled tile.
 __device__ __forceinline__ uint32_t swz(int r, int p) { return (uint32_t)(r * 128 + ((p ^ (r & 7)) * 16)); }
 
@@ -594,10 +604,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
 #pragma unroll 1
         for (int q = 0; q < S::kUnits; ++q) {
           if (!(ok = wait_bar_warp(&rawfull[q], (uint32_t)n & 1u, abort, wc.ns))) break;
-          uint4 codes = *reinterpret_cast<const uint4*>(from_codes + q * S::kRaw);
+          uint4 codes = load128(from_codes + q * S::kRaw);
           uint32_t par = *reinterpret_cast<const uint32_t*>(from_par + q * S::kRaw);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&rawempty[q]);
           if (j * CK + q * S::kTokens >= open) {
             if (q * S::kTokens >= seen) {
               par = 0u;  // past what any row sees: no value, whatever is there
@@ -629,6 +637,14 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
             o.z = bits2(__hfma2(code16<T>(w[e], 2), s2, z2));
             o.w = bits2(__hfma2(code16<T>(w[e], 3), s2, z2));
             *reinterpret_cast<uint4*>(dst + off[e]) = o;
+            // Not before this store, which needs both loads: an arrival does not wait
+            // for loads in flight, and the next copy overtook them (one unit of a warp
+            // in some 10 million held the next step's tokens).  After all four stores
+            // it costs 1 to 2 % more.
+            if (e == 0) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&rawempty[q]);
+            }
           }
         }
         if (!ok) break;

@@ -359,3 +359,31 @@ def test_queries_in_strided_and_transposed_layouts(lib, nq):
     wide[:, 3:11, :128] = q
     for view in (wide[:, 3:11, :128], q.transpose(0, 1).contiguous().transpose(0, 1)):
         assert torch.equal(plain, kv.attend(view, cache, table, lens, 32, "f16", [nq, nq]))
+
+
+@pytest.mark.parametrize("dim,seqs,nq,ln", [(64, 2, 2048, 8000), (128, 2, 2048, 8192), (256, 2, 500, 4000), (64, 24, 30, 9000),
+                                            (128, 24, 30, 9000), (128, 16, 5, 4001), (64, 48, 1, 9000)])
+def test_same_bits_over_many_launches(lib, dim, seqs, nq, ln):
+    # Enough work for every SM and enough launches to meet a rare order of
+    # copies, decoding and products.
+    from gptq_post_weight_gb300 import _lib
+
+    g = torch.Generator(device="cuda").manual_seed(81)
+    heads, group, page = 8, 4, 64
+    per = -(-ln // page)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    cache = _lib.kv4_cache(seqs * per, heads, dim, page)
+    table = torch.randperm(seqs * per, generator=g, device="cuda").to(torch.int32).view(seqs, per)
+    for b in range(seqs):
+        slots = (table[b].long().unsqueeze(1) * page + torch.arange(page, device="cuda")).flatten()
+        _lib.kv4_write(cache, draw(per * page, heads, dim), draw(per * page, heads, dim), slots, page)
+    lens = torch.randint(nq, ln + 1, (seqs,), generator=g, device="cuda", dtype=torch.int32)
+    lens[0] = ln
+    starts = torch.arange(0, seqs * nq + 1, nq, dtype=torch.int32, device="cuda")
+    q = draw(seqs * nq, heads * group, dim)
+    first = _lib.kv4_attention(q, cache, table, lens, page, q_starts=starts, max_q=nq)
+    same = torch.ones((), dtype=torch.bool, device="cuda")
+    for _ in range(80):
+        same &= (_lib.kv4_attention(q, cache, table, lens, page, q_starts=starts, max_q=nq) == first).all()
+    _lib.serve_check()
+    assert same
