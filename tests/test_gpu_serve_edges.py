@@ -387,3 +387,23 @@ def test_same_bits_over_many_launches(lib, dim, seqs, nq, ln):
         same &= (_lib.kv4_attention(q, cache, table, lens, page, q_starts=starts, max_q=nq) == first).all()
     _lib.serve_check()
     assert same
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens,rows,n", [(1, 5120, 17408), (2, 5120, 17408), (4, 4096, 14336), (8, 5120, 17408),
+                                           (45, 14336, 4096), (300, 4096, 4096), (1500, 4099, 1056)])
+def test_same_bits_of_the_product_over_many_launches(lib, tokens, rows, n, dtype):
+    import test_gpu_linear as lin
+    from gptq_post_weight_gb300 import _lib
+
+    g = torch.Generator(device="cuda").manual_seed(82)
+    x = torch.randn(tokens, n, generator=g, device="cuda").to(lin.DT[dtype])
+    nib = torch.randint(0, 256, (rows * n // 2,), generator=g, device="cuda", dtype=torch.uint8)
+    rungs = torch.randint(0, 32, (rows * n // 32,), generator=g, device="cuda", dtype=torch.uint8)
+    tab = torch.rand(rows, 32, generator=g, device="cuda") * 0.01
+    first = _lib.q4tp_linear(x, nib, rungs, tab)
+    same = torch.ones((), dtype=torch.bool, device="cuda")
+    for _ in range(300):
+        same &= (_lib.q4tp_linear(x, nib, rungs, tab) == first).all()
+    _lib.serve_check()
+    assert same
