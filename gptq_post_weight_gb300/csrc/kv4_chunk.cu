@@ -22,7 +22,7 @@
 // unnormalised output (f32) in the workspace, and k_kv4_chunk_join adds the
 // pieces in the order of the list.
 // Measured: 2 sequences of 2048 queries of 32 heads (8 key heads of 128),
-// contexts to 8192: 331 us, 0.91 PFLOP/s, the tensor cores 46 % busy.  A step
+// contexts to 8192: 335 us, 0.90 PFLOP/s, the tensor cores 46 % busy.  A step
 // of a tile is a chain of 3650 cycles (maximum 440, exchange 180, exponentials
 // 1400, products 1250 and their waits), of which two tiles overlap; tensor
 // memory has no room for a third.
