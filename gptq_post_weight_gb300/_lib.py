@@ -8,6 +8,7 @@ no fallback: without the built library every call fails loudly.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -48,10 +49,19 @@ SIGNATURES = {
     "gptq_gram_workspace_bytes": (_S, [_I]),
     "gptq_gram_add": (_I, [_P, _I, _P, _I, _P, _S, _P]),
     "gptq_q4tp_linear": (_I, [_I, _P, _L, _I, _P, _P, _P, _I, _I, _P, _I, _P, _L, _P, _L, _P, _P]),
+    "gptq_q4tp_gated": (_I, [_I, _P, _L, _I, _P, _P, _P, _I, _I, _P, _I, _P, _L, _P, _P]),
     "gptq_kv4_write": (_I, [_I, _P, _L, _I, _I, _I, _P, _P, _L, _L, _L, _L, _P, _I, _P]),
+    "gptq_rotary": (_I, [_I, _P, _L, _L, _I, _I, _I, _I, _I, _P, _P, _F, _P, _L, _L, _P]),
+    "gptq_kv4_write_rotary": (_I, [_I, _P, _L, _I, _I, _I, _P, _L, _L, _I, _P, _P, _L, _L, _L, _L, _P, _I, _I, _I, _P, _P,
+                                   _F, _P, _L, _L, _P]),
     "gptq_kv4_read": (_I, [_I, _P, _L, _I, _I, _I, _P, _I, _P, _P, _P]),
     "gptq_kv4_attention_workspace_bytes": (_S, [_I, _I, _I]),
     "gptq_kv4_attention_call_bytes": (_S, [_I, _I, _I, _I, _I, _I, _L]),
+    "gptq_kv4_attention_lse": (_I, [_I, _P, _L, _L, _I, _P, _L, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _F, _P, _P, _P,
+                                    _S, _P, _P]),
+    "gptq_kv4_attention_weights": (_I, [_I, _P, _L, _L, _I, _P, _P, _L, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _F, _P,
+                                        _P, _P]),
+    "gptq_kv4_evict": (_I, [_P, _L, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P]),
     "gptq_kv4_attention": (_I, [_I, _P, _L, _L, _I, _P, _L, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _F, _P, _P,
                                 _S, _P, _P]),
     "gptq_launch_count": (ctypes.c_longlong, []),
@@ -730,7 +740,7 @@ def _rows_of(t, name, tokens, rows, like):
         raise ValueError(f"{name} must have dense rows that do not overlap, got strides {st}")
 
 
-def _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out):
+def _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out, last=True):
     import torch
 
     _dtype16(x, "x")
@@ -758,7 +768,8 @@ def _refuse_linear(x, nibbles, rungs, tab, bias, act, residual, out):
     if out is not None:
         _rows_of(out, "out", tokens, rows, x)
     _no_gradient(x=x, bias=bias, residual=residual)
-    _here(x, "x")
+    if last:
+        _here(x, "x")
 
 
 def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, out=None, stream=None):
@@ -816,6 +827,64 @@ def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, ou
     return out
 
 
+def _refuse_gated(x, nibbles, rungs, tab, bias, act, out):
+    _refuse_linear(x, nibbles, rungs, tab, bias, act, None, None, last=False)
+    if tab.shape[0] == 0 or tab.shape[0] % 2:
+        raise ValueError(f"tab must have the gate's rows and as many of the up projection, got {tab.shape[0]}")
+    if out is not None:
+        _rows_of(out, "out", x.shape[0], tab.shape[0] // 2, x)
+    _here(x, "x")
+
+
+def q4tp_gated(x, nibbles, rungs, tab, bias=None, act="silu", out=None, stream=None):
+    """act(x Wg^T + bg) * (x Wu^T + bu), the first half of a gated feed-forward
+    block, in one launch.  W [2 * inner, n] in q4tp form holds the gate's rows and
+    then the up projection's, as quantize_group returns them for the two matrices
+    one above the other; bias [2 * inner].  x [tokens, n] and the result [tokens,
+    inner] as in q4tp_linear.  `out` overlaps no input."""
+    sv = _serve or _serving()
+    try:
+        xt, xs, u8 = x.dtype, x.shape, sv["u8"]
+        dt, dev = sv["dtypes"][xt], x.get_device()
+        tokens, n = xs
+        rows = tab.shape[0]
+        inner = rows // 2
+        code = ACTIVATIONS[act]
+        st = x.stride()
+        ldx = st[0] if tokens > 1 else n
+        fine = (dev >= 0 and dev == sv["current"]() and n > 0 and n % 32 == 0 and st[1] == 1 and ldx % 8 == 0
+                and ldx >= n and not x.requires_grad
+                and tab.dtype is sv["f32"] and tab.shape == (rows, 32) and tab.is_contiguous()
+                and tab.get_device() == dev and rows > 0 and rows % 2 == 0
+                and nibbles.dtype is u8 and nibbles.numel() == rows * n // 2 and nibbles.is_contiguous()
+                and nibbles.get_device() == dev
+                and rungs.dtype is u8 and rungs.numel() == rows * n // 32 and rungs.is_contiguous()
+                and rungs.get_device() == dev)
+        bp = None
+        if bias is not None:
+            fine = (fine and bias.dtype is xt and bias.numel() == rows and bias.is_contiguous()
+                    and bias.get_device() == dev and not bias.requires_grad)
+            bp = bias.data_ptr()
+        ldy = inner
+        if out is not None:
+            st = out.stride()
+            ldy = st[0] if tokens > 1 else inner
+            fine = (fine and out.dtype is xt and out.shape == (tokens, inner) and (inner == 1 or st[1] == 1)
+                    and ldy >= inner and out.get_device() == dev)
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _refuse_gated(x, nibbles, rungs, tab, bias, act, out)
+    if out is None:
+        out = (sv["empty"] if stream is None else _empty(sv, stream))((tokens, inner), dtype=xt, device=x.device)
+    status = _lib.gptq_q4tp_gated(dt, x.data_ptr(), ldx, tokens, nibbles.data_ptr(), rungs.data_ptr(), tab.data_ptr(),
+                                  inner, n, bp, code, out.data_ptr(), ldy,
+                                  (_serve_words.get(dev) or (0, _serve_word(dev)))[1], _raw_stream(sv, stream, dev))
+    if status:
+        raise GptqError("gptq_q4tp_gated", status)
+    return out
+
+
 def _cache(cache, dim, page_size):
     """pages, heads of a cache pool after checking it against dim and page_size."""
     import torch
@@ -840,7 +909,7 @@ def kv4_cache(pages, heads, dim, page_size, device="cuda"):
     return cache
 
 
-def _refuse_write(cache, k, v, slots, page_size):
+def _refuse_write(cache, k, v, slots, page_size, last=True):
     import torch
 
     _dtype16(k, "k")
@@ -855,7 +924,8 @@ def _refuse_write(cache, k, v, slots, page_size):
     _strided(k, "k", k.shape, k)
     _strided(v, "v", k.shape, k)
     _need(slots, "slots", dtype=torch.int64, numel=tokens, device=k.device)
-    _here(k, "k")
+    if last:
+        _here(k, "k")
 
 
 def kv4_write(cache, k, v, slots, page_size, stream=None):
@@ -890,6 +960,199 @@ def kv4_write(cache, k, v, slots, page_size, stream=None):
     if code:
         raise GptqError("gptq_kv4_write", code)
     return cache
+
+
+def rotary_frequencies(rot, base=10000.0, scaling="none", factor=1.0, length=8192, low=1.0, high=4.0):
+    """Radians a position of the rot / 2 pairs, base ** (-2 i / rot), as floats.
+    scaling, for contexts `factor` times as long as those trained on: "linear"
+    divides every frequency by factor; "base" raises the base to base * factor **
+    (rot / (rot - 2)), which divides the last frequency by factor and leaves the first; "ramp"
+    divides those that make less than `low` turns in `length` positions, leaves
+    those that make more than `high`, and goes from one to the other between."""
+    if rot <= 0 or rot % 2:
+        raise ValueError(f"rot must be a positive even number, got {rot}")
+    if not (base > 0 and factor > 0):
+        raise ValueError(f"base and factor must be positive, got {base} and {factor}")
+    if scaling not in ("none", "linear", "base", "ramp"):
+        raise ValueError(f"scaling must be one of none, linear, base, ramp, got {scaling!r}")
+    if scaling == "base":
+        if rot < 4:
+            raise ValueError(f"scaling by the base needs rot of 4 and more, got {rot}")
+        base = base * factor ** (rot / (rot - 2))
+    f = [base ** (-2 * i / rot) for i in range(rot // 2)]
+    if scaling == "linear":
+        f = [v / factor for v in f]
+    elif scaling == "ramp":
+        if not (high > low and length > 0):
+            raise ValueError(f"ramp needs high above low and a positive length, got {high}, {low} and {length}")
+        w = [min(max((length * v / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for v in f]
+        f = [v * (a + (1 - a) / factor) for v, a in zip(f, w)]
+    return f
+
+
+def rotary_turns(frequencies, device="cuda"):
+    """The form of frequencies (radians a position) that the rotary calls take:
+    i64, 2^64ths of a turn a position, modulo one turn."""
+    import torch
+
+    f = [float(v) for v in frequencies]
+    if not f or not all(math.isfinite(v) for v in f):
+        raise ValueError("frequencies must be finite numbers, at least one")
+    t = [(round(v / (2 * math.pi) * 2 ** 64) + 2 ** 63) % 2 ** 64 - 2 ** 63 for v in f]
+    return torch.tensor(t, dtype=torch.int64, device=device)
+
+
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _refuse_turns(positions, turns, layout, gain, tokens, dim, device):
+    import torch
+
+    _need(positions, "positions", dtype=torch.int64, numel=tokens, device=device)
+    _need(turns, "turns", dtype=torch.int64, device=device)
+    rot = 2 * turns.numel()
+    if rot == 0 or rot > dim or rot % 16:
+        raise ValueError(f"turns must have a multiple of 8 elements up to {dim // 2}, got {turns.numel()}")
+    if layout not in ROTARY_LAYOUTS:
+        raise ValueError(f"layout must be one of {', '.join(ROTARY_LAYOUTS)}, got {layout!r}")
+    if not math.isfinite(gain):
+        raise ValueError(f"gain must be finite, got {gain}")
+
+
+def _heads_out(out, name, x):
+    """Raise ValueError unless `out` can take what `x` [tokens, heads, dim] becomes."""
+    _strided(out, name, x.shape, x)
+    tokens, heads, dim = x.shape
+    ts, hs, _ = out.stride()
+    # Rows that do not overlap: heads inside a token's stride, or tokens inside a head's.
+    if out.numel() and ((heads > 1 and hs < dim) or (tokens > 1 and ts < dim) or (
+            tokens > 1 and heads > 1 and ts < (heads - 1) * hs + dim and hs < (tokens - 1) * ts + dim)):
+        raise ValueError(f"{name} must have rows that do not overlap, got strides {out.stride()}")
+    if out.data_ptr() == x.data_ptr() and out.numel() and any(
+            a != b and n > 1 for a, b, n in zip(out.stride(), x.stride(), x.shape)):
+        raise ValueError(f"{name} is the input with other strides: {out.stride()}, {x.stride()}")
+
+
+def _refuse_rotary(x, positions, turns, layout, gain, out):
+    _dtype16(x, "x")
+    if x.dim() != 3:
+        raise ValueError(f"x must be 3-D [tokens, heads, dim], got shape {tuple(x.shape)}")
+    tokens, heads, dim = x.shape
+    if heads == 0 or dim == 0 or dim % 16 or dim > 1024:
+        raise ValueError(f"x must have heads of a multiple of 16 channels, at most 1024, got shape {tuple(x.shape)}")
+    _strided(x, "x", x.shape, x)
+    _refuse_turns(positions, turns, layout, gain, tokens, dim, x.device)
+    if out is not None:
+        _heads_out(out, "out", x)
+    _no_gradient(x=x)
+    _here(x, "x")
+
+
+def rotary(x, positions, turns, layout="half", gain=1.0, out=None, stream=None):
+    """x [tokens, heads, dim] (bf16 or f16, strided views allowed) turned to
+    its positions [tokens] i64: pair i of a head's first 2 * len(turns) channels
+    by positions * turns[i] (see rotary_turns), times gain; the other channels
+    stay.  layout "half": pair i is channels (i, i + len(turns)); "interleaved":
+    (2 i, 2 i + 1).  `out` may be x itself, else overlaps no input."""
+    sv = _serve or _serving()
+    try:
+        xt, dev, i64 = x.dtype, x.get_device(), sv["i64"]
+        dt = sv["dtypes"][xt]
+        tokens, heads, dim = x.shape
+        ts, hs, x1 = x.stride()
+        rot = 2 * turns.numel()
+        code = ROTARY_LAYOUTS[layout]
+        fine = (dev >= 0 and dev == sv["current"]() and x1 == 1 and tokens > 1 and heads > 1 and 0 < dim <= 1024
+                and dim % 16 == 0 and (ts | hs) % 8 == 0 and not x.requires_grad
+                and positions.dtype is i64 and positions.numel() == tokens and positions.is_contiguous()
+                and positions.get_device() == dev and turns.dtype is i64 and turns.is_contiguous()
+                and turns.get_device() == dev and 0 < rot <= dim and rot % 16 == 0 and (out is None or out is x)
+                and -3e38 < gain < 3e38)
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _refuse_rotary(x, positions, turns, layout, gain, out)
+        # A dimension of one element may carry any stride (the library wants a multiple of 8).
+        ts, hs = ts if tokens > 1 else 0, hs if heads > 1 else 0
+    if out is None:
+        out = (sv["empty"] if stream is None else _empty(sv, stream))((tokens, heads, dim), dtype=xt, device=x.device)
+        ots, ohs = heads * dim, dim
+    else:
+        ots, ohs, _ = out.stride()
+        ots, ohs = ots if tokens > 1 else 0, ohs if heads > 1 else 0
+    status = _lib.gptq_rotary(dt, x.data_ptr(), ts, hs, tokens, heads, dim, rot, code, positions.data_ptr(),
+                              turns.data_ptr(), gain, out.data_ptr(), ots, ohs, _raw_stream(sv, stream, dev))
+    if status:
+        raise GptqError("gptq_rotary", status)
+    return out
+
+
+def _refuse_write_rotary(cache, q, k, v, slots, page_size, positions, turns, layout, gain, out):
+    _refuse_write(cache, k, v, slots, page_size, last=False)
+    tokens, _, dim = k.shape
+    _dtype16(q, "q")
+    if q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != dim or q.shape[1] == 0:
+        raise ValueError(f"q must be [{tokens}, heads, {dim}], got shape {tuple(q.shape)}")
+    _strided(q, "q", q.shape, k)
+    _refuse_turns(positions, turns, layout, gain, tokens, dim, k.device)
+    if out is not None:
+        _heads_out(out, "out", q)
+    _no_gradient(q=q, k=k, v=v)
+    _here(k, "k")
+
+
+def kv4_write_rotary(cache, q, k, v, slots, page_size, positions, turns, layout="half", gain=1.0, out=None,
+                     stream=None):
+    """What rotary does to q and k and kv4_write with the turned k and v, in one
+    call and with the same bits.  q [tokens, query heads, dim], k, v [tokens,
+    heads, dim] (strided views allowed), slots, positions [tokens] i64.  Returns
+    the turned q; `out` may be q itself, else overlaps no input."""
+    sv = _serve or _serving()
+    try:
+        kt, shape, dev, i64 = k.dtype, k.shape, k.get_device(), sv["i64"]
+        dt = sv["dtypes"][kt]
+        tokens, heads, dim = shape
+        hq = q.shape[1]
+        pages = cache.shape[0]
+        qts, qhs, q1 = q.stride()
+        kts, khs, k1 = k.stride()
+        vts, vhs, v1 = v.stride()
+        rot = 2 * turns.numel()
+        code = ROTARY_LAYOUTS[layout]
+        fine = (dev >= 0 and dev == sv["current"]() and dim in (64, 128, 256) and tokens > 1 and heads > 1 and hq > 1
+                and q.dtype is kt and q.shape == (tokens, hq, dim) and v.dtype is kt and v.shape == shape
+                and k1 == 1 and v1 == 1 and q1 == 1 and (kts | khs | vts | vhs | qts | qhs) % 8 == 0
+                and v.get_device() == dev and q.get_device() == dev
+                and not (q.requires_grad or k.requires_grad or v.requires_grad)
+                and 0 < page_size <= 4096 and page_size % 16 == 0 and cache.dtype is sv["u8"]
+                and cache.shape == (pages, heads, page_size * dim * 5 // 4) and cache.is_contiguous()
+                and cache.get_device() == dev
+                and slots.dtype is i64 and slots.numel() == tokens and slots.is_contiguous() and slots.get_device() == dev
+                and positions.dtype is i64 and positions.numel() == tokens and positions.is_contiguous()
+                and positions.get_device() == dev and turns.dtype is i64 and turns.is_contiguous()
+                and turns.get_device() == dev and 0 < rot <= dim and rot % 16 == 0 and (out is None or out is q)
+                and -3e38 < gain < 3e38)
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _refuse_write_rotary(cache, q, k, v, slots, page_size, positions, turns, layout, gain, out)
+        # A dimension of one element may carry any stride (the library wants a multiple of 8).
+        kts, vts, qts = (kts, vts, qts) if tokens > 1 else (0, 0, 0)
+        khs, vhs = (khs, vhs) if heads > 1 else (0, 0)
+        qhs = qhs if hq > 1 else 0
+    if out is None:
+        out = (sv["empty"] if stream is None else _empty(sv, stream))((tokens, hq, dim), dtype=kt, device=k.device)
+        ots, ohs = hq * dim, dim
+    else:
+        ots, ohs, _ = out.stride()
+        ots, ohs = ots if tokens > 1 else 0, ohs if hq > 1 else 0
+    status = _lib.gptq_kv4_write_rotary(dt, cache.data_ptr(), pages, heads, dim, page_size, q.data_ptr(), qts, qhs, hq,
+                                        k.data_ptr(), v.data_ptr(), kts, khs, vts, vhs, slots.data_ptr(), tokens, rot,
+                                        code, positions.data_ptr(), turns.data_ptr(), gain, out.data_ptr(), ots, ohs,
+                                        _raw_stream(sv, stream, dev))
+    if status:
+        raise GptqError("gptq_kv4_write_rotary", status)
+    return out
 
 
 def _refuse_read(cache, slots, dim, page_size, dtype):
@@ -928,7 +1191,7 @@ def kv4_read(cache, slots, dim, page_size, dtype, stream=None):
     return k, v
 
 
-def _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, out, ws):
+def _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, out, ws, lse, last=True):
     import torch
 
     _dtype16(q, "q")
@@ -955,21 +1218,26 @@ def _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, out,
         raise ValueError(f"max_q must be positive, got {max_q}")
     if out is not None:
         _need(out, "out", dtype=q.dtype, numel=q.numel(), device=dev)
+    if lse is not None:
+        _need(lse, "lse", numel=tq * hq, device=dev)
     if ws is not None:
         _ws(ws, dev)
     _no_gradient(q=q)
-    _here(q, "q")
+    if last:
+        _here(q, "q")
 
 
 def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, scale=None, out=None, ws=None,
-                  stream=None):
+                  stream=None, lse=None):
     """Causal attention of q [tokens, query heads, dim] (bf16 or f16) over the
     4-bit cache: softmax(scale q k^T) v per sequence and head, scale default
     1 / sqrt(dim).  table [seqs, pages per sequence] i32, kv_lens [seqs] i32
     (the queries' own keys included).  The queries of sequence b are its last
     tokens, rows q_starts[b] .. q_starts[b + 1] - 1 of q (i32 [seqs + 1], the
     first max_q of each); without q_starts, one a sequence.  Outputs of rows
-    that are no sequence's are zero.  `out` overlaps no input."""
+    that are no sequence's are zero.  `lse` (f32 [tokens, query heads]) receives
+    the logarithm of each row's sum of exponentials, -inf where it sees nothing.
+    `out` and `lse` overlap no input."""
     sv = _serve or _serving()
     try:
         qt, dev, i32 = q.dtype, q.get_device(), sv["i32"]
@@ -995,12 +1263,15 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
         if fine and out is not None:
             fine = (out.dtype is qt and out.numel() == tq * hq * dim and out.is_contiguous()
                     and out.get_device() == dev)
+        if fine and lse is not None:
+            fine = (lse.dtype is sv["f32"] and lse.numel() == tq * hq and lse.is_contiguous()
+                    and lse.get_device() == dev)
         if fine and ws is not None:
             fine = ws.dtype is sv["u8"] and ws.is_contiguous() and ws.get_device() == dev
     except (AttributeError, KeyError, TypeError, ValueError, IndexError):
         fine = False
     if not fine:
-        _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, out, ws)
+        _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, out, ws, lse)
         qts, qhs = qts if tq > 1 else 0, qhs if hq > 1 else 0
     if out is None:
         out = (sv["empty"] if stream is None else _empty(sv, stream))((tq, hq, dim), dtype=qt, device=q.device)
@@ -1016,11 +1287,156 @@ def kv4_attention(q, cache, table, kv_lens, page_size, q_starts=None, max_q=1, s
             ws = (sv["empty"] if stream is None else _empty(sv, stream))(wn, dtype=sv["u8"], device=q.device)
     if ws is not None:
         wp, wn = ws.data_ptr(), ws.numel()
-    code = _lib.gptq_kv4_attention(dt, q.data_ptr(), qts, qhs, tq, cache.data_ptr(), pages, heads, hq // heads, dim,
-                                   page_size, table.data_ptr(), per, kv_lens.data_ptr(), sp, seqs, int(max_q),
-                                   dim ** -0.5 if scale is None else float(scale), out.data_ptr(), wp, wn,
-                                   (_serve_words.get(dev) or (0, _serve_word(dev)))[1],
-                                   _raw_stream(sv, stream, dev))
+    scale = dim ** -0.5 if scale is None else float(scale)
+    word = (_serve_words.get(dev) or (0, _serve_word(dev)))[1]
+    if lse is None:
+        code = _lib.gptq_kv4_attention(dt, q.data_ptr(), qts, qhs, tq, cache.data_ptr(), pages, heads, hq // heads, dim,
+                                       page_size, table.data_ptr(), per, kv_lens.data_ptr(), sp, seqs, int(max_q),
+                                       scale, out.data_ptr(), wp, wn, word, _raw_stream(sv, stream, dev))
+    else:
+        code = _lib.gptq_kv4_attention_lse(dt, q.data_ptr(), qts, qhs, tq, cache.data_ptr(), pages, heads, hq // heads,
+                                           dim, page_size, table.data_ptr(), per, kv_lens.data_ptr(), sp, seqs,
+                                           int(max_q), scale, out.data_ptr(), lse.data_ptr(), wp, wn, word,
+                                           _raw_stream(sv, stream, dev))
     if code:
         raise GptqError("gptq_kv4_attention", code)
     return out
+
+
+def kv4_weights(table, page_size, heads):
+    """Running totals for kv4_attention_weights, zeros: f32 [seqs, heads, places
+    of a row of `table`]."""
+    import torch
+
+    return torch.zeros(table.shape[0], heads, table.shape[1] * page_size, dtype=torch.float32, device=table.device)
+
+
+def _refuse_weights(weights, q, lse, cache, table, kv_lens, page_size, q_starts, max_q):
+    _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, None, None, lse, last=False)
+    _need(lse, "lse", numel=q.shape[0] * q.shape[1], device=q.device)
+    shape = (table.shape[0], cache.shape[1], table.shape[1] * page_size)
+    _need(weights, "weights", device=q.device)
+    if weights.shape != shape:
+        raise ValueError(f"weights must be {shape}, got shape {tuple(weights.shape)}")
+    _no_gradient(weights=weights)
+    _here(q, "q")
+
+
+def kv4_attention_weights(weights, q, lse, cache, table, kv_lens, page_size, q_starts=None, max_q=1, scale=None,
+                          stream=None):
+    """Adds to `weights` (f32 [seqs, heads, places of a row of table], see
+    kv4_weights) what the queries of a kv4_attention call looked at: for each cached
+    token and key head the sum of exp(scale q k - lse) over the queries that see
+    it and the query heads of the key head.  `lse` is what that call gave, the
+    other arguments are its own.  Returns weights."""
+    sv = _serve or _serving()
+    try:
+        qt, dev, i32 = q.dtype, q.get_device(), sv["i32"]
+        dt = sv["dtypes"][qt]
+        tq, hq, dim = q.shape
+        pages, heads, size = cache.shape
+        seqs, per = table.shape
+        qts, qhs, q1 = q.stride()
+        fine = (dev >= 0 and dev == sv["current"]() and dim in (64, 128, 256) and tq > 0 and hq > 1
+                and hq % heads == 0 and q1 == 1 and not q.requires_grad
+                and (qts | qhs) % 8 == 0 and 0 < page_size <= 4096 and page_size % 16 == 0 and max_q > 0
+                and cache.dtype is sv["u8"] and size == page_size * dim * 5 // 4 and cache.is_contiguous()
+                and cache.get_device() == dev and table.dtype is i32 and per > 0 and table.is_contiguous()
+                and table.get_device() == dev and kv_lens.dtype is i32 and kv_lens.numel() == seqs
+                and kv_lens.is_contiguous() and kv_lens.get_device() == dev
+                and lse.dtype is sv["f32"] and lse.numel() == tq * hq and lse.is_contiguous() and lse.get_device() == dev
+                and weights.dtype is sv["f32"] and weights.shape == (seqs, heads, per * page_size)
+                and weights.is_contiguous() and weights.get_device() == dev and not weights.requires_grad)
+        sp = None
+        if q_starts is None:
+            fine = fine and tq == seqs and max_q == 1
+        else:
+            fine = (fine and q_starts.dtype is i32 and q_starts.numel() == seqs + 1 and q_starts.is_contiguous()
+                    and q_starts.get_device() == dev)
+            sp = q_starts.data_ptr()
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _refuse_weights(weights, q, lse, cache, table, kv_lens, page_size, q_starts, max_q)
+        qts, qhs = qts if tq > 1 else 0, qhs if hq > 1 else 0
+    code = _lib.gptq_kv4_attention_weights(dt, q.data_ptr(), qts, qhs, tq, lse.data_ptr(), cache.data_ptr(), pages, heads,
+                                           hq // heads, dim, page_size, table.data_ptr(), per, kv_lens.data_ptr(), sp,
+                                           seqs, int(max_q), dim ** -0.5 if scale is None else float(scale),
+                                           weights.data_ptr(), (_serve_words.get(dev) or (0, _serve_word(dev)))[1],
+                                           _raw_stream(sv, stream, dev))
+    if code:
+        raise GptqError("gptq_kv4_attention_weights", code)
+    return weights
+
+
+def _refuse_evict(cache, table, kv_lens, weights, keep, page_size, recent, out_table):
+    import torch
+
+    _need(cache, "cache", dtype=torch.uint8)
+    dev = cache.device
+    if cache.dim() != 3 or page_size <= 0 or cache.shape[2] * 4 % (page_size * 5):
+        raise ValueError(f"cache must be a pool of pages of {page_size} tokens, got shape {tuple(cache.shape)}")
+    _cache(cache, cache.shape[2] * 4 // (page_size * 5), page_size)
+    _need(table, "table", dtype=torch.int32, device=dev)
+    if table.dim() != 2 or table.shape[1] == 0:
+        raise ValueError(f"table must be 2-D [seqs, pages], got shape {tuple(table.shape)}")
+    seqs, per = table.shape
+    _need(kv_lens, "kv_lens", dtype=torch.int32, numel=seqs, device=dev)
+    _need(weights, "weights", device=dev)
+    if weights.shape != (seqs, cache.shape[1], per * page_size):
+        raise ValueError(f"weights must be {(seqs, cache.shape[1], per * page_size)}, got shape {tuple(weights.shape)}")
+    if out_table is not None:
+        _need(out_table, "out_table", dtype=torch.int32, device=dev)
+        if out_table.dim() != 2 or out_table.shape[0] != seqs or out_table.shape[1] == 0:
+            raise ValueError(f"out_table must be [{seqs}, pages], got shape {tuple(out_table.shape)}")
+        per = out_table.shape[1]
+    if keep <= 0 or keep > per * page_size:
+        raise ValueError(f"keep must be 1 to {per * page_size}, the places of a sequence, got {keep}")
+    if recent < 0:
+        raise ValueError(f"recent must not be negative, got {recent}")
+    _no_gradient(weights=weights)
+    _here(cache, "cache")
+
+
+def kv4_evict(cache, table, kv_lens, weights, keep, page_size, recent=0, out_table=None, stream=None):
+    """Cuts every sequence of the cache to `keep` tokens a key head: its last
+    `recent` ones and the heaviest of the others by `weights` (kv4_attention_weights;
+    equal ones: the earlier), each head its own, in order, from place 0 on.  They
+    move within their sequence's pages or, with `out_table` [seqs, pages] i32, into
+    those of it, which are in no row of `table`.  Pages that take tokens belong to one
+    sequence.  Returns (kept i32 [seqs, heads, keep]: the earlier place of each, -1
+    past the end; the new kv_lens; the new weights, zeros past the end)."""
+    sv = _serve or _serving()
+    try:
+        dev, i32 = cache.get_device(), sv["i32"]
+        pages, heads, size = cache.shape
+        seqs, per = table.shape
+        dim = size * 4 // (page_size * 5)
+        to, op, ostride = per, None, 0
+        fine = (dev >= 0 and dev == sv["current"]() and dim in (64, 128, 256) and 0 < page_size <= 4096
+                and page_size % 16 == 0 and cache.dtype is sv["u8"] and size == page_size * dim * 5 // 4
+                and cache.is_contiguous() and table.dtype is i32 and per > 0 and table.is_contiguous()
+                and table.get_device() == dev and kv_lens.dtype is i32 and kv_lens.numel() == seqs
+                and kv_lens.is_contiguous() and kv_lens.get_device() == dev and weights.dtype is sv["f32"]
+                and weights.shape == (seqs, heads, per * page_size) and weights.is_contiguous()
+                and weights.get_device() == dev and not weights.requires_grad and recent >= 0)
+        if out_table is not None:
+            fine = (fine and out_table.dtype is i32 and out_table.shape[0] == seqs and out_table.dim() == 2
+                    and out_table.is_contiguous() and out_table.get_device() == dev)
+            to = ostride = out_table.shape[1]
+            op = out_table.data_ptr()
+        fine = fine and 0 < keep <= to * page_size
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError, ZeroDivisionError):
+        fine = False
+    if not fine:
+        _refuse_evict(cache, table, kv_lens, weights, keep, page_size, recent, out_table)
+    empty = sv["empty"] if stream is None else _empty(sv, stream)
+    kept = empty((seqs, heads, keep), dtype=i32, device=cache.device)
+    lens = empty((seqs,), dtype=i32, device=cache.device)
+    out = empty((seqs, heads, to * page_size), dtype=sv["f32"], device=cache.device)
+    code = _lib.gptq_kv4_evict(cache.data_ptr(), pages, heads, dim, page_size, table.data_ptr(), per, op, ostride,
+                               kv_lens.data_ptr(), seqs, weights.data_ptr(), int(keep), min(int(recent), 2 ** 31 - 1),
+                               kept.data_ptr(), lens.data_ptr(), out.data_ptr(), _raw_stream(sv, stream, dev))
+    if code:
+        raise GptqError("gptq_kv4_evict", code)
+    return kept, lens, out

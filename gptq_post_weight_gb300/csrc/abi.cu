@@ -1,7 +1,7 @@
 // C ABI entry points (include/gptq_fold.h): argument checks, workspace
 // carving and the chaining of fold -> ladder -> sweep.  No device memory is
 // allocated here; every buffer is the caller's.
-#include "serve.cuh"
+#include "rotary.cuh"
 
 #include <math.h>
 #include <string.h>
@@ -63,13 +63,23 @@ size_t gram_ws_bytes(int n);
 gptq_status gram_run(float* Hp, int n, const float* X, int T, void* ws, size_t ws_bytes,
                      cudaStream_t s);
 gptq_status q4tp_linear_run(int dtype, const LinearArgs& a, cudaStream_t s);
+gptq_status q4tp_gated_run(int dtype, const LinearArgs& a, cudaStream_t s);
 gptq_status kv4_write_run(int dtype, uint8_t* cache, long long pages, int heads, int dim, int page_size,
                           const void* k, const void* v, long long kt, long long kh, long long vt, long long vh,
                           const long long* slots, int tokens, cudaStream_t s);
 gptq_status kv4_read_run(int dtype, const uint8_t* cache, long long pages, int heads, int dim, int page_size,
                          const long long* slots, int tokens, void* k, void* v, cudaStream_t s);
+gptq_status rotary_run(int dtype, bool half, const void* x, long long xt, long long xh, int tokens, int heads,
+                       const RotaryArgs& a, void* y, long long yt, long long yh, cudaStream_t s);
+gptq_status kv4_write_rotary_run(int dtype, bool half, uint8_t* cache, long long pages, int heads, int page_size,
+                                 const void* q, long long qt, long long qh, int q_heads, const void* k, const void* v,
+                                 long long kt, long long kh, long long vt, long long vh, const long long* slots,
+                                 int tokens, const RotaryArgs& a, void* y, long long yt, long long yh, cudaStream_t s);
 size_t kv4_attention_ws_bytes(int dim, int heads, int group, int max_q, int seqs, bool single, long long max_len);
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s);
+gptq_status kv4_no_sums_run(float* lse, long long n, cudaStream_t s);
+gptq_status kv4_weigh_run(int dtype, int dim, const AttnArgs& a, const float* lse, float* weights, cudaStream_t s);
+gptq_status kv4_evict_run(int dim, bool in_place, const EvictArgs& a, cudaStream_t s);
 }  // namespace gq
 
 using namespace gq;
@@ -88,6 +98,9 @@ bool bad_cache(long long pages, int heads, int dim, int page_size) {
          page_size <= 0 || page_size > 4096 || page_size % 16 != 0;
 }
 bool bad_stride(long long s) { return s < 0 || s % 8 != 0; }
+bool bad_rotary(int dim, int rot, int layout) {
+  return rot <= 0 || rot > dim || rot % 16 != 0 || (layout != GPTQ_ROTARY_HALF && layout != GPTQ_ROTARY_INTERLEAVED);
+}
 }  // namespace
 
 namespace {
@@ -674,6 +687,19 @@ gptq_status gptq_q4tp_linear(int dtype, const void* X, long long ldx, int tokens
   return q4tp_linear_run(dtype, a, as_stream(stream));
 }
 
+gptq_status gptq_q4tp_gated(int dtype, const void* X, long long ldx, int tokens, const uint8_t* nibbles,
+                            const uint8_t* rungs, const float* tab, int inner, int n, const void* bias, int act, void* Y,
+                            long long ldy, uint32_t* status, void* stream) {
+  if (bad_n(n) || inner <= 0 || inner > GPTQ_MAX_ROWS / 2 || n % GPTQ_GROUP != 0 || bad_tokens(tokens))
+    return GPTQ_ERR_SHAPE;
+  if (bad_dtype(dtype) || act < GPTQ_ACT_NONE || act > GPTQ_ACT_SILU) return GPTQ_ERR_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (ldx < n || bad_stride(ldx) || ldy < inner) return GPTQ_ERR_SHAPE;
+  if (!ptr_ok(X) || !ptr_ok(nibbles) || !ptr_ok(rungs) || !ptr_ok(tab) || !opt_ok(bias) || !ptr_ok(Y)) return GPTQ_ERR_ARG;
+  const LinearArgs a{X, ldx, tokens, nibbles, rungs, tab, 2 * inner, n, bias, act, nullptr, 0, Y, ldy, status};
+  return q4tp_gated_run(dtype, a, as_stream(stream));
+}
+
 gptq_status gptq_kv4_write(int dtype, uint8_t* cache, long long pages, int heads, int dim, int page_size,
                            const void* K, const void* V, long long kt, long long kh, long long vt,
                            long long vh, const long long* slots, int tokens, void* stream) {
@@ -684,6 +710,42 @@ gptq_status gptq_kv4_write(int dtype, uint8_t* cache, long long pages, int heads
   if (!ptr_ok(cache) || !ptr_ok(K) || !ptr_ok(V) || slots == nullptr) return GPTQ_ERR_ARG;
   return kv4_write_run(dtype, cache, pages, heads, dim, page_size, K, V, kt, kh, vt, vh, slots, tokens,
                        as_stream(stream));
+}
+
+gptq_status gptq_rotary(int dtype, const void* X, long long xt, long long xh, int tokens, int heads, int dim, int rot,
+                        int layout, const long long* positions, const long long* turns, float gain, void* Y,
+                        long long yt, long long yh, void* stream) {
+  if (bad_tokens(tokens) || heads <= 0 || heads > 65535 || dim <= 0 || dim > 1024 || dim % 16 != 0) return GPTQ_ERR_SHAPE;
+  if (bad_rotary(dim, rot, layout)) return GPTQ_ERR_SHAPE;
+  if (bad_dtype(dtype) || !isfinite(gain)) return GPTQ_ERR_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (bad_stride(xt) || bad_stride(xh) || bad_stride(yt) || bad_stride(yh)) return GPTQ_ERR_SHAPE;
+  if (!ptr_ok(X) || !ptr_ok(Y) || positions == nullptr || turns == nullptr) return GPTQ_ERR_ARG;
+  if (X == Y && (xt != yt || xh != yh)) return GPTQ_ERR_SHAPE;
+  const RotaryArgs a{dim, rot, positions, turns, gain};
+  return rotary_run(dtype, layout == GPTQ_ROTARY_HALF, X, xt, xh, tokens, heads, a, Y, yt, yh, as_stream(stream));
+}
+
+gptq_status gptq_kv4_write_rotary(int dtype, uint8_t* cache, long long pages, int heads, int dim, int page_size,
+                                  const void* Q, long long qt, long long qh, int q_heads, const void* K, const void* V,
+                                  long long kt, long long kh, long long vt, long long vh, const long long* slots,
+                                  int tokens, int rot, int layout, const long long* positions, const long long* turns,
+                                  float gain, void* Y, long long yt, long long yh, void* stream) {
+  if (bad_cache(pages, heads, dim, page_size) || bad_tokens(tokens) || q_heads <= 0 || q_heads > 32768)
+    return GPTQ_ERR_SHAPE;
+  if (bad_rotary(dim, rot, layout)) return GPTQ_ERR_SHAPE;
+  if (bad_dtype(dtype) || !isfinite(gain)) return GPTQ_ERR_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (bad_stride(qt) || bad_stride(qh) || bad_stride(kt) || bad_stride(kh) || bad_stride(vt) || bad_stride(vh) ||
+      bad_stride(yt) || bad_stride(yh))
+    return GPTQ_ERR_SHAPE;
+  if (!ptr_ok(cache) || !ptr_ok(Q) || !ptr_ok(K) || !ptr_ok(V) || !ptr_ok(Y) || slots == nullptr || positions == nullptr ||
+      turns == nullptr)
+    return GPTQ_ERR_ARG;
+  if (Q == Y && (qt != yt || qh != yh)) return GPTQ_ERR_SHAPE;
+  const RotaryArgs a{dim, rot, positions, turns, gain};
+  return kv4_write_rotary_run(dtype, layout == GPTQ_ROTARY_HALF, cache, pages, heads, page_size, Q, qt, qh, q_heads, K, V,
+                              kt, kh, vt, vh, slots, tokens, a, Y, yt, yh, as_stream(stream));
 }
 
 gptq_status gptq_kv4_read(int dtype, const uint8_t* cache, long long pages, int heads, int dim, int page_size,
@@ -716,13 +778,26 @@ size_t gptq_kv4_attention_call_bytes(int dim, int heads, int group, int max_q, i
   return kv4_attention_ws_bytes(dim, heads, group, max_q, seqs, single != 0, max_len);
 }
 
+static bool bad_paged_call(long long pages, int heads, int dim, int page_size, int table_stride, int seqs) {
+  return bad_cache(pages, heads, dim, page_size) || seqs < 0 || seqs > GPTQ_MAX_TOKENS || table_stride <= 0 ||
+         (long long)table_stride * page_size > (1ll << 30);
+}
+
 gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
                                const uint8_t* cache, long long pages, int heads, int group, int dim,
                                int page_size, const int* table, int table_stride, const int* kv_lens,
                                const int* q_starts, int seqs, int max_q, float scale, void* out, void* ws,
                                size_t ws_bytes, uint32_t* status, void* stream) {
-  if (bad_cache(pages, heads, dim, page_size) || bad_tokens(tq) || group <= 0 || group > 1024 || seqs < 0 ||
-      seqs > GPTQ_MAX_TOKENS || table_stride <= 0 || (long long)table_stride * page_size > (1ll << 30) ||
+  return gptq_kv4_attention_lse(dtype, Q, q_ts, q_hs, tq, cache, pages, heads, group, dim, page_size, table, table_stride,
+                                kv_lens, q_starts, seqs, max_q, scale, out, nullptr, ws, ws_bytes, status, stream);
+}
+
+gptq_status gptq_kv4_attention_lse(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
+                                   const uint8_t* cache, long long pages, int heads, int group, int dim,
+                                   int page_size, const int* table, int table_stride, const int* kv_lens,
+                                   const int* q_starts, int seqs, int max_q, float scale, void* out, float* lse,
+                                   void* ws, size_t ws_bytes, uint32_t* status, void* stream) {
+  if (bad_paged_call(pages, heads, dim, page_size, table_stride, seqs) || bad_tokens(tq) || group <= 0 || group > 1024 ||
       max_q <= 0 || max_q > GPTQ_MAX_TOKENS)
     return GPTQ_ERR_SHAPE;
   if (bad_dtype(dtype) || !isfinite(scale)) return GPTQ_ERR_ARG;
@@ -731,7 +806,7 @@ gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long lo
   if (seqs == 0) {  // every row is no sequence's
     if (!ptr_ok(out)) return GPTQ_ERR_ARG;
     GQ_CUDA(cudaMemsetAsync(out, 0, (size_t)tq * heads * group * dim * 2, as_stream(stream)));
-    return GPTQ_OK;
+    return lse == nullptr ? GPTQ_OK : kv4_no_sums_run(lse, (long long)tq * heads * group, as_stream(stream));
   }
   if (bad_stride(q_ts) || bad_stride(q_hs)) return GPTQ_ERR_SHAPE;
   if (!ptr_ok(Q) || !ptr_ok(cache) || table == nullptr || kv_lens == nullptr || !ptr_ok(out) || !opt_ok(ws))
@@ -739,11 +814,51 @@ gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long lo
   const size_t need = kv4_attention_ws_bytes(dim, heads, group, max_q, seqs, q_starts == nullptr,
                                              (long long)table_stride * page_size);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return GPTQ_ERR_NOMEM;
-  const AttnArgs a{Q,     q_ts,         q_hs,    tq,       cache, pages, heads, group, page_size,
+  AttnArgs a{Q,     q_ts,         q_hs,    tq,       cache, pages, heads, group, page_size,
                    table, table_stride, kv_lens, q_starts, seqs,  max_q, scale * 1.4426950408889634f,
                    out,   static_cast<int4*>(ws), reinterpret_cast<float*>(static_cast<char*>(ws) + kCutBytes),
                    dtype == GPTQ_BF16 ? 8u : 64u, status};
+  a.lse = lse;
   return kv4_attention_run(dtype, dim, a, as_stream(stream));
+}
+
+gptq_status gptq_kv4_attention_weights(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
+                                       const float* lse, const uint8_t* cache, long long pages, int heads,
+                                       int group, int dim, int page_size, const int* table, int table_stride,
+                                       const int* kv_lens, const int* q_starts, int seqs, int max_q, float scale,
+                                       float* weights, uint32_t* status, void* stream) {
+  if (bad_paged_call(pages, heads, dim, page_size, table_stride, seqs) || bad_tokens(tq) || group <= 0 || group > 1024 ||
+      max_q <= 0 || max_q > GPTQ_MAX_TOKENS)
+    return GPTQ_ERR_SHAPE;
+  if (bad_dtype(dtype) || !isfinite(scale)) return GPTQ_ERR_ARG;
+  if (q_starts == nullptr && (tq != seqs || max_q != 1)) return GPTQ_ERR_SHAPE;
+  if (tq == 0 || seqs == 0) return GPTQ_OK;
+  if (bad_stride(q_ts) || bad_stride(q_hs)) return GPTQ_ERR_SHAPE;
+  if (!ptr_ok(Q) || lse == nullptr || !ptr_ok(cache) || table == nullptr || kv_lens == nullptr || !ptr_ok(weights))
+    return GPTQ_ERR_ARG;
+  AttnArgs a{Q,     q_ts,         q_hs,    tq,       cache, pages, heads, group, page_size,
+             table, table_stride, kv_lens, q_starts, seqs,  max_q, scale * 1.4426950408889634f,
+             nullptr, nullptr, nullptr, dtype == GPTQ_BF16 ? 8u : 64u, status};
+  return kv4_weigh_run(dtype, dim, a, lse, weights, as_stream(stream));
+}
+
+gptq_status gptq_kv4_evict(uint8_t* cache, long long pages, int heads, int dim, int page_size, const int* table,
+                           int table_stride, const int* out_table, int out_stride, const int* kv_lens, int seqs,
+                           const float* weights, int keep, int recent, int* kept, int* out_lens,
+                           float* out_weights, void* stream) {
+  if (bad_paged_call(pages, heads, dim, page_size, table_stride, seqs) || keep <= 0 || recent < 0 ||
+      (long long)seqs * heads > (1 << 24))
+    return GPTQ_ERR_SHAPE;
+  const int to_stride = out_table != nullptr ? out_stride : table_stride;
+  if (to_stride <= 0 || (long long)to_stride * page_size > (1ll << 30) || (long long)to_stride * page_size < keep)
+    return GPTQ_ERR_SHAPE;
+  if (seqs == 0) return GPTQ_OK;
+  if (!ptr_ok(cache) || table == nullptr || kv_lens == nullptr || weights == nullptr || kept == nullptr ||
+      out_lens == nullptr || out_weights == nullptr)
+    return GPTQ_ERR_ARG;
+  const EvictArgs a{cache,   pages, heads,  page_size, table, table_stride, out_table != nullptr ? out_table : table, to_stride,
+                    kv_lens, seqs,  weights, keep,      std::min(recent, keep), kept, out_lens, out_weights};
+  return kv4_evict_run(dim, out_table == nullptr, a, as_stream(stream));
 }
 
 }  // extern "C"

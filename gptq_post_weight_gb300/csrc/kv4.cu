@@ -21,7 +21,7 @@
 // what a place costs.  They are bound by the memory: 131072 tokens of 8 heads
 // of 128 read back in 122 us, 5.78 TB/s of codes and values together, and
 // 16001 tokens written and read back in 37 us, 4.68 TB/s.
-#include "serve.cuh"
+#include "rotary.cuh"
 
 namespace gq {
 namespace {
@@ -214,6 +214,87 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// The write with rotary positions on its way: q turned into y, k turned into
+// the cache (rounded to T first, so that the codes are those of a turned key
+// that k_kv4_write is given), v as it is.  A lane has a token and eight channels and
+// walks over heads, the query's before the cache's, so that its sines and
+// cosines serve them all; in the half layout the other channels of its pairs
+// are another lane's, which hands them over (dim / 8 lanes of a warp are a
+// head's).  A lane reads and writes its own octets only: y may be q itself.
+struct TurnedHeads {
+  const void* q;
+  long long qt, qh;
+  int q_heads;
+  void* y;
+  long long yt, yh;
+  const void* k;
+  const void* v;
+  Strides st;
+};
+
+template <class T, bool HALF>
+__global__ void __launch_bounds__(256)
+    k_kv4_write_rotary(CacheShape c, TurnedHeads io, RotaryArgs a, const long long* __restrict__ slots, int tokens, int take) {
+  const int cl = c.dim == 256 ? 5 : c.dim == 128 ? 4 : 3;  // log2(dim / 8)
+  const int i = (int)(blockIdx.x * 256 + threadIdx.x), ch = (i & ((1 << cl) - 1)) * 8;
+  const bool in = i >> cl < tokens;
+  const int tok = in ? i >> cl : tokens - 1;
+  const int h0 = (int)blockIdx.y * take, h1 = min(h0 + take, io.q_heads + c.heads);
+  const bool turns = ch < a.rot, second = HALF && ch >= a.rot / 2;
+  const int step = turns ? a.rot / 16 : 0, lane = threadIdx.x % 32, partner = second ? lane - step : lane + step;
+  float co[8], si[8];
+  const long long position = a.positions[tok];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float2 t{0.f, 0.f};
+    if (turns && (HALF || k < 4)) t = turn_of(a, position, HALF ? (second ? ch - a.rot / 2 : ch) + k : ch / 2 + k);
+    co[k] = t.x, si[k] = HALF && !second ? -t.y : t.y;
+  }
+  auto turned8 = [&](uint4 x) {
+    uint4 o;
+    if (HALF) {
+      uint4 p;
+      p.x = __shfl_sync(0xffffffffu, x.x, partner), p.y = __shfl_sync(0xffffffffu, x.y, partner);
+      p.z = __shfl_sync(0xffffffffu, x.z, partner), p.w = __shfl_sync(0xffffffffu, x.w, partner);
+      o = turn_half<T>(x, p, co, si);
+    } else {
+      o = turn_pairs<T>(x, co, si);
+    }
+    return turns ? o : x;
+  };
+  const T* q = static_cast<const T*>(io.q) + tok * io.qt + ch;
+  T* y = static_cast<T*>(io.y) + tok * io.yt + ch;
+#pragma unroll 4
+  for (int h = h0; h < min(h1, io.q_heads); ++h) {
+    const uint4 o = turned8(*reinterpret_cast<const uint4*>(q + h * io.qh));
+    if (in) *reinterpret_cast<uint4*>(y + h * io.yh) = o;
+  }
+  if (h1 <= io.q_heads) return;
+  const long long slot = slots[tok];
+  uint8_t* blk = in ? block_of(c, slot) : nullptr;
+  const long long head_bytes = (long long)(c.page_size / KV_BLOCK) * kv_block_bytes(c.dim);
+  const int row = (int)(slot & (KV_BLOCK - 1));  // page_size is a multiple of the block
+  const T* kp = static_cast<const T*>(io.k) + tok * io.st.kt + ch;
+  const T* vp = static_cast<const T*>(io.v) + tok * io.st.vt + ch;
+#pragma unroll 2
+  for (int h = max(h0 - io.q_heads, 0); h < h1 - io.q_heads; ++h) {
+    const uint4 v8 = *reinterpret_cast<const uint4*>(vp + h * io.st.vh);
+    const uint4 k8 = turned8(*reinterpret_cast<const uint4*>(kp + h * io.st.kh));
+    uint32_t pk, pv;
+    const uint32_t wk = quantise8<T>(k8, pk), wv = quantise8<T>(v8, pv);
+    if (blk != nullptr) {
+      uint8_t* kb = blk + h * head_bytes + row * (c.dim / 2) + ch / 2;
+      *reinterpret_cast<uint32_t*>(kb) = wk;
+      *reinterpret_cast<uint32_t*>(kb + kv_value_off(c.dim)) = wv;
+      if (ch % 32 == 0) {
+        uint8_t* pb = blk + h * head_bytes + kv_param_off(c.dim) + row * (c.dim / 8) + ch / 8;
+        *reinterpret_cast<uint32_t*>(pb) = pk;
+        *reinterpret_cast<uint32_t*>(pb + kv_value_off(c.dim)) = pv;
+      }
+    }
+  }
+}
+
 // Tokens a CTA: four places a thread where that still gives every SM its eight
 // CTAs, else one.  Measured, 131072 tokens of 8 heads of 128 read back: two
 // places a thread 128.6 us, four 122.1, eight 121.0, sixteen 122.6; 16001
@@ -249,6 +330,30 @@ gptq_status kv4_write_run(int dtype, uint8_t* cache, long long pages, int heads,
     k_kv4_write<<<p.grid, 256, 0, s>>>(c, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, st, slots, tokens, per, p.per_inv, p.take);
   else
     k_kv4_write<<<p.grid, 256, 0, s>>>(c, (const __half*)k, (const __half*)v, st, slots, tokens, per, p.per_inv, p.take);
+  GQ_LAUNCHED();
+  return GPTQ_OK;
+}
+
+gptq_status kv4_write_rotary_run(int dtype, bool half, uint8_t* cache, long long pages, int heads, int page_size,
+                                 const void* q, long long qt, long long qh, int q_heads, const void* k, const void* v,
+                                 long long kt, long long kh, long long vt, long long vh, const long long* slots,
+                                 int tokens, const RotaryArgs& a, void* y, long long yt, long long yh, cudaStream_t s) {
+  if (tokens == 0) return GPTQ_OK;
+  const CacheShape c{cache, pages, heads, a.dim, page_size};
+  const TurnedHeads io{q, qt, qh, q_heads, y, yt, yh, k, v, Strides{kt, kh, vt, vh}};
+  const long long threads = (long long)tokens * (a.dim / 8);
+  // Heads a thread: as many as leave every SM its 2048 threads, sixteen at most.
+  const int every = q_heads + heads;
+  const int take = (int)std::min<long long>(std::max<long long>(threads * every / (num_sms() * 2048ll), 1), 16);
+  const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)((every + take - 1) / take));
+  GQ_PROF(K_KV4_WRITE_ROTARY, s);
+  if (dtype == GPTQ_BF16) {
+    if (half) k_kv4_write_rotary<__nv_bfloat16, true><<<grid, 256, 0, s>>>(c, io, a, slots, tokens, take);
+    else k_kv4_write_rotary<__nv_bfloat16, false><<<grid, 256, 0, s>>>(c, io, a, slots, tokens, take);
+  } else {
+    if (half) k_kv4_write_rotary<__half, true><<<grid, 256, 0, s>>>(c, io, a, slots, tokens, take);
+    else k_kv4_write_rotary<__half, false><<<grid, 256, 0, s>>>(c, io, a, slots, tokens, take);
+  }
   GQ_LAUNCHED();
   return GPTQ_OK;
 }

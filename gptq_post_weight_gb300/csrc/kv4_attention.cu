@@ -606,6 +606,8 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
           *reinterpret_cast<float2*>(part + r * D + d) = v;
       }
       __syncwarp();
+      if (CL == 0 && whole && lane == 0 && a.lse != nullptr)
+        a.lse[(long long)(sq.q0 + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group] = log_sum(sl, top, den);
       if (CL && lane == 0) {
         mls[0][r][0] = top;
         mls[0][r][1] = den;
@@ -636,8 +638,9 @@ __global__ void __launch_bounds__(ATHREADS, resident(D, NQ))
           den += ml[c].y * f[c];
         }
         const float inv = den != 0.f ? 1.f / den : 0.f;  // a row that sees nothing: zeros
-        T* dst = static_cast<T*>(a.out) +
-                 ((long long)(sq.q0 + r / a.group) * a.heads * a.group + head * a.group + r % a.group) * D;
+        const long long at = (long long)(sq.q0 + r / a.group) * a.heads * a.group + head * a.group + r % a.group;
+        if (lane == 0 && a.lse != nullptr) a.lse[at] = log_sum(sl, top, den);
+        T* dst = static_cast<T*>(a.out) + at * D;
 #pragma unroll
         for (int d = 2 * lane; d < D; d += 64) {
           float2 v{0.f, 0.f};
@@ -726,8 +729,9 @@ __global__ void __launch_bounds__(ATHREADS) k_kv4_join(AttnArgs a) {
   }
   const float inv = den != 0.f ? 1.f / den : 0.f;  // a row that sees nothing: zeros
   const int rr = cut.y + r;
-  T* dst = static_cast<T*>(a.out) +
-           ((long long)(cut.x + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group) * D;
+  const long long at = (long long)(cut.x + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group;
+  if (lane == 0 && a.lse != nullptr) a.lse[at] = log_sum(sl, top, den);
+  T* dst = static_cast<T*>(a.out) + at * D;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = Elem<T>::from(acc[i] * inv);
 }
@@ -841,6 +845,7 @@ gptq_status attn_launch(const AttnArgs& a, long long shares, cudaStream_t s) {
     } else {
       p.q = static_cast<const T*>(a.q) + b0 * a.q_ts;
       p.out = static_cast<T*>(a.out) + (long long)b0 * a.heads * a.group * D;
+      if (a.lse != nullptr) p.lse = a.lse + (long long)b0 * a.heads * a.group;
       p.tq = p.seqs;
     }
     {
@@ -887,6 +892,19 @@ gptq_status attn_queries(int dim, const AttnArgs& a, const Plan& p, cudaStream_t
 
 size_t kv4_attention_ws_bytes(int dim, int heads, int group, int max_q, int seqs, bool single, long long max_len) {
   return plan_of(dim, heads, group, max_q, seqs, single, max_len).ws;
+}
+
+__global__ void __launch_bounds__(256) k_no_sums(float* lse, long long n) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) lse[i] = -INFINITY;
+}
+
+// -inf for n rows that no sequence has.
+gptq_status kv4_no_sums_run(float* lse, long long n, cudaStream_t s) {
+  GQ_PROF(K_KV4_JOIN, s);
+  k_no_sums<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(lse, n);
+  GQ_LAUNCHED();
+  return GPTQ_OK;
 }
 
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s) {

@@ -565,6 +565,8 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
           }
         }
       }
+      if (a.lse != nullptr && pc.whole && mine && half == 0)
+        a.lse[(long long)(pc.t.q0 + qi) * a.heads * a.group + hq] = log_sum(sl, m, l);
       if (!pc.whole && mine && half == 0)
         *reinterpret_cast<float2*>(part + (size_t)kRows<D> * D + 2 * (128 * x + rt)) = float2{m, l};
       tc_fence_before();
@@ -892,8 +894,10 @@ __global__ void __launch_bounds__(128) k_kv4_chunk_join(AttnArgs a) {
     if (r0 + k >= rows) continue;
     const float inv = dk != 0.f ? 1.f / dk : 0.f;  // a row that sees nothing: zeros
     const int rr = cut.y + r0 + k;
-    T* dst = static_cast<T*>(a.out) +
-             ((long long)(cut.x + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group) * D;
+    const long long at = (long long)(cut.x + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group;
+    const float tk = __shfl_sync(0xffffffffu, top, k);
+    if (lane == 0 && a.lse != nullptr) a.lse[at] = log_sum(sl, tk, dk);
+    T* dst = static_cast<T*>(a.out) + at * D;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = Elem<T>::from(acc[k][i] * inv);
   }

@@ -26,6 +26,13 @@
 // TB/s of codes and rungs; 6 000 of 30 000 cycles load ladders, rungs and x,
 // 4 000 join the cluster, and a box takes a warp 1400, shared by the ALU's
 // shifts and masks, the products and the shared-memory reads of twelve warps).
+//
+// The gated product (GATED): act(x Wg^T + bg) * (x Wu^T + bu) with W the gate's
+// rows and then as many of the up projection.  A tile's rows come in sixteens,
+// in turns of the gate and of the same outputs of the up projection (wrow), so
+// that the two sums of an output are in one warp's reach when a tile is
+// written out, in all three kernels; what differs from the plain product is
+// that map, boxes of 16 rows for the codes, and the end.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -79,6 +86,17 @@ __device__ __forceinline__ float activate(float v, int act) {
 }
 
 namespace {
+
+// The weight row of local row r of a tile whose rows start at row0 (a multiple
+// of 32).  Gated: sixteen rows of the gate, the same sixteen of the up
+// projection, the next ones; the tile has half as many outputs, from row0 / 2.
+// (Past the gate's end its sixteens run into the up projection's rows: nothing
+// of that is written out.)
+template <bool GATED>
+__device__ __forceinline__ int wrow(const LinearArgs& a, int row0, int r) {
+  if (!GATED) return row0 + r;
+  return row0 / 2 + (r / 32 * 16 + r % 16) + (r / 16 % 2 ? a.rows / 2 : 0);
+}
 
 // The epilogue of eight outputs: rows r .. r + 7 of a token (r a multiple of
 // 8), with 16-byte accesses where the rows of y and the residual allow it.
@@ -138,6 +156,82 @@ __device__ __forceinline__ void finish8(const LinearArgs& a, int tok, int r, boo
   }
 }
 
+// Eight gated outputs, r .. r + 7 of a token, of the sums g of the gate and u of
+// the up projection.
+template <class T>
+__device__ __forceinline__ void finish_gated8(const LinearArgs& a, int tok, int r, float (&g)[8], float (&u)[8]) {
+  const int outs = a.rows / 2;
+  const T* bias = static_cast<const T*>(a.bias);
+  T* y = static_cast<T*>(a.y) + (size_t)tok * a.ldy + r;
+  if (r + 8 <= outs && a.ldy % 8 == 0 && outs % 8 == 0) {
+    if (bias != nullptr) {
+      add8<T>(g, *reinterpret_cast<const uint4*>(bias + r));
+      add8<T>(u, *reinterpret_cast<const uint4*>(bias + outs + r));
+    }
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {  // (as in finish8)
+      float x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = activate(g[k], a.act);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) g[k] = g[k + 4], g[k + 4] = x[k];
+    }
+    uint4 o;
+    o.x = bits2(Elem<T>::make2(g[0] * u[0], g[1] * u[1]));
+    o.y = bits2(Elem<T>::make2(g[2] * u[2], g[3] * u[3]));
+    o.z = bits2(Elem<T>::make2(g[4] * u[4], g[5] * u[5]));
+    o.w = bits2(Elem<T>::make2(g[6] * u[6], g[7] * u[7]));
+    *reinterpret_cast<uint4*>(y) = o;
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      float x = g[0], w = u[0];
+#pragma unroll
+      for (int k = 0; k < 7; ++k) g[k] = g[k + 1], u[k] = u[k + 1];
+      if (r + i < outs) {
+        if (bias != nullptr) x += Elem<T>::to(bias[r + i]), w += Elem<T>::to(bias[outs + r + i]);
+        y[i] = Elem<T>::from(activate(x, a.act) * w);
+      }
+    }
+  }
+}
+
+// v += eight sums at this CTA's address `at`, of the cluster's CTA `rank`.
+__device__ __forceinline__ void add_peer8(float (&v)[8], uint32_t at, int rank) {
+  const uint32_t ra = mapa_u32(at, (uint32_t)rank);
+  float4 p, q;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w) : "r"(ra) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w) : "r"(ra + 16u) : "memory");
+  v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
+  v[4] += q.x; v[5] += q.y; v[6] += q.z; v[7] += q.w;
+}
+
+// reduce_finish of a gated tile.
+template <class T, int ROWS>
+__device__ __forceinline__ void reduce_finish_gated(const LinearArgs& a, const float* part, int rank, int nrank, int nthreads,
+                                                    int ntok, int tok0, int row0) {
+  for (int i = rank * nthreads + threadIdx.x; i < ntok * (ROWS / 16); i += nrank * nthreads) {
+    const int tok = i / (ROWS / 16), o = i % (ROWS / 16) * 8, r = row0 / 2 + o;
+    if (r >= a.rows / 2) continue;
+    const float* gate = part + tok * ROWS + o / 16 * 32 + o % 16;
+    float g[8], u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.f;
+    if (nrank > 1) {
+      for (int k = 0; k < nrank; ++k) {
+        add_peer8(g, smem_u32(gate), k);
+        add_peer8(u, smem_u32(gate + 16), k);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = gate[e], u[e] = gate[16 + e];
+    }
+    finish_gated8<T>(a, tok0 + tok, r, g, u);
+  }
+}
+
 // Sums of a row tile in shared memory, [token][ROWS], of this CTA or of
 // the `nrank` CTAs of its cluster (added in rank order, each rank finishing
 // its share of the outputs).
@@ -155,16 +249,7 @@ __device__ __forceinline__ void reduce_finish(const LinearArgs& a, const float* 
       const uint32_t la = smem_u32(part + i * 8);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = 0.f;
-      for (int k = 0; k < nrank; ++k) {
-        const uint32_t ra = mapa_u32(la, (uint32_t)k);
-        float4 p, q;
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w) : "r"(ra) : "memory");
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w) : "r"(ra + 16u) : "memory");
-        v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
-        v[4] += q.x; v[5] += q.y; v[6] += q.z; v[7] += q.w;
-      }
+      for (int k = 0; k < nrank; ++k) add_peer8(v, la, k);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = part[i * 8 + e];
@@ -195,7 +280,7 @@ __device__ __forceinline__ uint2 box_rungs(const LinearArgs& a, int row, int b, 
 // x and the weights, weight by weight.  (Where it is comes from the special
 // registers once more, opaque to the compiler: kept from the kernel's start,
 // it cost two tokens a tenth of their time.)
-template <class T, int TT, int FROWS>
+template <class T, int TT, int FROWS, bool GATED>
 __device__ __forceinline__ void sum_again(const LinearArgs& a, int boxes, float* part) {
   uint32_t tid, bx, by, bz;
   asm volatile("mov.u32 %0, %%tid.x;\n mov.u32 %1, %%ctaid.x;\n mov.u32 %2, %%ctaid.y;\n mov.u32 %3, %%ctaid.z;"
@@ -207,7 +292,7 @@ __device__ __forceinline__ void sum_again(const LinearArgs& a, int boxes, float*
   for (int e = 0; e < 4; ++e) {
     const int tok = TT <= 2 ? t / 2 : 2 * t + (e & 1), r = row + (e >> 1) * 8;
     if (tok >= TT || (TT <= 2 && (e | t) % 2 != 0)) continue;  // not this lane's
-    const int token = (int)bz * TT + tok, rr = (int)bx * FROWS + r;
+    const int token = (int)bz * TT + tok, rr = wrow<GATED>(a, (int)bx * FROWS, r);
     if (token >= a.tokens || rr >= a.rows || fabsf(part[tok * FROWS + r]) < INFINITY) continue;
     const T* x = static_cast<const T*>(a.x) + (size_t)token * a.ldx + (size_t)grp0 * 32;
     const uint8_t* nibbles = a.nibbles + ((size_t)rr * gpr + grp0) * 16;
@@ -244,7 +329,7 @@ constexpr int kScaleFloats = TT <= 2 ? 0 : 128;
 // two factors a lane and half a box, looked up by the lane that needs them,
 // where one column takes 32 multiply-adds and an exchange through shared
 // memory.  Measured, one token, 5120 x 17408: 16.9 us against 17.8.
-template <class T, int TT, int FW>
+template <class T, int TT, int FW, bool GATED>
 __global__ void __launch_bounds__(32 * FW)
     k_q4_few(const __grid_constant__ CUtensorMap wmap, LinearArgs a, int boxes, WaitCfg wc) {
   static_assert(TT <= 8, "one token tile");
@@ -282,7 +367,7 @@ __global__ void __launch_bounds__(32 * FW)
     if (!wc.no_loads)
       for (int s = 0; s < FST && s < nbox; ++s) {
         mbar_expect_tx(&full[warp * FST + s], FBOX);
-        tma_load_2d(smem_u32(ring + s * FBOX), &wmap, (box0 + s) * 128, row0 + warp * 16, &full[warp * FST + s]);
+        tma_load_2d(smem_u32(ring + s * FBOX), &wmap, (box0 + s) * 128, wrow<GATED>(a, row0, warp * 16), &full[warp * FST + s]);
       }
   }
 
@@ -291,15 +376,15 @@ __global__ void __launch_bounds__(32 * FW)
   float4 tv[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int at = threadIdx.x + i * NTHR, r = at / 8;
-    tv[i] = row0 + r < a.rows ? *reinterpret_cast<const float4*>(a.tab + (size_t)(row0 + r) * 32 + at % 8 * 4) : float4{};
+    const int at = threadIdx.x + i * NTHR, wr = wrow<GATED>(a, row0, at / 8);
+    tv[i] = wr < a.rows ? *reinterpret_cast<const float4*>(a.tab + (size_t)wr * 32 + at % 8 * 4) : float4{};
   }
   {
     const int r = threadIdx.x / 2;  // two threads a row
     for (int b0 = threadIdx.x % 2; b0 < nbox; b0 += 8) {
       uint2 v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = b0 + 2 * i < nbox ? box_rungs(a, row0 + r, box0 + b0 + 2 * i, gpr) : uint2{};
+      for (int i = 0; i < 4; ++i) v[i] = b0 + 2 * i < nbox ? box_rungs(a, wrow<GATED>(a, row0, r), box0 + b0 + 2 * i, gpr) : uint2{};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (b0 + 2 * i < nbox)  // a rung above 31 is entry 32 of its ladder: 0
@@ -354,7 +439,8 @@ __global__ void __launch_bounds__(32 * FW)
     __syncwarp();
     if (lane == 0 && b + FST < nbox) {
       mbar_expect_tx(&full[warp * FST + st], FBOX);
-      tma_load_2d(smem_u32(ring + st * FBOX), &wmap, (box0 + b + FST) * 128, row0 + warp * 16, &full[warp * FST + st]);
+      tma_load_2d(smem_u32(ring + st * FBOX), &wmap, (box0 + b + FST) * 128, wrow<GATED>(a, row0, warp * 16),
+                  &full[warp * FST + st]);
     }
   };
   // Row of the box that lane g's first half of a fragment is (the other one
@@ -501,13 +587,16 @@ __global__ void __launch_bounds__(32 * FW)
   }
   // An infinite x has an infinite offset, so that its sums are infinity minus
   // infinity (and the offsets of numbers near bf16's end leave f32's range).
-  if (!finite) sum_again<T, TT, FROWS>(a, boxes, part);
+  if (!finite) sum_again<T, TT, FROWS, GATED>(a, boxes, part);
   namespace cg = cooperative_groups;
   if (nrank > 1)
     cg::this_cluster().sync();
   else
     __syncthreads();
-  reduce_finish<T, FROWS>(a, part, rank, nrank, NTHR, ntok, tok0, row0);
+  if constexpr (GATED)
+    reduce_finish_gated<T, FROWS>(a, part, rank, nrank, NTHR, ntok, tok0, row0);
+  else
+    reduce_finish<T, FROWS>(a, part, rank, nrank, NTHR, ntok, tok0, row0);
   if (nrank > 1) cg::this_cluster().sync();  // peers read this CTA's sums until here
 }
 
@@ -637,10 +726,10 @@ __device__ __forceinline__ bool wait_both(uint64_t* x, uint32_t xp, uint64_t* y,
 
 // The rows' ladders as (hi, lo) pairs, and the powers of two taken out.  The
 // dequantising threads: four a row, eight rungs each; barrier 2 is theirs.
-template <class T>
+template <class T, bool GATED>
 __device__ __forceinline__ void load_ladders(const LinearArgs& a, int row0, uint32_t* tab, float* rowscale,
                                              float* rowmax) {
-  const int i = threadIdx.x - 128, r = i % QROWS, part = i / QROWS, row = row0 + r;
+  const int i = threadIdx.x - 128, r = i % QROWS, part = i / QROWS, row = wrow<GATED>(a, row0, r);
   float s[8];
   float m = 0.f;
 #pragma unroll
@@ -701,7 +790,7 @@ __device__ __forceinline__ void dequant_stage(const uint8_t* box, int r, int j, 
 // warps (the lane quarters) halve a box: a warp decodes two stages of its 32
 // rows between looks at the barriers, always into the same columns of tensor
 // memory.  (With one stage a look, looking cost as much as decoding.)
-template <class T, bool PAIR, int NS>  // NS: boxes in the ring
+template <class T, bool PAIR, int NS, bool GATED>  // NS: boxes in the ring
 struct Dequant {
   int slot;        // of the next box of this team in the ring
   uint32_t phase;  // of its barrier
@@ -719,8 +808,9 @@ struct Dequant {
     const int team = (warp - 4) / 8, h = (warp - 4) / 4 % 2, r = (warp & 3) * 32 + lane;
     const int half = 2 * team + h, gpr = a.n / GROUP;
     const uint32_t taddr = (uint32_t)(QACOL + 64 * half) + ((uint32_t)(r & ~31) << 16);
-    const bool in = row0 + r < a.rows;
-    const uint8_t* rungs = a.rungs + (size_t)(in ? row0 + r : 0) * gpr;
+    const int wr = wrow<GATED>(a, row0, r);
+    const bool in = wr < a.rows;
+    const uint8_t* rungs = a.rungs + (size_t)(in ? wr : 0) * gpr;
     int b = (team ^ seq) & 1;
     int g0 = 8 * (box0 + b) + 4 * h;
     uint32_t q0 = four_rungs(rungs, in, g0, gpr), q1 = four_rungs(rungs, in, g0 + 16, gpr),
@@ -760,6 +850,18 @@ struct Dequant {
   }
 };
 
+// Copies of a box of codes (columns 256 b ..) of a tile's rows.
+template <bool GATED>
+__device__ __forceinline__ void load_box(const LinearArgs& a, uint32_t dst, const CUtensorMap* wmap, int b, int row0,
+                                         uint64_t* bar) {
+  if (GATED) {
+#pragma unroll 1
+    for (int r = 0; r < QROWS; r += 16) tma_load_2d(dst + r * 128, wmap, b * 128, wrow<true>(a, row0, r), bar);
+  } else {
+    tma_load_2d(dst, wmap, b * 128, row0, bar);
+  }
+}
+
 // ---- up to some hundreds of tokens: one SM a tile, the columns split over a cluster
 
 // Measured: 45 tokens, 14336 x 4096, GELU: 22.5 us, 112 tiles on 152 SMs.  A
@@ -771,7 +873,7 @@ constexpr int MNS = 4;     // boxes of codes
 constexpr int MXS = 4;     // double stages of x (up to 128 tokens a tile; half of them above)
 constexpr int MTN = 256;   // tokens per tile at most
 
-template <class T>
+template <class T, bool GATED>
 __global__ void __launch_bounds__(640, 1)
     k_q4_mid(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LinearArgs a, int tn,
              int boxes, int nx, WaitCfg wc) {
@@ -820,7 +922,7 @@ __global__ void __launch_bounds__(640, 1)
           const int b = h / 2, k = b % MNS;
           if (!wait_bar(&nempty[k], ((uint32_t)(b / MNS) & 1u) ^ 1u, abort, wc.ns)) break;
           mbar_expect_tx(&nfull[k], QBOX);
-          tma_load_2d(smem_u32(nring + k * QBOX), &wmap, (box0 + b) * 128, row0, &nfull[k]);
+          load_box<GATED>(a, smem_u32(nring + k * QBOX), &wmap, box0 + b, row0, &nfull[k]);
         }
         if (!wait_bar(&xempty[s], ph, abort, wc.ns)) break;
         mbar_expect_tx(&xfull[s], 2u * (uint32_t)xbytes);
@@ -866,8 +968,8 @@ __global__ void __launch_bounds__(640, 1)
     }
   } else if (warp >= 4) {
     const int j = (warp - 4) / 4, q = warp & 3, r = q * 32 + lane;
-    load_ladders<T>(a, row0, tab, rowscale, rowmax);
-    Dequant<T, false, MNS> dq;
+    load_ladders<T, GATED>(a, row0, tab, rowscale, rowmax);
+    Dequant<T, false, MNS, GATED> dq;
     bool ok = dq.tile(a, row0, box0, nbox, 0, nring, tab, nfull, nempty, afull, aempty, abort, wc.ns);
     // Sums to shared memory [token][row] (over the x ring: its MMAs are done).
     if (ok) ok = wait_bar_warp(&done, 0u, abort, wc.ns);
@@ -898,7 +1000,10 @@ __global__ void __launch_bounds__(640, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base_sh), "r"(512u) : "memory");
   namespace cg = cooperative_groups;
   if (nrank > 1) cg::this_cluster().sync();
-  reduce_finish<T, QROWS>(a, reinterpret_cast<const float*>(smem), rank, nrank, 640, min(tn, a.tokens - tok0), tok0, row0);
+  if constexpr (GATED)
+    reduce_finish_gated<T, QROWS>(a, reinterpret_cast<const float*>(smem), rank, nrank, 640, min(tn, a.tokens - tok0), tok0, row0);
+  else
+    reduce_finish<T, QROWS>(a, reinterpret_cast<const float*>(smem), rank, nrank, 640, min(tn, a.tokens - tok0), tok0, row0);
   if (nrank > 1) cg::this_cluster().sync();  // peers read this CTA's sums until here
 }
 
@@ -920,7 +1025,7 @@ constexpr int PTN = 256;  // tokens per tile at most
 // through the tile (two sums of 160 tokens and four stages did not: 640
 // cycles a stage), and the next tile's first stages are ready when the sums
 // have been read.
-template <class T>
+template <class T, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
     k_q4_many(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LinearArgs a, int tn,
               int mt, int tiles, WaitCfg wc) {
@@ -977,7 +1082,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
             const int s = box % PNS;
             if (!(ok = wait_bar(&nempty[s], ((uint32_t)(box / PNS) & 1u) ^ 1u, abort, wc.ns))) break;
             mbar_expect_tx(&nfull[s], QBOX);
-            tma_load_2d(smem_u32(nring + s * QBOX), &wmap, (h / 2) * 128, row0, &nfull[s]);
+            load_box<GATED>(a, smem_u32(nring + s * QBOX), &wmap, h / 2, row0, &nfull[s]);
             ++box;
           }
           const int s = half % PXS;
@@ -1026,12 +1131,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
       }
     }
   } else if (warp >= 4 && warp < 4 + QDEQ) {
-    Dequant<T, true, PNS> dq;
+    Dequant<T, true, PNS, GATED> dq;
     int k = 0;
     bool ok = true;
     for (int t = pair; t < tiles; t += npairs, ++k) {
       const int row0 = (t % mt) * 2 * QROWS + (int)rank * QROWS;
-      load_ladders<T>(a, row0, tab, rowscale[k & 3], rowmax);
+      load_ladders<T, GATED>(a, row0, tab, rowscale[k & 3], rowmax);
       if (threadIdx.x == 128) mbar_arrive(&scaled[k & 3]);  // (behind load_ladders' last barrier)
       // After a wait has run out the warps only keep meeting at the ladders' barriers.
       if (ok) ok = dq.tile(a, row0, 0, nbox, k * nbox, nring, tab, nfull, nempty, afull, aempty, abort, wc.ns);
@@ -1052,7 +1157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
       int c = half == 0 ? 0 : tn / 2;
       uint4 raw[2] = {};
       auto fetch = [&](int cc) {
-        if (cc + tk < c1) {
+        if (!GATED && cc + tk < c1) {
           residual8<T>(a, tok0 + cc + tk, row0 + tr, v0, raw[0]);
           residual8<T>(a, tok0 + cc + tk, row0 + tr + 8, v1, raw[1]);
         }
@@ -1074,14 +1179,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
         float w[2][8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 f = *reinterpret_cast<const float4*>(turn + tk * 36 + lane % 2 * 16 + 4 * i);
+          // Gated: eight rows of the gate, the same eight outputs of the up projection.
+          const int at = GATED ? lane % 2 * 8 + i / 2 * 16 + i % 2 * 4 : lane % 2 * 16 + 4 * i;
+          const float4 f = *reinterpret_cast<const float4*>(turn + tk * 36 + at);
           w[i / 2][i % 2 * 4] = f.x; w[i / 2][i % 2 * 4 + 1] = f.y;
           w[i / 2][i % 2 * 4 + 2] = f.z; w[i / 2][i % 2 * 4 + 3] = f.w;
         }
         __syncwarp();
         const uint4 now[2] = {raw[0], raw[1]};
         fetch(c + 16);
-        if (c + tk < c1) {
+        if (GATED) {
+          const int r8 = row0 / 2 + q * 16 + lane % 2 * 8;
+          if (c + tk < c1 && r8 < a.rows / 2) finish_gated8<T>(a, tok0 + c + tk, r8, w[0], w[1]);
+        } else if (c + tk < c1) {
           if (row0 + tr < a.rows) finish8<T>(a, tok0 + c + tk, row0 + tr, v0, w[0], now[0]);
           if (row0 + tr + 8 < a.rows) finish8<T>(a, tok0 + c + tk, row0 + tr + 8, v1, w[1], now[1]);
         }
@@ -1145,17 +1255,17 @@ struct FewLaunch {
 constexpr int kFewSlots = 8;  // CTAs an SM at most
 constexpr size_t few_slot_smem(int slots) { return 233472 / slots - 1536; }
 
-template <class T, int TT, int FW>
+template <class T, int TT, int FW, bool GATED>
 gptq_status few_launch(const LinearArgs& a, cudaStream_t s) {
   constexpr int FROWS = 16 * FW;
   static DeviceOnce attr;
   static int active[9][kFewSlots + 1];  // clusters of k that run at once, by CTAs an SM
   GQ_TRY(attr.run([](int) -> gptq_status {
-    GQ_CUDA(cudaFuncSetAttribute(k_q4_few<T, TT, FW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem));
+    GQ_CUDA(cudaFuncSetAttribute(k_q4_few<T, TT, FW, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem));
     for (int k = 1; k <= 8; ++k)
       for (int n = 1; n <= kFewSlots; ++n) {
         FewLaunch<T, TT, FW> l(1, (unsigned)k, 1, std::min(few_slot_smem(n), kFewSmem));
-        GQ_CUDA(cudaOccupancyMaxActiveClusters(&active[k][n], k_q4_few<T, TT, FW>, &l.cfg));
+        GQ_CUDA(cudaOccupancyMaxActiveClusters(&active[k][n], k_q4_few<T, TT, FW, GATED>, &l.cfg));
       }
     return GPTQ_OK;
   }));
@@ -1188,7 +1298,7 @@ gptq_status few_launch(const LinearArgs& a, cudaStream_t s) {
   FewLaunch<T, TT, FW> l((unsigned)rb, (unsigned)split, (unsigned)tz, few_smem<TT, FW>(boxes));
   l.cfg.stream = s;
   GQ_PROF(K_Q4_LINEAR, s);
-  GQ_CUDA(cudaLaunchKernelEx(&l.cfg, k_q4_few<T, TT, FW>, m, a, boxes, wait_cfg()));
+  GQ_CUDA(cudaLaunchKernelEx(&l.cfg, k_q4_few<T, TT, FW, GATED>, m, a, boxes, wait_cfg()));
   return GPTQ_OK;
 }
 
@@ -1198,12 +1308,12 @@ bool few_fits(const LinearArgs& a) {
   return few_smem<TT, FW>(((a.n / GROUP + 7) / 8 + 7) / 8) <= kFewSmem;
 }
 
-template <class T>
+template <class T, bool GATED>
 gptq_status few_tokens(const LinearArgs& a, cudaStream_t s) {
-  if (a.tokens == 1) return few_launch<T, 1, 4>(a, s);
-  if (a.tokens == 2) return few_launch<T, 2, 4>(a, s);
-  if (a.tokens > 4 && few_fits<8, 8>(a)) return few_launch<T, 8, 8>(a, s);
-  return few_launch<T, 4, 8>(a, s);
+  if (a.tokens == 1) return few_launch<T, 1, 4, GATED>(a, s);
+  if (a.tokens == 2) return few_launch<T, 2, 4, GATED>(a, s);
+  if (a.tokens > 4 && few_fits<8, 8>(a)) return few_launch<T, 8, 8, GATED>(a, s);
+  return few_launch<T, 4, 8, GATED>(a, s);
 }
 
 // x [tokens][n] of T as boxes of 64 columns, 128-byte swizzle.
@@ -1231,13 +1341,13 @@ struct MidShape {
 // SM; clusters stay within a part of the GPU, so that 152 SMs hold 36 clusters
 // of four, 23 of six and 15 of eight: 2048 x 4096, 45 tokens, in sixteen of
 // eight took 25.2 us, in sixteen of six it takes 12.7).
-template <class T>
+template <class T, bool GATED>
 gptq_status mid_clusters(const int** out) {
   static DeviceOnce attr;
   static int active[9];
   GQ_TRY(attr.run([](int) -> gptq_status {
     constexpr int most = 1024 + MNS * QBOX + 128 * 1024 + QROWS * QTAB * 4;
-    GQ_CUDA(cudaFuncSetAttribute(k_q4_mid<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    GQ_CUDA(cudaFuncSetAttribute(k_q4_mid<T, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     for (int k = 1; k <= 8; ++k) {
       cudaLaunchConfig_t cfg{};
       cfg.gridDim = dim3(1, 1, (unsigned)k);
@@ -1250,7 +1360,7 @@ gptq_status mid_clusters(const int** out) {
       cfg.attrs = at;
       cfg.numAttrs = 1;
       int n = 0;
-      GQ_CUDA(cudaOccupancyMaxActiveClusters(&n, k_q4_mid<T>, &cfg));
+      GQ_CUDA(cudaOccupancyMaxActiveClusters(&n, k_q4_mid<T, GATED>, &cfg));
       active[k] = n < 1 ? 1 : n;
     }
     return GPTQ_OK;
@@ -1279,12 +1389,12 @@ MidShape mid_shape(const LinearArgs& a, const int* active) {
   return best;
 }
 
-template <class T>
+template <class T, bool GATED>
 gptq_status mid_launch(const LinearArgs& a, const MidShape& ms, cudaStream_t s) {
   const int rb = (a.rows + QROWS - 1) / QROWS, nt = ms.nt, tn = ms.tn, boxes = ms.boxes, split = ms.split;
   const int nx = tn > 128 ? MXS / 2 : MXS;
   CUtensorMap wm, xm;
-  GQ_TRY(make_code_map(&wm, a.nibbles, a.rows, a.n, QROWS));
+  GQ_TRY(make_code_map(&wm, a.nibbles, a.rows, a.n, GATED ? 16 : QROWS));
   GQ_TRY(make_x_map(&xm, a, std::is_same<T, __nv_bfloat16>::value, tn));
   size_t smem = 1024 + (size_t)MNS * QBOX + (size_t)2 * nx * tn * 128 + (size_t)QROWS * QTAB * 4;
   cudaLaunchConfig_t cfg{};
@@ -1300,7 +1410,7 @@ gptq_status mid_launch(const LinearArgs& a, const MidShape& ms, cudaStream_t s) 
   cfg.attrs = at;
   cfg.numAttrs = 1;
   GQ_PROF(K_Q4_MID, s);
-  GQ_CUDA(cudaLaunchKernelEx(&cfg, k_q4_mid<T>, wm, xm, a, tn, boxes, nx, wait_cfg()));
+  GQ_CUDA(cudaLaunchKernelEx(&cfg, k_q4_mid<T, GATED>, wm, xm, a, tn, boxes, nx, wait_cfg()));
   return GPTQ_OK;
 }
 
@@ -1316,12 +1426,12 @@ int many_tile(int tokens, int mt, int pairs, long long& rounds) {
   return best;
 }
 
-template <class T>
+template <class T, bool GATED>
 gptq_status many_launch(const LinearArgs& a, cudaStream_t s) {
   static DeviceOnce attr;
   constexpr int most = 1024 + PNS * QBOX + 2 * PXS * (PTN / 2) * 128 + QROWS * QTAB * 4 + 8 * 16 * 36 * 4;
   GQ_TRY(attr.run([](int) -> gptq_status {
-    GQ_CUDA(cudaFuncSetAttribute(k_q4_many<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    GQ_CUDA(cudaFuncSetAttribute(k_q4_many<T, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     return GPTQ_OK;
   }));
   const int mt = (a.rows + 2 * QROWS - 1) / (2 * QROWS);
@@ -1331,40 +1441,45 @@ gptq_status many_launch(const LinearArgs& a, cudaStream_t s) {
   const long long tiles = (long long)mt * ((a.tokens + tn - 1) / tn);
   if (tiles > (1ll << 30)) return GPTQ_ERR_SHAPE;
   CUtensorMap wm, xm;
-  GQ_TRY(make_code_map(&wm, a.nibbles, a.rows, a.n, QROWS));
+  GQ_TRY(make_code_map(&wm, a.nibbles, a.rows, a.n, GATED ? 16 : QROWS));
   GQ_TRY(make_x_map(&xm, a, std::is_same<T, __nv_bfloat16>::value, tn / 2));
   const int np = tiles < pairs ? (int)tiles : pairs;
   const size_t smem = 1024 + (size_t)PNS * QBOX + (size_t)2 * PXS * (tn / 2) * 128 + (size_t)QROWS * QTAB * 4 +
                       8 * 16 * 36 * 4;
   GQ_PROF(K_Q4_MANY, s);
-  k_q4_many<T><<<2 * np, 896, smem, s>>>(wm, xm, a, tn, mt, (int)tiles, wait_cfg());
+  k_q4_many<T, GATED><<<2 * np, 896, smem, s>>>(wm, xm, a, tn, mt, (int)tiles, wait_cfg());
   GQ_LAUNCHED();
   return GPTQ_OK;
 }
 
-template <class T>
+template <class T, bool GATED>
 gptq_status linear_t(const LinearArgs& a, cudaStream_t s) {
   // Up to 8 tokens the few-token kernel is the faster (5120 x 17408: 18 / 27
   // us for 1 / 8 tokens against 28); at 16 its blocks of x leave one CTA a SM
   // (58 us against 29).
-  if (a.tokens <= 8) return few_tokens<T>(a, s);
+  if (a.tokens <= 8) return few_tokens<T, GATED>(a, s);
   // Cycles of the two kernels as measured over 17 .. 4096 tokens (4096 x
   // 4096, 5120 x 17408, 14336 x 4096): mid_shape has the first's; a stage takes
   // 540 on a pair of SMs, which spends 13000 more on a tile.
   const int* active = nullptr;
-  GQ_TRY(mid_clusters<T>(&active));
+  GQ_TRY((mid_clusters<T, GATED>(&active)));
   const MidShape ms = mid_shape(a, active);
   long long rounds;
   many_tile(a.tokens, (a.rows + 2 * QROWS - 1) / (2 * QROWS), num_sms() / 2, rounds);
   const double many = (double)rounds * ((a.n / GROUP + 7) / 8 * 4 * 540.0 + 13000.0);
-  return ms.cycles <= many ? mid_launch<T>(a, ms, s) : many_launch<T>(a, s);
+  return ms.cycles <= many ? mid_launch<T, GATED>(a, ms, s) : many_launch<T, GATED>(a, s);
 }
 
 }  // namespace
 
 gptq_status q4tp_linear_run(int dtype, const LinearArgs& a, cudaStream_t s) {
   if (a.tokens == 0) return GPTQ_OK;
-  return dtype == GPTQ_BF16 ? linear_t<__nv_bfloat16>(a, s) : linear_t<__half>(a, s);
+  return dtype == GPTQ_BF16 ? linear_t<__nv_bfloat16, false>(a, s) : linear_t<__half, false>(a, s);
+}
+
+gptq_status q4tp_gated_run(int dtype, const LinearArgs& a, cudaStream_t s) {
+  if (a.tokens == 0) return GPTQ_OK;
+  return dtype == GPTQ_BF16 ? linear_t<__nv_bfloat16, true>(a, s) : linear_t<__half, true>(a, s);
 }
 
 }  // namespace gq

@@ -206,9 +206,16 @@ struct AttnArgs {
   uint32_t up;       // 2^kPos of T (see code16)
   unsigned* status;
   bool first = true, last = true;  // the launch has the call's first, last sequence
+  float* lse = nullptr;            // [tq][heads * group] logarithm of each row's sum (may be null)
 };
 
-// Zeros for the output rows that are no sequence's: before the first one's,
+// The logarithm of a row's sum of exp(score): of the maximum `top` of its
+// unscaled scores and the sum `den` relative to it.
+__device__ __forceinline__ float log_sum(float sl, float top, float den) {
+  return den != 0.f ? fmaf(sl, top, log2f(den)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Zeros (and sums of nothing) for the output rows that are no sequence's: before the first one's,
 // after the last one's and past max_q of their own.  By `ctas` CTAs of a
 // launch, this one number `cta`; a.q_starts is given.
 template <class T, int D>
@@ -218,6 +225,9 @@ __device__ __forceinline__ void zero_other_rows(const AttnArgs& a, int cta, int 
     const int n = a.heads * a.group * (D / 8);  // 16 bytes each
     uint4* dst = static_cast<uint4*>(a.out) + (long long)row * n;
     for (int i = threadIdx.x; i < n; i += blockDim.x) dst[i] = uint4{};
+    if (a.lse != nullptr)
+      for (int i = threadIdx.x; i < a.heads * a.group; i += blockDim.x)
+        a.lse[(long long)row * a.heads * a.group + i] = -INFINITY;
   };
   if (a.first)
     for (int r = cta, end = start(0); r < end; r += ctas) zero(r);
@@ -226,6 +236,24 @@ __device__ __forceinline__ void zero_other_rows(const AttnArgs& a, int cta, int 
   for (int b = cta; b < a.seqs; b += ctas)
     for (int r = start(b), end = start(b + 1), i = a.max_q; i < end - r; ++i) zero(r + i);
 }
+
+// Arguments of the eviction: tables of where tokens are and where they go.
+struct EvictArgs {
+  uint8_t* cache;
+  long long pages;
+  int heads, page_size;
+  const int* table;
+  int table_stride;
+  const int* out_table;
+  int out_stride;
+  const int* kv_lens;
+  int seqs;
+  const float* weights;  // [seqs][heads][table_stride * page_size]
+  int keep, recent;      // recent <= keep
+  int* kept;             // [seqs][heads][keep]
+  int* out_lens;
+  float* out_weights;  // [seqs][heads][out_stride * page_size]
+};
 
 // The driver's tensor-map encoder (null when it cannot be had).
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();

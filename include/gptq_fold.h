@@ -429,6 +429,22 @@ gptq_status gptq_q4tp_linear(int dtype, const void* X, long long ldx, int tokens
                              long long ldr, void* Y, long long ldy, uint32_t* status, void* stream);
 
 /*
+ * gptq_q4tp_gated -- Y = act(X Wg^T + bg) * (X Wu^T + bu) in one launch, with
+ * the gate's `inner` rows and then the up projection's in one q4tp matrix W of
+ * 2 * inner rows (one Hessian group: both read X).  Sums, activation and the
+ * product in f32, one rounding to T; weights as in gptq_q4tp_linear.
+ *
+ *   nibbles  in  u8 inner*n;  rungs in u8 2*inner*n/32;  tab in f32 2*inner*32.
+ *   bias     in  T 2*inner (may be NULL).
+ *   Y        out T tokens*inner, row stride ldy.
+ *   n % 32 == 0; ldx a multiple of 8; ldy >= inner; 2 * inner <= GPTQ_MAX_ROWS.
+ */
+gptq_status gptq_q4tp_gated(int dtype, const void* X, long long ldx, int tokens,
+                            const uint8_t* nibbles, const uint8_t* rungs, const float* tab,
+                            int inner, int n, const void* bias, int act, void* Y, long long ldy,
+                            uint32_t* status, void* stream);
+
+/*
  * The cache: a pool of `pages` pages of page_size tokens (a multiple of 16,
  * at most 4096) for `heads` key heads of `dim` channels (64, 128 or 256), u8
  * [pages][heads][page_size * dim * 5 / 4].  A page holds blocks of 16
@@ -457,6 +473,39 @@ gptq_status gptq_kv4_write(int dtype, uint8_t* cache, long long pages, int heads
                            int page_size, const void* K, const void* V, long long kt, long long kh,
                            long long vt, long long vh, const long long* slots, int tokens,
                            void* stream);
+
+/*
+ * Rotary positions: a pair (x0, x1) of channels of a head with frequency f
+ * becomes, at position p,
+ *   y0 = x0 c - x1 s, y1 = x1 c + x0 s, c = gain cos(p f), s = gain sin(p f)
+ * in f32, rounded once to T.  The first `rot` channels of a head turn (rot a
+ * multiple of 16), the others stay; pair i is channels (i, i + rot/2) or
+ * (2i, 2i + 1).  turns (device i64 [rot/2]) holds f as 2^64ths of a turn a
+ * position, round(f / (2 pi) 2^64) modulo 2^64: the angle is exact to 2^-32 of
+ * a turn for every position.  positions: device i64 [tokens], any sign.
+ *
+ * gptq_rotary            Y = X turned, T [tokens][heads][dim] each with strides
+ *                        (xt, yt between tokens, xh, yh between heads; multiples
+ *                        of 8).  Y may be X itself (then of the same strides),
+ *                        else they do not overlap.  dim a multiple of 16, at most
+ *                        1024.
+ * gptq_kv4_write_rotary  Y = Q turned, K turned and V quantised into the cache:
+ *                        the bits of gptq_rotary on Q and on K, then
+ *                        gptq_kv4_write.  Q, Y have q_heads heads, K and V the
+ *                        cache's.  Rows of a slot outside the pool still turn Q.
+ */
+typedef enum { GPTQ_ROTARY_HALF = 0, GPTQ_ROTARY_INTERLEAVED = 1 } gptq_rotary_layout;
+gptq_status gptq_rotary(int dtype, const void* X, long long xt, long long xh, int tokens, int heads,
+                        int dim, int rot, int layout, const long long* positions,
+                        const long long* turns, float gain, void* Y, long long yt, long long yh,
+                        void* stream);
+gptq_status gptq_kv4_write_rotary(int dtype, uint8_t* cache, long long pages, int heads, int dim,
+                                  int page_size, const void* Q, long long qt, long long qh,
+                                  int q_heads, const void* K, const void* V, long long kt,
+                                  long long kh, long long vt, long long vh, const long long* slots,
+                                  int tokens, int rot, int layout, const long long* positions,
+                                  const long long* turns, float gain, void* Y, long long yt,
+                                  long long yh, void* stream);
 
 /*
  * gptq_kv4_read -- the values of the slots: K, V out T [tokens][heads][dim]
@@ -505,6 +554,67 @@ gptq_status gptq_kv4_attention(int dtype, const void* Q, long long q_ts, long lo
                                const int* kv_lens, const int* q_starts, int seqs, int max_q,
                                float scale, void* out, void* ws, size_t ws_bytes, uint32_t* status,
                                void* stream);
+
+/*
+ * gptq_kv4_attention_lse -- gptq_kv4_attention, and lse (f32 [tq][heads*group],
+ * may be NULL): the logarithm of each row's sum of exp(scale q k) over the keys
+ * that it sees, -inf where it sees none or is no sequence's row.
+ */
+gptq_status gptq_kv4_attention_lse(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
+                                   const uint8_t* cache, long long pages, int heads, int group,
+                                   int dim, int page_size, const int* table, int table_stride,
+                                   const int* kv_lens, const int* q_starts, int seqs, int max_q,
+                                   float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                                   uint32_t* status, void* stream);
+
+/*
+ * gptq_kv4_attention_weights -- what the queries of a gptq_kv4_attention call
+ * looked at, added up:
+ *   weights[b][h][t] += sum exp(scale q k_t - lse(q))
+ * over the queries q of sequence b that see its token t, of the `group` query
+ * heads of key head h.  Other arguments as there, and lse as it returned it.
+ *   weights  in/out f32 [seqs][heads][table_stride * page_size], by the token's
+ *            place in the sequence.  Places past kv_lens and sequences without
+ *            queries stay as they are.
+ * f32 scores, exponentials and sums, each place's in one fixed order.  A key that
+ * is NaN makes its own place NaN.
+ */
+gptq_status gptq_kv4_attention_weights(int dtype, const void* Q, long long q_ts, long long q_hs,
+                                       int tq, const float* lse, const uint8_t* cache,
+                                       long long pages, int heads, int group, int dim,
+                                       int page_size, const int* table, int table_stride,
+                                       const int* kv_lens, const int* q_starts, int seqs,
+                                       int max_q, float scale, float* weights, uint32_t* status,
+                                       void* stream);
+
+/*
+ * gptq_kv4_evict -- cut every sequence to at most `keep` tokens a key head.  A
+ * head of a longer one keeps its last min(recent, keep) tokens and the heaviest
+ * of the others (equal weights: the earlier token; a NaN is the lightest), each
+ * head its own, in their order and one after the other from place 0: keys carry
+ * their positions in them, so that attention does not care where they lie.  A
+ * shorter one keeps all it has.  Bytes move as they are (any T).
+ *
+ *   table       in  i32 [seqs][table_stride], as for the attention.
+ *   out_table   in  i32 [seqs][out_stride]: pages that take the kept tokens; NULL:
+ *               those of `table` itself.  A page that takes tokens is one sequence's
+ *               and, unless out_table is NULL, in no row of `table` (pages that
+ *               only lose tokens may be shared).  Tokens for an entry outside the
+ *               pool are dropped.
+ *   kv_lens     in  i32 [seqs];  out_lens out i32 [seqs]: min(kv_lens, keep).
+ *   weights     in  f32 [seqs][heads][table_stride * page_size].
+ *   kept        out i32 [seqs][heads][keep]: earlier place of the token now at each
+ *               place, -1 past the end.
+ *   out_weights out f32 [seqs][heads][out_stride (NULL: table_stride) * page_size]:
+ *               the kept tokens' weights, zeros past them.
+ *   keep at most the places of the row of the table that takes the tokens;
+ *   seqs * heads at most 2^24.
+ *   Outputs overlap no input.
+ */
+gptq_status gptq_kv4_evict(uint8_t* cache, long long pages, int heads, int dim, int page_size,
+                           const int* table, int table_stride, const int* out_table, int out_stride,
+                           const int* kv_lens, int seqs, const float* weights, int keep, int recent,
+                           int* kept, int* out_lens, float* out_weights, void* stream);
 
 /*
  * Tracing: launch accounting and per-kernel timing.  Every kernel launch of

@@ -124,3 +124,76 @@ def attention(q, k, v, lens, group, scale, q_lens=None):
                     out[at + i, h] = p @ vv / p.sum()
         at += nq
     return out
+
+
+def gated(x, nibbles, rungs, tab, bias=None, act="silu"):
+    """act(x Wg^T + bg) * (x Wu^T + bu): the gate's rows come first."""
+    y = linear(x, nibbles, rungs, tab, bias)
+    half = y.shape[1] // 2
+    with np.errstate(all="ignore"):
+        return activate(y[:, :half], act) * y[:, half:]
+
+
+def angles(positions, turns):
+    """Radians [tokens, pairs] of positions times turns (2^64ths of a turn a
+    position), modulo one turn: exact in whole numbers but for the last step."""
+    return np.array([[2 * math.pi * ((int(p) * int(t)) % 2 ** 64) / 2 ** 64 for t in turns] for p in positions])
+
+
+def rotary(x, angle, layout="half", gain=1.0):
+    """x [tokens, heads, dim] turned by angle [tokens, pairs]."""
+    y = np.array(x, dtype=F64)
+    n = angle.shape[1]
+    i, j = (slice(0, n), slice(n, 2 * n)) if layout == "half" else (slice(0, 2 * n, 2), slice(1, 2 * n, 2))
+    a, b = y[..., i].copy(), y[..., j].copy()
+    c, s = gain * np.cos(angle)[:, None], gain * np.sin(angle)[:, None]
+    with np.errstate(all="ignore"):
+        y[..., i], y[..., j] = a * c - b * s, b * c + a * s
+    return y
+
+
+def log_sums(q, k, lens, group, scale, q_lens=None):
+    """Logarithm of each row's sum of exp(score), as `attention` sees its keys;
+    -inf where a row sees none."""
+    q = np.asarray(q, dtype=F64)
+    out = np.full(q.shape[:2], -np.inf)
+    at = 0
+    for b, ln in enumerate(lens):
+        nq = 1 if q_lens is None else q_lens[b]
+        for i in range(nq):
+            m = ln - nq + i + 1
+            if m > 0:
+                for h in range(q.shape[1]):
+                    sc = k[b][:m, h // group].astype(F64) @ q[at + i, h] * scale
+                    out[at + i, h] = sc.max() + math.log(np.exp(sc - sc.max()).sum())
+        at += nq
+    return out
+
+
+def attention_weights(q, k, lens, group, scale, lse, q_lens=None):
+    """One array [heads, len] a sequence: the sum of exp(score - lse) over the
+    rows that see a token."""
+    q = np.asarray(q, dtype=F64)
+    out, at = [], 0
+    for b, ln in enumerate(lens):
+        nq = 1 if q_lens is None else q_lens[b]
+        w = np.zeros((q.shape[1] // group, ln))
+        for i in range(nq):
+            m = ln - nq + i + 1
+            if m > 0:
+                for h in range(q.shape[1]):
+                    w[h // group, :m] += np.exp(k[b][:m, h // group].astype(F64) @ q[at + i, h] * scale - lse[at + i, h])
+        out.append(w)
+        at += nq
+    return out
+
+
+def kept(weights, length, keep, recent):
+    """Places of one head that stay, in order: the last min(recent, keep) and the
+    heaviest of the others, equal ones the earlier first, a NaN the lightest."""
+    if length <= keep:
+        return list(range(length))
+    old = length - min(recent, keep)
+    w = np.asarray(weights, dtype=F64)[:old]
+    order = sorted(range(old), key=lambda t: (0 if np.isnan(w[t]) else -1, 0.0 if np.isnan(w[t]) else -w[t], t))
+    return sorted(order[:keep - (length - old)]) + list(range(old, length))
