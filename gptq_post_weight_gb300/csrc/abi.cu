@@ -78,7 +78,7 @@ gptq_status kv4_write_rotary_run(int dtype, bool half, uint8_t* cache, long long
 size_t kv4_attention_ws_bytes(int dim, int heads, int group, int max_q, int seqs, bool single, long long max_len);
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s);
 gptq_status kv4_no_sums_run(float* lse, long long n, cudaStream_t s);
-gptq_status kv4_weigh_run(int dtype, int dim, const AttnArgs& a, const float* lse, float* weights, cudaStream_t s);
+gptq_status kv4_weigh_run(int dtype, int dim, const AttnArgs& a, float scale, const float* lse, float* weights, cudaStream_t s);
 gptq_status kv4_evict_run(int dim, bool in_place, const EvictArgs& a, cudaStream_t s);
 }  // namespace gq
 
@@ -839,7 +839,7 @@ gptq_status gptq_kv4_attention_weights(int dtype, const void* Q, long long q_ts,
   AttnArgs a{Q,     q_ts,         q_hs,    tq,       cache, pages, heads, group, page_size,
              table, table_stride, kv_lens, q_starts, seqs,  max_q, scale * 1.4426950408889634f,
              nullptr, nullptr, nullptr, dtype == GPTQ_BF16 ? 8u : 64u, status};
-  return kv4_weigh_run(dtype, dim, a, lse, weights, as_stream(stream));
+  return kv4_weigh_run(dtype, dim, a, scale, lse, weights, as_stream(stream));
 }
 
 gptq_status gptq_kv4_evict(uint8_t* cache, long long pages, int heads, int dim, int page_size, const int* table,

@@ -86,7 +86,7 @@ def test_write_rotary(blib):  # noqa: F811
     refused(f, cache, q, k, k, s, 16, p[:4], t, match="positions must have 5")
     refused(f, cache, q, k, k, s, 16, p, t[:4], match="turns must have")
     refused(f, cache, q, k, k, s, 16, p, t, out=b16(5, 8, 32), match="out must have shape")
-    refused(f, cache, q, k, k.clone().requires_grad_(), s, 16, p, t, match="k requires a gradient")
+    refused(f, cache, q, k, k.clone().requires_grad_(), s, 16, p, t, match="v requires a gradient")
     refused(f, cache, q, k, k, s, 16, p, t, match="CUDA tensors")
 
 
