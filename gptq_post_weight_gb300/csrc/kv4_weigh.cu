@@ -12,27 +12,32 @@
 // reads its lane then has one key's scores, and the sum over the query rows
 // stays in its registers: no maximum, no exchange between lanes, and no second
 // product.  A CTA fills an SM and is a line of workers:
-//   warp 16      copies the key halves of a tile's eight cache blocks;
-//   warps 8-15   decode them into 128-byte swizzled rows (operand A), once for
-//                all query rows, and bring the rows' q (operand B), in the
-//                order in which the nibbles come out;
-//   warp 17      issues the products, four tiles of sums ahead in tensor memory;
-//   warps 0-7    exponentials and sums, two teams of a lane quarter a warp.
+//   warps 8-23   decode codes into 128-byte swizzled rows (operand A), once for
+//                all query rows: crews that take turns at the tiles, each with its
+//                next tile's codes on their way in registers;
+//   the last     issues the products, several steps ahead of the sums;
+//   warps 0-7    exponentials and sums, a lane quarter a warp: two teams, one
+//                for each of the two tiles (256 keys) that make a step.
 // Few rows a sequence and key head (!MANY: one column tile): a CTA takes a
-// contiguous share of the list of (sequence, key head, key tile), q stays while
-// the head does, and the teams take turns at the tiles.  Many: key tiles go
-// round the CTAs, and for each of them all the rows' tiles that see it come by,
-// a half of the columns a team.
+// contiguous share of the list of (sequence, key head, step), q (operand B, in
+// the order in which the nibbles come out; warp 24) stays while the head does.
+// Many: steps go round the CTAs, and for each of them all the rows' tiles that
+// see it come by, which the crews bring between the keys.
 #include "serve.cuh"
 
 namespace gq {
 namespace {
 
-constexpr int WKEYS = 128;           // keys of a tile
-constexpr int WTHREADS = 576;
+constexpr int WKEYS = 128;           // keys of a tile; two tiles are a step, one a team
+// (Registers go by eights a thread: without the warp that brings q, 80 and not 72.)
+constexpr int wthreads(bool many) { return many ? 800 : 832; }
 constexpr int WSEQS = 512;           // sequences of a launch at most
-constexpr int WRAW = 4;              // tiles of codes in flight at most
-constexpr int WD = 4;                // tiles of sums in tensor memory
+constexpr int WROWS = 8;             // rows' tiles whose logarithms are kept (more than WD + 2)
+constexpr int WD = 4;                // steps' sums in tensor memory at most
+// Tiles of keys in shared memory, and crews that take turns at them: a place is
+// always the same crew's.
+template <int D>
+constexpr int kTurns = D == 256 ? 2 : 4;
 template <int D>
 constexpr int kMostRows = D == 256 ? 64 : 128;  // query rows of a tile (shared memory)
 
@@ -51,7 +56,7 @@ struct WeighArgs {
   const float* lse;
   float* weights;
   int nt;    // columns of a tile: a multiple of 16
-  int nraw;  // tiles of codes in flight
+  int nd;    // steps' sums in tensor memory
 };
 
 __device__ __forceinline__ uint64_t pair2(float x, float y) {
@@ -80,40 +85,75 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   return r;
 }
 
-// Barrier of a team's 128 threads, AND-reducing: they go on or leave together.
-__device__ __forceinline__ bool team_all(int team, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.and.pred po, %2, 128, pi;\n"
-      " selp.u32 %0, 1, 0, po;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)p), "r"(1 + team)
-      : "memory");
-  return r != 0u;
-}
-// The same for both teams.
-__device__ __forceinline__ bool teams_all(bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.and.pred po, 3, 256, pi;\n"
-      " selp.u32 %0, 1, 0, po;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)p)
-      : "memory");
-  return r != 0u;
-}
-
-__device__ __forceinline__ void mma_keys(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accum)
-      : "memory");
+// wait_bar_warp, suspended for up to a microsecond a try: 26 warps that look again
+// at once take the issue slots of the ones at work.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  uint64_t t0 = 0;
+  bool ok = true;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (done != 0u) break;
+    if (*abort) {
+      ok = false;
+      break;
+    }
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit) {
+      *abort = 1;
+      ok = false;
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
-// A sequence: first query row, queries, keys, query rows of a key head, key tiles.
+// 32 lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// Waits on three barriers at once.
+__device__ __forceinline__ bool look_at(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ bool wait_three(uint64_t* x, uint32_t xp, uint64_t* y, uint32_t yp, uint64_t* z, uint32_t zp,
+                                           volatile int* abort, uint64_t limit) {
+  const bool ok = (look_at(x, xp) & look_at(y, yp) & look_at(z, zp)) ||
+                  (wait_bar(x, xp, abort, limit) && wait_bar(y, yp, abort, limit) && wait_bar(z, zp, abort, limit));
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The four products of 64 channels: A and B 32 bytes on per 16 of them; first: overwrite D.
+__device__ __forceinline__ void mma_keys(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool first) {
+  asm volatile(
+      "{\n .reg .pred p, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n setp.eq.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " add.u64 a1, %1, 2;\n add.u64 a2, %1, 4;\n add.u64 a3, %1, 6;\n"
+      " add.u64 b1, %2, 2;\n add.u64 b2, %2, 4;\n add.u64 b3, %2, 6;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)first)
+      : "memory");
+}
+
+// A sequence: first query row, queries, keys, query rows of a key head, steps of two key tiles.
 struct WSeq {
-  int q0, nq, len, rows, tiles;
+  int q0, nq, len, rows, steps;
 };
 __device__ __forceinline__ WSeq wseq_of(const AttnArgs& a, int b) {
   WSeq s;
@@ -121,17 +161,17 @@ __device__ __forceinline__ WSeq wseq_of(const AttnArgs& a, int b) {
   s.nq = a.q_starts != nullptr ? min(min(max(a.q_starts[b + 1], s.q0), a.tq) - s.q0, a.max_q) : 1;
   s.len = (int)min((long long)max(a.kv_lens[b], 0), (long long)a.table_stride * a.page_size);
   s.rows = s.nq * a.group;
-  s.tiles = s.nq > 0 ? (s.len + WKEYS - 1) / WKEYS : 0;
+  s.steps = s.nq > 0 ? (s.len + 2 * WKEYS - 1) / (2 * WKEYS) : 0;
   return s;
 }
 
-// A CTA's walk over the list of (sequence, key head, key tile).
+// A CTA's walk over the list of (sequence, key head, step).
 template <bool MANY>
 struct Walk {
   const AttnArgs& a;
   const long long* pref;
   long long u, end;
-  int b, head, tile;
+  int b, head, step;
   WSeq s;
 
   __device__ __forceinline__ Walk(const AttnArgs& args, const long long* prefix) : a(args), pref(prefix) {
@@ -156,61 +196,63 @@ struct Walk {
     b = lo;
     s = wseq_of(a, b);
     const long long rem = u - pref[b];
-    head = (int)(rem / s.tiles);
-    tile = (int)(rem % s.tiles);
+    head = (int)(rem / s.steps);
+    step = (int)(rem % s.steps);
   }
-  // Whether the next item has other query rows.
-  __device__ __forceinline__ bool next() {
+  // Steps from this one on that are neighbours in one head, `most` at most.
+  __device__ __forceinline__ int run(int most) const { return MANY ? 1 : (int)min((long long)min(most, s.steps - step), end - u); }
+  // On by so many steps of a run.  Whether the next one has other query rows.
+  __device__ __forceinline__ bool next(int n = 1) {
     if (MANY) {
       u += gridDim.x;
       find();
       return true;
     }
-    ++u;
-    if (++tile < s.tiles) return false;
-    tile = 0;
+    u += n;
+    if ((step += n) < s.steps) return false;
+    step = 0;
     if (++head == a.heads) find();
     return true;
   }
-  // The first tile of query rows that sees a key of this tile.
+  // The first tile of query rows that sees a key of this step.
   __device__ __forceinline__ int first_rows(int nt) const {
-    return max((tile * WKEYS - s.len + s.nq) * a.group, 0) / nt;
+    return max((step * 2 * WKEYS - s.len + s.nq) * a.group, 0) / nt;
   }
 };
 
 template <class T, int D, bool MANY>
-__global__ void __launch_bounds__(WTHREADS, 1) k_kv4_weigh(AttnArgs a, WeighArgs w, WaitCfg wc) {
+__global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, WeighArgs w, WaitCfg wc) {
   using T2 = typename Elem<T>::T2;
-  constexpr int HALVES = D / 64, RB = 10 * D, RAW = WKEYS / KV_BLOCK * RB, ATILE = WKEYS * D * 2;
+  constexpr int WTHREADS = wthreads(MANY), MMA = WTHREADS / 32 - 1;  // the warp that issues the products
+  constexpr int HALVES = D / 64, ATILE = WKEYS * D * 2, TURNS = kTurns<D>, CREW = 512 / TURNS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t rawfull[WRAW], rawempty[WRAW], afull[2], aempty[2], qfull[2], qempty[2], dfull[WD],
-      dempty[WD];
+  __shared__ __align__(8) uint64_t afull[TURNS], aempty[TURNS / 2], qfull[2], qempty[2], dfull[WD], dempty[WD];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ long long pref[WSEQS + 1], scratch[WTHREADS / 32];
-  __shared__ __align__(16) float nlse[2][2][128];  // [team][turn][row]: minus its logarithm of the sum
-  __shared__ int lastkey[2][2][128];               // the last key it sees
-  __shared__ float other[2][WKEYS];                // MANY: team 1's sums
+  __shared__ long long pref[WSEQS + 1], scratch[26];
+  // Of each row of a tile: minus its logarithm of the sum (-inf past the end: its
+  // exponentials are 0), and the last key that it sees.  Written with the tile, read
+  // by the sums, which may be WD steps behind the products, those two tiles behind
+  // the writer: a place's last readers are long gone.
+  __shared__ __align__(16) float nlse[WROWS][128];
+  __shared__ int lastkey[WROWS][128];
   volatile int* abort = &abort_sh;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int nt = w.nt, qtile = nt * D * 2;
-  uint8_t* asm_ = smem;                     // two tiles of keys
-  uint8_t* qsm = smem + 2 * ATILE;          // two tiles of query rows
-  uint8_t* raw = qsm + 2 * qtile;           // tiles of codes
+  uint8_t* asm_ = smem;                  // tiles of keys
+  uint8_t* qsm = smem + TURNS * ATILE;   // two tiles of query rows
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < WRAW; ++i) mbar_init(&rawfull[i], 1), mbar_init(&rawempty[i], 8);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&afull[i], 256), mbar_init(&aempty[i], 1);
-      mbar_init(&qfull[i], 256), mbar_init(&qempty[i], 1);
-    }
-    for (int i = 0; i < WD; ++i) mbar_init(&dfull[i], 1), mbar_init(&dempty[i], MANY ? 8 : 4);
+    for (int i = 0; i < TURNS; ++i) mbar_init(&afull[i], CREW);
+    for (int i = 0; i < TURNS / 2; ++i) mbar_init(&aempty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&qfull[i], MANY ? 256 : 32), mbar_init(&qempty[i], 1);
+    for (int i = 0; i < WD; ++i) mbar_init(&dfull[i], 1), mbar_init(&dempty[i], 8);
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == 17) {
+  if (warp == MMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_sh)),
                  "r"(512u)
                  : "memory");
@@ -221,7 +263,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_kv4_weigh(AttnArgs a, WeighArgs
     long long before = 0;
     for (int p0 = 0; p0 < a.seqs; p0 += WTHREADS) {
       const int p = p0 + (int)threadIdx.x;
-      const long long mine = p < a.seqs ? (long long)a.heads * wseq_of(a, p).tiles : 0;
+      const long long mine = p < a.seqs ? (long long)a.heads * wseq_of(a, p).steps : 0;
       long long inc = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -243,70 +285,92 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_kv4_weigh(AttnArgs a, WeighArgs
   }
   tc_fence_after();
 
+  struct Row {
+    float nlse;
+    int last;
+  };
+  auto row_of = [&](const Walk<MANY>& it, int r, bool in) {
+    Row row{-INFINITY, -1};
+    if (in && r < it.s.rows) {
+      const int qi = r / a.group;
+      row.nlse = -w.lse[((long long)it.s.q0 + qi) * a.heads * a.group + it.head * a.group + r % a.group];
+      row.last = it.s.len - it.s.nq + qi;
+    }
+    return row;
+  };
   if (warp < 8) {
     const int team = warp / 4, key = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int c0 = MANY ? team * (nt / 2) : 0, cn = MANY ? nt / 2 : nt;  // this team's columns
     const long long cap = (long long)a.table_stride * a.page_size;
     const float scale = a.scale_log2;  // (here the plain scale: see the launch)
     const uint64_t scale2 = pair2(scale, scale), log2e2 = pair2(1.4426950408889634f, 1.4426950408889634f);
-    int d = 0, turn = 0;
+    int d = 0, qn = MANY ? -1 : 0;
     uint32_t dph = 0u;
-    bool ok = true, fresh = true;
-    int i = 0;
-    // Row r of the rows' tile rt: what this team needs of it, into the buffer of `turn`.
-    auto look_up = [&](const Walk<MANY>& it, int rt) {
-      if (key < cn) {
-        const int rr = rt * nt + c0 + key, qi = rr / a.group;
-        const bool in = rr < it.s.rows;
-        const long long at = ((long long)it.s.q0 + qi) * a.heads * a.group + it.head * a.group + rr % a.group;
-        nlse[team][turn][key] = in ? -w.lse[at] : 0.f;
-        lastkey[team][turn][key] = in ? it.s.len - it.s.nq + qi : -1;
-      }
-    };
-    for (Walk<MANY> it(a, pref); it.there() && ok; ++i) {
-      const bool mine = MANY || (i & 1) == team;
-      const int t = it.tile * WKEYS + key;
-      float* out = w.weights + ((long long)it.b * a.heads + it.head) * cap + t;
-      const float old = mine && t < it.s.len && (!MANY || team == 0) ? *out : 0.f;
+    bool ok = true;
+    Walk<MANY> it(a, pref);
+    while (it.there()) {
+      const int k0 = (2 * it.step + team) * WKEYS, t = k0 + key;
       uint64_t sum2[2] = {0ull, 0ull};
       float masked_sum = 0.f;
       const int rt1 = MANY ? (it.s.rows + nt - 1) / nt : 1;
+#pragma unroll 1
       for (int rt = MANY ? it.first_rows(nt) : 0; rt < rt1; ++rt) {
-        if (mine) {
-          if (MANY || fresh) {
-            turn ^= 1;
-            look_up(it, rt);
-          }
-          fresh = false;
-          // (A row sees at least the keys of the rows before it.)
-          const int r0 = rt * nt + c0, have = min(cn, it.s.rows - r0);
-          const int first_last = it.s.len - it.s.nq + r0 / a.group;
-          ok = team_all(team, wait_bar_warp(&dfull[d], dph, abort, wc.ns));
-          if (!ok) break;
+        if (MANY) ++qn;
+        const int r0 = MANY ? rt * nt : 0, have = min(nt, it.s.rows - r0);
+        // Whether a row does not see a key of the tile that is there (a row sees
+        // at least the keys of the rows before it).
+        const bool masked = min(k0 + WKEYS, it.s.len) - 1 > it.s.len - it.s.nq + (MANY ? r0 / a.group : 0);
+        if (!(ok = wait_long(&dfull[d], dph, abort, wc.ns))) break;
+        {
           tc_fence_after();
-          const bool masked = it.tile * WKEYS + WKEYS - 1 > first_last;
-          const uint32_t ts = (uint32_t)(d * nt + c0) + lanes;
-          const float* nl = nlse[team][turn];
-          const int* lk = lastkey[team][turn];
-          for (int c = 0; c < have; c += 16) {
-            uint32_t v[16];
-            tmem_ld16(ts + (uint32_t)c, v);
-            tmem_ld_wait();
-            if (!masked && c + 16 <= have) {
+          const uint32_t ts = (uint32_t)((2 * d + team) * nt) + lanes;
+          const float* nl = nlse[qn % WROWS];
+          const int* lk = lastkey[qn % WROWS];
+          if (!masked) {
+            auto some = [&](auto& v, int c) {
+              constexpr int N = sizeof(v) / 8;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float2 l = *reinterpret_cast<const float2*>(nl + c + 2 * k);
+              for (int k = 0; k < N; ++k) {
+                const float2 l = *reinterpret_cast<const float2*>(nl + c + 2 * k);  // (the same for every lane)
                 const uint64_t e2 = mul2(fma2(pair2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), scale2,
                                               pair2(l.x, l.y)), log2e2);
                 const float2 e = both(e2);
                 sum2[k & 1] = add2(sum2[k & 1], pair2(ex2(e.x), ex2(e.y)));
               }
-            } else {
+            };
+            int c = 0;
+            if (MANY) {
+#pragma unroll 1
+              for (; c + 32 <= have; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(ts + (uint32_t)c, v);
+                tmem_ld_wait();
+                some(v, c);
+              }
+            }
+#pragma unroll 1
+            for (; c + 8 < have; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(ts + (uint32_t)c, v);
+              tmem_ld_wait();
+              some(v, c);
+            }
+            if (c < have) {
+              uint32_t v[8];
+              tmem_ld8(ts + (uint32_t)c, v);
+              tmem_ld_wait();
+              some(v, c);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < have; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(ts + (uint32_t)c, v);
+              tmem_ld_wait();
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 const float e = fmaf(__uint_as_float(v[k]), scale, nl[c + k]) * 1.4426950408889634f;
-                if (t <= lk[c + k] && c + k < have) masked_sum += ex2(e);
+                if (t <= lk[c + k]) masked_sum += ex2(e);
               }
             }
           }
@@ -314,21 +378,22 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_kv4_weigh(AttnArgs a, WeighArgs
           __syncwarp();
           if (lane == 0) mbar_arrive_relaxed(&dempty[d]);
         }
-        if (++d == WD) d = 0, dph ^= 1u;
+        if (++d == w.nd) d = 0, dph ^= 1u;
       }
+      if (!ok) break;
       const float2 x = both(sum2[0]), y = both(sum2[1]);
-      float sum = ((x.x + x.y) + (y.x + y.y)) + masked_sum;
-      if (MANY) {
-        if (team == 1) other[i & 1][key] = sum;
-        if (!(ok = teams_all(ok))) break;
-        sum += other[i & 1][key];
-      }
-      if (ok && mine && t < it.s.len && (!MANY || team == 0)) *out = old + sum;
-      if (it.next()) fresh = true;
+      // The only addition to this place of the launch: its order is no question,
+      // and the total need not come here.
+      if (t < it.s.len)
+        atomicAdd(w.weights + ((long long)it.b * a.heads + it.head) * cap + t, ((x.x + x.y) + (y.x + y.y)) + masked_sum);
+      if (it.next() && !MANY) ++qn;
     }
-  } else if (warp < 16) {
-    const int dt = (int)threadIdx.x - 256;
-    constexpr int GR = D / 32, STEP = 256 / GR;  // groups a key; keys between a thread's
+  } else if (warp < 24) {
+    // Steps are two tiles: crew number c has tile c % 2 of every second step (of
+    // every one where there are two crews).
+    const int ct = (int)threadIdx.x - 256, crew = ct / CREW, dt = ct % CREW, half = crew & 1;
+    const int minq = ct / 256, dq = ct % 256;  // MANY: tiles of query rows, 256 threads each
+    constexpr int GR = D / 32, STRIDE = CREW / GR, U = WKEYS / STRIDE;  // groups a key; keys between a thread's; its keys
     const int grp = dt % GR, tok = dt / GR;
     // (As in the attention for prompt chunks: eight lanes' pieces meet no bank twice.)
     const int order = GR == 8 ? grp / 2 : GR == 4 ? grp / 2 * 2 : 0;
@@ -336,116 +401,160 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_kv4_weigh(AttnArgs a, WeighArgs
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       off[u] = (uint32_t)(grp / 2 * (WKEYS * 128) + tok * 128 + (((grp % 2 * 4 + (u ^ order)) ^ (tok & 7)) * 16));
-    const uint8_t* from_codes = raw + tok / KV_BLOCK * RB + tok % KV_BLOCK * (D / 2) + grp * 16;
-    const uint8_t* from_par = raw + tok / KV_BLOCK * RB + kv_param_off(D) + tok % KV_BLOCK * (D / 8) + grp * 4;
-    int i = 0, rs = 0, qn = 0;
-    uint32_t rph = 0u;
-    bool ok = true, fresh = true;
-    for (Walk<MANY> it(a, pref); it.there() && ok; ++i) {
-      if (!(ok = wait_bar_warp(&aempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, wc.ns))) break;
-      if (!(ok = wait_bar_warp(&rawfull[rs], rph, abort, wc.ns))) break;
-      uint8_t* tile = asm_ + (i & 1) * ATILE;
+    const int bpp = a.page_size / KV_BLOCK, jump = STRIDE / KV_BLOCK / bpp, rest = STRIDE / KV_BLOCK % bpp;
+    const uint8_t* mine = a.cache + tok % KV_BLOCK * (D / 2) + grp * 16;
+    const int par_off = kv_param_off(D) + tok % KV_BLOCK * (D / 8) + grp * 4 - (tok % KV_BLOCK * (D / 2) + grp * 16);
+    uint4 codes[U];
+    uint32_t par[U];
+    // The thread's codes of its crew's tile of a step.  Nothing is asked about keys
+    // past the end: their rows of the product go nowhere, and what stands in the
+    // table for them is looked at like any other entry.
+    auto fetch = [&](const Walk<MANY>& it) {
+      const uint32_t blk = (uint32_t)((2 * it.step + half) * WKEYS + tok) / KV_BLOCK;
+      int page = (int)(blk / (uint32_t)bpp), in = (int)(blk % (uint32_t)bpp);
+      const int* row = a.table + (long long)it.b * a.table_stride;
 #pragma unroll
-      for (int x = 0; x < WKEYS / STEP; ++x) {
-        const int at = rs * RAW + x * (STEP / KV_BLOCK) * RB;
-        uint4 codes;
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(codes.x), "=r"(codes.y), "=r"(codes.z), "=r"(codes.w)
-                     : "r"(smem_u32(from_codes + at))
-                     : "memory");
-        const uint32_t par = *reinterpret_cast<const uint32_t*>(from_par + at);
-        if (GR >= 4) {
-          const bool two = (order & 2) != 0;
-          const uint4 c = codes;
-          codes.x = two ? c.z : c.x, codes.y = two ? c.w : c.y;
-          codes.z = two ? c.x : c.z, codes.w = two ? c.y : c.w;
-        }
-        if (GR == 8) {
-          const bool one = (order & 1) != 0;
-          const uint4 c = codes;
-          codes.x = one ? c.y : c.x, codes.y = one ? c.x : c.y;
-          codes.z = one ? c.w : c.z, codes.w = one ? c.z : c.w;
-        }
-        const T2 s2 = from_bits2<T2>(__byte_perm(par, par, 0x1010)), z2 = from_bits2<T2>(__byte_perm(par, par, 0x3232));
-        const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+      for (int x = 0; x < U; ++x) {
+        const unsigned e = (unsigned)row[min(page, a.table_stride - 1)];  // (an entry outside the pool reads page 0)
+        // (A pool has less than 2^32 blocks of 1280 bytes and more.)
+        const uint32_t at = ((e < (unsigned long long)a.pages ? e : 0u) * (uint32_t)a.heads + (uint32_t)it.head) * (uint32_t)bpp + (uint32_t)in;
+        const uint8_t* src = mine + (unsigned long long)at * kv_block_bytes(D);
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(codes[x].x), "=r"(codes[x].y), "=r"(codes[x].z), "=r"(codes[x].w)
+                     : "l"(src));
+        asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(par[x]) : "l"(src + par_off));
+        page += jump;
+        if ((in += rest) >= bpp) in -= bpp, ++page;
+      }
+    };
+    int i = 0, qn = 0;
+    uint32_t aph = 1u;
+    bool ok = true;
+    Walk<MANY> it(a, pref), ahead(a, pref);
+    if (TURNS == 4 && crew >= 2 && ahead.there()) ahead.next();
+    if (!MANY && !wc.no_loads && ahead.there()) fetch(ahead);
+    for (; it.there() && ok && !wc.no_loads; it.next(), ++i) {
+      if (TURNS == 2 || (i & 1) == crew / 2) {
+        const int as = crew;
+        if (MANY) fetch(it);  // (kept through the query rows' tiles, the codes would be spilled)
+        if (!(ok = wait_long(&aempty[as / 2], aph, abort, wc.ns))) break;
+        aph ^= 1u;
+        uint8_t* tile = asm_ + as * ATILE;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 o;
-          o.x = bits2(__hfma2(code16<T>(cw[e], 0, a.up), s2, z2));
-          o.y = bits2(__hfma2(code16<T>(cw[e], 1), s2, z2));
-          o.z = bits2(__hfma2(code16<T>(cw[e], 2), s2, z2));
-          o.w = bits2(__hfma2(code16<T>(cw[e], 3), s2, z2));
-          *reinterpret_cast<uint4*>(tile + x * STEP * 128 + off[e]) = o;
+        for (int x = 0; x < U; ++x) {
+          uint4 v = codes[x];
+          if (GR >= 4) {
+            const bool two = (order & 2) != 0;
+            const uint4 c = v;
+            v.x = two ? c.z : c.x, v.y = two ? c.w : c.y;
+            v.z = two ? c.x : c.z, v.w = two ? c.y : c.w;
+          }
+          if (GR == 8) {
+            const bool one = (order & 1) != 0;
+            const uint4 c = v;
+            v.x = one ? c.y : c.x, v.y = one ? c.x : c.y;
+            v.z = one ? c.w : c.z, v.w = one ? c.z : c.w;
+          }
+          const T2 s2 = from_bits2<T2>(__byte_perm(par[x], par[x], 0x1010)), z2 = from_bits2<T2>(__byte_perm(par[x], par[x], 0x3232));
+          const uint32_t cw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 o;
+            o.x = bits2(__hfma2(code16<T>(cw[e], 0, a.up), s2, z2));
+            o.y = bits2(__hfma2(code16<T>(cw[e], 1), s2, z2));
+            o.z = bits2(__hfma2(code16<T>(cw[e], 2), s2, z2));
+            o.w = bits2(__hfma2(code16<T>(cw[e], 3), s2, z2));
+            *reinterpret_cast<uint4*>(tile + x * STRIDE * 128 + off[e]) = o;
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&afull[as]);
+        if (!MANY) {
+          ahead.next();
+          if (TURNS == 4 && ahead.there()) ahead.next();
+          if (ahead.there()) fetch(ahead);
         }
       }
-      // Behind the stores, which need what was loaded: a copy into the place may follow at once.
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&rawempty[rs]);
-      mbar_arrive(&afull[i & 1]);
-      if (++rs == w.nraw) rs = 0, rph ^= 1u;
-      const int rt1 = MANY ? (it.s.rows + nt - 1) / nt : 1;
-      for (int rt = MANY ? it.first_rows(nt) : 0; rt < rt1 && (MANY || fresh); ++rt, ++qn) {
-        if (!(ok = wait_bar_warp(&qempty[qn & 1], ((uint32_t)(qn >> 1) & 1u) ^ 1u, abort, wc.ns))) break;
+      if (MANY) {
+        const int rt1 = (it.s.rows + nt - 1) / nt;
+#pragma unroll 1
+        for (int rt = it.first_rows(nt); rt < rt1; ++rt, ++qn) {
+          if ((qn & 1) != minq) continue;
+          uint8_t* dst = qsm + (qn & 1) * qtile;
+          constexpr int C = D / 8, B = 8;  // 16-byte pieces of a row; pieces at a time
+          auto bring = [&](uint4 (&v)[B], int p0) {
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+              const int p = p0 + k * 256, r = p / C, c = p % C, rr = rt * nt + r;
+              v[k] = uint4{};
+              if (r < nt && rr < it.s.rows)
+                v[k] = *reinterpret_cast<const uint4*>(
+                    static_cast<const T*>(a.q) + ((long long)it.s.q0 + rr / a.group) * a.q_ts +
+                    (long long)(it.head * a.group + rr % a.group) * a.q_hs + c * 8);
+            }
+          };
+          uint4 v[B];
+          bring(v, dq);  // the first ones before the place is free
+          const Row row = row_of(it, rt * nt + dq, dq < nt);
+          if (!(ok = wait_long(&qempty[qn & 1], ((uint32_t)(qn >> 1) & 1u) ^ 1u, abort, wc.ns))) break;
+          for (int p0 = dq; p0 < nt * C; p0 += B * 256) {
+            if (p0 != dq) bring(v, p0);
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+              const int p = p0 + k * 256, r = p / C, c = p % C;
+              if (r < nt)
+                *reinterpret_cast<uint4*>(dst + c / 8 * (nt * 128) + r * 128 + (((c & 7) ^ (r & 7)) * 16)) = pair_order(v[k]);
+            }
+          }
+          if (dq < nt) nlse[qn % WROWS][dq] = row.nlse, lastkey[qn % WROWS][dq] = row.last;
+          fence_proxy_async_smem();
+          mbar_arrive(&qfull[qn & 1]);
+        }
+      }
+    }
+  } else if (warp != MMA) {
+    if (!wc.no_loads) {  // the query rows of each head
+      int qn = 0;
+      for (Walk<MANY> it(a, pref); it.there(); it.next(it.run(1 << 30)), ++qn) {
+        if (!wait_long(&qempty[qn & 1], ((uint32_t)(qn >> 1) & 1u) ^ 1u, abort, wc.ns)) break;
         uint8_t* dst = qsm + (qn & 1) * qtile;
         constexpr int C = D / 8;  // 16-byte pieces of a row
 #pragma unroll 4
-        for (int p = dt; p < nt * C; p += 256) {
-          const int r = p / C, c = p % C, rr = rt * nt + r;
+        for (int p = lane; p < nt * C; p += 32) {
+          const int r = p / C, c = p % C;
           uint4 v{};
-          if (rr < it.s.rows)
+          if (r < it.s.rows)
             v = pair_order(*reinterpret_cast<const uint4*>(
-                static_cast<const T*>(a.q) + ((long long)it.s.q0 + rr / a.group) * a.q_ts +
-                (long long)(it.head * a.group + rr % a.group) * a.q_hs + c * 8));
+                static_cast<const T*>(a.q) + ((long long)it.s.q0 + r / a.group) * a.q_ts +
+                (long long)(it.head * a.group + r % a.group) * a.q_hs + c * 8));
           *reinterpret_cast<uint4*>(dst + c / 8 * (nt * 128) + r * 128 + (((c & 7) ^ (r & 7)) * 16)) = v;
+        }
+        for (int r = lane; r < nt; r += 32) {
+          const Row row = row_of(it, r, true);
+          nlse[qn % WROWS][r] = row.nlse, lastkey[qn % WROWS][r] = row.last;
         }
         fence_proxy_async_smem();
         mbar_arrive(&qfull[qn & 1]);
-      }
-      fresh = false;
-      if (!ok) break;
-      if (it.next()) fresh = true;
-    }
-  } else if (warp == 16) {
-    if (!wc.no_loads) {
-      const int bpp = a.page_size / KV_BLOCK;
-      int rs = 0;
-      uint32_t rph = 1u;
-      // The page of a lane's block, one item ahead.
-      auto page_of = [&](const Walk<MANY>& it) {
-        const int blk = it.tile * (WKEYS / KV_BLOCK) + lane;
-        return it.there() && lane < WKEYS / KV_BLOCK && blk * KV_BLOCK < it.s.len
-                   ? (unsigned)a.table[(long long)it.b * a.table_stride + blk / bpp]
-                   : 0u;
-      };
-      Walk<MANY> it(a, pref);
-      unsigned entry = page_of(it);
-      while (it.there()) {
-        const int blk = it.tile * (WKEYS / KV_BLOCK) + lane;
-        const int have = min(WKEYS / KV_BLOCK, (it.s.len + KV_BLOCK - 1) / KV_BLOCK - it.tile * (WKEYS / KV_BLOCK));
-        // (An entry outside the pool reads page 0.)
-        const long long page = entry < (unsigned long long)a.pages ? (long long)entry : 0;
-        const uint8_t* src = a.cache + ((page * a.heads + it.head) * bpp + blk % bpp) * (long long)kv_block_bytes(D);
-        it.next();
-        entry = page_of(it);
-        if (!wait_bar_warp(&rawempty[rs], rph, abort, wc.ns)) break;
-        if (lane == 0) mbar_expect_tx(&rawfull[rs], (uint32_t)(have * RB));
-        __syncwarp();
-        if (lane < have) bulk_load(smem_u32(raw + rs * RAW + lane * RB), src, RB, &rawfull[rs]);
-        if (++rs == w.nraw) rs = 0, rph ^= 1u;
       }
     }
   } else {
     const bool one = elect_one();
     const uint32_t idesc = (1u << 4) | (WFormat<T>::k << 7) | (WFormat<T>::k << 10) | ((uint32_t)(nt >> 3) << 17) | (8u << 24);
     const uint64_t ad = sdesc(smem_u32(asm_)), qd = sdesc(smem_u32(qsm));
-    int i = 0, d = 0, qn = 0;
-    uint32_t dph = 1u;
+    // Every step goes through this warp's loop, and beside 25 others an instruction
+    // of it takes some ten cycles and a look at a barrier 200: three barriers are
+    // looked at together, a step is two tiles of keys, and nothing of the list is
+    // looked up but where a run of steps ends.
+    const uint32_t halfa = WKEYS * 128 >> 4, halfb = (uint32_t)nt * 128 >> 4;
+    int as = 0, d = 0, qn = 0;
+    uint32_t dph = 1u, aph = 0u;
     bool ok = true, fresh = true;
-    for (Walk<MANY> it(a, pref); it.there() && ok; ++i) {
-      if (!(ok = wait_bar_warp(&afull[i & 1], (uint32_t)(i >> 1) & 1u, abort, wc.ns))) break;
-      const int rt1 = MANY ? (it.s.rows + nt - 1) / nt : 1;
-      for (int rt = MANY ? it.first_rows(nt) : 0; rt < rt1; ++rt) {
+    Walk<MANY> it(a, pref);
+    while (it.there() && ok) {
+      // Steps of one head, or rows' tiles of one step.
+      const int n = MANY ? (it.s.rows + nt - 1) / nt - it.first_rows(nt) : it.run(1 << 30);
+#pragma unroll 1
+      for (int k = 0; k < n; ++k) {
         if (MANY || fresh) {
           // The rows' tile before this one is read by what has been issued.
           if (one && qn > 0) mma_commit(&qempty[(qn - 1) & 1]);
@@ -454,24 +563,25 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_kv4_weigh(AttnArgs a, WeighArgs
           ++qn;
           fresh = false;
         }
-        if (!(ok = wait_bar_warp(&dempty[d], dph, abort, wc.ns))) break;
+        if (!(ok = wait_three(&afull[as], aph, &afull[as + 1], aph, &dempty[d], dph, abort, wc.ns))) break;
         tc_fence_after();
         if (one) {
+          const uint64_t at = ad + (uint32_t)(as * (ATILE >> 4)), bt = qd + (uint32_t)(((qn - 1) & 1) * (qtile >> 4));
 #pragma unroll
-          for (int h = 0; h < HALVES; ++h)
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_keys((uint32_t)(d * nt), ad + (uint64_t)(((i & 1) * ATILE + h * WKEYS * 128 + 32 * k) >> 4),
-                       qd + (uint64_t)((((qn - 1) & 1) * qtile + h * nt * 128 + 32 * k) >> 4), idesc, (h || k) ? 1u : 0u);
+            for (int h = 0; h < HALVES; ++h)
+              mma_keys((uint32_t)((2 * d + x) * nt), at + (uint32_t)(x * (ATILE >> 4)) + h * halfa, bt + h * halfb, idesc, h == 0);
           mma_commit(&dfull[d]);
+          if (!MANY || k == n - 1) mma_commit(&aempty[as / 2]);
         }
-        __syncwarp();
-        if (++d == WD) d = 0, dph ^= 1u;
+        if (++d == w.nd) d = 0, dph ^= 1u;
+        if (!MANY || k == n - 1)
+          if ((as += 2) == TURNS) as = 0, aph ^= 1u;
       }
       if (!ok) break;
-      if (one) mma_commit(&aempty[i & 1]);
-      __syncwarp();
-      if (it.next()) fresh = true;
+      it.next(n);
+      fresh = true;  // (a run ends where the head does)
     }
     if (!ok) {
       // Whatever was issued has to end before the memory is given back.
@@ -489,22 +599,21 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_kv4_weigh(AttnArgs a, WeighArgs
     if (threadIdx.x == 0 && a.status != nullptr) atomicOr(a.status, 2u);
   }
   tc_fence_after();
-  if (warp == 17)
+  if (warp == MMA)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base_sh), "r"(512u) : "memory");
 }
 
 template <class T, int D, bool MANY>
 gptq_status weigh_launch(const AttnArgs& a, const float* lse, float* weights, int nt, cudaStream_t s) {
-  constexpr int RAW = WKEYS / KV_BLOCK * 10 * D, ATILE = WKEYS * D * 2, most = 217 << 10;
+  constexpr int most = 1024 + kTurns<D> * WKEYS * D * 2 + 2 * kMostRows<D> * D * 2;
   static DeviceOnce attr;
   GQ_TRY(attr.run([](int) -> gptq_status {
     GQ_CUDA(cudaFuncSetAttribute(k_kv4_weigh<T, D, MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     return GPTQ_OK;
   }));
-  const int fixed = 1024 + 2 * ATILE + 2 * nt * D * 2;
-  WeighArgs w{lse, weights, nt, std::min((most - fixed) / RAW, WRAW)};
-  const size_t smem = fixed + (size_t)w.nraw * RAW;
-  const long long tiles = ((long long)a.table_stride * a.page_size + WKEYS - 1) / WKEYS;
+  WeighArgs w{lse, weights, nt, std::min(WD, 256 / nt)};
+  const size_t smem = 1024 + (size_t)kTurns<D> * WKEYS * D * 2 + (size_t)2 * nt * D * 2;
+  const long long steps = ((long long)a.table_stride * a.page_size + 2 * WKEYS - 1) / (2 * WKEYS);
   for (int b0 = 0; b0 < a.seqs; b0 += WSEQS) {
     AttnArgs p = a;
     p.seqs = std::min(a.seqs - b0, WSEQS);
@@ -518,9 +627,9 @@ gptq_status weigh_launch(const AttnArgs& a, const float* lse, float* weights, in
       p.tq = p.seqs;
       w.lse = lse + (long long)b0 * a.heads * a.group;
     }
-    const unsigned grid = (unsigned)std::min<long long>(num_sms(), std::min<long long>(tiles * a.heads, 1 << 20) * p.seqs);
+    const unsigned grid = (unsigned)std::min<long long>(num_sms(), std::min<long long>(steps * a.heads, 1 << 20) * p.seqs);
     GQ_PROF(K_KV4_WEIGH, s);
-    k_kv4_weigh<T, D, MANY><<<grid, WTHREADS, smem, s>>>(p, w, wait_cfg());
+    k_kv4_weigh<T, D, MANY><<<grid, wthreads(MANY), smem, s>>>(p, w, wait_cfg());
     GQ_LAUNCHED();
   }
   return GPTQ_OK;
