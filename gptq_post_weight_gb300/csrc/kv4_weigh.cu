@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
   __shared__ int lastkey[WROWS][128];
   volatile int* abort = &abort_sh;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int nt = w.nt, qtile = nt * D * 2;
+  const int nt = MANY ? kMostRows<D> : w.nt, qtile = nt * D * 2;
   uint8_t* asm_ = smem;                  // tiles of keys
   uint8_t* qsm = smem + TURNS * ATILE;   // two tiles of query rows
 
@@ -328,24 +328,32 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
           const int* lk = lastkey[qn % WROWS];
           if (!masked) {
             auto some = [&](auto& v, int c) {
-              constexpr int N = sizeof(v) / 8;
+              constexpr int N = sizeof(v) / 16;
 #pragma unroll
               for (int k = 0; k < N; ++k) {
-                const float2 l = *reinterpret_cast<const float2*>(nl + c + 2 * k);  // (the same for every lane)
-                const uint64_t e2 = mul2(fma2(pair2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), scale2,
-                                              pair2(l.x, l.y)), log2e2);
-                const float2 e = both(e2);
-                sum2[k & 1] = add2(sum2[k & 1], pair2(ex2(e.x), ex2(e.y)));
+                const float4 l = *reinterpret_cast<const float4*>(nl + c + 4 * k);  // (the same for every lane)
+                const float2 e = both(mul2(fma2(pair2(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1])), scale2,
+                                                pair2(l.x, l.y)), log2e2));
+                const float2 f = both(mul2(fma2(pair2(__uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3])), scale2,
+                                                pair2(l.z, l.w)), log2e2));
+                sum2[0] = add2(sum2[0], pair2(ex2(e.x), ex2(e.y)));
+                sum2[1] = add2(sum2[1], pair2(ex2(f.x), ex2(f.y)));
               }
             };
             int c = 0;
-            if (MANY) {
+            if (MANY || have >= 32) {
+              // Sixteen columns on their way while sixteen are summed.
+              uint32_t v[16], u[16];
+              tmem_ld16(ts, v);
+              tmem_ld_wait();
 #pragma unroll 1
               for (; c + 32 <= have; c += 32) {
-                uint32_t v[32];
-                tmem_ld32(ts + (uint32_t)c, v);
-                tmem_ld_wait();
+                tmem_ld16(ts + (uint32_t)c + 16u, u);
                 some(v, c);
+                tmem_ld_wait();
+                if (c + 32 < have) tmem_ld16(ts + (uint32_t)c + 32u, v);
+                some(u, c + 16);
+                tmem_ld_wait();
               }
             }
 #pragma unroll 1
@@ -394,13 +402,15 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     const int ct = (int)threadIdx.x - 256, crew = ct / CREW, dt = ct % CREW, half = crew & 1;
     const int minq = ct / 256, dq = ct % 256;  // MANY: tiles of query rows, 256 threads each
     constexpr int GR = D / 32, STRIDE = CREW / GR, U = WKEYS / STRIDE;  // groups a key; keys between a thread's; its keys
-    const int grp = dt % GR, tok = dt / GR;
-    // (As in the attention for prompt chunks: eight lanes' pieces meet no bank twice.)
-    const int order = GR == 8 ? grp / 2 : GR == 4 ? grp / 2 * 2 : 0;
+    // A warp's lanes: eight that store together have four keys of two neighbouring
+    // groups, whose pieces meet no bank twice.
+    const int l3 = lane >> 3;
+    const int grp = (lane & 1) | (GR == 8 ? l3 << 1 : GR == 4 ? (l3 & 1) << 1 : 0);
+    const int tok = dt / 32 * (32 / GR) + ((lane >> 1 & 3) | (GR == 2 ? l3 << 2 : GR == 4 ? (l3 & 2) << 1 : 0));
     uint32_t off[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      off[u] = (uint32_t)(grp / 2 * (WKEYS * 128) + tok * 128 + (((grp % 2 * 4 + (u ^ order)) ^ (tok & 7)) * 16));
+      off[u] = (uint32_t)(grp / 2 * (WKEYS * 128) + tok * 128 + (((grp % 2 * 4 + u) ^ (tok & 7)) * 16));
     const int bpp = a.page_size / KV_BLOCK, jump = STRIDE / KV_BLOCK / bpp, rest = STRIDE / KV_BLOCK % bpp;
     const uint8_t* mine = a.cache + tok % KV_BLOCK * (D / 2) + grp * 16;
     const int par_off = kv_param_off(D) + tok % KV_BLOCK * (D / 8) + grp * 4 - (tok % KV_BLOCK * (D / 2) + grp * 16);
@@ -427,6 +437,9 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
         if ((in += rest) >= bpp) in -= bpp, ++page;
       }
     };
+    // MANY: from a thread's piece of a tile of rows to its next one.
+    const int apart = 256 / (D / 8), gmore = apart % a.group;
+    const long long more = apart / a.group * a.q_ts + gmore * a.q_hs, wrap = a.q_ts - a.group * a.q_hs;
     int i = 0, qn = 0;
     uint32_t aph = 1u;
     bool ok = true;
@@ -442,21 +455,8 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
         uint8_t* tile = asm_ + as * ATILE;
 #pragma unroll
         for (int x = 0; x < U; ++x) {
-          uint4 v = codes[x];
-          if (GR >= 4) {
-            const bool two = (order & 2) != 0;
-            const uint4 c = v;
-            v.x = two ? c.z : c.x, v.y = two ? c.w : c.y;
-            v.z = two ? c.x : c.z, v.w = two ? c.y : c.w;
-          }
-          if (GR == 8) {
-            const bool one = (order & 1) != 0;
-            const uint4 c = v;
-            v.x = one ? c.y : c.x, v.y = one ? c.x : c.y;
-            v.z = one ? c.w : c.z, v.w = one ? c.z : c.w;
-          }
           const T2 s2 = from_bits2<T2>(__byte_perm(par[x], par[x], 0x1010)), z2 = from_bits2<T2>(__byte_perm(par[x], par[x], 0x3232));
-          const uint32_t cw[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t cw[4] = {codes[x].x, codes[x].y, codes[x].z, codes[x].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint4 o;
@@ -480,32 +480,26 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
 #pragma unroll 1
         for (int rt = it.first_rows(nt); rt < rt1; ++rt, ++qn) {
           if ((qn & 1) != minq) continue;
-          uint8_t* dst = qsm + (qn & 1) * qtile;
-          constexpr int C = D / 8, B = 8;  // 16-byte pieces of a row; pieces at a time
-          auto bring = [&](uint4 (&v)[B], int p0) {
+          // Sixteen bytes of each of P rows, one division for all of them.
+          constexpr int C = D / 8, APART = 256 / C, P = kMostRows<D> / APART;  // pieces of a row; rows between a thread's
+          const int r0 = dq / C, c = dq % C, first = rt * nt + r0;
+          int g = first % a.group;
+          const T* src = static_cast<const T*>(a.q) + ((long long)it.s.q0 + first / a.group) * a.q_ts +
+                         (long long)(it.head * a.group + g) * a.q_hs + c * 8;
+          uint4 v[P];
 #pragma unroll
-            for (int k = 0; k < B; ++k) {
-              const int p = p0 + k * 256, r = p / C, c = p % C, rr = rt * nt + r;
-              v[k] = uint4{};
-              if (r < nt && rr < it.s.rows)
-                v[k] = *reinterpret_cast<const uint4*>(
-                    static_cast<const T*>(a.q) + ((long long)it.s.q0 + rr / a.group) * a.q_ts +
-                    (long long)(it.head * a.group + rr % a.group) * a.q_hs + c * 8);
-            }
-          };
-          uint4 v[B];
-          bring(v, dq);  // the first ones before the place is free
-          const Row row = row_of(it, rt * nt + dq, dq < nt);
-          if (!(ok = wait_long(&qempty[qn & 1], ((uint32_t)(qn >> 1) & 1u) ^ 1u, abort, wc.ns))) break;
-          for (int p0 = dq; p0 < nt * C; p0 += B * 256) {
-            if (p0 != dq) bring(v, p0);
-#pragma unroll
-            for (int k = 0; k < B; ++k) {
-              const int p = p0 + k * 256, r = p / C, c = p % C;
-              if (r < nt)
-                *reinterpret_cast<uint4*>(dst + c / 8 * (nt * 128) + r * 128 + (((c & 7) ^ (r & 7)) * 16)) = pair_order(v[k]);
-            }
+          for (int k = 0; k < P; ++k) {
+            v[k] = uint4{};
+            if (first + k * APART < it.s.rows) v[k] = *reinterpret_cast<const uint4*>(src);
+            src += more;
+            if ((g += gmore) >= a.group) g -= a.group, src += wrap;
           }
+          const Row row = row_of(it, rt * nt + dq, dq < nt);
+          // (Before the place is free.)
+          if (!(ok = wait_long(&qempty[qn & 1], ((uint32_t)(qn >> 1) & 1u) ^ 1u, abort, wc.ns))) break;
+          uint8_t* dst = qsm + (qn & 1) * qtile + c / 8 * (nt * 128) + r0 * 128 + (((c & 7) ^ (r0 & 7)) * 16);
+#pragma unroll
+          for (int k = 0; k < P; ++k) *reinterpret_cast<uint4*>(dst + k * APART * 128) = pair_order(v[k]);
           if (dq < nt) nlse[qn % WROWS][dq] = row.nlse, lastkey[qn % WROWS][dq] = row.last;
           fence_proxy_async_smem();
           mbar_arrive(&qfull[qn & 1]);
