@@ -2,8 +2,10 @@
 // `recent` tokens and the heaviest of the others, in order, from place 0 on.
 //
 // k_kv4_select finds, for one head of one sequence, the weight of the last token
-// kept (a radix selection over the weights' bits, eight at a time) and lists
-// the places that stay; k_kv4_move carries their bytes.
+// kept (a radix selection over the weights' bits, eleven at a time: more bins
+// than the exponent's alone, in which the first digits of most weights would
+// meet) and lists the places that stay, a warp a stretch of them.
+// k_kv4_move carries their bytes.
 //
 // In place a token moves towards the front, over tokens that may have to move
 // themselves.  The CTAs of a cluster share a head and go through its places in
@@ -15,7 +17,9 @@
 namespace gq {
 namespace {
 
-constexpr int SEL = 1024;  // threads that select
+constexpr int SEL = 512;           // threads that select
+constexpr int SBINS = 2048;
+constexpr int kStaged = 40 << 10;  // places of a head that are kept in shared memory at most
 
 // Weights in the order of whole numbers; a NaN is the lightest, both zeros are one.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -29,11 +33,15 @@ __device__ __forceinline__ int length_of(const EvictArgs& a, int b) {
   return (int)min((long long)max(a.kv_lens[b], 0), (long long)a.table_stride * a.page_size);
 }
 
+// STAGED: the keys of a head fit shared memory (else they are read again for each digit).
+template <bool STAGED>
 __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int warp_above[SEL / 32], warp_tie[SEL / 32];
+  extern __shared__ uint32_t keys[];
+  __shared__ __align__(16) int hist[SBINS];
+  __shared__ int2 part[SEL / 32];
   __shared__ uint32_t prefix_sh;
   __shared__ int need_sh;
+  constexpr int W = SEL / 32;
   const int b = (int)(blockIdx.x / (unsigned)a.heads), tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int len = length_of(a, b), n = min(len, a.keep);
   const int old = max(len - min(a.recent, n), 0);  // up to here the weights decide
@@ -43,74 +51,106 @@ __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
   float* out_w = a.out_weights + (long long)blockIdx.x * out_cap;
   if (blockIdx.x % (unsigned)a.heads == 0 && tid == 0) a.out_lens[b] = n;
   for (int i = n + tid; i < a.keep; i += SEL) kept[i] = -1;
-  for (long long i = n + tid; i < out_cap; i += SEL) out_w[i] = 0.f;
-  if (len <= a.keep) {
+  if (len <= a.keep)
     for (int i = tid; i < n; i += SEL) kept[i] = i, out_w[i] = w[i];
-    return;
-  }
-  // The key of the last one kept, and how many equal to it are.
-  uint32_t prefix = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_kv4_move may set itself up
+  for (long long i = n + tid; i < out_cap; i += SEL) out_w[i] = 0.f;
+  if (len <= a.keep) return;
   int need = n - (len - old);
-  for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+  const bool any = need > 0;
+  auto key = [&](int i) { return STAGED ? keys[i] : weight_key(w[i]); };
+  if (STAGED && any) {
+#pragma unroll 8
+    for (int i = tid; i < old; i += SEL) keys[i] = weight_key(w[i]);
+  }
+  // The key of the last one kept, and how many of those equal to it stay.
+  uint32_t prefix = 0;
+  for (int shift = 21; any; shift = max(shift - 11, 0)) {
+    const uint32_t mask = shift == 21 ? 0u : shift == 10 ? ~0u << 21 : ~0u << 10;  // the digits found
+    const uint32_t bins = shift == 0 ? 1023u : 2047u;
+    for (int i = tid; i < SBINS; i += SEL) hist[i] = 0;
     __syncthreads();
+#pragma unroll 8
     for (int i = tid; i < old; i += SEL) {
-      const uint32_t k = weight_key(w[i]);
-      if (shift == 24 || k >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&hist[k >> shift & 255u], 1);
+      const uint32_t k = key(i);
+      if ((k & mask) == prefix) atomicAdd(&hist[k >> shift & bins], 1);
     }
     __syncthreads();
-    if (tid == 0) {
-      int d = 255, left = need;
-      while (hist[d] < left) left -= hist[d--];
+    // Keys in the bins above: each thread has four bins, from the highest down.
+    const int4 mine = reinterpret_cast<const int4*>(hist)[SEL - 1 - tid];
+    const int sum = (mine.x + mine.y) + (mine.z + mine.w);
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) part[warp].x = inc;
+    __syncthreads();
+    int above = inc - sum;
+    for (int x = 0; x < warp; ++x) above += part[x].x;
+    if (above < need && need <= above + sum) {  // one thread's
+      int d = 4 * (SEL - 1 - tid) + 3;
+      const int c[4] = {mine.w, mine.z, mine.y, mine.x};
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        if (d % 4 == 3 - x && above + c[x] < need) above += c[x], --d;
       prefix_sh = prefix | (uint32_t)d << shift;
-      need_sh = left;
+      need_sh = need - above;
     }
     __syncthreads();
     prefix = prefix_sh;
     need = need_sh;
+    if (shift == 0) break;
   }
-  const bool any = n > len - old;
-  // The list, SEL places at a time.
-  int at = 0, ties = 0;
-  for (int i0 = 0; i0 < len; i0 += SEL) {
-    const int i = i0 + tid;
-    const float v = i < len ? w[i] : 0.f;
-    const uint32_t k = weight_key(v);
-    bool above = i < len && (i >= old || (any && k > prefix));
-    const bool tie = any && i < old && k == prefix;
-    const unsigned tie_mask = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) warp_tie[warp] = __popc(tie_mask);
-    __syncthreads();
-    int before = ties + __popc(tie_mask & ((1u << lane) - 1));
-    for (int x = 0; x < SEL / 32; ++x) {
-      if (x < warp) before += warp_tie[x];
-      ties += warp_tie[x];
+  // A warp lists a stretch of the places: first how many stay before it.
+  const int each = (len + W * 32 - 1) / (W * 32) * 32, i0 = min(warp * each, len), i1 = min(i0 + each, len);
+  int above = 0, ties = 0;
+#pragma unroll 4
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const uint32_t k = any && i < min(i1, old) ? key(i) : 0u;
+    above += __popc(__ballot_sync(0xffffffffu, i < i1 && (i >= old || (any && k > prefix))));
+    ties += __popc(__ballot_sync(0xffffffffu, any && i < min(i1, old) && k == prefix));
+  }
+  __syncthreads();  // (part is read above)
+  if (lane == 0) part[warp] = int2{above, ties};
+  __syncthreads();
+  int place = 0, tied = 0;
+  for (int x = 0; x < warp; ++x) {
+    place += part[x].x;
+    tied += part[x].y;
+  }
+  place += min(tied, need);
+  const unsigned before = (1u << lane) - 1u;
+#pragma unroll 2
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const uint32_t k = any && i < min(i1, old) ? key(i) : 0u;
+    const bool tie = any && i < min(i1, old) && k == prefix;
+    const unsigned equal = __ballot_sync(0xffffffffu, tie);
+    const bool stays = i < i1 && (i >= old || (any && k > prefix) || (tie && tied + __popc(equal & before) < need));
+    const unsigned all = __ballot_sync(0xffffffffu, stays);
+    if (stays) {
+      const int at = place + __popc(all & before);
+      kept[at] = i;
+      out_w[at] = w[i];
     }
-    above = above || (tie && before < need);
-    const unsigned mask = __ballot_sync(0xffffffffu, above);
-    if (lane == 0) warp_above[warp] = __popc(mask);
-    __syncthreads();
-    int place = at + __popc(mask & ((1u << lane) - 1));
-    for (int x = 0; x < SEL / 32; ++x) {
-      if (x < warp) place += warp_above[x];
-      at += warp_above[x];
-    }
-    if (above) kept[place] = i, out_w[place] = v;
-    __syncthreads();
+    place += __popc(all);
+    tied += __popc(equal);
   }
 }
 
-constexpr int MOVE = 256;  // threads that move, and pieces each has in flight
-constexpr int PER = 8;
-constexpr int CLU = 8;  // CTAs of a cluster
+constexpr int MOVE = 256;  // threads that move
+constexpr int CLU = 8;     // CTAs of a head
 
 // Pieces of a block of 16 tokens, in the order of its bytes: 16 bytes of codes,
 // a token's (s, z) pairs (8 or 16 bytes; heads of 256: two).
 template <int D>
 struct Pieces {
+  static constexpr int blocks = D == 256 ? 8 : 16;  // of a CTA's round
   static constexpr int codes = 16 * (D / 32), params = 16 * (D == 256 ? 2 : 1), half = codes + params, all = 2 * half;
-  static constexpr int param_bytes = D == 64 ? 8 : 16;
-  // The token of piece p of a block, and its bytes' offset from the block's start for token row 0.
+  static constexpr int each = blocks * all / MOVE;  // pieces of a thread: as many loads in flight
+  // The token of piece p of a block, its bytes' offset from the block's start for
+  // token 0, and bytes from token to token; whether it is sixteen.
   static __device__ __forceinline__ void at(int p, int& row, int& off, int& step, bool& wide) {
     const int v = p >= half, q = v ? p - half : p;
     if (q < codes) {
@@ -124,64 +164,80 @@ struct Pieces {
 };
 
 template <int D>
-__device__ __forceinline__ uint8_t* block_at(const EvictArgs& a, const int* row, int head, int t, bool write) {
-  const unsigned e = (unsigned)row[t / a.page_size];
+__device__ __forceinline__ uint8_t* block_at(const EvictArgs& a, const int* row, int head, int blk, bool write) {
+  const int bpp = a.page_size / KV_BLOCK, page = blk / bpp;
+  const unsigned e = (unsigned)row[page];
   const bool in = e < (unsigned long long)a.pages;
   if (write && !in) return nullptr;  // dropped; a read outside the pool takes page 0
-  const int bpp = a.page_size / KV_BLOCK;
-  return a.cache + (((in ? (long long)e : 0) * a.heads + head) * bpp + t % a.page_size / KV_BLOCK) * (long long)kv_block_bytes(D);
+  return a.cache + (((in ? (long long)e : 0) * a.heads + head) * bpp + (blk - page * bpp)) * (long long)kv_block_bytes(D);
 }
 
 template <int D, bool IN_PLACE>
 __global__ void __launch_bounds__(MOVE) k_kv4_move(EvictArgs a) {
   using P = Pieces<D>;
+  static_assert(P::blocks * P::all % MOVE == 0 && P::blocks * 16 <= MOVE, "a round is a thread's pieces");
+  struct From {
+    const uint8_t* block;  // null: stays where it is, or goes nowhere
+    int row;
+  };
+  __shared__ From from[P::blocks * 16];
+  __shared__ uint8_t* to[P::blocks];
   const int item = (int)(blockIdx.x / CLU), rank = (int)(blockIdx.x % CLU);
   const int b = item / a.heads, head = item % a.heads;
-  const int len = length_of(a, b), n = min(len, a.keep);
-  if (IN_PLACE && n == len) return;  // (the whole cluster)
-  const int* from = a.table + (long long)b * a.table_stride;
-  const int* to = a.out_table + (long long)b * a.out_stride;
+  const int len = length_of(a, b), n = min(len, a.keep), blocks = (n + 15) / 16;
+  const int* table = a.table + (long long)b * a.table_stride;
+  const int* out = a.out_table + (long long)b * a.out_stride;
   const int* kept = a.kept + (long long)item * a.keep;
-  const long long total = (long long)((n + 15) / 16) * P::all;
-  for (long long p0 = 0; p0 < total; p0 += (long long)CLU * MOVE * PER) {
-    uint4 data[PER];
-    uint8_t* dst[PER];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list is there
+  if (IN_PLACE && n == len) return;                   // (the whole cluster)
+  for (int b0 = 0; b0 < blocks; b0 += CLU * P::blocks) {
+    const int first = b0 + rank * P::blocks, have = min(P::blocks, blocks - first);  // this CTA's blocks
+    if ((int)threadIdx.x < P::blocks * 16) {
+      const int lb = threadIdx.x / 16, t = first * 16 + (int)threadIdx.x;
+      From f{nullptr, 0};
+      if (t < n) {
+        const int src = kept[t];
+        uint8_t* dst = block_at<D>(a, out, head, first + lb, true);
+        if (threadIdx.x % 16 == 0) to[lb] = dst;
+        if (dst != nullptr && !(IN_PLACE && src == t)) f = From{block_at<D>(a, table, head, src / KV_BLOCK, false), src % KV_BLOCK};
+      }
+      from[threadIdx.x] = f;
+    }
+    __syncthreads();
+    uint4 data[P::each];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const long long p = p0 + ((long long)rank * PER + i) * MOVE + threadIdx.x;
-      dst[i] = nullptr;
-      if (p >= total) continue;
+    for (int i = 0; i < P::each; ++i) {
+      const int l = i * MOVE + (int)threadIdx.x, lb = l / P::all;
       int row, off, step;
       bool wide;
-      P::at((int)(p % P::all), row, off, step, wide);
-      const int t = (int)(p / P::all) * 16 + row;
-      if (t >= n) continue;
-      const int src = kept[t];
-      if (IN_PLACE && src == t) continue;
-      uint8_t* d = block_at<D>(a, to, head, t, true);
-      if (d == nullptr) continue;
-      dst[i] = d + off + row * step;
-      const uint8_t* s = block_at<D>(a, from, head, src, false) + off + src % 16 * step;
+      P::at(l - lb * P::all, row, off, step, wide);
+      if (lb >= have) break;
+      const From f = from[lb * 16 + row];
+      if (f.block == nullptr) continue;
+      const uint8_t* s = f.block + off + f.row * step;
       if (wide) {
         data[i] = *reinterpret_cast<const uint4*>(s);
       } else {
         const uint2 v = *reinterpret_cast<const uint2*>(s);
-        data[i] = uint4{v.x, v.y, 0u, 0u};
+        data[i].x = v.x, data[i].y = v.y;
       }
     }
     if (IN_PLACE) cluster_sync_all();
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (dst[i] == nullptr) continue;
-      const long long p = p0 + ((long long)rank * PER + i) * MOVE + threadIdx.x;
+    for (int i = 0; i < P::each; ++i) {
+      const int l = i * MOVE + (int)threadIdx.x, lb = l / P::all;
       int row, off, step;
       bool wide;
-      P::at((int)(p % P::all), row, off, step, wide);
+      P::at(l - lb * P::all, row, off, step, wide);
+      if (lb >= have) break;
+      if (from[lb * 16 + row].block == nullptr) continue;
+      uint8_t* d = to[lb] + off + row * step;
       if (wide)
-        *reinterpret_cast<uint4*>(dst[i]) = data[i];
+        *reinterpret_cast<uint4*>(d) = data[i];
       else
-        *reinterpret_cast<uint2*>(dst[i]) = uint2{data[i].x, data[i].y};
+        *reinterpret_cast<uint2*>(d) = uint2{data[i].x, data[i].y};
     }
+    __syncthreads();  // the lists are written again
   }
 }
 
@@ -191,12 +247,14 @@ gptq_status move_launch(const EvictArgs& a, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(a.seqs * a.heads * CLU));
   cfg.blockDim = dim3(MOVE);
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CLU;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = CLU;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = IN_PLACE ? 1 : 0;
+  cfg.numAttrs = IN_PLACE ? 2 : 1;
   GQ_PROF(K_KV4_MOVE, s);
   GQ_CUDA(cudaLaunchKernelEx(&cfg, k_kv4_move<D, IN_PLACE>, a));
   return GPTQ_OK;
@@ -205,9 +263,19 @@ gptq_status move_launch(const EvictArgs& a, cudaStream_t s) {
 }  // namespace
 
 gptq_status kv4_evict_run(int dim, bool in_place, const EvictArgs& a, cudaStream_t s) {
+  static DeviceOnce attr;
+  GQ_TRY(attr.run([](int) -> gptq_status {
+    GQ_CUDA(cudaFuncSetAttribute(k_kv4_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStaged * 4));
+    return GPTQ_OK;
+  }));
+  const long long cap = (long long)a.table_stride * a.page_size;
   {
     GQ_PROF(K_KV4_SELECT, s);
-    k_kv4_select<<<(unsigned)(a.seqs * a.heads), SEL, 0, s>>>(a);
+    const unsigned grid = (unsigned)(a.seqs * a.heads);
+    if (cap <= kStaged)
+      k_kv4_select<true><<<grid, SEL, (size_t)cap * 4, s>>>(a);
+    else
+      k_kv4_select<false><<<grid, SEL, 0, s>>>(a);
     GQ_LAUNCHED();
   }
   if (dim == 64) return in_place ? move_launch<64, true>(a, s) : move_launch<64, false>(a, s);

@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
               }
             };
             int c = 0;
-            if (MANY || have >= 32) {
+            if (MANY) {
               // Sixteen columns on their way while sixteen are summed.
               uint32_t v[16], u[16];
               tmem_ld16(ts, v);
@@ -632,7 +632,7 @@ gptq_status weigh_launch(const AttnArgs& a, const float* lse, float* weights, in
 template <class T, int D>
 gptq_status weigh_dim(const AttnArgs& a, const float* lse, float* weights, cudaStream_t s) {
   const long long rows = (long long)a.max_q * a.group;
-  if (rows > kMostRows<D>) return weigh_launch<T, D, true>(a, lse, weights, kMostRows<D>, s);
+  if (rows > 64) return weigh_launch<T, D, true>(a, lse, weights, kMostRows<D>, s);
   return weigh_launch<T, D, false>(a, lse, weights, (int)(rows + 15) / 16 * 16, s);
 }
 
