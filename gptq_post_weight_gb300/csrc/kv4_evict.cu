@@ -17,8 +17,8 @@
 namespace gq {
 namespace {
 
-constexpr int SEL = 512;           // threads that select
-constexpr int SBINS = 2048;
+constexpr int SEL = 1024;          // threads that select
+constexpr int SBINS = 2048, SCAN = SBINS / 4;  // bins, and threads that look through them
 constexpr int kStaged = 40 << 10;  // places of a head that are kept in shared memory at most
 
 // Weights in the order of whole numbers; a NaN is the lightest, both zeros are one.
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
       if ((k & mask) == prefix) atomicAdd(&hist[k >> shift & bins], 1);
     }
     __syncthreads();
-    // Keys in the bins above: each thread has four bins, from the highest down.
-    const int4 mine = reinterpret_cast<const int4*>(hist)[SEL - 1 - tid];
+    // Keys in the bins above: a thread has four bins, from the highest down.
+    const int4 mine = tid < SCAN ? reinterpret_cast<const int4*>(hist)[SCAN - 1 - tid] : int4{};
     const int sum = (mine.x + mine.y) + (mine.z + mine.w);
     int inc = sum;
 #pragma unroll
@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
     __syncthreads();
     int above = inc - sum;
     for (int x = 0; x < warp; ++x) above += part[x].x;
-    if (above < need && need <= above + sum) {  // one thread's
-      int d = 4 * (SEL - 1 - tid) + 3;
+    if (above < need && need <= above + sum) {  // one thread's (threads without bins have a sum of 0)
+      int d = 4 * (SCAN - 1 - tid) + 3;
       const int c[4] = {mine.w, mine.z, mine.y, mine.x};
 #pragma unroll
       for (int x = 0; x < 3; ++x)
@@ -146,7 +146,7 @@ constexpr int CLU = 8;     // CTAs of a head
 // a token's (s, z) pairs (8 or 16 bytes; heads of 256: two).
 template <int D>
 struct Pieces {
-  static constexpr int blocks = D == 256 ? 8 : 16;  // of a CTA's round
+  static constexpr int blocks = D == 256 ? 4 : 8;  // of a CTA's round
   static constexpr int codes = 16 * (D / 32), params = 16 * (D == 256 ? 2 : 1), half = codes + params, all = 2 * half;
   static constexpr int each = blocks * all / MOVE;  // pieces of a thread: as many loads in flight
   // The token of piece p of a block, its bytes' offset from the block's start for
@@ -173,7 +173,7 @@ __device__ __forceinline__ uint8_t* block_at(const EvictArgs& a, const int* row,
 }
 
 template <int D, bool IN_PLACE>
-__global__ void __launch_bounds__(MOVE) k_kv4_move(EvictArgs a) {
+__global__ void __launch_bounds__(MOVE, 4) k_kv4_move(EvictArgs a) {
   using P = Pieces<D>;
   static_assert(P::blocks * P::all % MOVE == 0 && P::blocks * 16 <= MOVE, "a round is a thread's pieces");
   struct From {
