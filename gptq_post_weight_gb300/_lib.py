@@ -49,7 +49,8 @@ SIGNATURES = {
     "gptq_gram_workspace_bytes": (_S, [_I]),
     "gptq_gram_add": (_I, [_P, _I, _P, _I, _P, _S, _P]),
     "gptq_q4tp_linear": (_I, [_I, _P, _L, _I, _P, _P, _P, _I, _I, _P, _I, _P, _L, _P, _L, _P, _P]),
-    "gptq_q4tp_gated": (_I, [_I, _P, _L, _I, _P, _P, _P, _I, _I, _P, _I, _P, _L, _P, _P]),
+    "gptq_q4tp_gated_workspace_bytes": (_S, [_I, _I, _I]),
+    "gptq_q4tp_gated": (_I, [_I, _P, _L, _I, _P, _P, _P, _I, _I, _P, _I, _P, _L, _P, _S, _P, _P]),
     "gptq_kv4_write": (_I, [_I, _P, _L, _I, _I, _I, _P, _P, _L, _L, _L, _L, _P, _I, _P]),
     "gptq_rotary": (_I, [_I, _P, _L, _L, _I, _I, _I, _I, _I, _P, _P, _F, _P, _L, _L, _P]),
     "gptq_kv4_write_rotary": (_I, [_I, _P, _L, _I, _I, _I, _P, _L, _L, _I, _P, _P, _L, _L, _L, _L, _P, _I, _I, _I, _P, _P,
@@ -827,16 +828,18 @@ def q4tp_linear(x, nibbles, rungs, tab, bias=None, act="none", residual=None, ou
     return out
 
 
-def _refuse_gated(x, nibbles, rungs, tab, bias, act, out):
+def _refuse_gated(x, nibbles, rungs, tab, bias, act, out, ws):
     _refuse_linear(x, nibbles, rungs, tab, bias, act, None, None, last=False)
     if tab.shape[0] == 0 or tab.shape[0] % 2:
         raise ValueError(f"tab must have the gate's rows and as many of the up projection, got {tab.shape[0]}")
     if out is not None:
         _rows_of(out, "out", x.shape[0], tab.shape[0] // 2, x)
+    if ws is not None:
+        _ws(ws, x.device)
     _here(x, "x")
 
 
-def q4tp_gated(x, nibbles, rungs, tab, bias=None, act="silu", out=None, stream=None):
+def q4tp_gated(x, nibbles, rungs, tab, bias=None, act="silu", out=None, ws=None, stream=None):
     """act(x Wg^T + bg) * (x Wu^T + bu), the first half of a gated feed-forward
     block, in one launch.  W [2 * inner, n] in q4tp form holds the gate's rows and
     then the up projection's, as quantize_group returns them for the two matrices
@@ -871,14 +874,22 @@ def q4tp_gated(x, nibbles, rungs, tab, bias=None, act="silu", out=None, stream=N
             ldy = st[0] if tokens > 1 else inner
             fine = (fine and out.dtype is xt and out.shape == (tokens, inner) and (inner == 1 or st[1] == 1)
                     and ldy >= inner and out.get_device() == dev)
+        if ws is not None:
+            fine = fine and ws.dtype is u8 and ws.is_contiguous() and ws.get_device() == dev
     except (AttributeError, KeyError, TypeError, ValueError, IndexError):
         fine = False
     if not fine:
-        _refuse_gated(x, nibbles, rungs, tab, bias, act, out)
+        _refuse_gated(x, nibbles, rungs, tab, bias, act, out, ws)
     if out is None:
         out = (sv["empty"] if stream is None else _empty(sv, stream))((tokens, inner), dtype=xt, device=x.device)
+    wp = wn = 0
+    if ws is None and dt == 0 and tokens > 8:
+        wn = _lib.gptq_q4tp_gated_workspace_bytes(dt, tokens, n)
+        ws = (sv["empty"] if stream is None else _empty(sv, stream))(wn, dtype=u8, device=x.device)
+    if ws is not None:
+        wp, wn = ws.data_ptr(), ws.numel()
     status = _lib.gptq_q4tp_gated(dt, x.data_ptr(), ldx, tokens, nibbles.data_ptr(), rungs.data_ptr(), tab.data_ptr(),
-                                  inner, n, bp, code, out.data_ptr(), ldy,
+                                  inner, n, bp, code, out.data_ptr(), ldy, wp, wn,
                                   (_serve_words.get(dev) or (0, _serve_word(dev)))[1], _raw_stream(sv, stream, dev))
     if status:
         raise GptqError("gptq_q4tp_gated", status)

@@ -63,7 +63,8 @@ size_t gram_ws_bytes(int n);
 gptq_status gram_run(float* Hp, int n, const float* X, int T, void* ws, size_t ws_bytes,
                      cudaStream_t s);
 gptq_status q4tp_linear_run(int dtype, const LinearArgs& a, cudaStream_t s);
-gptq_status q4tp_gated_run(int dtype, const LinearArgs& a, cudaStream_t s);
+size_t q4tp_gated_ws_bytes(int dtype, int tokens, int n);
+gptq_status q4tp_gated_run(int dtype, const LinearArgs& a, void* ws, cudaStream_t s);
 gptq_status kv4_write_run(int dtype, uint8_t* cache, long long pages, int heads, int dim, int page_size,
                           const void* k, const void* v, long long kt, long long kh, long long vt, long long vh,
                           const long long* slots, int tokens, cudaStream_t s);
@@ -687,17 +688,24 @@ gptq_status gptq_q4tp_linear(int dtype, const void* X, long long ldx, int tokens
   return q4tp_linear_run(dtype, a, as_stream(stream));
 }
 
+size_t gptq_q4tp_gated_workspace_bytes(int dtype, int tokens, int n) {
+  return bad_dtype(dtype) || bad_tokens(tokens) || bad_n(n) ? 0 : q4tp_gated_ws_bytes(dtype, tokens, n);
+}
+
 gptq_status gptq_q4tp_gated(int dtype, const void* X, long long ldx, int tokens, const uint8_t* nibbles,
                             const uint8_t* rungs, const float* tab, int inner, int n, const void* bias, int act, void* Y,
-                            long long ldy, uint32_t* status, void* stream) {
+                            long long ldy, void* ws, size_t ws_bytes, uint32_t* status, void* stream) {
   if (bad_n(n) || inner <= 0 || inner > GPTQ_MAX_ROWS / 2 || n % GPTQ_GROUP != 0 || bad_tokens(tokens))
     return GPTQ_ERR_SHAPE;
   if (bad_dtype(dtype) || act < GPTQ_ACT_NONE || act > GPTQ_ACT_SILU) return GPTQ_ERR_ARG;
   if (tokens == 0) return GPTQ_OK;
   if (ldx < n || bad_stride(ldx) || ldy < inner) return GPTQ_ERR_SHAPE;
-  if (!ptr_ok(X) || !ptr_ok(nibbles) || !ptr_ok(rungs) || !ptr_ok(tab) || !opt_ok(bias) || !ptr_ok(Y)) return GPTQ_ERR_ARG;
+  if (!ptr_ok(X) || !ptr_ok(nibbles) || !ptr_ok(rungs) || !ptr_ok(tab) || !opt_ok(bias) || !ptr_ok(Y) || !opt_ok(ws))
+    return GPTQ_ERR_ARG;
+  const size_t need = q4tp_gated_ws_bytes(dtype, tokens, n);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return GPTQ_ERR_NOMEM;
   const LinearArgs a{X, ldx, tokens, nibbles, rungs, tab, 2 * inner, n, bias, act, nullptr, 0, Y, ldy, status};
-  return q4tp_gated_run(dtype, a, as_stream(stream));
+  return q4tp_gated_run(dtype, a, ws, as_stream(stream));
 }
 
 gptq_status gptq_kv4_write(int dtype, uint8_t* cache, long long pages, int heads, int dim, int page_size,

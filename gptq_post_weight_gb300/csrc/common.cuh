@@ -49,7 +49,7 @@ enum Kind : int {
   K_SWEEP_GEMM, K_GROUP, K_COPY, K_GRAM_PREP, K_GRAM_GEMM, K_PLACE, K_DEBIAS, K_DEBIAS_GEMM, K_FOLD_STRIP,
   K_Q4_LINEAR, K_KV4_WRITE, K_KV4_READ, K_KV4_ATTENTION, K_KV4_JOIN,
   K_KV4_CHUNK, K_Q4_MID, K_Q4_MANY, K_ROTARY, K_KV4_WRITE_ROTARY, K_KV4_WEIGH,
-  K_KV4_SELECT, K_KV4_MOVE, K_NKINDS
+  K_KV4_SELECT, K_KV4_MOVE, K_Q4_SCALE_X, K_NKINDS
 };
 
 // Every launch site calls prof_begin/prof_end around its <<<>>>: they count

@@ -29,7 +29,8 @@ const char* kNames[K_NKINDS] = {"diag", "build", "potrf", "trsm", "fold_gemm", "
                                 "gram_prep", "gram_gemm", "place", "debias",
                                 "debias_gemm", "fold_strip", "q4_linear", "kv4_write", "kv4_read",
                                 "kv4_attention", "kv4_join", "kv4_chunk", "q4_linear_mid", "q4_linear_many",
-                                "rotary", "kv4_write_rotary", "kv4_weigh", "kv4_select", "kv4_move"};
+                                "rotary", "kv4_write_rotary", "kv4_weigh", "kv4_select", "kv4_move",
+                                "q4_scale_x"};
 
 }  // namespace
 

@@ -33,6 +33,12 @@
 // that the two sums of an output are in one warp's reach when a tile is
 // written out, in all three kernels; what differs from the plain product is
 // that map, boxes of 16 rows for the codes, and the end.
+// Both sums enter the product, and with them the rounding of their weights: in
+// bf16 above 8 tokens the error against 64 bits was 0.0029 of the result, where
+// a result rounded once has 0.0017.  The weights of a gated product are therefore
+// f16 numbers there too (their row's power of two is taken out in any case), and
+// x enters as f16 times a power of two a token (k_q4_scale_x): eight bits of
+// significand fit f16's eleven, down to 2^-32 of the token's largest element.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -156,10 +162,21 @@ __device__ __forceinline__ void finish8(const LinearArgs& a, int tok, int r, boo
   }
 }
 
+// The activation of a gate, by the approximate exponential and reciprocal (2^-22
+// of the result): with a full division an output took some forty instructions,
+// which the writing warps of k_q4_many share their issue slots for.
+__device__ __forceinline__ float gate(float v, int act) {
+  if (act != GPTQ_ACT_SILU && act != GPTQ_ACT_GELU_TANH) return activate(v, act);
+  const float u = act == GPTQ_ACT_SILU ? v : 1.5957691216057308f * (v + 0.044715f * v * v * v);
+  return __fdividef(v, 1.f + ex2(-1.4426950408889634f * u));
+}
+
 // Eight gated outputs, r .. r + 7 of a token, of the sums g of the gate and u of
-// the up projection.
+// the up projection; times `ts` (see LinearArgs::x_scale).
 template <class T>
-__device__ __forceinline__ void finish_gated8(const LinearArgs& a, int tok, int r, float (&g)[8], float (&u)[8]) {
+__device__ __forceinline__ void finish_gated8(const LinearArgs& a, int tok, int r, float (&g)[8], float (&u)[8], float ts) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] *= ts, u[k] *= ts;
   const int outs = a.rows / 2;
   const T* bias = static_cast<const T*>(a.bias);
   T* y = static_cast<T*>(a.y) + (size_t)tok * a.ldy + r;
@@ -172,7 +189,7 @@ __device__ __forceinline__ void finish_gated8(const LinearArgs& a, int tok, int 
     for (int i = 0; i < 2; ++i) {  // (as in finish8)
       float x[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = activate(g[k], a.act);
+      for (int k = 0; k < 4; ++k) x[k] = gate(g[k], a.act);
 #pragma unroll
       for (int k = 0; k < 4; ++k) g[k] = g[k + 4], g[k + 4] = x[k];
     }
@@ -190,7 +207,7 @@ __device__ __forceinline__ void finish_gated8(const LinearArgs& a, int tok, int 
       for (int k = 0; k < 7; ++k) g[k] = g[k + 1], u[k] = u[k + 1];
       if (r + i < outs) {
         if (bias != nullptr) x += Elem<T>::to(bias[r + i]), w += Elem<T>::to(bias[outs + r + i]);
-        y[i] = Elem<T>::from(activate(x, a.act) * w);
+        y[i] = Elem<T>::from(gate(x, a.act) * w);
       }
     }
   }
@@ -228,7 +245,7 @@ __device__ __forceinline__ void reduce_finish_gated(const LinearArgs& a, const f
 #pragma unroll
       for (int e = 0; e < 8; ++e) g[e] = gate[e], u[e] = gate[16 + e];
     }
-    finish_gated8<T>(a, tok0 + tok, r, g, u);
+    finish_gated8<T>(a, tok0 + tok, r, g, u, a.x_scale != nullptr ? a.x_scale[tok0 + tok] : 1.f);
   }
 }
 
@@ -873,7 +890,8 @@ constexpr int MNS = 4;     // boxes of codes
 constexpr int MXS = 4;     // double stages of x (up to 128 tokens a tile; half of them above)
 constexpr int MTN = 256;   // tokens per tile at most
 
-template <class T, bool GATED>
+// TO: type of the result (T, but for a gated product of bf16).
+template <class T, bool GATED, class TO>
 __global__ void __launch_bounds__(640, 1)
     k_q4_mid(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LinearArgs a, int tn,
              int boxes, int nx, WaitCfg wc) {
@@ -1001,7 +1019,7 @@ __global__ void __launch_bounds__(640, 1)
   namespace cg = cooperative_groups;
   if (nrank > 1) cg::this_cluster().sync();
   if constexpr (GATED)
-    reduce_finish_gated<T, QROWS>(a, reinterpret_cast<const float*>(smem), rank, nrank, 640, min(tn, a.tokens - tok0), tok0, row0);
+    reduce_finish_gated<TO, QROWS>(a, reinterpret_cast<const float*>(smem), rank, nrank, 640, min(tn, a.tokens - tok0), tok0, row0);
   else
     reduce_finish<T, QROWS>(a, reinterpret_cast<const float*>(smem), rank, nrank, 640, min(tn, a.tokens - tok0), tok0, row0);
   if (nrank > 1) cg::this_cluster().sync();  // peers read this CTA's sums until here
@@ -1025,7 +1043,7 @@ constexpr int PTN = 256;  // tokens per tile at most
 // through the tile (two sums of 160 tokens and four stages did not: 640
 // cycles a stage), and the next tile's first stages are ready when the sums
 // have been read.
-template <class T, bool GATED>
+template <class T, bool GATED, class TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
     k_q4_many(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LinearArgs a, int tn,
               int mt, int tiles, WaitCfg wc) {
@@ -1190,7 +1208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
         fetch(c + 16);
         if (GATED) {
           const int r8 = row0 / 2 + q * 16 + lane % 2 * 8;
-          if (c + tk < c1 && r8 < a.rows / 2) finish_gated8<T>(a, tok0 + c + tk, r8, w[0], w[1]);
+          if (c + tk < c1 && r8 < a.rows / 2) finish_gated8<TO>(a, tok0 + c + tk, r8, w[0], w[1], a.x_scale != nullptr ? a.x_scale[tok0 + c + tk] : 1.f);
         } else if (c + tk < c1) {
           if (row0 + tr < a.rows) finish8<T>(a, tok0 + c + tk, row0 + tr, v0, w[0], now[0]);
           if (row0 + tr + 8 < a.rows) finish8<T>(a, tok0 + c + tk, row0 + tr + 8, v1, w[1], now[1]);
@@ -1341,13 +1359,13 @@ struct MidShape {
 // SM; clusters stay within a part of the GPU, so that 152 SMs hold 36 clusters
 // of four, 23 of six and 15 of eight: 2048 x 4096, 45 tokens, in sixteen of
 // eight took 25.2 us, in sixteen of six it takes 12.7).
-template <class T, bool GATED>
+template <class T, bool GATED, class TO>
 gptq_status mid_clusters(const int** out) {
   static DeviceOnce attr;
   static int active[9];
   GQ_TRY(attr.run([](int) -> gptq_status {
     constexpr int most = 1024 + MNS * QBOX + 128 * 1024 + QROWS * QTAB * 4;
-    GQ_CUDA(cudaFuncSetAttribute(k_q4_mid<T, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    GQ_CUDA(cudaFuncSetAttribute(k_q4_mid<T, GATED, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     for (int k = 1; k <= 8; ++k) {
       cudaLaunchConfig_t cfg{};
       cfg.gridDim = dim3(1, 1, (unsigned)k);
@@ -1360,7 +1378,7 @@ gptq_status mid_clusters(const int** out) {
       cfg.attrs = at;
       cfg.numAttrs = 1;
       int n = 0;
-      GQ_CUDA(cudaOccupancyMaxActiveClusters(&n, k_q4_mid<T, GATED>, &cfg));
+      GQ_CUDA(cudaOccupancyMaxActiveClusters(&n, k_q4_mid<T, GATED, TO>, &cfg));
       active[k] = n < 1 ? 1 : n;
     }
     return GPTQ_OK;
@@ -1389,7 +1407,7 @@ MidShape mid_shape(const LinearArgs& a, const int* active) {
   return best;
 }
 
-template <class T, bool GATED>
+template <class T, bool GATED, class TO>
 gptq_status mid_launch(const LinearArgs& a, const MidShape& ms, cudaStream_t s) {
   const int rb = (a.rows + QROWS - 1) / QROWS, nt = ms.nt, tn = ms.tn, boxes = ms.boxes, split = ms.split;
   const int nx = tn > 128 ? MXS / 2 : MXS;
@@ -1410,7 +1428,7 @@ gptq_status mid_launch(const LinearArgs& a, const MidShape& ms, cudaStream_t s) 
   cfg.attrs = at;
   cfg.numAttrs = 1;
   GQ_PROF(K_Q4_MID, s);
-  GQ_CUDA(cudaLaunchKernelEx(&cfg, k_q4_mid<T, GATED>, wm, xm, a, tn, boxes, nx, wait_cfg()));
+  GQ_CUDA(cudaLaunchKernelEx(&cfg, k_q4_mid<T, GATED, TO>, wm, xm, a, tn, boxes, nx, wait_cfg()));
   return GPTQ_OK;
 }
 
@@ -1426,12 +1444,12 @@ int many_tile(int tokens, int mt, int pairs, long long& rounds) {
   return best;
 }
 
-template <class T, bool GATED>
+template <class T, bool GATED, class TO>
 gptq_status many_launch(const LinearArgs& a, cudaStream_t s) {
   static DeviceOnce attr;
   constexpr int most = 1024 + PNS * QBOX + 2 * PXS * (PTN / 2) * 128 + QROWS * QTAB * 4 + 8 * 16 * 36 * 4;
   GQ_TRY(attr.run([](int) -> gptq_status {
-    GQ_CUDA(cudaFuncSetAttribute(k_q4_many<T, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    GQ_CUDA(cudaFuncSetAttribute(k_q4_many<T, GATED, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     return GPTQ_OK;
   }));
   const int mt = (a.rows + 2 * QROWS - 1) / (2 * QROWS);
@@ -1447,39 +1465,105 @@ gptq_status many_launch(const LinearArgs& a, cudaStream_t s) {
   const size_t smem = 1024 + (size_t)PNS * QBOX + (size_t)2 * PXS * (tn / 2) * 128 + (size_t)QROWS * QTAB * 4 +
                       8 * 16 * 36 * 4;
   GQ_PROF(K_Q4_MANY, s);
-  k_q4_many<T, GATED><<<2 * np, 896, smem, s>>>(wm, xm, a, tn, mt, (int)tiles, wait_cfg());
+  k_q4_many<T, GATED, TO><<<2 * np, 896, smem, s>>>(wm, xm, a, tn, mt, (int)tiles, wait_cfg());
   GQ_LAUNCHED();
   return GPTQ_OK;
 }
 
-template <class T, bool GATED>
-gptq_status linear_t(const LinearArgs& a, cudaStream_t s) {
-  // Up to 8 tokens the few-token kernel is the faster (5120 x 17408: 18 / 27
-  // us for 1 / 8 tokens against 28); at 16 its blocks of x leave one CTA a SM
-  // (58 us against 29).
-  if (a.tokens <= 8) return few_tokens<T, GATED>(a, s);
+// Above 8 tokens: which of the two kernels.
+template <class T, bool GATED, class TO>
+gptq_status some_tokens(const LinearArgs& a, cudaStream_t s) {
   // Cycles of the two kernels as measured over 17 .. 4096 tokens (4096 x
   // 4096, 5120 x 17408, 14336 x 4096): mid_shape has the first's; a stage takes
   // 540 on a pair of SMs, which spends 13000 more on a tile.
   const int* active = nullptr;
-  GQ_TRY((mid_clusters<T, GATED>(&active)));
+  GQ_TRY((mid_clusters<T, GATED, TO>(&active)));
   const MidShape ms = mid_shape(a, active);
   long long rounds;
   many_tile(a.tokens, (a.rows + 2 * QROWS - 1) / (2 * QROWS), num_sms() / 2, rounds);
   const double many = (double)rounds * ((a.n / GROUP + 7) / 8 * 4 * 540.0 + 13000.0);
-  return ms.cycles <= many ? mid_launch<T, GATED>(a, ms, s) : many_launch<T, GATED>(a, s);
+  return ms.cycles <= many ? mid_launch<T, GATED, TO>(a, ms, s) : many_launch<T, GATED, TO>(a, s);
 }
+
+// Up to 8 tokens the few-token kernel is the faster (5120 x 17408: 18 / 27
+// us for 1 / 8 tokens against 28); at 16 its blocks of x leave one CTA a SM
+// (58 us against 29).
+constexpr int kFewTokens = 8;
+
+template <class T>
+gptq_status linear_t(const LinearArgs& a, cudaStream_t s) {
+  return a.tokens <= kFewTokens ? few_tokens<T, false>(a, s) : some_tokens<T, false, T>(a, s);
+}
+
+// x [tokens][n] of bf16 as f16 numbers times a power of two a token, which brings
+// its largest finite element to 2^14 and above; infinities and NaN stay.  A CTA a
+// token.
+__global__ void __launch_bounds__(256) k_q4_scale_x(const __nv_bfloat16* __restrict__ x, long long ldx, int n,
+                                                    __half* __restrict__ y, float* __restrict__ scale) {
+  __shared__ uint32_t part[8];
+  const int tok = (int)blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const uint4* src = reinterpret_cast<const uint4*>(x + tok * ldx);
+  uint4* dst = reinterpret_cast<uint4*>(y + (size_t)tok * n);
+  uint32_t most = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n / 8; i += 256) {
+    const uint4 v = src[i];
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = u[k] & 0x7fffu, hi = u[k] >> 16 & 0x7fffu;
+      most = max(most, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+    }
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) part[warp] = most;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) most = max(most, part[k]);
+  const int up = min(141 - (int)(most >> 7), 126);  // to 2^14 .. 2^15
+  const float f = __int_as_float((127 + up) << 23);
+  if (threadIdx.x == 0) scale[tok] = __int_as_float((127 - up) << 23);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n / 8; i += 256) {
+    const uint4 v = src[i];
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 w = Elem<__nv_bfloat16>::to2(from_bits2<__nv_bfloat162>(u[k]));
+      o[k] = bits2(Elem<__half>::make2(w.x * f, w.y * f));
+    }
+    dst[i] = uint4{o[0], o[1], o[2], o[3]};
+  }
+}
+
+size_t scale_bytes(int tokens) { return round_up((size_t)tokens * 4, 256); }
 
 }  // namespace
 
 gptq_status q4tp_linear_run(int dtype, const LinearArgs& a, cudaStream_t s) {
   if (a.tokens == 0) return GPTQ_OK;
-  return dtype == GPTQ_BF16 ? linear_t<__nv_bfloat16, false>(a, s) : linear_t<__half, false>(a, s);
+  return dtype == GPTQ_BF16 ? linear_t<__nv_bfloat16>(a, s) : linear_t<__half>(a, s);
 }
 
-gptq_status q4tp_gated_run(int dtype, const LinearArgs& a, cudaStream_t s) {
+size_t q4tp_gated_ws_bytes(int dtype, int tokens, int n) {
+  return dtype == GPTQ_BF16 && tokens > kFewTokens ? scale_bytes(tokens) + (size_t)tokens * n * 2 : 0;
+}
+
+gptq_status q4tp_gated_run(int dtype, const LinearArgs& a, void* ws, cudaStream_t s) {
   if (a.tokens == 0) return GPTQ_OK;
-  return dtype == GPTQ_BF16 ? linear_t<__nv_bfloat16, true>(a, s) : linear_t<__half, true>(a, s);
+  if (a.tokens <= kFewTokens) return dtype == GPTQ_BF16 ? few_tokens<__nv_bfloat16, true>(a, s) : few_tokens<__half, true>(a, s);
+  if (dtype == GPTQ_F16) return some_tokens<__half, true, __half>(a, s);
+  LinearArgs p = a;
+  float* scale = static_cast<float*>(ws);
+  __half* x = reinterpret_cast<__half*>(static_cast<char*>(ws) + scale_bytes(a.tokens));
+  {
+    GQ_PROF(K_Q4_SCALE_X, s);
+    k_q4_scale_x<<<(unsigned)a.tokens, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(a.x), a.ldx, a.n, x, scale);
+    GQ_LAUNCHED();
+  }
+  p.x = x, p.ldx = a.n, p.x_scale = scale;
+  return some_tokens<__half, true, __nv_bfloat16>(p, s);
 }
 
 }  // namespace gq

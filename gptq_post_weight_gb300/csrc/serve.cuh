@@ -183,6 +183,7 @@ struct LinearArgs {
   void* y;
   long long ldy;
   unsigned* status;
+  const float* x_scale = nullptr;  // gated: what each token's row of x is to be multiplied by (may be null)
 };
 
 // Arguments of the attention over the cache.

@@ -432,17 +432,22 @@ gptq_status gptq_q4tp_linear(int dtype, const void* X, long long ldx, int tokens
  * gptq_q4tp_gated -- Y = act(X Wg^T + bg) * (X Wu^T + bu) in one launch, with
  * the gate's `inner` rows and then the up projection's in one q4tp matrix W of
  * 2 * inner rows (one Hessian group: both read X).  Sums, activation and the
- * product in f32, one rounding to T; weights as in gptq_q4tp_linear.
+ * product in f32, one rounding to T.  Up to 8 tokens no weight is rounded; above
+ * that a weight is rounded once to 11 bits, in either type (bf16: X is taken
+ * as f16 times a power of two a token, exact down to 2^-32 of its largest element).
  *
  *   nibbles  in  u8 inner*n;  rungs in u8 2*inner*n/32;  tab in f32 2*inner*32.
  *   bias     in  T 2*inner (may be NULL).
  *   Y        out T tokens*inner, row stride ldy.
+ *   ws       >= gptq_q4tp_gated_workspace_bytes(dtype, tokens, n), which is 0 but
+ *            for bf16 above 8 tokens (ws may then be NULL).
  *   n % 32 == 0; ldx a multiple of 8; ldy >= inner; 2 * inner <= GPTQ_MAX_ROWS.
  */
+size_t gptq_q4tp_gated_workspace_bytes(int dtype, int tokens, int n);
 gptq_status gptq_q4tp_gated(int dtype, const void* X, long long ldx, int tokens,
                             const uint8_t* nibbles, const uint8_t* rungs, const float* tab,
                             int inner, int n, const void* bias, int act, void* Y, long long ldy,
-                            uint32_t* status, void* stream);
+                            void* ws, size_t ws_bytes, uint32_t* status, void* stream);
 
 /*
  * The cache: a pool of `pages` pages of page_size tokens (a multiple of 16,

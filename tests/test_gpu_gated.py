@@ -2,7 +2,7 @@
 
 Tolerance, per output act(g) * u: the two sums are off by eg and eu as a plain
 product's are (test_gpu_linear.py: f32 sums of 32 products of x and a code, the
-groups' sums, above 8 tokens half a step of T for every weight), so the product
+groups' sums, above 8 tokens half a step of f16, in either type, for every weight), so the product
 by 1.13 eg (|u| + eu) + |act(g)| eu with the activations' largest slope; an
 activation and the product in f32 add 2^-20 of the result and, where 1 + erf
 or a large exponential cancels, 2^-22 |g| |u|; and the result rounds to T by
@@ -39,7 +39,7 @@ def check(y, p, dtype, act):
     mag = ax @ np.abs(w).T
     err = 34 * 143 * 2.0 ** -22 * (ax @ np.abs(sc).T) + (n / 32) * 2.0 ** -23 * mag
     if tokens > 8:
-        err = err + HALF[dtype] * mag
+        err = err + HALF["f16"] * mag
     if p["bias"] is not None:
         err = err + 2.0 ** -23 * np.abs(p["bias"])
     half = both.shape[1] // 2
@@ -96,7 +96,7 @@ def test_pairs_of_sms(lib, tokens, inner, n, dtype):
 
     p = problem(tokens, inner, n, dtype, tokens, bias=True)
     y, ran = many.kernels_of(lambda: run(p, dtype, "gelu_tanh"))
-    assert ran == {"q4_linear_many": 1}
+    assert ran == ({"q4_linear_many": 1, "q4_scale_x": 1} if dtype == "bf16" else {"q4_linear_many": 1})
     check(y, p, dtype, "gelu_tanh")
 
 
@@ -193,3 +193,43 @@ def test_captured_and_replayed(lib):
     x.mul_(2)
     g.replay()
     assert torch.equal(y, _lib.q4tp_gated(x, nib, rungs, tab)) and not torch.equal(y, first)
+
+
+@pytest.mark.parametrize("tokens", [12, 1500])
+def test_tokens_of_any_size(lib, tokens):
+    # Above 8 tokens bf16 rows are f16 numbers times a power of two each: rows from
+    # 2^-120 to 2^100, elements 2^30 apart in one row, a row of zeros.  (No
+    # activation, and gate and up projection alike in size, so that the results
+    # of the small rows are what bf16 holds of their squares: those past its ends
+    # are left out.)
+    inner, n = (70, 256) if tokens < 1000 else (2051, 256)
+    p = problem(tokens, inner, n, "bf16", 31)
+    size = np.array([0, 20, 40, 60, -20, -40, -60, 100, -120, 3, -3, 0])[np.arange(tokens) % 12]
+    p["x"] = np.ldexp(p["x"], size[:, None])
+    p["x"][3, ::2] = serve.round_to(np.ldexp(p["x"][3, ::2], -30), "bf16")
+    p["x"][11] = 0
+    y = run(p, "bf16", "none")
+    fits = (np.abs(size) <= 60)
+    p["x"] = p["x"][fits]
+    check(y[torch.from_numpy(fits).cuda()], p, "bf16", "none")
+    assert not y[11].any()
+    assert torch.isinf(y[7]).any() and torch.isfinite(y[8]).all()
+
+
+def test_infinite_and_nan_rows_above_eight_tokens(lib):
+    p = problem(20, 40, 128, "bf16", 18)
+    p["x"][4, 5], p["x"][7, 9] = -np.inf, np.nan
+    p["nib"][:] |= 0x11  # no code is 8: no weight 0
+    y = run(p, "bf16", "none").float().cpu().numpy()
+    want = serve.gated(p["x"], p["nib"], p["rungs"], p["tab"], None, "none")
+    np.testing.assert_array_equal(y[4], want[4].astype(np.float32))
+    assert np.isnan(y[7]).all() and np.isfinite(np.delete(y, [4, 7], 0)).all()
+
+
+def test_given_workspace(lib):
+    from gptq_post_weight_gb300 import _lib
+
+    p = problem(30, 50, 160, "bf16", 20)
+    want = run(p, "bf16", "silu")
+    ws = _lib.workspace(lib.gptq_q4tp_gated_workspace_bytes(0, 30, 160), "cuda")
+    assert torch.equal(run(p, "bf16", "silu", ws=ws), want)

@@ -102,6 +102,7 @@ def test_gated(blib):  # noqa: F811
     odd = (u8(5 * n // 2), u8(10), torch.zeros(5, 32))
     refused(f, x, *odd, match="as many of the up projection")
     refused(f, x, nib, rungs, tab, out=b16(t, 6), match="out must have shape")
+    refused(f, x, nib, rungs, tab, ws=torch.zeros(4), match="ws must be")
     refused(f, x, nib, rungs, tab, out=b16(3, t).t(), match="dense rows")
     refused(f, x.clone().requires_grad_(), nib, rungs, tab, match="requires a gradient")
 
@@ -170,8 +171,13 @@ def test_c_entries(blib):  # noqa: F811
     assert write(dt=5) == 1 and write(cache=None) == 1 and write(q=mis) == 1 and write(k=None) == 1
     assert write(slots=None) == 1 and write(p=None) == 1 and write(t=0, q=None) == 0
 
-    def gated(dt=0, x=ok, ldx=64, t=3, nib=ok, inner=6, n=64, act=4, bias=None, y=ok, ldy=6):
-        return lib.gptq_q4tp_gated(dt, x, ldx, t, nib, ok, ok, inner, n, bias, act, y, ldy, None, None)
+    def gated(dt=0, x=ok, ldx=64, t=3, nib=ok, inner=6, n=64, act=4, bias=None, y=ok, ldy=6, ws=None, wn=0):
+        return lib.gptq_q4tp_gated(dt, x, ldx, t, nib, ok, ok, inner, n, bias, act, y, ldy, ws, wn, None, None)
+
+    need = lib.gptq_q4tp_gated_workspace_bytes(0, 9, 64)
+    assert need >= 9 * (64 * 2 + 4) and gated(t=9) == 3 and gated(t=9, ws=ok, wn=need - 1) == 3 and gated(t=9, ws=mis, wn=need) == 1
+    assert lib.gptq_q4tp_gated_workspace_bytes(0, 8, 64) == 0 and lib.gptq_q4tp_gated_workspace_bytes(1, 100, 64) == 0
+    assert lib.gptq_q4tp_gated_workspace_bytes(2, 100, 64) == 0 and lib.gptq_q4tp_gated_workspace_bytes(0, -1, 64) == 0
 
     assert gated(n=48, ldx=48) == 2 and gated(t=-1) == 2 and gated(inner=0) == 2 and gated(inner=(1 << 23) + 1) == 2
     assert gated(ldx=32) == 2 and gated(ldx=68) == 2 and gated(ldy=5) == 2
