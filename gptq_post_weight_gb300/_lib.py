@@ -60,8 +60,9 @@ SIGNATURES = {
     "gptq_kv4_attention_call_bytes": (_S, [_I, _I, _I, _I, _I, _I, _L]),
     "gptq_kv4_attention_lse": (_I, [_I, _P, _L, _L, _I, _P, _L, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _F, _P, _P, _P,
                                     _S, _P, _P]),
+    "gptq_kv4_attention_weights_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _L]),
     "gptq_kv4_attention_weights": (_I, [_I, _P, _L, _L, _I, _P, _P, _L, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _F, _P,
-                                        _P, _P]),
+                                        _P, _S, _P, _P]),
     "gptq_kv4_evict": (_I, [_P, _L, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P]),
     "gptq_kv4_attention": (_I, [_I, _P, _L, _L, _I, _P, _L, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _F, _P, _P,
                                 _S, _P, _P]),
@@ -1322,8 +1323,8 @@ def kv4_weights(table, page_size, heads):
     return torch.zeros(table.shape[0], heads, table.shape[1] * page_size, dtype=torch.float32, device=table.device)
 
 
-def _refuse_weights(weights, q, lse, cache, table, kv_lens, page_size, q_starts, max_q):
-    _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, None, None, lse, last=False)
+def _refuse_weights(weights, q, lse, cache, table, kv_lens, page_size, q_starts, max_q, ws):
+    _refuse_attention(q, cache, table, kv_lens, page_size, q_starts, max_q, None, ws, lse, last=False)
     _need(lse, "lse", numel=q.shape[0] * q.shape[1], device=q.device)
     shape = (table.shape[0], cache.shape[1], table.shape[1] * page_size)
     _need(weights, "weights", device=q.device)
@@ -1334,7 +1335,7 @@ def _refuse_weights(weights, q, lse, cache, table, kv_lens, page_size, q_starts,
 
 
 def kv4_attention_weights(weights, q, lse, cache, table, kv_lens, page_size, q_starts=None, max_q=1, scale=None,
-                          stream=None):
+                          ws=None, stream=None):
     """Adds to `weights` (f32 [seqs, heads, places of a row of table], see
     kv4_weights) what the queries of a kv4_attention call looked at: for each cached
     token and key head the sum of exp(scale q k - lse) over the queries that see
@@ -1365,15 +1366,25 @@ def kv4_attention_weights(weights, q, lse, cache, table, kv_lens, page_size, q_s
             fine = (fine and q_starts.dtype is i32 and q_starts.numel() == seqs + 1 and q_starts.is_contiguous()
                     and q_starts.get_device() == dev)
             sp = q_starts.data_ptr()
+        if ws is not None:
+            fine = fine and ws.dtype is sv["u8"] and ws.is_contiguous() and ws.get_device() == dev
     except (AttributeError, KeyError, TypeError, ValueError, IndexError):
         fine = False
     if not fine:
-        _refuse_weights(weights, q, lse, cache, table, kv_lens, page_size, q_starts, max_q)
+        _refuse_weights(weights, q, lse, cache, table, kv_lens, page_size, q_starts, max_q, ws)
         qts, qhs = qts if tq > 1 else 0, qhs if hq > 1 else 0
+    wp = wn = 0
+    if ws is None and max_q * hq > 64 * heads:
+        wn = _lib.gptq_kv4_attention_weights_workspace_bytes(dim, heads, hq // heads, max_q, seqs, per * page_size)
+        if wn:
+            ws = (sv["empty"] if stream is None else _empty(sv, stream))(wn, dtype=sv["u8"], device=q.device)
+    if ws is not None:
+        wp, wn = ws.data_ptr(), ws.numel()
     code = _lib.gptq_kv4_attention_weights(dt, q.data_ptr(), qts, qhs, tq, lse.data_ptr(), cache.data_ptr(), pages, heads,
                                            hq // heads, dim, page_size, table.data_ptr(), per, kv_lens.data_ptr(), sp,
                                            seqs, int(max_q), dim ** -0.5 if scale is None else float(scale),
-                                           weights.data_ptr(), (_serve_words.get(dev) or (0, _serve_word(dev)))[1],
+                                           weights.data_ptr(), wp, wn,
+                                           (_serve_words.get(dev) or (0, _serve_word(dev)))[1],
                                            _raw_stream(sv, stream, dev))
     if code:
         raise GptqError("gptq_kv4_attention_weights", code)

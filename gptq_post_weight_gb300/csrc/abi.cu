@@ -79,7 +79,9 @@ gptq_status kv4_write_rotary_run(int dtype, bool half, uint8_t* cache, long long
 size_t kv4_attention_ws_bytes(int dim, int heads, int group, int max_q, int seqs, bool single, long long max_len);
 gptq_status kv4_attention_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s);
 gptq_status kv4_no_sums_run(float* lse, long long n, cudaStream_t s);
-gptq_status kv4_weigh_run(int dtype, int dim, const AttnArgs& a, float scale, const float* lse, float* weights, cudaStream_t s);
+size_t kv4_weigh_ws_bytes(int dim, int heads, int group, int max_q, int seqs, long long max_len);
+gptq_status kv4_weigh_run(int dtype, int dim, const AttnArgs& a, float scale, const float* lse, float* weights, void* ws,
+                          cudaStream_t s);
 gptq_status kv4_evict_run(int dim, bool in_place, const EvictArgs& a, cudaStream_t s);
 }  // namespace gq
 
@@ -830,11 +832,18 @@ gptq_status gptq_kv4_attention_lse(int dtype, const void* Q, long long q_ts, lon
   return kv4_attention_run(dtype, dim, a, as_stream(stream));
 }
 
+size_t gptq_kv4_attention_weights_workspace_bytes(int dim, int heads, int group, int max_q, int seqs, long long max_len) {
+  if (bad_attention(dim, group, max_q) || heads <= 0 || heads > 1024 || seqs <= 0 || seqs > GPTQ_MAX_TOKENS ||
+      max_len <= 0 || max_len > (1ll << 30))
+    return 0;
+  return kv4_weigh_ws_bytes(dim, heads, group, max_q, seqs, max_len);
+}
+
 gptq_status gptq_kv4_attention_weights(int dtype, const void* Q, long long q_ts, long long q_hs, int tq,
                                        const float* lse, const uint8_t* cache, long long pages, int heads,
                                        int group, int dim, int page_size, const int* table, int table_stride,
                                        const int* kv_lens, const int* q_starts, int seqs, int max_q, float scale,
-                                       float* weights, uint32_t* status, void* stream) {
+                                       float* weights, void* ws, size_t ws_bytes, uint32_t* status, void* stream) {
   if (bad_paged_call(pages, heads, dim, page_size, table_stride, seqs) || bad_tokens(tq) || group <= 0 || group > 1024 ||
       max_q <= 0 || max_q > GPTQ_MAX_TOKENS)
     return GPTQ_ERR_SHAPE;
@@ -842,12 +851,14 @@ gptq_status gptq_kv4_attention_weights(int dtype, const void* Q, long long q_ts,
   if (q_starts == nullptr && (tq != seqs || max_q != 1)) return GPTQ_ERR_SHAPE;
   if (tq == 0 || seqs == 0) return GPTQ_OK;
   if (bad_stride(q_ts) || bad_stride(q_hs)) return GPTQ_ERR_SHAPE;
-  if (!ptr_ok(Q) || lse == nullptr || !ptr_ok(cache) || table == nullptr || kv_lens == nullptr || !ptr_ok(weights))
+  if (!ptr_ok(Q) || lse == nullptr || !ptr_ok(cache) || table == nullptr || kv_lens == nullptr || !ptr_ok(weights) || !opt_ok(ws))
     return GPTQ_ERR_ARG;
+  const size_t need = kv4_weigh_ws_bytes(dim, heads, group, max_q, seqs, (long long)table_stride * page_size);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return GPTQ_ERR_NOMEM;
   AttnArgs a{Q,     q_ts,         q_hs,    tq,       cache, pages, heads, group, page_size,
              table, table_stride, kv_lens, q_starts, seqs,  max_q, scale * 1.4426950408889634f,
              nullptr, nullptr, nullptr, dtype == GPTQ_BF16 ? 8u : 64u, status};
-  return kv4_weigh_run(dtype, dim, a, scale, lse, weights, as_stream(stream));
+  return kv4_weigh_run(dtype, dim, a, scale, lse, weights, ws, as_stream(stream));
 }
 
 gptq_status gptq_kv4_evict(uint8_t* cache, long long pages, int heads, int dim, int page_size, const int* table,

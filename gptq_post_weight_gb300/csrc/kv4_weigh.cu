@@ -22,7 +22,10 @@
 // contiguous share of the list of (sequence, key head, step), q (operand B, in
 // the order in which the nibbles come out; warp 24) stays while the head does.
 // Many: steps go round the CTAs, and for each of them all the rows' tiles that
-// see it come by, which the crews bring between the keys.
+// see it come by, which the crews bring between the keys.  Where the steps are too
+// few for the SMs, or a last round of them nearly empty, their rows are cut into
+// parts: each leaves its sums in the workspace, and k_kv4_weigh_join adds them in
+// order.
 #include "serve.cuh"
 
 namespace gq {
@@ -57,6 +60,9 @@ struct WeighArgs {
   float* weights;
   int nt;    // columns of a tile: a multiple of 16
   int nd;    // steps' sums in tensor memory
+  int split;        // MANY: parts that a step's rows are cut into at most
+  float* part;      // their sums, `apart` floats from part to part, laid out like the weights
+  long long apart;
 };
 
 __device__ __forceinline__ uint64_t pair2(float x, float y) {
@@ -165,6 +171,16 @@ __device__ __forceinline__ WSeq wseq_of(const AttnArgs& a, int b) {
   return s;
 }
 
+// x / y of numbers that mostly fit 32 bits, where a division is a quarter as long.
+__device__ __forceinline__ long long quotient(long long x, int y) {
+  return x >> 31 ? x / y : (long long)((unsigned)x / (unsigned)y);
+}
+
+// The first tile of query rows that sees a key of a step.
+__device__ __forceinline__ int first_rows(const AttnArgs& a, const WSeq& s, int step, int nt) {
+  return max((step * 2 * WKEYS - s.len + s.nq) * a.group, 0) / nt;
+}
+
 // A CTA's walk over the list of (sequence, key head, step).
 template <bool MANY>
 struct Walk {
@@ -173,12 +189,14 @@ struct Walk {
   long long u, end;
   int b, head, step;
   WSeq s;
+  int split, nt, seg, lo, hi;  // MANY: part of the rows, its tiles of them
 
-  __device__ __forceinline__ Walk(const AttnArgs& args, const long long* prefix) : a(args), pref(prefix) {
+  __device__ __forceinline__ Walk(const AttnArgs& args, const long long* prefix, const WeighArgs& w, int rows_of_tile)
+      : a(args), pref(prefix), split(w.split), nt(rows_of_tile), seg(0), lo(0), hi(1) {
     const long long W = pref[a.seqs];
     if (MANY) {
       u = blockIdx.x;
-      end = W;
+      end = W * split;
     } else {
       u = W * blockIdx.x / gridDim.x;
       end = W * (blockIdx.x + 1) / gridDim.x;
@@ -187,17 +205,29 @@ struct Walk {
   }
   __device__ __forceinline__ bool there() const { return u < end; }
   __device__ __forceinline__ void find() {
-    if (u >= end) return;
-    int lo = 0, hi = a.seqs - 1;  // the last sequence that starts at or before u
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (pref[mid] <= u) lo = mid; else hi = mid - 1;
+#pragma unroll 1
+    for (; u < end; u += gridDim.x) {
+      const long long item = MANY && split > 1 ? quotient(u, split) : u;
+      int below = 0, last = a.seqs - 1;  // the last sequence that starts at or before the item
+      while (below < last) {
+        const int mid = (below + last + 1) / 2;
+        if (pref[mid] <= item) below = mid; else last = mid - 1;
+      }
+      b = below;
+      s = wseq_of(a, b);
+      const long long rem = item - pref[b];
+      head = (int)quotient(rem, s.steps);
+      step = (int)(rem - (long long)head * s.steps);
+      if (!MANY) return;
+      const int first = first_rows(a, s, step, nt), n = (s.rows + nt - 1) / nt - first;
+      lo = first, hi = first + n;
+      if (split == 1) return;
+      const int parts = min(split, n);
+      seg = (int)(u - item * split);
+      lo = first + (int)((unsigned)(n * seg) / (unsigned)parts);  // (less than 2^24 tiles, sixteen parts)
+      hi = first + (int)((unsigned)(n * (seg + 1)) / (unsigned)parts);
+      if (seg < parts) return;  // (else fewer tiles of rows than parts: none here)
     }
-    b = lo;
-    s = wseq_of(a, b);
-    const long long rem = u - pref[b];
-    head = (int)(rem / s.steps);
-    step = (int)(rem % s.steps);
   }
   // Steps from this one on that are neighbours in one head, `most` at most.
   __device__ __forceinline__ int run(int most) const { return MANY ? 1 : (int)min((long long)min(most, s.steps - step), end - u); }
@@ -213,10 +243,6 @@ struct Walk {
     step = 0;
     if (++head == a.heads) find();
     return true;
-  }
-  // The first tile of query rows that sees a key of this step.
-  __device__ __forceinline__ int first_rows(int nt) const {
-    return max((step * 2 * WKEYS - s.len + s.nq) * a.group, 0) / nt;
   }
 };
 
@@ -307,14 +333,13 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     int d = 0, qn = MANY ? -1 : 0;
     uint32_t dph = 0u;
     bool ok = true;
-    Walk<MANY> it(a, pref);
+    Walk<MANY> it(a, pref, w, nt);
     while (it.there()) {
       const int k0 = (2 * it.step + team) * WKEYS, t = k0 + key;
       uint64_t sum2[2] = {0ull, 0ull};
       float masked_sum = 0.f;
-      const int rt1 = MANY ? (it.s.rows + nt - 1) / nt : 1;
 #pragma unroll 1
-      for (int rt = MANY ? it.first_rows(nt) : 0; rt < rt1; ++rt) {
+      for (int rt = MANY ? it.lo : 0; rt < (MANY ? it.hi : 1); ++rt) {
         if (MANY) ++qn;
         const int r0 = MANY ? rt * nt : 0, have = min(nt, it.s.rows - r0);
         // Whether a row does not see a key of the tile that is there (a row sees
@@ -390,10 +415,16 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
       }
       if (!ok) break;
       const float2 x = both(sum2[0]), y = both(sum2[1]);
+      const float sum = ((x.x + x.y) + (y.x + y.y)) + masked_sum;
+      const long long at = ((long long)it.b * a.heads + it.head) * cap + t;
       // The only addition to this place of the launch: its order is no question,
       // and the total need not come here.
-      if (t < it.s.len)
-        atomicAdd(w.weights + ((long long)it.b * a.heads + it.head) * cap + t, ((x.x + x.y) + (y.x + y.y)) + masked_sum);
+      if (t < it.s.len) {
+        if (MANY && w.split > 1)
+          w.part[it.seg * w.apart + at] = sum;
+        else
+          atomicAdd(w.weights + at, sum);
+      }
       if (it.next() && !MANY) ++qn;
     }
   } else if (warp < 24) {
@@ -443,7 +474,7 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     int i = 0, qn = 0;
     uint32_t aph = 1u;
     bool ok = true;
-    Walk<MANY> it(a, pref), ahead(a, pref);
+    Walk<MANY> it(a, pref, w, nt), ahead = it;
     if (TURNS == 4 && crew >= 2 && ahead.there()) ahead.next();
     if (!MANY && !wc.no_loads && ahead.there()) fetch(ahead);
     for (; it.there() && ok && !wc.no_loads; it.next(), ++i) {
@@ -476,9 +507,8 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
         }
       }
       if (MANY) {
-        const int rt1 = (it.s.rows + nt - 1) / nt;
 #pragma unroll 1
-        for (int rt = it.first_rows(nt); rt < rt1; ++rt, ++qn) {
+        for (int rt = it.lo; rt < it.hi; ++rt, ++qn) {
           if ((qn & 1) != minq) continue;
           // Sixteen bytes of each of P rows, one division for all of them.
           constexpr int C = D / 8, APART = 256 / C, P = kMostRows<D> / APART;  // pieces of a row; rows between a thread's
@@ -509,7 +539,7 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
   } else if (warp != MMA) {
     if (!wc.no_loads) {  // the query rows of each head
       int qn = 0;
-      for (Walk<MANY> it(a, pref); it.there(); it.next(it.run(1 << 30)), ++qn) {
+      for (Walk<MANY> it(a, pref, w, nt); it.there(); it.next(it.run(1 << 30)), ++qn) {
         if (!wait_long(&qempty[qn & 1], ((uint32_t)(qn >> 1) & 1u) ^ 1u, abort, wc.ns)) break;
         uint8_t* dst = qsm + (qn & 1) * qtile;
         constexpr int C = D / 8;  // 16-byte pieces of a row
@@ -543,10 +573,10 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     int as = 0, d = 0, qn = 0;
     uint32_t dph = 1u, aph = 0u;
     bool ok = true, fresh = true;
-    Walk<MANY> it(a, pref);
+    Walk<MANY> it(a, pref, w, nt);
     while (it.there() && ok) {
       // Steps of one head, or rows' tiles of one step.
-      const int n = MANY ? (it.s.rows + nt - 1) / nt - it.first_rows(nt) : it.run(1 << 30);
+      const int n = MANY ? it.hi - it.lo : it.run(1 << 30);
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
         if (MANY || fresh) {
@@ -597,15 +627,57 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base_sh), "r"(512u) : "memory");
 }
 
+// The parts of a step's rows added to the weights, in order.  A CTA a step.
+__global__ void __launch_bounds__(2 * WKEYS) k_kv4_weigh_join(AttnArgs a, WeighArgs w) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
+  const int step = (int)blockIdx.x, head = (int)blockIdx.y, b = (int)blockIdx.z, t = step * 2 * WKEYS + (int)threadIdx.x;
+  const WSeq s = wseq_of(a, b);
+  if (s.nq == 0 || t >= s.len) return;
+  const int parts = min(w.split, (s.rows + w.nt - 1) / w.nt - first_rows(a, s, step, w.nt));
+  const long long at = ((long long)b * a.heads + head) * a.table_stride * a.page_size + t;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) sum += w.part[i * w.apart + at];
+  w.weights[at] += sum;
+}
+
+// Query rows a sequence and key head from which on they come in many tiles.
+// Measured, 16 sequences to 16384: 64 rows of 128 in one tile 71 us; 128 rows 100,
+// as one of many 95.
+constexpr int kFewRows = 64;
+int many_rows(int dim) { return dim == 256 ? kMostRows<256> : kMostRows<128>; }
+
+// Parts that a step's rows are cut into: the least time of the CTA with the most
+// to do, in tiles of rows (four of them at least a part; a part costs two more, for
+// its keys).  The lengths are on the device: the table's width is what is looked at.
+int split_of(int dim, int heads, int group, int max_q, int seqs, long long max_len) {
+  const long long rows = (long long)max_q * group;
+  if (rows <= kFewRows) return 1;
+  const long long tiles = (rows + many_rows(dim) - 1) / many_rows(dim);
+  const long long steps = (max_len + 2 * WKEYS - 1) / (2 * WKEYS) * heads;  // of a sequence
+  const long long sms = num_sms();
+  if (steps >= 16 * sms || steps * std::min(seqs, WSEQS) >= 16 * sms) return 1;
+  const long long items = steps * std::min(seqs, WSEQS);
+  int best = 1;
+  long long least = -1;
+  for (int k = 1; k <= 16 && (k == 1 || tiles >= 4 * k); ++k) {
+    const long long time = (items * k + sms - 1) / sms * ((tiles + k - 1) / k + 2) + (k > 1 ? 4 : 0);
+    if (least < 0 || time < least) least = time, best = k;
+  }
+  return best;
+}
+
 template <class T, int D, bool MANY>
-gptq_status weigh_launch(const AttnArgs& a, const float* lse, float* weights, int nt, cudaStream_t s) {
+gptq_status weigh_launch(const AttnArgs& a, const float* lse, float* weights, int nt, int split, float* part,
+                         cudaStream_t s) {
   constexpr int most = 1024 + kTurns<D> * WKEYS * D * 2 + 2 * kMostRows<D> * D * 2;
   static DeviceOnce attr;
   GQ_TRY(attr.run([](int) -> gptq_status {
     GQ_CUDA(cudaFuncSetAttribute(k_kv4_weigh<T, D, MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     return GPTQ_OK;
   }));
-  WeighArgs w{lse, weights, nt, std::min(WD, 256 / nt)};
+  const long long head_places = (long long)a.table_stride * a.page_size;
+  WeighArgs w{lse, weights, nt, std::min(WD, 256 / nt), split, part, head_places * a.heads * std::min(a.seqs, WSEQS)};
   const size_t smem = 1024 + (size_t)kTurns<D> * WKEYS * D * 2 + (size_t)2 * nt * D * 2;
   const long long steps = ((long long)a.table_stride * a.page_size + 2 * WKEYS - 1) / (2 * WKEYS);
   for (int b0 = 0; b0 < a.seqs; b0 += WSEQS) {
@@ -621,37 +693,59 @@ gptq_status weigh_launch(const AttnArgs& a, const float* lse, float* weights, in
       p.tq = p.seqs;
       w.lse = lse + (long long)b0 * a.heads * a.group;
     }
-    const unsigned grid = (unsigned)std::min<long long>(num_sms(), std::min<long long>(steps * a.heads, 1 << 20) * p.seqs);
-    GQ_PROF(K_KV4_WEIGH, s);
-    k_kv4_weigh<T, D, MANY><<<grid, wthreads(MANY), smem, s>>>(p, w, wait_cfg());
-    GQ_LAUNCHED();
+    const unsigned grid = (unsigned)std::min<long long>(num_sms(), std::min<long long>(steps * a.heads, 1 << 20) * p.seqs * split);
+    {
+      GQ_PROF(K_KV4_WEIGH, s);
+      k_kv4_weigh<T, D, MANY><<<grid, wthreads(MANY), smem, s>>>(p, w, wait_cfg());
+      GQ_LAUNCHED();
+    }
+    if (split == 1) continue;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)steps, (unsigned)a.heads, (unsigned)p.seqs);
+    cfg.blockDim = dim3(2 * WKEYS);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    GQ_PROF(K_KV4_JOIN, s);
+    GQ_CUDA(cudaLaunchKernelEx(&cfg, k_kv4_weigh_join, p, w));
   }
   return GPTQ_OK;
 }
 
 template <class T, int D>
-gptq_status weigh_dim(const AttnArgs& a, const float* lse, float* weights, cudaStream_t s) {
+gptq_status weigh_dim(const AttnArgs& a, const float* lse, float* weights, int split, float* part, cudaStream_t s) {
   const long long rows = (long long)a.max_q * a.group;
-  if (rows > 64) return weigh_launch<T, D, true>(a, lse, weights, kMostRows<D>, s);
-  return weigh_launch<T, D, false>(a, lse, weights, (int)(rows + 15) / 16 * 16, s);
+  if (rows > kFewRows) return weigh_launch<T, D, true>(a, lse, weights, kMostRows<D>, split, part, s);
+  return weigh_launch<T, D, false>(a, lse, weights, (int)(rows + 15) / 16 * 16, 1, nullptr, s);
 }
 
 template <class T>
-gptq_status weigh_t(int dim, const AttnArgs& a, const float* lse, float* weights, cudaStream_t s) {
-  if (dim == 64) return weigh_dim<T, 64>(a, lse, weights, s);
-  if (dim == 128) return weigh_dim<T, 128>(a, lse, weights, s);
-  return weigh_dim<T, 256>(a, lse, weights, s);
+gptq_status weigh_t(int dim, const AttnArgs& a, const float* lse, float* weights, int split, float* part, cudaStream_t s) {
+  if (dim == 64) return weigh_dim<T, 64>(a, lse, weights, split, part, s);
+  if (dim == 128) return weigh_dim<T, 128>(a, lse, weights, split, part, s);
+  return weigh_dim<T, 256>(a, lse, weights, split, part, s);
 }
 
 }  // namespace
 
+size_t kv4_weigh_ws_bytes(int dim, int heads, int group, int max_q, int seqs, long long max_len) {
+  const int k = split_of(dim, heads, group, max_q, seqs, max_len);
+  return k == 1 ? 0 : (size_t)k * std::min(seqs, WSEQS) * heads * max_len * 4;
+}
+
 // `scale` as it is: a score less its logarithm is rounded once, at its own size,
 // before the change of base (in base 2 throughout, the logarithms' rounding
 // alone was 3e-7 of a weight).
-gptq_status kv4_weigh_run(int dtype, int dim, const AttnArgs& a, float scale, const float* lse, float* weights, cudaStream_t s) {
+gptq_status kv4_weigh_run(int dtype, int dim, const AttnArgs& a, float scale, const float* lse, float* weights, void* ws,
+                          cudaStream_t s) {
   AttnArgs p = a;
   p.scale_log2 = scale;
-  return dtype == GPTQ_BF16 ? weigh_t<__nv_bfloat16>(dim, p, lse, weights, s) : weigh_t<__half>(dim, p, lse, weights, s);
+  const int split = split_of(dim, a.heads, a.group, a.max_q, a.seqs, (long long)a.table_stride * a.page_size);
+  return dtype == GPTQ_BF16 ? weigh_t<__nv_bfloat16>(dim, p, lse, weights, split, static_cast<float*>(ws), s)
+                            : weigh_t<__half>(dim, p, lse, weights, split, static_cast<float*>(ws), s);
 }
 
 }  // namespace gq

@@ -581,16 +581,21 @@ gptq_status gptq_kv4_attention_lse(int dtype, const void* Q, long long q_ts, lon
  *   weights  in/out f32 [seqs][heads][table_stride * page_size], by the token's
  *            place in the sequence.  Places past kv_lens and sequences without
  *            queries stay as they are.
+ *   ws       >= gptq_kv4_attention_weights_workspace_bytes(...) of this call
+ *            (max_len: table_stride * page_size), which is 0 for few query rows and
+ *            for many tokens (ws may then be NULL).
  * f32 scores, exponentials and sums, each place's in one fixed order.  A key that
  * is NaN makes its own place NaN.
  */
+size_t gptq_kv4_attention_weights_workspace_bytes(int dim, int heads, int group, int max_q, int seqs,
+                                                  long long max_len);
 gptq_status gptq_kv4_attention_weights(int dtype, const void* Q, long long q_ts, long long q_hs,
                                        int tq, const float* lse, const uint8_t* cache,
                                        long long pages, int heads, int group, int dim,
                                        int page_size, const int* table, int table_stride,
                                        const int* kv_lens, const int* q_starts, int seqs,
-                                       int max_q, float scale, float* weights, uint32_t* status,
-                                       void* stream);
+                                       int max_q, float scale, float* weights, void* ws,
+                                       size_t ws_bytes, uint32_t* status, void* stream);
 
 /*
  * gptq_kv4_evict -- cut every sequence to at most `keep` tokens a key head.  A

@@ -120,6 +120,50 @@ def test_long_contexts(lib, lens, heads, group, dim, page, dtype, q_lens):
     one(lens, heads, group, dim, page, dtype, q_lens, seed=6)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_in_parts(lib, dim):
+    # Few steps of keys and many query rows: the rows of a step are cut, and steps
+    # that only the last rows see have fewer tiles of rows than parts.
+    size = lib.gptq_kv4_attention_weights_workspace_bytes
+    for lens, group, q_lens in (([900], 4, [600]), ([700, 300, 1500], 16, [80, 300, 70]), ([300], 300, None)):
+        max_q = 1 if q_lens is None else max(q_lens)
+        assert size(dim, 1, group, max_q, len(lens), -(-max(lens) // 16) * 16) > 0 or q_lens is None
+        one(lens, 1, group, dim, 16, "bf16", q_lens, seed=19)
+
+
+def test_given_workspace(lib):
+    from gptq_post_weight_gb300 import _lib
+
+    qd, lse, cache, table, lens, starts, max_q = one([900], 1, 4, 64, 16, "f16", [600], seed=21)
+    want, got = _lib.kv4_weights(table, 16, 1), _lib.kv4_weights(table, 16, 1)
+    _lib.kv4_attention_weights(want, qd, lse, cache, table, lens, 16, starts, max_q)
+    ws = _lib.workspace(lib.gptq_kv4_attention_weights_workspace_bytes(64, 1, 4, max_q, 1, table.shape[1] * 16), "cuda")
+    ws.fill_(0xFF)
+    _lib.kv4_attention_weights(got, qd, lse, cache, table, lens, 16, starts, max_q, ws=ws)
+    assert torch.equal(got, want)
+
+
+def test_waits_of_the_weights_run_out(lib):
+    from gptq_post_weight_gb300 import _lib
+
+    for q_lens in (None, [3], [200]):
+        qd, lse, cache, table, lens, starts, max_q = one([500], 2, 2, 128, 16, "bf16", q_lens, seed=22)
+        want = _lib.kv4_weights(table, 16, 2)
+        _lib.kv4_attention_weights(want, qd, lse, cache, table, lens, 16, starts, max_q)
+        try:
+            _lib.test_set_wait(1_000_000, no_loads=True)
+            _lib.kv4_attention_weights(_lib.kv4_weights(table, 16, 2), qd, lse, cache, table, lens, 16, starts, max_q)
+            with pytest.raises(_lib.GptqError) as ei:
+                _lib.serve_check()
+            assert ei.value.code == 6
+        finally:
+            _lib.test_set_wait()
+        got = _lib.kv4_weights(table, 16, 2)
+        _lib.kv4_attention_weights(got, qd, lse, cache, table, lens, 16, starts, max_q)
+        _lib.serve_check()
+        assert torch.equal(got, want)
+
+
 def test_many_sequences(lib):
     r = np.random.default_rng(9)
     one([int(n) for n in r.integers(0, 40, 1500)], 1, 2, 64, 16, "bf16", seed=9)

@@ -118,6 +118,7 @@ def test_attention_weights_and_lse(blib):  # noqa: F811
     refused(f, w, q, lse[:2], cache, table, lens, 16, match="lse must have 12")
     refused(f, w, q, None, cache, table, lens, 16, match="lse must be a torch tensor")
     refused(f, w, q, lse, cache, table[:2], lens[:2], 16, match="one query a sequence")
+    refused(f, w, q, lse, cache, table, lens, 16, ws=torch.zeros(4), match="ws must be")
     refused(f, w[:, :1], q, lse, cache, table, lens, 16, match="weights must be")
     refused(f, w.double(), q, lse, cache, table, lens, 16, match="weights must be torch.float32")
     refused(f, w, q.clone().requires_grad_(), lse, cache, table, lens, 16, match="q requires a gradient")
@@ -184,9 +185,19 @@ def test_c_entries(blib):  # noqa: F811
     assert gated(dt=2) == 1 and gated(act=5) == 1 and gated(x=None) == 1 and gated(nib=mis) == 1 and gated(bias=mis) == 1
     assert gated(t=0, x=None, y=None) == 0
 
-    def weigh(dt=0, q=ok, qt=256, tq=3, lse=ok, group=2, stride=2, lens=ok, starts=None, seqs=3, max_q=1, scale=1.0, w=ok):
+    def weigh(dt=0, q=ok, qt=256, tq=3, lse=ok, group=2, stride=2, lens=ok, starts=None, seqs=3, max_q=1, scale=1.0, w=ok, ws=None,
+              wn=0):
         return lib.gptq_kv4_attention_weights(dt, q, qt, 64, tq, lse, ok, 4, 2, group, 64, 16, ok, stride, lens, starts,
-                                              seqs, max_q, scale, w, None, None)
+                                              seqs, max_q, scale, w, ws, wn, None, None)
+
+    size = lib.gptq_kv4_attention_weights_workspace_bytes
+    need = size(64, 2, 2, 5000, 3, 32)
+    assert need > 0 and need % (3 * 2 * 32 * 4) == 0
+    assert weigh(starts=ok, max_q=5000) == 3 and weigh(starts=ok, max_q=5000, ws=ok, wn=need - 1) == 3
+    assert weigh(starts=ok, max_q=5000, ws=mis, wn=need) == 1
+    assert size(64, 2, 2, 16, 3, 32) == 0 and size(96, 2, 2, 5000, 3, 32) == 0 and size(64, 2, 2, 5000, 0, 32) == 0
+    assert size(64, 8, 4, 2048, 400, 1 << 15) == 0  # enough steps for every SM
+    assert size(64, 1024, 1024, 1 << 20, 1 << 20, 1 << 30) == 0
 
     assert weigh(group=0) == 2 and weigh(stride=0) == 2 and weigh(tq=4) == 2 and weigh(max_q=2) == 2 and weigh(qt=4) == 2
     assert weigh(dt=3) == 1 and weigh(scale=float("nan")) == 1 and weigh(q=mis) == 1 and weigh(lse=None) == 1
