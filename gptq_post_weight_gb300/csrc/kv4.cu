@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(256)
 // The write with rotary positions on its way: q turned into y, k turned into
 // the cache (rounded to T first, so that the codes are those of a turned key
 // that k_kv4_write is given), v as it is.  A lane has a token and eight channels and
-// walks over heads, the query's before the cache's, so that its sines and
+// walks over heads, so that its sines and
 // cosines serve them all; in the half layout the other channels of its pairs
 // are another lane's, which hands them over (dim / 8 lanes of a warp are a
 // head's).  A lane reads and writes its own octets only: y may be q itself.
@@ -262,36 +262,44 @@ __global__ void __launch_bounds__(256)
     }
     return turns ? o : x;
   };
+  // The cache's heads come first: they take longest.
+  const int kv1 = min(h1, c.heads);
+  if (h0 < kv1) {
+    const long long slot = slots[tok];
+    const T* kp = static_cast<const T*>(io.k) + tok * io.st.kt + ch;
+    const T* vp = static_cast<const T*>(io.v) + tok * io.st.vt + ch;
+    uint4 rk = *reinterpret_cast<const uint4*>(kp + h0 * io.st.kh), rv = *reinterpret_cast<const uint4*>(vp + h0 * io.st.vh);
+    const long long head_bytes = (long long)(c.page_size / KV_BLOCK) * kv_block_bytes(c.dim);
+    const int row = (int)(slot & (KV_BLOCK - 1));  // page_size is a multiple of the block
+    uint8_t* blk = in ? block_of(c, slot) : nullptr;
+    const bool stored = blk != nullptr;
+    blk += h0 * head_bytes + row * (c.dim / 2) + ch / 2;
+    const int par = kv_param_off(c.dim) + row * (c.dim / 8) + ch / 8 - (row * (c.dim / 2) + ch / 2);
+#pragma unroll 2
+    for (int h = h0; h < kv1; ++h, blk += head_bytes) {
+      const uint4 k8 = turned8(rk), v8 = rv;
+      if (h + 1 < kv1) {  // ahead: under the quantisation
+        rk = *reinterpret_cast<const uint4*>(kp + (h + 1) * io.st.kh);
+        rv = *reinterpret_cast<const uint4*>(vp + (h + 1) * io.st.vh);
+      }
+      uint32_t pk, pv;
+      const uint32_t wk = quantise8<T>(k8, pk), wv = quantise8<T>(v8, pv);
+      if (stored) {
+        *reinterpret_cast<uint32_t*>(blk) = wk;
+        *reinterpret_cast<uint32_t*>(blk + kv_value_off(c.dim)) = wv;
+        if (ch % 32 == 0) {
+          *reinterpret_cast<uint32_t*>(blk + par) = pk;
+          *reinterpret_cast<uint32_t*>(blk + par + kv_value_off(c.dim)) = pv;
+        }
+      }
+    }
+  }
   const T* q = static_cast<const T*>(io.q) + tok * io.qt + ch;
   T* y = static_cast<T*>(io.y) + tok * io.yt + ch;
 #pragma unroll 4
-  for (int h = h0; h < min(h1, io.q_heads); ++h) {
+  for (int h = max(h0 - c.heads, 0); h < h1 - c.heads; ++h) {
     const uint4 o = turned8(*reinterpret_cast<const uint4*>(q + h * io.qh));
     if (in) *reinterpret_cast<uint4*>(y + h * io.yh) = o;
-  }
-  if (h1 <= io.q_heads) return;
-  const long long slot = slots[tok];
-  uint8_t* blk = in ? block_of(c, slot) : nullptr;
-  const long long head_bytes = (long long)(c.page_size / KV_BLOCK) * kv_block_bytes(c.dim);
-  const int row = (int)(slot & (KV_BLOCK - 1));  // page_size is a multiple of the block
-  const T* kp = static_cast<const T*>(io.k) + tok * io.st.kt + ch;
-  const T* vp = static_cast<const T*>(io.v) + tok * io.st.vt + ch;
-#pragma unroll 2
-  for (int h = max(h0 - io.q_heads, 0); h < h1 - io.q_heads; ++h) {
-    const uint4 v8 = *reinterpret_cast<const uint4*>(vp + h * io.st.vh);
-    const uint4 k8 = turned8(*reinterpret_cast<const uint4*>(kp + h * io.st.kh));
-    uint32_t pk, pv;
-    const uint32_t wk = quantise8<T>(k8, pk), wv = quantise8<T>(v8, pv);
-    if (blk != nullptr) {
-      uint8_t* kb = blk + h * head_bytes + row * (c.dim / 2) + ch / 2;
-      *reinterpret_cast<uint32_t*>(kb) = wk;
-      *reinterpret_cast<uint32_t*>(kb + kv_value_off(c.dim)) = wv;
-      if (ch % 32 == 0) {
-        uint8_t* pb = blk + h * head_bytes + kv_param_off(c.dim) + row * (c.dim / 8) + ch / 8;
-        *reinterpret_cast<uint32_t*>(pb) = pk;
-        *reinterpret_cast<uint32_t*>(pb + kv_value_off(c.dim)) = pv;
-      }
-    }
   }
 }
 
