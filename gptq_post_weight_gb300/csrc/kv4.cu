@@ -350,9 +350,12 @@ gptq_status kv4_write_rotary_run(int dtype, bool half, uint8_t* cache, long long
   const CacheShape c{cache, pages, heads, a.dim, page_size};
   const TurnedHeads io{q, qt, qh, q_heads, y, yt, yh, k, v, Strides{kt, kh, vt, vh}};
   const long long threads = (long long)tokens * (a.dim / 8);
-  // Heads a thread: as many as leave every SM its 2048 threads, sixteen at most.
+  // Heads a thread: as many as leave every SM 1024 threads, sixteen at most.
+  // Measured, 32 + 8 heads of 128 (2048 / 1024 / 512 / 256 threads an SM): 500 tokens
+  // 8.1 / 6.2 / 6.0 / 8.0 us, 1000 9.3 / 7.6 / 8.5 / 10.3, 2000 11.8 / 11.2 / 13.0 / 13.0;
+  // 8001 tokens with sixteen heads 41.2, with eight 44.5.
   const int every = q_heads + heads;
-  const int take = (int)std::min<long long>(std::max<long long>(threads * every / (num_sms() * 2048ll), 1), 16);
+  const int take = (int)std::min<long long>(std::max<long long>(threads * every / (num_sms() * 1024ll), 1), 16);
   const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)((every + take - 1) / take));
   GQ_PROF(K_KV4_WRITE_ROTARY, s);
   if (dtype == GPTQ_BF16) {
