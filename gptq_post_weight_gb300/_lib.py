@@ -1374,7 +1374,7 @@ def kv4_attention_weights(weights, q, lse, cache, table, kv_lens, page_size, q_s
         _refuse_weights(weights, q, lse, cache, table, kv_lens, page_size, q_starts, max_q, ws)
         qts, qhs = qts if tq > 1 else 0, qhs if hq > 1 else 0
     wp = wn = 0
-    if ws is None and max_q * hq > 64 * heads:
+    if ws is None and max_q * hq > 64 * heads:  # (fewer rows never need one)
         wn = _lib.gptq_kv4_attention_weights_workspace_bytes(dim, heads, hq // heads, max_q, seqs, per * page_size)
         if wn:
             ws = (sv["empty"] if stream is None else _empty(sv, stream))(wn, dtype=sv["u8"], device=q.device)

@@ -11,16 +11,19 @@
 // tile (the lanes of tensor memory), the query rows its columns.  A thread that
 // reads its lane then has one key's scores, and the sum over the query rows
 // stays in its registers: no maximum, no exchange between lanes, and no second
-// product.  A CTA fills an SM and is a line of workers:
-//   warps 8-23   decode codes into 128-byte swizzled rows (operand A), once for
-//                all query rows: crews that take turns at the tiles, each with its
-//                next tile's codes on their way in registers;
+// product.  A CTA fills an SM and is a line of workers; two tiles (256 keys) make
+// a step:
+//   crews        decode codes into 128-byte swizzled rows (operand A), once for
+//                all query rows, 16 warps (many rows: 8) that take turns at the
+//                tiles;
 //   the last     issues the products, several steps ahead of the sums;
-//   warps 0-7    exponentials and sums, a lane quarter a warp: two teams, one
-//                for each of the two tiles (256 keys) that make a step.
+//   the first    8 warps (many rows: 16) take exponentials and sums, a lane
+//                quarter a warp, a team for each tile of a step (many rows: two,
+//                half of the columns each).
 // Few rows a sequence and key head (!MANY: one column tile): a CTA takes a
-// contiguous share of the list of (sequence, key head, step), q (operand B, in
-// the order in which the nibbles come out; warp 24) stays while the head does.
+// contiguous share of the list of (sequence, key head, step), a crew's next codes
+// are on their way in registers, and q (operand B, in the order in which the
+// nibbles come out; warp 24) stays while the head does.
 // Many: steps go round the CTAs, and for each of them all the rows' tiles that
 // see it come by, which the crews bring between the keys.  Where the steps are too
 // few for the SMs, or a last round of them nearly empty, their rows are cut into
@@ -37,8 +40,7 @@ constexpr int wthreads(bool many) { return many ? 800 : 832; }
 constexpr int WSEQS = 512;           // sequences of a launch at most
 constexpr int WROWS = 8;             // rows' tiles whose logarithms are kept (more than WD + 2)
 constexpr int WD = 4;                // steps' sums in tensor memory at most
-// Tiles of keys in shared memory, and crews that take turns at them: a place is
-// always the same crew's.
+// Tiles of keys in shared memory: a place is always the same crew's.
 template <int D>
 constexpr int kTurns = D == 256 ? 2 : 4;
 template <int D>
@@ -124,6 +126,18 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
+}
+
+// Barrier of the 256 threads that sum tile x of a step, AND-reducing.
+__device__ __forceinline__ bool tile_all(int x, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.and.pred po, %2, 256, pi;\n"
+      " selp.u32 %0, 1, 0, po;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(1 + x)
+      : "memory");
+  return r != 0u;
 }
 
 // Waits on three barriers at once.
@@ -250,7 +264,8 @@ template <class T, int D, bool MANY>
 __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, WeighArgs w, WaitCfg wc) {
   using T2 = typename Elem<T>::T2;
   constexpr int WTHREADS = wthreads(MANY), MMA = WTHREADS / 32 - 1;  // the warp that issues the products
-  constexpr int HALVES = D / 64, ATILE = WKEYS * D * 2, TURNS = kTurns<D>, CREW = 512 / TURNS;
+  constexpr int SUM = MANY ? 16 : 8;  // warps that sum
+  constexpr int HALVES = D / 64, ATILE = WKEYS * D * 2, TURNS = kTurns<D>, CREW = MANY ? 128 : 512 / TURNS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t afull[TURNS], aempty[TURNS / 2], qfull[2], qempty[2], dfull[WD], dempty[WD];
@@ -263,6 +278,7 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
   // the writer: a place's last readers are long gone.
   __shared__ __align__(16) float nlse[WROWS][128];
   __shared__ int lastkey[WROWS][128];
+  __shared__ float other[2][2][WKEYS];  // MANY: [turn][tile] sums of the second half of the columns
   volatile int* abort = &abort_sh;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int nt = MANY ? kMostRows<D> : w.nt, qtile = nt * D * 2;
@@ -273,7 +289,7 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     for (int i = 0; i < TURNS; ++i) mbar_init(&afull[i], CREW);
     for (int i = 0; i < TURNS / 2; ++i) mbar_init(&aempty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&qfull[i], MANY ? 256 : 32), mbar_init(&qempty[i], 1);
-    for (int i = 0; i < WD; ++i) mbar_init(&dfull[i], 1), mbar_init(&dempty[i], 8);
+    for (int i = 0; i < WD; ++i) mbar_init(&dfull[i], 1), mbar_init(&dempty[i], SUM);
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -324,13 +340,14 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     }
     return row;
   };
-  if (warp < 8) {
-    const int team = warp / 4, key = threadIdx.x & 127;
+  if (warp < SUM) {
+    const int team = warp / 4 % 2, key = threadIdx.x & 127;
+    const int part = MANY ? warp / 8 : 0, c0 = MANY ? part * (nt / 2) : 0;  // of the columns
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const long long cap = (long long)a.table_stride * a.page_size;
     const float scale = a.scale_log2;  // (here the plain scale: see the launch)
     const uint64_t scale2 = pair2(scale, scale), log2e2 = pair2(1.4426950408889634f, 1.4426950408889634f);
-    int d = 0, qn = MANY ? -1 : 0;
+    int d = 0, qn = MANY ? -1 : 0, turn = 0;
     uint32_t dph = 0u;
     bool ok = true;
     Walk<MANY> it(a, pref, w, nt);
@@ -341,16 +358,16 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
 #pragma unroll 1
       for (int rt = MANY ? it.lo : 0; rt < (MANY ? it.hi : 1); ++rt) {
         if (MANY) ++qn;
-        const int r0 = MANY ? rt * nt : 0, have = min(nt, it.s.rows - r0);
+        const int r0 = MANY ? rt * nt + c0 : 0, have = min(MANY ? nt / 2 : nt, it.s.rows - r0);
         // Whether a row does not see a key of the tile that is there (a row sees
         // at least the keys of the rows before it).
         const bool masked = min(k0 + WKEYS, it.s.len) - 1 > it.s.len - it.s.nq + (MANY ? r0 / a.group : 0);
         if (!(ok = wait_long(&dfull[d], dph, abort, wc.ns))) break;
         {
           tc_fence_after();
-          const uint32_t ts = (uint32_t)((2 * d + team) * nt) + lanes;
-          const float* nl = nlse[qn % WROWS];
-          const int* lk = lastkey[qn % WROWS];
+          const uint32_t ts = (uint32_t)((2 * d + team) * nt + c0) + lanes;
+          const float* nl = nlse[qn % WROWS] + c0;
+          const int* lk = lastkey[qn % WROWS] + c0;
           if (!masked) {
             auto some = [&](auto& v, int c) {
               constexpr int N = sizeof(v) / 16;
@@ -413,13 +430,20 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
         }
         if (++d == w.nd) d = 0, dph ^= 1u;
       }
-      if (!ok) break;
+      if (!MANY && !ok) break;
       const float2 x = both(sum2[0]), y = both(sum2[1]);
-      const float sum = ((x.x + x.y) + (y.x + y.y)) + masked_sum;
+      float sum = ((x.x + x.y) + (y.x + y.y)) + masked_sum;
+      if (MANY) {
+        // (A warp whose wait has run out comes here all the same: a tile's warps leave together.)
+        if (part == 1) other[turn][team][key] = sum;
+        if (!(ok = tile_all(team, ok))) break;
+        sum += other[turn][team][key];
+        turn ^= 1;
+      }
       const long long at = ((long long)it.b * a.heads + it.head) * cap + t;
       // The only addition to this place of the launch: its order is no question,
       // and the total need not come here.
-      if (t < it.s.len) {
+      if (t < it.s.len && part == 0) {
         if (MANY && w.split > 1)
           w.part[it.seg * w.apart + at] = sum;
         else
@@ -428,10 +452,10 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
       if (it.next() && !MANY) ++qn;
     }
   } else if (warp < 24) {
-    // Steps are two tiles: crew number c has tile c % 2 of every second step (of
-    // every one where there are two crews).
-    const int ct = (int)threadIdx.x - 256, crew = ct / CREW, dt = ct % CREW, half = crew & 1;
-    const int minq = ct / 256, dq = ct % 256;  // MANY: tiles of query rows, 256 threads each
+    // Crew number c has tile c % 2 of every step, or, where there are four, of
+    // every second one.
+    constexpr int CREWS = (24 - SUM) * 32 / CREW;
+    const int ct = (int)threadIdx.x - SUM * 32, crew = ct / CREW, dt = ct % CREW, half = crew & 1;
     constexpr int GR = D / 32, STRIDE = CREW / GR, U = WKEYS / STRIDE;  // groups a key; keys between a thread's; its keys
     // A warp's lanes: eight that store together have four keys of two neighbouring
     // groups, whose pieces meet no bank twice.
@@ -445,17 +469,18 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     const int bpp = a.page_size / KV_BLOCK, jump = STRIDE / KV_BLOCK / bpp, rest = STRIDE / KV_BLOCK % bpp;
     const uint8_t* mine = a.cache + tok % KV_BLOCK * (D / 2) + grp * 16;
     const int par_off = kv_param_off(D) + tok % KV_BLOCK * (D / 8) + grp * 4 - (tok % KV_BLOCK * (D / 2) + grp * 16);
-    uint4 codes[U];
-    uint32_t par[U];
+    constexpr int B = U < 4 ? U : 4;  // of its keys at a time
+    uint4 codes[B];
+    uint32_t par[B];
     // The thread's codes of its crew's tile of a step.  Nothing is asked about keys
     // past the end: their rows of the product go nowhere, and what stands in the
     // table for them is looked at like any other entry.
-    auto fetch = [&](const Walk<MANY>& it) {
-      const uint32_t blk = (uint32_t)((2 * it.step + half) * WKEYS + tok) / KV_BLOCK;
+    auto fetch = [&](const Walk<MANY>& it, int x0) {
+      const uint32_t blk = (uint32_t)((2 * it.step + half) * WKEYS + tok + x0 * STRIDE) / KV_BLOCK;
       int page = (int)(blk / (uint32_t)bpp), in = (int)(blk % (uint32_t)bpp);
       const int* row = a.table + (long long)it.b * a.table_stride;
 #pragma unroll
-      for (int x = 0; x < U; ++x) {
+      for (int x = 0; x < B; ++x) {
         const unsigned e = (unsigned)row[min(page, a.table_stride - 1)];  // (an entry outside the pool reads page 0)
         // (A pool has less than 2^32 blocks of 1280 bytes and more.)
         const uint32_t at = ((e < (unsigned long long)a.pages ? e : 0u) * (uint32_t)a.heads + (uint32_t)it.head) * (uint32_t)bpp + (uint32_t)in;
@@ -471,48 +496,51 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     // MANY: from a thread's piece of a tile of rows to its next one.
     const int apart = 256 / (D / 8), gmore = apart % a.group;
     const long long more = apart / a.group * a.q_ts + gmore * a.q_hs, wrap = a.q_ts - a.group * a.q_hs;
+    static_assert(MANY || B == U, "codes ahead are a whole tile's");
     int i = 0, qn = 0;
-    uint32_t aph = 1u;
     bool ok = true;
     Walk<MANY> it(a, pref, w, nt), ahead = it;
-    if (TURNS == 4 && crew >= 2 && ahead.there()) ahead.next();
-    if (!MANY && !wc.no_loads && ahead.there()) fetch(ahead);
+    if (CREWS == 4 && crew >= 2 && ahead.there()) ahead.next();
+    if (!MANY && !wc.no_loads && ahead.there()) fetch(ahead, 0);
     for (; it.there() && ok && !wc.no_loads; it.next(), ++i) {
-      if (TURNS == 2 || (i & 1) == crew / 2) {
-        const int as = crew;
-        if (MANY) fetch(it);  // (kept through the query rows' tiles, the codes would be spilled)
-        if (!(ok = wait_long(&aempty[as / 2], aph, abort, wc.ns))) break;
-        aph ^= 1u;
+      if (CREWS == 2 || (i & 1) == crew / 2) {
+        // Its place, and which use of it this is.
+        const int as = (TURNS == 4 ? i % 2 * 2 : 0) + half, use = TURNS == 4 ? i / 2 : i;
+        if (MANY) fetch(it, 0);  // (kept through the query rows' tiles, the codes would be spilled)
+        if (!(ok = wait_long(&aempty[as / 2], ((uint32_t)use & 1u) ^ 1u, abort, wc.ns))) break;
         uint8_t* tile = asm_ + as * ATILE;
 #pragma unroll
-        for (int x = 0; x < U; ++x) {
-          const T2 s2 = from_bits2<T2>(__byte_perm(par[x], par[x], 0x1010)), z2 = from_bits2<T2>(__byte_perm(par[x], par[x], 0x3232));
-          const uint32_t cw[4] = {codes[x].x, codes[x].y, codes[x].z, codes[x].w};
+        for (int x0 = 0; x0 < U; x0 += B) {
+          if (x0 > 0) fetch(it, x0);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint4 o;
-            o.x = bits2(__hfma2(code16<T>(cw[e], 0, a.up), s2, z2));
-            o.y = bits2(__hfma2(code16<T>(cw[e], 1), s2, z2));
-            o.z = bits2(__hfma2(code16<T>(cw[e], 2), s2, z2));
-            o.w = bits2(__hfma2(code16<T>(cw[e], 3), s2, z2));
-            *reinterpret_cast<uint4*>(tile + x * STRIDE * 128 + off[e]) = o;
+          for (int x = 0; x < B; ++x) {
+            const T2 s2 = from_bits2<T2>(__byte_perm(par[x], par[x], 0x1010)), z2 = from_bits2<T2>(__byte_perm(par[x], par[x], 0x3232));
+            const uint32_t cw[4] = {codes[x].x, codes[x].y, codes[x].z, codes[x].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint4 o;
+              o.x = bits2(__hfma2(code16<T>(cw[e], 0, a.up), s2, z2));
+              o.y = bits2(__hfma2(code16<T>(cw[e], 1), s2, z2));
+              o.z = bits2(__hfma2(code16<T>(cw[e], 2), s2, z2));
+              o.w = bits2(__hfma2(code16<T>(cw[e], 3), s2, z2));
+              *reinterpret_cast<uint4*>(tile + (x0 + x) * STRIDE * 128 + off[e]) = o;
+            }
           }
         }
         fence_proxy_async_smem();
         mbar_arrive(&afull[as]);
         if (!MANY) {
           ahead.next();
-          if (TURNS == 4 && ahead.there()) ahead.next();
-          if (ahead.there()) fetch(ahead);
+          if (CREWS == 4 && ahead.there()) ahead.next();
+          if (ahead.there()) fetch(ahead, 0);
         }
       }
       if (MANY) {
 #pragma unroll 1
         for (int rt = it.lo; rt < it.hi; ++rt, ++qn) {
-          if ((qn & 1) != minq) continue;
           // Sixteen bytes of each of P rows, one division for all of them.
           constexpr int C = D / 8, APART = 256 / C, P = kMostRows<D> / APART;  // pieces of a row; rows between a thread's
-          const int r0 = dq / C, c = dq % C, first = rt * nt + r0;
+          const int r0 = ct / C, c = ct % C, first = rt * nt + r0;
           int g = first % a.group;
           const T* src = static_cast<const T*>(a.q) + ((long long)it.s.q0 + first / a.group) * a.q_ts +
                          (long long)(it.head * a.group + g) * a.q_hs + c * 8;
@@ -524,13 +552,13 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
             src += more;
             if ((g += gmore) >= a.group) g -= a.group, src += wrap;
           }
-          const Row row = row_of(it, rt * nt + dq, dq < nt);
+          const Row row = row_of(it, rt * nt + ct, ct < nt);
           // (Before the place is free.)
           if (!(ok = wait_long(&qempty[qn & 1], ((uint32_t)(qn >> 1) & 1u) ^ 1u, abort, wc.ns))) break;
           uint8_t* dst = qsm + (qn & 1) * qtile + c / 8 * (nt * 128) + r0 * 128 + (((c & 7) ^ (r0 & 7)) * 16);
 #pragma unroll
           for (int k = 0; k < P; ++k) *reinterpret_cast<uint4*>(dst + k * APART * 128) = pair_order(v[k]);
-          if (dq < nt) nlse[qn % WROWS][dq] = row.nlse, lastkey[qn % WROWS][dq] = row.last;
+          if (ct < nt) nlse[qn % WROWS][ct] = row.nlse, lastkey[qn % WROWS][ct] = row.last;
           fence_proxy_async_smem();
           mbar_arrive(&qfull[qn & 1]);
         }
@@ -641,10 +669,9 @@ __global__ void __launch_bounds__(2 * WKEYS) k_kv4_weigh_join(AttnArgs a, WeighA
   w.weights[at] += sum;
 }
 
-// Query rows a sequence and key head from which on they come in many tiles.
-// Measured, 16 sequences to 16384: 64 rows of 128 in one tile 71 us; 128 rows 100,
-// as one of many 95.
-constexpr int kFewRows = 64;
+// Query rows of a tile.  Up to as many a sequence and key head stay in shared
+// memory (measured, 16 sequences to 16384, 128 rows of 128: 101 us, brought again for
+// each step, as tiles of many are, 115).
 int many_rows(int dim) { return dim == 256 ? kMostRows<256> : kMostRows<128>; }
 
 // Parts that a step's rows are cut into: the least time of the CTA with the most
@@ -652,7 +679,7 @@ int many_rows(int dim) { return dim == 256 ? kMostRows<256> : kMostRows<128>; }
 // its keys).  The lengths are on the device: the table's width is what is looked at.
 int split_of(int dim, int heads, int group, int max_q, int seqs, long long max_len) {
   const long long rows = (long long)max_q * group;
-  if (rows <= kFewRows) return 1;
+  if (rows <= many_rows(dim)) return 1;
   const long long tiles = (rows + many_rows(dim) - 1) / many_rows(dim);
   const long long steps = (max_len + 2 * WKEYS - 1) / (2 * WKEYS) * heads;  // of a sequence
   const long long sms = num_sms();
@@ -718,7 +745,7 @@ gptq_status weigh_launch(const AttnArgs& a, const float* lse, float* weights, in
 template <class T, int D>
 gptq_status weigh_dim(const AttnArgs& a, const float* lse, float* weights, int split, float* part, cudaStream_t s) {
   const long long rows = (long long)a.max_q * a.group;
-  if (rows > kFewRows) return weigh_launch<T, D, true>(a, lse, weights, kMostRows<D>, split, part, s);
+  if (rows > kMostRows<D>) return weigh_launch<T, D, true>(a, lse, weights, kMostRows<D>, split, part, s);
   return weigh_launch<T, D, false>(a, lse, weights, (int)(rows + 15) / 16 * 16, 1, nullptr, s);
 }
 
