@@ -1072,21 +1072,25 @@ def rotary(x, positions, turns, layout="half", gain=1.0, out=None, stream=None):
         dt = sv["dtypes"][xt]
         tokens, heads, dim = x.shape
         ts, hs, x1 = x.stride()
+        # A dimension of one element may carry any stride (the library wants a multiple of 8).
+        ts, hs = ts if tokens > 1 else 0, hs if heads > 1 else 0
         rot = 2 * turns.numel()
         code = ROTARY_LAYOUTS[layout]
-        fine = (dev >= 0 and dev == sv["current"]() and x1 == 1 and tokens > 1 and heads > 1 and 0 < dim <= 1024
+        fine = (dev >= 0 and dev == sv["current"]() and x1 == 1 and heads > 0 and 0 < dim <= 1024
                 and dim % 16 == 0 and (ts | hs) % 8 == 0 and not x.requires_grad
                 and positions.dtype is i64 and positions.numel() == tokens and positions.is_contiguous()
                 and positions.get_device() == dev and turns.dtype is i64 and turns.is_contiguous()
-                and turns.get_device() == dev and 0 < rot <= dim and rot % 16 == 0 and (out is None or out is x)
+                and turns.get_device() == dev and 0 < rot <= dim and rot % 16 == 0
+                and (out is None or (out is x and (hs >= dim or heads == 1)
+                                     and (ts >= (heads - 1) * hs + dim or tokens <= 1)))
                 and -3e38 < gain < 3e38)
     except (AttributeError, KeyError, TypeError, ValueError, IndexError):
         fine = False
     if not fine:
         _refuse_rotary(x, positions, turns, layout, gain, out)
-        # A dimension of one element may carry any stride (the library wants a multiple of 8).
-        ts, hs = ts if tokens > 1 else 0, hs if heads > 1 else 0
-    if out is None:
+    if out is x:
+        ots, ohs = ts, hs
+    elif out is None:
         out = (sv["empty"] if stream is None else _empty(sv, stream))((tokens, heads, dim), dtype=xt, device=x.device)
         ots, ohs = heads * dim, dim
     else:
@@ -1117,8 +1121,9 @@ def kv4_write_rotary(cache, q, k, v, slots, page_size, positions, turns, layout=
                      stream=None):
     """What rotary does to q and k and kv4_write with the turned k and v, in one
     call and with the same bits.  q [tokens, query heads, dim], k, v [tokens,
-    heads, dim] (strided views allowed), slots, positions [tokens] i64.  Returns
-    the turned q; `out` may be q itself, else overlaps no input."""
+    heads, dim] (strided views allowed), slots (each different, or outside the
+    pool), positions [tokens] i64.  Returns the turned q; `out` may be q itself,
+    else overlaps no input."""
     sv = _serve or _serving()
     try:
         kt, shape, dev, i64 = k.dtype, k.shape, k.get_device(), sv["i64"]
@@ -1129,9 +1134,16 @@ def kv4_write_rotary(cache, q, k, v, slots, page_size, positions, turns, layout=
         qts, qhs, q1 = q.stride()
         kts, khs, k1 = k.stride()
         vts, vhs, v1 = v.stride()
+        # (As in rotary: what one element does not use.)
+        if tokens <= 1:
+            qts = kts = vts = 0
+        if heads == 1:
+            khs = vhs = 0
+        if hq == 1:
+            qhs = 0
         rot = 2 * turns.numel()
         code = ROTARY_LAYOUTS[layout]
-        fine = (dev >= 0 and dev == sv["current"]() and dim in (64, 128, 256) and tokens > 1 and heads > 1 and hq > 1
+        fine = (dev >= 0 and dev == sv["current"]() and dim in (64, 128, 256) and heads > 0 and hq > 0
                 and q.dtype is kt and q.shape == (tokens, hq, dim) and v.dtype is kt and v.shape == shape
                 and k1 == 1 and v1 == 1 and q1 == 1 and (kts | khs | vts | vhs | qts | qhs) % 8 == 0
                 and v.get_device() == dev and q.get_device() == dev
@@ -1142,17 +1154,17 @@ def kv4_write_rotary(cache, q, k, v, slots, page_size, positions, turns, layout=
                 and slots.dtype is i64 and slots.numel() == tokens and slots.is_contiguous() and slots.get_device() == dev
                 and positions.dtype is i64 and positions.numel() == tokens and positions.is_contiguous()
                 and positions.get_device() == dev and turns.dtype is i64 and turns.is_contiguous()
-                and turns.get_device() == dev and 0 < rot <= dim and rot % 16 == 0 and (out is None or out is q)
+                and turns.get_device() == dev and 0 < rot <= dim and rot % 16 == 0
+                and (out is None or (out is q and (qhs >= dim or hq == 1)
+                                     and (qts >= (hq - 1) * qhs + dim or tokens <= 1)))
                 and -3e38 < gain < 3e38)
     except (AttributeError, KeyError, TypeError, ValueError, IndexError):
         fine = False
     if not fine:
         _refuse_write_rotary(cache, q, k, v, slots, page_size, positions, turns, layout, gain, out)
-        # A dimension of one element may carry any stride (the library wants a multiple of 8).
-        kts, vts, qts = (kts, vts, qts) if tokens > 1 else (0, 0, 0)
-        khs, vhs = (khs, vhs) if heads > 1 else (0, 0)
-        qhs = qhs if hq > 1 else 0
-    if out is None:
+    if out is q:
+        ots, ohs = qts, qhs
+    elif out is None:
         out = (sv["empty"] if stream is None else _empty(sv, stream))((tokens, hq, dim), dtype=kt, device=k.device)
         ots, ohs = hq * dim, dim
     else:
@@ -1411,6 +1423,8 @@ def _refuse_evict(cache, table, kv_lens, weights, keep, page_size, recent, out_t
         _need(out_table, "out_table", dtype=torch.int32, device=dev)
         if out_table.dim() != 2 or out_table.shape[0] != seqs or out_table.shape[1] == 0:
             raise ValueError(f"out_table must be [{seqs}, pages], got shape {tuple(out_table.shape)}")
+        if seqs and out_table.data_ptr() == table.data_ptr():
+            raise ValueError("out_table is table: leave it out to keep the tokens in their sequence's pages")
         per = out_table.shape[1]
     if keep <= 0 or keep > per * page_size:
         raise ValueError(f"keep must be 1 to {per * page_size}, the places of a sequence, got {keep}")
@@ -1447,6 +1461,7 @@ def kv4_evict(cache, table, kv_lens, weights, keep, page_size, recent=0, out_tab
                     and out_table.is_contiguous() and out_table.get_device() == dev)
             to = ostride = out_table.shape[1]
             op = out_table.data_ptr()
+            fine = fine and op != table.data_ptr()
         fine = fine and 0 < keep <= to * page_size
     except (AttributeError, KeyError, TypeError, ValueError, IndexError, ZeroDivisionError):
         fine = False

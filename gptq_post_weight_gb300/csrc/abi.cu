@@ -873,7 +873,7 @@ gptq_status gptq_kv4_evict(uint8_t* cache, long long pages, int heads, int dim, 
     return GPTQ_ERR_SHAPE;
   if (seqs == 0) return GPTQ_OK;
   if (!ptr_ok(cache) || table == nullptr || kv_lens == nullptr || weights == nullptr || kept == nullptr ||
-      out_lens == nullptr || out_weights == nullptr)
+      out_lens == nullptr || out_weights == nullptr || out_table == table)
     return GPTQ_ERR_ARG;
   const EvictArgs a{cache,   pages, heads,  page_size, table, table_stride, out_table != nullptr ? out_table : table, to_stride,
                     kv_lens, seqs,  weights, keep,      std::min(recent, keep), kept, out_lens, out_weights};

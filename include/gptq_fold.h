@@ -606,8 +606,8 @@ gptq_status gptq_kv4_attention_weights(int dtype, const void* Q, long long q_ts,
  * shorter one keeps all it has.  Bytes move as they are (any T).
  *
  *   table       in  i32 [seqs][table_stride], as for the attention.
- *   out_table   in  i32 [seqs][out_stride]: pages that take the kept tokens; NULL:
- *               those of `table` itself.  A page that takes tokens is one sequence's
+ *   out_table   in  i32 [seqs][out_stride]: pages that take the kept tokens; NULL
+ *               (and not `table` again): those of `table` itself.  A page that takes tokens is one sequence's
  *               and, unless out_table is NULL, in no row of `table` (pages that
  *               only lose tokens may be shared).  Tokens for an entry outside the
  *               pool are dropped.

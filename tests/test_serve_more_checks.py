@@ -68,6 +68,9 @@ def test_rotary(blib):  # noqa: F811
     flat = b16(2000)
     refused(f, torch.as_strided(flat, (3, 4, 64), (256, 64, 1)), p, t, out=torch.as_strided(flat, (3, 4, 64), (512, 64, 1)),
             match="the input with other strides")
+    # In place, the rows may not overlap either.
+    rows = b16(1, 4, 64).expand(3, 4, 64)
+    refused(f, rows, p, t, out=rows, match="out must have rows that do not overlap")
     refused(f, x.clone().requires_grad_(), p, t, match="requires a gradient")
     refused(f, x, p, t, match="CUDA tensors")
 
@@ -143,6 +146,7 @@ def test_evict(blib):  # noqa: F811
     refused(f, cache, table, lens, w, 4, 16, recent=-1, match="recent must not be negative")
     out = torch.zeros(3, 1, dtype=torch.int32)
     refused(f, cache, table, lens, w, 17, 16, out_table=out, match="keep must be 1 to 16")
+    refused(f, cache, table, lens, w, 4, 16, out_table=table, match="out_table is table")
     refused(f, cache, table, lens, w, 4, 16, out_table=out[:2], match="out_table must be")
     refused(f, cache, table, lens, w, 4, 16, out_table=out.long(), match="out_table must be torch.int32")
     refused(f, cache, table, lens, w.clone().requires_grad_(), 4, 16, match="requires a gradient")
@@ -209,8 +213,10 @@ def test_c_entries(blib):  # noqa: F811
                                   kept, ok, ok, None)
 
     assert evict(d=32) == 2 and evict(page=8) == 2 and evict(stride=0) == 2 and evict(keep=0) == 2 and evict(keep=33) == 2
-    assert evict(recent=-1) == 2 and evict(out=ok) == 2 and evict(out=ok, out_stride=1, keep=17) == 2
+    other = P(1 << 22)
+    assert evict(recent=-1) == 2 and evict(out=other) == 2 and evict(out=other, out_stride=1, keep=17) == 2
     assert evict(seqs=1 << 20, heads=1000) == 2
+    assert evict(out=ok, out_stride=2) == 1  # table itself
     assert evict(cache=None) == 1 and evict(lens=None) == 1 and evict(w=None) == 1 and evict(kept=None) == 1
     assert evict(seqs=0, cache=None) == 0
 
@@ -261,3 +267,16 @@ def test_strides_that_one_element_does_not_use(rec):  # noqa: F811
     _lib.rotary(x, p, turns, out=x, stream=Stream)
     _, a = rec.calls[-1]
     assert a[2] % 8 == 0 and a[3] % 8 == 0 and a[13] % 8 == 0 and a[14] % 8 == 0
+
+
+def test_overlapping_rows_are_not_turned_in_place(rec):  # noqa: F811
+    from gptq_post_weight_gb300 import _lib
+
+    turns, p = gpu(torch.zeros(32, dtype=torch.int64)), gpu(torch.zeros(3, dtype=torch.int64))
+    rows = gpu(torch.zeros(1, 4, 64, dtype=torch.bfloat16)).expand(3, 4, 64)
+    with pytest.raises(ValueError, match="do not overlap"):
+        _lib.rotary(rows, p, turns, out=rows, stream=Stream)
+    cache, k = gpu(torch.zeros(4, 2, 16 * 64 * 5 // 4, dtype=torch.uint8)), gpu(torch.zeros(3, 2, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="do not overlap"):
+        _lib.kv4_write_rotary(cache, rows, k, k, p, 16, p, turns, out=rows, stream=Stream)
+    assert not rec.calls
