@@ -1177,7 +1177,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
       const bool v0 = rows_vec(a, row0 + tr), v1 = rows_vec(a, row0 + tr + 8);
       int c = half == 0 ? 0 : tn / 2;
       uint4 raw[2] = {};
+      float ts = 1.f;
       auto fetch = [&](int cc) {
+        if (GATED && a.x_scale != nullptr && cc + tk < c1) ts = a.x_scale[tok0 + cc + tk];
         if (!GATED && cc + tk < c1) {
           residual8<T>(a, tok0 + cc + tk, row0 + tr, v0, raw[0]);
           residual8<T>(a, tok0 + cc + tk, row0 + tr + 8, v1, raw[1]);
@@ -1208,10 +1210,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
         }
         __syncwarp();
         const uint4 now[2] = {raw[0], raw[1]};
+        const float scale = ts;
         fetch(c + 16);
         if (GATED) {
           const int r8 = row0 / 2 + q * 16 + lane % 2 * 8;
-          if (c + tk < c1 && r8 < a.rows / 2) finish_gated8<TO>(a, tok0 + c + tk, r8, w[0], w[1], a.x_scale != nullptr ? a.x_scale[tok0 + c + tk] : 1.f);
+          if (c + tk < c1 && r8 < a.rows / 2) finish_gated8<TO>(a, tok0 + c + tk, r8, w[0], w[1], scale);
         } else if (c + tk < c1) {
           if (row0 + tr < a.rows) finish8<T>(a, tok0 + c + tk, row0 + tr, v0, w[0], now[0]);
           if (row0 + tr + 8 < a.rows) finish8<T>(a, tok0 + c + tk, row0 + tr + 8, v1, w[1], now[1]);

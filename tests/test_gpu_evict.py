@@ -169,6 +169,15 @@ def test_many_sequences(lib):
     one([int(n) for n in r.integers(0, 40, 1500)], 1, 2, 64, 16, "bf16", seed=9)
 
 
+def test_many_sequences_of_many_rows(lib):
+    # More sequences than a launch takes, tiles of many rows (the longest has 160)
+    # and parts of them; some sequences have no queries, some no keys.
+    r = np.random.default_rng(10)
+    q_lens = [int(n) for n in r.integers(0, 4, 700)]
+    q_lens[3] = q_lens[600] = 10
+    one([int(n) for n in r.integers(0, 30, 700)], 1, 16, 64, 16, "bf16", q_lens, seed=10)
+
+
 def test_scales(lib):
     one([300], 1, 2, 128, 16, "bf16", seed=10, scale=3.0)
     one([77], 1, 2, 64, 16, "f16", [9], seed=11, scale=0.0)
