@@ -38,10 +38,13 @@
 // a result rounded once has 0.0017.  The weights of a gated product are therefore
 // f16 numbers there too (their row's power of two is taken out in any case), and
 // x enters as f16 times a power of two a token (k_q4_scale_x): eight bits of
-// significand fit f16's eleven, down to 2^-32 of the token's largest element.
-// Measured, 14336 outputs, n = 4096: one token 19.0 us (3.5 TB/s), 45 tokens 47 us (224
-// tiles on 152 SMs: two rounds of the plain product's one), 4096 tokens 675 us, 1.43
-// PFLOP/s (tensor cores 64 %: with 4096 columns a tile's end is a quarter of it).
+// significand fit f16's eleven, down to 2^-32 of the token's largest element.  In
+// f16 itself eleven bits raised the error from 0.00021 to 0.00036; there half of the
+// columns' weights enter with what their rounding leaves (FINE: 0.00029).
+// Measured, 14336 outputs, n = 4096: one token 17.0 us (3.9 TB/s), 45 tokens of f16 55 us
+// (224 tiles on 152 SMs: two rounds of the plain product's one), 4096 tokens 658 us, 1.46
+// PFLOP/s (tensor cores 64 %: with 4096 columns a tile's end is a quarter of it), of
+// f16 1050.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -174,13 +177,49 @@ __device__ __forceinline__ float gate(float v, int act) {
   return __fdividef(v, 1.f + ex2(-1.4426950408889634f * u));
 }
 
+// The sum of a token and a weight row, weight by weight.
+template <class T>
+__device__ __noinline__ float row_sum(const T* x, const uint8_t* nibbles, const uint8_t* rungs, const float* tab, int n) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < n / GROUP; ++k) {
+    const float s = rungs[k] < 32 ? tab[rungs[k]] : 0.f;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const int b = nibbles[k * 16 + i];
+      sum = fmaf((float)((b & 15) - 8) * s, Elem<T>::to(x[k * 32 + 2 * i]), sum);
+      sum = fmaf((float)((b >> 4) - 8) * s, Elem<T>::to(x[k * 32 + 2 * i + 1]), sum);
+    }
+  }
+  return sum;
+}
+
+// Sums of rows r .. r + 7 that are no finite number, again: an infinite x times a
+// weight and times what its rounding left may be infinity minus infinity (FINE).
+template <class T>
+__device__ __forceinline__ void sums_again(const LinearArgs& a, int tok, int r, int rows, float (&v)[8]) {
+  bool finite = true;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) finite = finite && fabsf(v[k]) < INFINITY;
+  if (__builtin_expect(finite, 1)) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (r + k < rows && !(fabsf(v[k]) < INFINITY))
+      v[k] = row_sum<T>(static_cast<const T*>(a.x) + (size_t)tok * a.ldx, a.nibbles + (size_t)(r + k) * (a.n / 2),
+                        a.rungs + (size_t)(r + k) * (a.n / GROUP), a.tab + (size_t)(r + k) * 32, a.n);
+}
+
 // Eight gated outputs, r .. r + 7 of a token, of the sums g of the gate and u of
 // the up projection; times `ts` (see LinearArgs::x_scale).
-template <class T>
+template <class T, bool FINE>
 __device__ __forceinline__ void finish_gated8(const LinearArgs& a, int tok, int r, float (&g)[8], float (&u)[8], float ts) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) g[k] *= ts, u[k] *= ts;
   const int outs = a.rows / 2;
+  if (FINE) {
+    sums_again<T>(a, tok, r, outs, g);
+    sums_again<T>(a, tok, outs + r, a.rows, u);
+  }
   const T* bias = static_cast<const T*>(a.bias);
   T* y = static_cast<T*>(a.y) + (size_t)tok * a.ldy + r;
   if (r + 8 <= outs && a.ldy % 8 == 0 && outs % 8 == 0) {
@@ -229,7 +268,7 @@ __device__ __forceinline__ void add_peer8(float (&v)[8], uint32_t at, int rank) 
 }
 
 // reduce_finish of a gated tile.
-template <class T, int ROWS>
+template <class T, int ROWS, bool FINE>
 __device__ __forceinline__ void reduce_finish_gated(const LinearArgs& a, const float* part, int rank, int nrank, int nthreads,
                                                     int ntok, int tok0, int row0) {
   for (int i = rank * nthreads + threadIdx.x; i < ntok * (ROWS / 16); i += nrank * nthreads) {
@@ -248,7 +287,7 @@ __device__ __forceinline__ void reduce_finish_gated(const LinearArgs& a, const f
 #pragma unroll
       for (int e = 0; e < 8; ++e) g[e] = gate[e], u[e] = gate[16 + e];
     }
-    finish_gated8<T>(a, tok0 + tok, r, g, u, a.x_scale != nullptr ? a.x_scale[tok0 + tok] : 1.f);
+    finish_gated8<T, FINE>(a, tok0 + tok, r, g, u, a.x_scale != nullptr ? a.x_scale[tok0 + tok] : 1.f);
   }
 }
 
@@ -614,7 +653,7 @@ __global__ void __launch_bounds__(32 * FW)
   else
     __syncthreads();
   if constexpr (GATED)
-    reduce_finish_gated<T, FROWS>(a, part, rank, nrank, NTHR, ntok, tok0, row0);
+    reduce_finish_gated<T, FROWS, false>(a, part, rank, nrank, NTHR, ntok, tok0, row0);
   else
     reduce_finish<T, FROWS>(a, part, rank, nrank, NTHR, ntok, tok0, row0);
   if (nrank > 1) cg::this_cluster().sync();  // peers read this CTA's sums until here
@@ -670,6 +709,28 @@ __device__ __forceinline__ void dequant32(uint4 v, uint32_t s, uint32_t (&o)[16]
     for (int j = 0; j < 4; ++j) {
       const T2 c = __hsub2(from_bits2<T2>(and_or<0x000F000Fu>(p[j], Code8<T>::kMagic)), bias);
       o[4 * i + j] = bits2(__hfma2(c, hi, __hmul2(c, lo)));
+    }
+  }
+}
+
+// The same with what the rounding left: o + rest is the product to some 21 bits.
+template <class T>
+__device__ __forceinline__ void dequant32(uint4 v, uint32_t s, uint32_t (&o)[16], uint32_t (&rest)[16]) {
+  using T2 = typename Elem<T>::T2;
+  const T2 hi = from_bits2<T2>(__byte_perm(s, s, 0x1010)), lo = from_bits2<T2>(__byte_perm(s, s, 0x3232));
+  const T2 bias = from_bits2<T2>(Code8<T>::kBias);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = w[i] >> 4;
+    const uint32_t p[4] = {__byte_perm(w[i], h, 0x4400), __byte_perm(w[i], h, 0x5511), __byte_perm(w[i], h, 0x6622),
+                           __byte_perm(w[i], h, 0x7733)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const T2 c = __hsub2(from_bits2<T2>(and_or<0x000F000Fu>(p[j], Code8<T>::kMagic)), bias);
+      const T2 full = __hfma2(c, hi, __hmul2(c, lo));
+      o[4 * i + j] = bits2(full);
+      rest[4 * i + j] = bits2(__hfma2(c, lo, __hfma2(c, hi, __hneg2(full))));
     }
   }
 }
@@ -804,13 +865,32 @@ __device__ __forceinline__ void dequant_stage(const uint8_t* box, int r, int j, 
   tmem_st16(taddr + 16, o);
 }
 
+// The same, and what the rounding left 32 columns on.
+template <class T>
+__device__ __forceinline__ void dequant_stage_both(const uint8_t* box, int r, int j, uint32_t rungs, const uint32_t* tab,
+                                                   uint32_t taddr) {
+#pragma unroll 1
+  for (int g = 0; g < 2; ++g) {
+    const uint4 v = *reinterpret_cast<const uint4*>(box + r * 128 + (((2 * j + g) ^ (r & 7)) * 16));
+    const uint32_t s = tab[r * QTAB + min(rungs >> (8 * g) & 0xffu, 32u)];
+    uint32_t o[16], rest[16];
+    dequant32<T>(v, s, o, rest);
+    tmem_st16(taddr + 16 * g, o);
+    tmem_st16(taddr + 32 + 16 * g, rest);
+  }
+}
+
 // What a dequantising warp does with the boxes 0 .. nbox - 1 of a tile, the
 // first of which is box number `seq` of the kernel's life.  The sixteen warps
 // are two teams that take turns at the boxes, and a team's two groups of four
 // warps (the lane quarters) halve a box: a warp decodes two stages of its 32
 // rows between looks at the barriers, always into the same columns of tensor
 // memory.  (With one stage a look, looking cost as much as decoding.)
-template <class T, bool PAIR, int NS, bool GATED>  // NS: boxes in the ring
+//
+// FINE: the first half of each box (h == 0) is decoded with what the rounding of
+// its weights leaves, one stage at a time in the columns of two: half of the
+// weights then add no error.
+template <class T, bool PAIR, int NS, bool GATED, bool FINE>  // NS: boxes in the ring
 struct Dequant {
   int slot;        // of the next box of this team in the ring
   uint32_t phase;  // of its barrier
@@ -843,21 +923,30 @@ struct Dequant {
       g0 += 16;
       q2 = four_rungs(rungs, in, g0 + 32, gpr);
       if (!wait_bar_warp(&nfull[slot], phase, abort, limit)) return false;
-      if (!wait_bar_warp(&aempty[half], aphase, abort, limit)) return false;
-      tc_fence_after();
       const uint8_t* box = ring + slot * QBOX;
+      const bool fine = FINE && h == 0;
 #pragma unroll 1
-      for (int u = 0; u < 2; ++u)
-        dequant_stage<T>(box, r, 2 * h + u, rg >> (16 * u), tab, taddr + 32 * u);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR)
-          mbar_arrive_leader(&afull[half]);
-        else
-          mbar_arrive_relaxed(&afull[half]);
-        mbar_arrive_relaxed(&nempty[slot]);
+      for (int k = 0; k < (fine ? 2 : 1); ++k) {
+        // (Two uses of the place a box: its phases are even and odd by turns.)
+        if (!wait_bar_warp(&aempty[half], fine ? (uint32_t)k ^ 1u : aphase, abort, limit)) return false;
+        tc_fence_after();
+        if (fine) {
+          dequant_stage_both<T>(box, r, k, rg >> (16 * k), tab, taddr);
+        } else {
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u)
+            dequant_stage<T>(box, r, 2 * h + u, rg >> (16 * u), tab, taddr + 32 * u);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_leader(&afull[half]);
+          else
+            mbar_arrive_relaxed(&afull[half]);
+          if (!fine || k == 1) mbar_arrive_relaxed(&nempty[slot]);
+        }
       }
       slot += 2;
       if (slot >= NS) {
@@ -894,7 +983,7 @@ constexpr int MXS = 4;     // double stages of x (up to 128 tokens a tile; half 
 constexpr int MTN = 256;   // tokens per tile at most
 
 // TO: type of the result (T, but for a gated product of bf16).
-template <class T, bool GATED, class TO>
+template <class T, bool GATED, class TO, bool FINE>
 __global__ void __launch_bounds__(640, 1)
     k_q4_mid(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LinearArgs a, int tn,
              int boxes, int nx, WaitCfg wc) {
@@ -970,6 +1059,22 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int as = 2 * (b & 1) + h;
+        if (FINE && h == 0) {  // a stage and its rest, both times the stage's x
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (!(ok = wait_both(&xfull[xs], xph, &afull[as], (uint32_t)u, abort, wc.ns))) break;
+            tc_fence_after();
+            if (one) {
+              const uint64_t xd = xdesc + (uint64_t)((2u * (uint32_t)xs + (uint32_t)u) * step);
+              mma_two<false>(0u, QACOL + 64 * as, xd, xd, idesc, b == 0 && u == 0);
+              if (u == 1) mma_commit(&xempty[xs]);
+              mma_commit(&aempty[as]);
+            }
+          }
+          if (!ok) break;
+          if (++xs == nx) xs = 0, xph ^= 1u;
+          continue;
+        }
         if (!(ok = wait_both(&xfull[xs], xph, &afull[as], (uint32_t)(b >> 1) & 1u, abort, wc.ns))) break;
         tc_fence_after();
         if (one) {
@@ -990,7 +1095,7 @@ __global__ void __launch_bounds__(640, 1)
   } else if (warp >= 4) {
     const int j = (warp - 4) / 4, q = warp & 3, r = q * 32 + lane;
     load_ladders<T, GATED>(a, row0, tab, rowscale, rowmax);
-    Dequant<T, false, MNS, GATED> dq;
+    Dequant<T, false, MNS, GATED, FINE> dq;
     bool ok = dq.tile(a, row0, box0, nbox, 0, nring, tab, nfull, nempty, afull, aempty, abort, wc.ns);
     // Sums to shared memory [token][row] (over the x ring: its MMAs are done).
     if (ok) ok = wait_bar_warp(&done, 0u, abort, wc.ns);
@@ -1022,7 +1127,7 @@ __global__ void __launch_bounds__(640, 1)
   namespace cg = cooperative_groups;
   if (nrank > 1) cg::this_cluster().sync();
   if constexpr (GATED)
-    reduce_finish_gated<TO, QROWS>(a, reinterpret_cast<const float*>(smem), rank, nrank, 640, min(tn, a.tokens - tok0), tok0, row0);
+    reduce_finish_gated<TO, QROWS, FINE>(a, reinterpret_cast<const float*>(smem), rank, nrank, 640, min(tn, a.tokens - tok0), tok0, row0);
   else
     reduce_finish<T, QROWS>(a, reinterpret_cast<const float*>(smem), rank, nrank, 640, min(tn, a.tokens - tok0), tok0, row0);
   if (nrank > 1) cg::this_cluster().sync();  // peers read this CTA's sums until here
@@ -1046,7 +1151,7 @@ constexpr int PTN = 256;  // tokens per tile at most
 // through the tile (two sums of 160 tokens and four stages did not: 640
 // cycles a stage), and the next tile's first stages are ready when the sums
 // have been read.
-template <class T, bool GATED, class TO>
+template <class T, bool GATED, class TO, bool FINE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
     k_q4_many(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LinearArgs a, int tn,
               int mt, int tiles, WaitCfg wc) {
@@ -1132,6 +1237,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
           for (int h = 0; h < 2; ++h) {
             const int xs = 2 * (box & 1) + h;  // x and A turn over together: two boxes
             const uint32_t ph = (uint32_t)(box >> 1) & 1u;
+            if (FINE && h == 0) {  // as in k_q4_mid
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                if (!(ok = wait_both(&xfull[xs], ph, &afull[xs], (uint32_t)u, abort, wc.ns))) break;
+                tc_fence_after();
+                if (one) {
+                  const uint64_t xd = xdesc + (uint64_t)((2u * (uint32_t)xs + (uint32_t)u) * step);
+                  mma_two<true>(0u, QACOL + 64 * xs, xd, xd, idesc, b == 0 && u == 0);
+                  if (u == 1) mma_commit_pair(&xempty[xs]);
+                  mma_commit_pair(&aempty[xs]);
+                }
+              }
+              if (!ok) break;
+              continue;
+            }
             if (!(ok = wait_both(&xfull[xs], ph, &afull[xs], ph, abort, wc.ns))) break;
             tc_fence_after();
             if (one) {
@@ -1152,7 +1272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
       }
     }
   } else if (warp >= 4 && warp < 4 + QDEQ) {
-    Dequant<T, true, PNS, GATED> dq;
+    Dequant<T, true, PNS, GATED, FINE> dq;
     int k = 0;
     bool ok = true;
     for (int t = pair; t < tiles; t += npairs, ++k) {
@@ -1214,7 +1334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(896, 1)
         fetch(c + 16);
         if (GATED) {
           const int r8 = row0 / 2 + q * 16 + lane % 2 * 8;
-          if (c + tk < c1 && r8 < a.rows / 2) finish_gated8<TO>(a, tok0 + c + tk, r8, w[0], w[1], scale);
+          if (c + tk < c1 && r8 < a.rows / 2) finish_gated8<TO, FINE>(a, tok0 + c + tk, r8, w[0], w[1], scale);
         } else if (c + tk < c1) {
           if (row0 + tr < a.rows) finish8<T>(a, tok0 + c + tk, row0 + tr, v0, w[0], now[0]);
           if (row0 + tr + 8 < a.rows) finish8<T>(a, tok0 + c + tk, row0 + tr + 8, v1, w[1], now[1]);
@@ -1365,13 +1485,13 @@ struct MidShape {
 // SM; clusters stay within a part of the GPU, so that 152 SMs hold 36 clusters
 // of four, 23 of six and 15 of eight: 2048 x 4096, 45 tokens, in sixteen of
 // eight took 25.2 us, in sixteen of six it takes 12.7).
-template <class T, bool GATED, class TO>
+template <class T, bool GATED, class TO, bool FINE>
 gptq_status mid_clusters(const int** out) {
   static DeviceOnce attr;
   static int active[9];
   GQ_TRY(attr.run([](int) -> gptq_status {
     constexpr int most = 1024 + MNS * QBOX + 128 * 1024 + QROWS * QTAB * 4;
-    GQ_CUDA(cudaFuncSetAttribute(k_q4_mid<T, GATED, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    GQ_CUDA(cudaFuncSetAttribute(k_q4_mid<T, GATED, TO, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     for (int k = 1; k <= 8; ++k) {
       cudaLaunchConfig_t cfg{};
       cfg.gridDim = dim3(1, 1, (unsigned)k);
@@ -1384,7 +1504,7 @@ gptq_status mid_clusters(const int** out) {
       cfg.attrs = at;
       cfg.numAttrs = 1;
       int n = 0;
-      GQ_CUDA(cudaOccupancyMaxActiveClusters(&n, k_q4_mid<T, GATED, TO>, &cfg));
+      GQ_CUDA(cudaOccupancyMaxActiveClusters(&n, k_q4_mid<T, GATED, TO, FINE>, &cfg));
       active[k] = n < 1 ? 1 : n;
     }
     return GPTQ_OK;
@@ -1413,7 +1533,7 @@ MidShape mid_shape(const LinearArgs& a, const int* active) {
   return best;
 }
 
-template <class T, bool GATED, class TO>
+template <class T, bool GATED, class TO, bool FINE>
 gptq_status mid_launch(const LinearArgs& a, const MidShape& ms, cudaStream_t s) {
   const int rb = (a.rows + QROWS - 1) / QROWS, nt = ms.nt, tn = ms.tn, boxes = ms.boxes, split = ms.split;
   const int nx = tn > 128 ? MXS / 2 : MXS;
@@ -1434,7 +1554,7 @@ gptq_status mid_launch(const LinearArgs& a, const MidShape& ms, cudaStream_t s) 
   cfg.attrs = at;
   cfg.numAttrs = 1;
   GQ_PROF(K_Q4_MID, s);
-  GQ_CUDA(cudaLaunchKernelEx(&cfg, k_q4_mid<T, GATED, TO>, wm, xm, a, tn, boxes, nx, wait_cfg()));
+  GQ_CUDA(cudaLaunchKernelEx(&cfg, k_q4_mid<T, GATED, TO, FINE>, wm, xm, a, tn, boxes, nx, wait_cfg()));
   return GPTQ_OK;
 }
 
@@ -1450,12 +1570,12 @@ int many_tile(int tokens, int mt, int pairs, long long& rounds) {
   return best;
 }
 
-template <class T, bool GATED, class TO>
+template <class T, bool GATED, class TO, bool FINE>
 gptq_status many_launch(const LinearArgs& a, cudaStream_t s) {
   static DeviceOnce attr;
   constexpr int most = 1024 + PNS * QBOX + 2 * PXS * (PTN / 2) * 128 + QROWS * QTAB * 4 + 8 * 16 * 36 * 4;
   GQ_TRY(attr.run([](int) -> gptq_status {
-    GQ_CUDA(cudaFuncSetAttribute(k_q4_many<T, GATED, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    GQ_CUDA(cudaFuncSetAttribute(k_q4_many<T, GATED, TO, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     return GPTQ_OK;
   }));
   const int mt = (a.rows + 2 * QROWS - 1) / (2 * QROWS);
@@ -1471,24 +1591,26 @@ gptq_status many_launch(const LinearArgs& a, cudaStream_t s) {
   const size_t smem = 1024 + (size_t)PNS * QBOX + (size_t)2 * PXS * (tn / 2) * 128 + (size_t)QROWS * QTAB * 4 +
                       8 * 16 * 36 * 4;
   GQ_PROF(K_Q4_MANY, s);
-  k_q4_many<T, GATED, TO><<<2 * np, 896, smem, s>>>(wm, xm, a, tn, mt, (int)tiles, wait_cfg());
+  k_q4_many<T, GATED, TO, FINE><<<2 * np, 896, smem, s>>>(wm, xm, a, tn, mt, (int)tiles, wait_cfg());
   GQ_LAUNCHED();
   return GPTQ_OK;
 }
 
 // Above 8 tokens: which of the two kernels.
-template <class T, bool GATED, class TO>
+template <class T, bool GATED, class TO, bool FINE>
 gptq_status some_tokens(const LinearArgs& a, cudaStream_t s) {
   // Cycles of the two kernels as measured over 17 .. 4096 tokens (4096 x
   // 4096, 5120 x 17408, 14336 x 4096): mid_shape has the first's; a stage takes
   // 540 on a pair of SMs, which spends 13000 more on a tile.
   const int* active = nullptr;
-  GQ_TRY((mid_clusters<T, GATED, TO>(&active)));
+  GQ_TRY((mid_clusters<T, GATED, TO, FINE>(&active)));
   const MidShape ms = mid_shape(a, active);
   long long rounds;
   many_tile(a.tokens, (a.rows + 2 * QROWS - 1) / (2 * QROWS), num_sms() / 2, rounds);
-  const double many = (double)rounds * ((a.n / GROUP + 7) / 8 * 4 * 540.0 + 13000.0);
-  return ms.cycles <= many ? mid_launch<T, GATED, TO>(a, ms, s) : many_launch<T, GATED, TO>(a, s);
+  // FINE decodes and multiplies half of the stages twice: 45 tokens, 14336 outputs of
+  // 4096, 44.5 -> 55 us in the first, 4096 tokens 651 -> 1050 in the other.
+  const double many = (double)rounds * ((a.n / GROUP + 7) / 8 * 4 * (FINE ? 870.0 : 540.0) + 13000.0);
+  return ms.cycles * (FINE ? 1.25 : 1.0) <= many ? mid_launch<T, GATED, TO, FINE>(a, ms, s) : many_launch<T, GATED, TO, FINE>(a, s);
 }
 
 // Up to 8 tokens the few-token kernel is the faster (5120 x 17408: 18 / 27
@@ -1498,7 +1620,7 @@ constexpr int kFewTokens = 8;
 
 template <class T>
 gptq_status linear_t(const LinearArgs& a, cudaStream_t s) {
-  return a.tokens <= kFewTokens ? few_tokens<T, false>(a, s) : some_tokens<T, false, T>(a, s);
+  return a.tokens <= kFewTokens ? few_tokens<T, false>(a, s) : some_tokens<T, false, T, false>(a, s);
 }
 
 // x [tokens][n] of bf16 as f16 numbers times a power of two a token, which brings
@@ -1559,7 +1681,7 @@ size_t q4tp_gated_ws_bytes(int dtype, int tokens, int n) {
 gptq_status q4tp_gated_run(int dtype, const LinearArgs& a, void* ws, cudaStream_t s) {
   if (a.tokens == 0) return GPTQ_OK;
   if (a.tokens <= kFewTokens) return dtype == GPTQ_BF16 ? few_tokens<__nv_bfloat16, true>(a, s) : few_tokens<__half, true>(a, s);
-  if (dtype == GPTQ_F16) return some_tokens<__half, true, __half>(a, s);
+  if (dtype == GPTQ_F16) return some_tokens<__half, true, __half, true>(a, s);
   LinearArgs p = a;
   float* scale = static_cast<float*>(ws);
   __half* x = reinterpret_cast<__half*>(static_cast<char*>(ws) + scale_bytes(a.tokens));
@@ -1569,7 +1691,7 @@ gptq_status q4tp_gated_run(int dtype, const LinearArgs& a, void* ws, cudaStream_
     GQ_LAUNCHED();
   }
   p.x = x, p.ldx = a.n, p.x_scale = scale;
-  return some_tokens<__half, true, __nv_bfloat16>(p, s);
+  return some_tokens<__half, true, __nv_bfloat16, false>(p, s);
 }
 
 }  // namespace gq

@@ -216,14 +216,24 @@ def test_tokens_of_any_size(lib, tokens):
     assert torch.isinf(y[7]).any() and torch.isfinite(y[8]).all()
 
 
-def test_infinite_and_nan_rows_above_eight_tokens(lib):
-    p = problem(20, 40, 128, "bf16", 18)
-    p["x"][4, 5], p["x"][7, 9] = -np.inf, np.nan
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens,inner,n", [(20, 40, 128), (20, 41, 608), (1500, 2051, 1056)])
+def test_infinite_and_nan_rows_above_eight_tokens(lib, tokens, inner, n, dtype):
+    # Columns of both halves of a box; scales that are powers of two, so that the
+    # weights' rounding leaves nothing, among others.
+    p = problem(tokens, inner, n, dtype, 18)
+    p["tab"][::2] = np.exp2(np.round(np.log2(p["tab"][::2])))
+    p["x"][4, 5], p["x"][7, 9], p["x"][11, 100] = -np.inf, np.nan, np.inf
+    if n > 300:
+        p["x"][13, 200] = np.inf
     p["nib"][:] |= 0x11  # no code is 8: no weight 0
-    y = run(p, "bf16", "none").float().cpu().numpy()
-    want = serve.gated(p["x"], p["nib"], p["rungs"], p["tab"], None, "none")
-    np.testing.assert_array_equal(y[4], want[4].astype(np.float32))
-    assert np.isnan(y[7]).all() and np.isfinite(np.delete(y, [4, 7], 0)).all()
+    y = run(p, dtype, "none").float().cpu().numpy()
+    some = slice(0, 20)
+    want = serve.gated(p["x"][some], p["nib"], p["rungs"], p["tab"], None, "none")
+    rows = [4, 11] + ([13] if n > 300 else [])
+    assert np.isinf(want[rows]).all()
+    np.testing.assert_array_equal(y[rows], want[rows].astype(np.float32))
+    assert np.isnan(y[7]).all() and np.isfinite(np.delete(y, rows + [7], 0)).all()
 
 
 def test_given_workspace(lib):
