@@ -115,7 +115,7 @@ def test_prompt_chunks(lib, q_lens, lens, dim, dtype):
     ([20001, 3, 4096], 1, 8, 128, 64, "bf16", None), ([9001], 2, 4, 128, 16, "f16", [5]),
     ([9001, 700], 1, 2, 64, 16, "bf16", None), ([5000, 130], 1, 3, 256, 16, "f16", [4, 1]),
     ([3000, 2000], 1, 4, 128, 16, "bf16", [7, 8]), ([12000], 1, 4, 64, 16, "bf16", [20]),
-    ([5000], 1, 4, 128, 16, "f16", [40])])
+    ([5000], 1, 4, 128, 16, "f16", [40]), ([150001], 1, 2, 64, 64, "f16", None), ([70000], 1, 16, 64, 64, "bf16", [9])])
 def test_long_contexts(lib, lens, heads, group, dim, page, dtype, q_lens):
     one(lens, heads, group, dim, page, dtype, q_lens, seed=6)
 
@@ -364,7 +364,8 @@ def test_evict(lib, keep, recent, dim, page, other):
 @pytest.mark.parametrize("other", [False, True])
 @pytest.mark.parametrize("lens,heads,dim,keep,recent", [
     ([5000], 3, 128, 1000, 64), ([3001, 2500], 1, 64, 2400, 0), ([1030, 1024, 1023], 2, 256, 1023, 31),
-    ([20000], 1, 64, 700, 1), ([4100], 1, 128, 4099, 10), ([2500], 9, 64, 2000, 1999)])
+    ([20000], 1, 64, 700, 1), ([4100], 1, 128, 4099, 10), ([2500], 9, 64, 2000, 1999),
+    ([45000, 100], 1, 64, 3000, 16)])  # (the last: more places than the selection keeps in shared memory)
 def test_evict_long(lib, lens, heads, dim, keep, recent, other):
     evict(lens, heads, dim, 16, keep, recent, other, seed=keep)
 

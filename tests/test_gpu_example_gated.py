@@ -108,3 +108,54 @@ def test_example_runs(lib, monkeypatch, capsys):
                                      "--budget", "96"])
     m.main()
     assert "prompt: 450 tokens in 3 chunks" in capsys.readouterr().out
+
+
+def test_two_streams_at_once(lib):
+    # Every call twice side by side, on two streams and other data, against one
+    # after the other: nothing is shared but the status word.
+    from gptq_post_weight_gb300 import _lib
+
+    heads, group, dim, page, inner, n = 2, 4, 128, 16, 700, 512
+    turns = _lib.rotary_turns(_lib.rotary_frequencies(dim))
+    sides = []
+    for seed in (1, 2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        tokens, length = 300 + 40 * seed, 1500
+        rand = lambda *shape: torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+        sides.append(dict(
+            qkv=rand(length, heads * (group + 2), dim), x=rand(tokens, n), tokens=tokens, length=length,
+            nib=torch.randint(0, 256, (inner * n,), generator=g, device="cuda", dtype=torch.uint8),
+            rungs=torch.randint(0, 32, (2 * inner * n // 32,), generator=g, device="cuda", dtype=torch.uint8),
+            tab=torch.rand(2 * inner, 32, generator=g, device="cuda") * 0.01,
+            table=torch.randperm(100, generator=g, device="cuda").int()[None]))
+
+    def run(s):
+        hq, at = heads * group, torch.arange(s["length"], device="cuda")
+        cache = _lib.kv4_cache(100, heads, dim, page)
+        slots = s["table"][0].long()[at // page] * page + at % page
+        q = _lib.kv4_write_rotary(cache, s["qkv"][:, :hq], s["qkv"][:, hq:hq + heads], s["qkv"][:, hq + heads:], slots, page,
+                                  at, turns)
+        lens = torch.tensor([s["length"]], device="cuda", dtype=torch.int32)
+        starts = torch.tensor([0, s["tokens"]], device="cuda", dtype=torch.int32)
+        last = q[s["length"] - s["tokens"]:].contiguous()
+        lse = torch.empty(s["tokens"], hq, device="cuda")
+        o = _lib.kv4_attention(last, cache, s["table"], lens, page, starts, s["tokens"], lse=lse)
+        w = _lib.kv4_weights(s["table"], page, heads)
+        _lib.kv4_attention_weights(w, last, lse, cache, s["table"], lens, page, starts, s["tokens"])
+        y = _lib.q4tp_gated(s["x"], s["nib"], s["rungs"], s["tab"])
+        kept, new, left = _lib.kv4_evict(cache, s["table"], lens, w, 400, page, recent=30)
+        return [q, o, lse, w, y, kept, new, left, cache, _lib.rotary(last, at[:s["tokens"]], turns, layout="interleaved")]
+
+    alone = [run(s) for s in sides]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sides]
+    together = [[], []]
+    for _ in range(5):
+        for k, s in enumerate(sides):
+            with torch.cuda.stream(streams[k]):
+                together[k].append(run(s))
+    torch.cuda.synchronize()
+    _lib.serve_check()
+    for want, runs in zip(alone, together):
+        for got in runs:
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
