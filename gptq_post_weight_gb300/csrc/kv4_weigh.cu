@@ -371,71 +371,69 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
         const int r0 = MANY ? rt * nt + c0 : 0, have = min(MANY ? nt / 2 : nt, it.s.rows - r0);
         const bool masked = r0 < open;
         if (!(ok = wait_long(&dfull[d], dph, abort, wc.ns))) break;
-        {
-          tc_fence_after();
-          const uint32_t ts = (uint32_t)((2 * d + team) * nt + c0) + lanes;
-          const float* nl = nlse[qn % WROWS] + c0;
-          const int* lk = lastkey[qn % WROWS] + c0;
-          if (!masked) {
-            auto some = [&](auto& v, int c) {
-              constexpr int N = sizeof(v) / 16;
+        tc_fence_after();
+        const uint32_t ts = (uint32_t)((2 * d + team) * nt + c0) + lanes;
+        const float* nl = nlse[qn % WROWS] + c0;
+        const int* lk = lastkey[qn % WROWS] + c0;
+        if (!masked) {
+          auto some = [&](auto& v, int c) {
+            constexpr int N = sizeof(v) / 16;
 #pragma unroll
-              for (int k = 0; k < N; ++k) {
-                const float4 l = *reinterpret_cast<const float4*>(nl + c + 4 * k);  // (the same for every lane)
-                const float2 e = both(mul2(fma2(pair2(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1])), scale2,
-                                                pair2(l.x, l.y)), log2e2));
-                const float2 f = both(mul2(fma2(pair2(__uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3])), scale2,
-                                                pair2(l.z, l.w)), log2e2));
-                sum2[0] = add2(sum2[0], pair2(ex2(e.x), ex2(e.y)));
-                sum2[1] = add2(sum2[1], pair2(ex2(f.x), ex2(f.y)));
-              }
-            };
-            int c = 0;
-            if (MANY) {
-              // Sixteen columns on their way while sixteen are summed.
-              uint32_t v[16], u[16];
-              tmem_ld16(ts, v);
-              tmem_ld_wait();
-#pragma unroll 1
-              for (; c + 32 <= have; c += 32) {
-                tmem_ld16(ts + (uint32_t)c + 16u, u);
-                some(v, c);
-                tmem_ld_wait();
-                if (c + 32 < have) tmem_ld16(ts + (uint32_t)c + 32u, v);
-                some(u, c + 16);
-                tmem_ld_wait();
-              }
+            for (int k = 0; k < N; ++k) {
+              const float4 l = *reinterpret_cast<const float4*>(nl + c + 4 * k);  // (the same for every lane)
+              const float2 e = both(mul2(fma2(pair2(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1])), scale2,
+                                              pair2(l.x, l.y)), log2e2));
+              const float2 f = both(mul2(fma2(pair2(__uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3])), scale2,
+                                              pair2(l.z, l.w)), log2e2));
+              sum2[0] = add2(sum2[0], pair2(ex2(e.x), ex2(e.y)));
+              sum2[1] = add2(sum2[1], pair2(ex2(f.x), ex2(f.y)));
             }
+          };
+          int c = 0;
+          if (MANY) {
+            // Sixteen columns on their way while sixteen are summed.
+            uint32_t v[16], u[16];
+            tmem_ld16(ts, v);
+            tmem_ld_wait();
 #pragma unroll 1
-            for (; c + 8 < have; c += 16) {
-              uint32_t v[16];
-              tmem_ld16(ts + (uint32_t)c, v);
-              tmem_ld_wait();
+            for (; c + 32 <= have; c += 32) {
+              tmem_ld16(ts + (uint32_t)c + 16u, u);
               some(v, c);
-            }
-            if (c < have) {
-              uint32_t v[8];
-              tmem_ld8(ts + (uint32_t)c, v);
               tmem_ld_wait();
-              some(v, c);
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < have; c += 16) {
-              uint32_t v[16];
-              tmem_ld16(ts + (uint32_t)c, v);
+              if (c + 32 < have) tmem_ld16(ts + (uint32_t)c + 32u, v);
+              some(u, c + 16);
               tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float e = fmaf(__uint_as_float(v[k]), scale, nl[c + k]) * 1.4426950408889634f;
-                if (t <= lk[c + k]) masked_sum += ex2(e);
-              }
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_relaxed(&dempty[d]);
+#pragma unroll 1
+          for (; c + 8 < have; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(ts + (uint32_t)c, v);
+            tmem_ld_wait();
+            some(v, c);
+          }
+          if (c < have) {
+            uint32_t v[8];
+            tmem_ld8(ts + (uint32_t)c, v);
+            tmem_ld_wait();
+            some(v, c);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < have; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(ts + (uint32_t)c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float e = fmaf(__uint_as_float(v[k]), scale, nl[c + k]) * 1.4426950408889634f;
+              if (t <= lk[c + k]) masked_sum += ex2(e);
+            }
+          }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(&dempty[d]);
         if (++d == w.nd) d = 0, dph ^= 1u;
       }
       if (!MANY && !ok) break;
