@@ -23,7 +23,6 @@
 namespace gq {
 namespace {
 
-constexpr int SEL = 1024;          // threads that select
 constexpr int SBINS = 2048, SCAN = SBINS / 4;  // bins, and threads that look through them
 constexpr int kStaged = 40 << 10;  // places of a head that are kept in shared memory at most
 
@@ -40,7 +39,8 @@ __device__ __forceinline__ int length_of(const EvictArgs& a, int b) {
 }
 
 // STAGED: the keys of a head fit shared memory (else they are read again for each digit).
-template <bool STAGED>
+// SEL: threads.
+template <bool STAGED, int SEL>
 __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) int hist[SBINS];
@@ -59,7 +59,9 @@ __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
   for (int i = n + tid; i < a.keep; i += SEL) kept[i] = -1;
   if (len <= a.keep)
     for (int i = tid; i < n; i += SEL) kept[i] = i, out_w[i] = w[i];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_kv4_move may set itself up
+  // k_kv4_move may set itself up.  (Not beside many heads: its CTAs would fill the SMs
+  // whose heads are short, and start there, not where memory is idle: 113 us, not 92.)
+  if (SEL == 1024) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (long long i = n + tid; i < out_cap; i += SEL) out_w[i] = 0.f;
   if (len <= a.keep) return;
   int need = n - (len - old);
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
   auto key = [&](int i) { return STAGED ? keys[i] : weight_key(w[i]); };
   if (STAGED && any) {
 #pragma unroll 8
-    for (int i = tid; i < old; i += SEL) keys[i] = weight_key(w[i]);
+    for (int i = tid; i < len; i += SEL) keys[i] = weight_key(w[i]);
   }
   // The key of the last one kept, and how many of those equal to it stay.
   uint32_t prefix = 0;
@@ -138,7 +140,9 @@ __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
     if (stays) {
       const int at = place + __popc(all & before);
       kept[at] = i;
-      out_w[at] = w[i];
+      // The weight from its key, without a load's latency, if it has one of its own.
+      const uint32_t own = STAGED && any ? keys[i] : 0u;
+      out_w[at] = own == 0u || own == 0x80000000u ? w[i] : __uint_as_float(own >> 31 ? own & ~(1u << 31) : ~own);
     }
     place += __popc(all);
     tied += __popc(equal);
@@ -271,17 +275,23 @@ gptq_status move_launch(const EvictArgs& a, cudaStream_t s) {
 gptq_status kv4_evict_run(int dim, bool in_place, const EvictArgs& a, cudaStream_t s) {
   static DeviceOnce attr;
   GQ_TRY(attr.run([](int) -> gptq_status {
-    GQ_CUDA(cudaFuncSetAttribute(k_kv4_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStaged * 4));
+    GQ_CUDA(cudaFuncSetAttribute(k_kv4_select<true, 1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStaged * 4));
+    GQ_CUDA(cudaFuncSetAttribute(k_kv4_select<true, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStaged * 4));
     return GPTQ_OK;
   }));
   const long long cap = (long long)a.table_stride * a.page_size;
   {
     GQ_PROF(K_KV4_SELECT, s);
-    const unsigned grid = (unsigned)(a.seqs * a.heads);
-    if (cap <= kStaged)
-      k_kv4_select<true><<<grid, SEL, (size_t)cap * 4, s>>>(a);
+    // Two CTAs of 1024 threads fit an SM; more heads start together where three of 512 and
+    // their keys do (one sequence to 16384: 19.4 us with 1024 threads, 23 with 512; 48 of
+    // them 95 and 92, 48 to 4096 45 and 42).
+    const unsigned grid = (unsigned)(a.seqs * a.heads), bytes = cap <= kStaged ? (unsigned)cap * 4 : 0;
+    if (bytes == 0)
+      k_kv4_select<false, 1024><<<grid, 1024, 0, s>>>(a);
+    else if (grid <= 2u * (unsigned)num_sms() || bytes > 65 << 10)
+      k_kv4_select<true, 1024><<<grid, 1024, bytes, s>>>(a);
     else
-      k_kv4_select<false><<<grid, SEL, 0, s>>>(a);
+      k_kv4_select<true, 512><<<grid, 512, bytes, s>>>(a);
     GQ_LAUNCHED();
   }
   if (dim == 64) return in_place ? move_launch<64, true>(a, s) : move_launch<64, false>(a, s);

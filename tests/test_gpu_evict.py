@@ -370,6 +370,17 @@ def test_evict_long(lib, lens, heads, dim, keep, recent, other):
     evict(lens, heads, dim, 16, keep, recent, other, seed=keep)
 
 
+@pytest.mark.parametrize("other", [False, True])
+def test_many_heads(lib, other):
+    """More heads than start at once, of unequal lengths; weights of either sign, zeros of either, NaN."""
+    def weights(r, shape):
+        w = heavy(r, shape) * np.where(r.uniform(size=shape) < 0.3, -1, 1).astype(np.float32)
+        return np.where(r.uniform(size=shape) < 0.02, np.float32(np.nan), w)
+
+    lens = [0, 1, 99, 100, 101, 513, 1500, 1040] + [int(n) for n in np.random.default_rng(4).integers(0, 700, 70)]
+    evict(lens, 8, 64, 16, 100, 7, other, seed=3, weights=weights)
+
+
 def test_ties_nan_and_signs(lib):
     evict([700], 2, 64, 16, 100, 10, False, weights=lambda r, s: np.zeros(s, np.float32))
     evict([700], 2, 64, 16, 100, 10, True, weights=lambda r, s: np.full(s, 3.5, np.float32))
