@@ -113,29 +113,37 @@ __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
   }
   // A warp lists a stretch of the places: first how many stay before it.
   const int each = (len + W * 32 - 1) / (W * 32) * 32, i0 = min(warp * each, len), i1 = min(i0 + each, len);
+  const int i2 = any ? min(i1, old) : i0;  // up to here the keys decide, from `old` on all stay
   int above = 0, ties = 0;
-#pragma unroll 4
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const uint32_t k = any && i < min(i1, old) ? key(i) : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, i < i1 && (i >= old || (any && k > prefix))));
-    ties += __popc(__ballot_sync(0xffffffffu, any && i < min(i1, old) && k == prefix));
+#pragma unroll 8
+  for (int i = i0 + lane; i < i2; i += 32) {
+    const uint32_t k = key(i);
+    above += k > prefix;
+    ties += k == prefix;
   }
+  above = __reduce_add_sync(0xffffffffu, above) + max(i1 - max(i0, old), 0);
+  ties = __reduce_add_sync(0xffffffffu, ties);
   __syncthreads();  // (part is read above)
   if (lane == 0) part[warp] = int2{above, ties};
   __syncthreads();
-  int place = 0, tied = 0;
-  for (int x = 0; x < warp; ++x) {
-    place += part[x].x;
-    tied += part[x].y;
+  int place = 0, tied = 0, all_ties = 0;
+  for (int x = 0; x < W; ++x) {
+    if (x < warp) place += part[x].x, tied += part[x].y;
+    all_ties += part[x].y;
   }
   place += min(tied, need);
   const unsigned before = (1u << lane) - 1u;
-#pragma unroll 2
+  const bool some = all_ties > need;  // (else all of them stay: the same for every thread)
+#pragma unroll 4
   for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const uint32_t k = any && i < min(i1, old) ? key(i) : 0u;
-    const bool tie = any && i < min(i1, old) && k == prefix;
-    const unsigned equal = __ballot_sync(0xffffffffu, tie);
-    const bool stays = i < i1 && (i >= old || (any && k > prefix) || (tie && tied + __popc(equal & before) < need));
+    const uint32_t k = i < i2 ? key(i) : 0u;
+    bool stays = i < i1 && (i >= old || (i < i2 && k >= prefix));
+    if (some) {
+      const bool tie = i < i2 && k == prefix;
+      const unsigned equal = __ballot_sync(0xffffffffu, tie);
+      if (tie && tied + __popc(equal & before) >= need) stays = false;
+      tied += __popc(equal);
+    }
     const unsigned all = __ballot_sync(0xffffffffu, stays);
     if (stays) {
       const int at = place + __popc(all & before);
@@ -145,7 +153,6 @@ __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
       out_w[at] = own == 0u || own == 0x80000000u ? w[i] : __uint_as_float(own >> 31 ? own & ~(1u << 31) : ~own);
     }
     place += __popc(all);
-    tied += __popc(equal);
   }
 }
 
