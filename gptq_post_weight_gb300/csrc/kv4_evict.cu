@@ -13,10 +13,10 @@
 // behind what an earlier one wrote (a token comes from its own place or a
 // later one), so that the barrier is all the order it takes.
 //
-// Measured: 8 heads of 128, one sequence of 4096 tokens to 1024, in place: 11.7 us,
+// Measured: 8 heads of 128, one sequence of 4096 tokens to 1024, in place: 12 us,
 // two launches' latencies.  48 sequences of up to 16384 tokens to 2000, into other
-// pages: 99 us; the selection is some 40 of them (one CTA a head: 384 of unequal
-// length on 152 SMs, 54 % of the issue slots), the moves 57 (72 % of the memory's
+// pages: 88 us; the selection is some 32 of them (one CTA a head: 384 of unequal
+// length on 152 SMs, 60 % of the issue slots), the moves 57 (72 % of the memory's
 // cycles: a kept token is four pieces, of which the two of parameters are 16 bytes).
 #include "serve.cuh"
 
@@ -290,8 +290,8 @@ gptq_status kv4_evict_run(int dim, bool in_place, const EvictArgs& a, cudaStream
   {
     GQ_PROF(K_KV4_SELECT, s);
     // Two CTAs of 1024 threads fit an SM; more heads start together where three of 512 and
-    // their keys do (one sequence to 16384: 19.4 us with 1024 threads, 23 with 512; 48 of
-    // them 95 and 92, 48 to 4096 45 and 42).
+    // their keys do (measured before the listing's last form: one sequence to 16384 19.4 us with
+    // 1024 threads, 23 with 512; 48 of them 95 and 92, 48 to 4096 45 and 42).
     const unsigned grid = (unsigned)(a.seqs * a.heads), bytes = cap <= kStaged ? (unsigned)cap * 4 : 0;
     if (bytes == 0)
       k_kv4_select<false, 1024><<<grid, 1024, 0, s>>>(a);
