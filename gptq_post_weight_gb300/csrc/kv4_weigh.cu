@@ -198,9 +198,14 @@ __device__ __forceinline__ long long quotient(long long x, int y) {
   return x >> 31 ? x / y : (long long)((unsigned)x / (unsigned)y);
 }
 
+// Query rows before the first one that sees key k.  (Cut off at 0 before the
+// product: nq * group is at most 2^30, len * group is not.)
+__device__ __forceinline__ int rows_before(const AttnArgs& a, const WSeq& s, int k) {
+  return max(k - s.len + s.nq, 0) * a.group;
+}
 // The first tile of query rows that sees a key of a step.
 __device__ __forceinline__ int first_rows(const AttnArgs& a, const WSeq& s, int step, int nt) {
-  return max((step * 2 * WKEYS - s.len + s.nq) * a.group, 0) / nt;
+  return rows_before(a, s, step * 2 * WKEYS) / nt;
 }
 
 // A CTA's walk over the list of (sequence, key head, step).
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
       uint64_t sum2[2] = {0ull, 0ull};
       float masked_sum = 0.f;
       // Rows before this one do not see some key of the tile that is there.
-      const int open = max((min(k0 + WKEYS, it.s.len) - 1 - it.s.len + it.s.nq) * a.group, 0);
+      const int open = rows_before(a, it.s, min(k0 + WKEYS, it.s.len) - 1);
 #pragma unroll 1
       for (int rt = MANY ? it.lo : 0; rt < (MANY ? it.hi : 1); ++rt) {
         if (MANY) ++qn;
