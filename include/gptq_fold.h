@@ -487,8 +487,10 @@ gptq_status gptq_kv4_write(int dtype, uint8_t* cache, long long pages, int heads
  * in f32, rounded once to T.  The first `rot` channels of a head turn (rot a
  * multiple of 16), the others stay; pair i is channels (i, i + rot/2) or
  * (2i, 2i + 1).  turns (device i64 [rot/2]) holds f as 2^64ths of a turn a
- * position, round(f / (2 pi) 2^64) modulo 2^64: the angle is exact to 2^-32 of
- * a turn for every position.  positions: device i64 [tokens], any sign.
+ * position, round(f / (2 pi) 2^64) modulo 2^64: position times turns modulo one
+ * turn is exact, and the angle taken from it is off by at most pi (2^-27 + 2^-32)
+ * at every position.  (f's own rounding to 2^-65 of a turn counts once a position:
+ * 2^-32 of a turn at position 2^33.)  positions: device i64 [tokens], any sign.
  *
  * gptq_rotary            Y = X turned, T [tokens][heads][dim] each with strides
  *                        (xt, yt between tokens, xh, yh between heads; multiples
