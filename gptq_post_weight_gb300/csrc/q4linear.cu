@@ -807,6 +807,9 @@ __device__ __forceinline__ bool wait_both(uint64_t* x, uint32_t xp, uint64_t* y,
 
 // The rows' ladders as (hi, lo) pairs, and the powers of two taken out.  The
 // dequantising threads: four a row, eight rungs each; barrier 2 is theirs.
+// A row's largest rung comes to 1 to 2; of a gated product's, whose weights are f16
+// numbers in either type, to 2^11 to 2^12: times 8 it still fits f16, and weights keep
+// their eleven bits down to 2^-22 of it (with 1 to 2 they lost them from 2^-11 on).
 template <class T, bool GATED>
 __device__ __forceinline__ void load_ladders(const LinearArgs& a, int row0, uint32_t* tab, float* rowscale,
                                              float* rowmax) {
@@ -823,7 +826,8 @@ __device__ __forceinline__ void load_ladders(const LinearArgs& a, int row0, uint
   rowmax[part * QROWS + r] = m;
   asm volatile("bar.sync 2, 512;" ::: "memory");  // also: nobody reads the last tile's ladders any more
   m = fmaxf(fmaxf(rowmax[r], rowmax[QROWS + r]), fmaxf(rowmax[2 * QROWS + r], rowmax[3 * QROWS + r]));
-  const int e = (m > 0.f && isfinite(m)) ? ilogbf(m) : 0;
+  // (2^-149 is the smallest power of two there is.)
+  const int e = (m > 0.f && isfinite(m)) ? max(ilogbf(m) - (GATED ? 11 : 0), -149) : 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const float v = scalbnf(s[k], -e);

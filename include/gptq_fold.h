@@ -433,9 +433,10 @@ gptq_status gptq_q4tp_linear(int dtype, const void* X, long long ldx, int tokens
  * the gate's `inner` rows and then the up projection's in one q4tp matrix W of
  * 2 * inner rows (one Hessian group: both read X).  Sums, activation and the
  * product in f32, one rounding to T.  Up to 8 tokens no weight is rounded; above
- * that to 11 bits, in either type (bf16: X is taken as f16 times a power of two
- * a token, exact down to 2^-32 of its largest element; f16: half of the columns'
- * weights to some 21).
+ * that to 11 bits, in either type, those of rungs below 2^-22 of their row's largest to
+ * 2^-33 of that one (bf16: X is taken as f16 times a power of two a token, exact down
+ * to 2^-32 of its largest element; f16: columns 0 to 127 of every 256 to some 21
+ * bits).
  *
  *   nibbles  in  u8 inner*n;  rungs in u8 2*inner*n/32;  tab in f32 2*inner*32.
  *   bias     in  T 2*inner (may be NULL).
