@@ -308,7 +308,7 @@ constexpr size_t piece_floats(int dim) { return (size_t)rows_of(dim) * (dim + 2)
 // and take turns at the steps, so that two chains run for them too, and join
 // at the end of a piece (112 rows of 128, 8 sequences to 32000: 168 -> 144 us;
 // of 64, 48 sequences: 674 -> 523; decoding is then the longer part).
-template <class T, int D, bool TURNS>
+template <class T, int D, bool TURNS, bool LSE>
 __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk, WaitCfg wc) {
   using T2 = typename Elem<T>::T2;
   using S = ChunkSmem<D>;
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
           }
         }
       }
-      if (a.lse != nullptr && pc.whole && mine && half == 0)
+      if (LSE && pc.whole && mine && half == 0)
         a.lse[(long long)(pc.t.q0 + qi) * a.heads * a.group + hq] = log_sum(sl, m, l);
       if (!pc.whole && mine && half == 0)
         *reinterpret_cast<float2*>(part + (size_t)kRows<D> * D + 2 * (128 * x + rt)) = float2{m, l};
@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(CTHREADS, 1) k_kv4_chunk(AttnArgs a, int nblk,
 // those of the tile whose first piece share c ends with, sixteen rows of it
 // (heads of 256: eight), a warp RW, whose pieces come through shared memory
 // four at a time.
-template <class T, int D>
+template <class T, int D, bool LSE>
 __global__ void __launch_bounds__(128) k_kv4_chunk_join(AttnArgs a) {
   constexpr int RW = D == 256 ? 2 : 4;
   __shared__ __align__(16) float batch[4][4 * RW][D];  // [warp][piece, row]
@@ -895,19 +895,21 @@ __global__ void __launch_bounds__(128) k_kv4_chunk_join(AttnArgs a) {
     const float inv = dk != 0.f ? 1.f / dk : 0.f;  // a row that sees nothing: zeros
     const int rr = cut.y + r0 + k;
     const long long at = (long long)(cut.x + rr / a.group) * a.heads * a.group + head * a.group + rr % a.group;
-    const float tk = __shfl_sync(0xffffffffu, top, k);
-    if (lane == 0 && a.lse != nullptr) a.lse[at] = log_sum(sl, tk, dk);
+    if (LSE) {
+      const float tk = __shfl_sync(0xffffffffu, top, k);
+      if (lane == 0) a.lse[at] = log_sum(sl, tk, dk);
+    }
     T* dst = static_cast<T*>(a.out) + at * D;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = Elem<T>::from(acc[k][i] * inv);
   }
 }
 
-template <class T, int D, bool TURNS>
+template <class T, int D, bool TURNS, bool LSE>
 gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
   static DeviceOnce attr;
   GQ_TRY(attr.run([](int) -> gptq_status {
-    GQ_CUDA(cudaFuncSetAttribute(k_kv4_chunk<T, D, TURNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<D>::bytes));
+    GQ_CUDA(cudaFuncSetAttribute(k_kv4_chunk<T, D, TURNS, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<D>::bytes));
     return GPTQ_OK;
   }));
   const int nblk = (int)(((long long)a.max_q * a.group + kRows<D> - 1) / kRows<D>);
@@ -922,7 +924,7 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
     const int grid = num_sms();
     {
       GQ_PROF(K_KV4_CHUNK, s);
-      k_kv4_chunk<T, D, TURNS><<<grid, CTHREADS, ChunkSmem<D>::bytes, s>>>(p, nblk, wait_cfg());
+      k_kv4_chunk<T, D, TURNS, LSE><<<grid, CTHREADS, ChunkSmem<D>::bytes, s>>>(p, nblk, wait_cfg());
       GQ_LAUNCHED();
     }
     cudaLaunchConfig_t cfg{};
@@ -935,7 +937,7 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     GQ_PROF(K_KV4_JOIN, s);
-    GQ_CUDA(cudaLaunchKernelEx(&cfg, k_kv4_chunk_join<T, D>, p));
+    GQ_CUDA(cudaLaunchKernelEx(&cfg, k_kv4_chunk_join<T, D, LSE>, p));
   }
   return GPTQ_OK;
 }
@@ -944,16 +946,20 @@ gptq_status chunk_launch(const AttnArgs& a, cudaStream_t s) {
 
 size_t kv4_chunk_ws_bytes(int dim) { return kCutBytes + (size_t)num_sms() * 2 * piece_floats(dim) * 4; }
 
-template <class T>
+template <class T, bool LSE>
 static gptq_status chunk_dim(int dim, const AttnArgs& a, cudaStream_t s) {
   const bool turns = (long long)a.max_q * a.group <= 128;
-  if (dim == 64) return turns ? chunk_launch<T, 64, true>(a, s) : chunk_launch<T, 64, false>(a, s);
-  if (dim == 128) return turns ? chunk_launch<T, 128, true>(a, s) : chunk_launch<T, 128, false>(a, s);
-  return chunk_launch<T, 256, false>(a, s);
+  if (dim == 64) return turns ? chunk_launch<T, 64, true, LSE>(a, s) : chunk_launch<T, 64, false, LSE>(a, s);
+  if (dim == 128) return turns ? chunk_launch<T, 128, true, LSE>(a, s) : chunk_launch<T, 128, false, LSE>(a, s);
+  return chunk_launch<T, 256, false, LSE>(a, s);
+}
+template <class T>
+static gptq_status chunk_sums(int dim, const AttnArgs& a, cudaStream_t s) {
+  return a.lse != nullptr ? chunk_dim<T, true>(dim, a, s) : chunk_dim<T, false>(dim, a, s);
 }
 
 gptq_status kv4_chunk_run(int dtype, int dim, const AttnArgs& a, cudaStream_t s) {
-  return dtype == GPTQ_BF16 ? chunk_dim<__nv_bfloat16>(dim, a, s) : chunk_dim<__half>(dim, a, s);
+  return dtype == GPTQ_BF16 ? chunk_sums<__nv_bfloat16>(dim, a, s) : chunk_sums<__half>(dim, a, s);
 }
 
 }  // namespace gq
