@@ -41,7 +41,7 @@ __device__ __forceinline__ int length_of(const EvictArgs& a, int b) {
 // STAGED: the keys of a head fit shared memory (else they are read again for each digit).
 // SEL: threads.
 template <bool STAGED, int SEL>
-__global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
+__global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a, bool few) {
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) int hist[SBINS];
   __shared__ int2 part[SEL / 32];
@@ -60,8 +60,9 @@ __global__ void __launch_bounds__(SEL) k_kv4_select(EvictArgs a) {
   if (len <= a.keep)
     for (int i = tid; i < n; i += SEL) kept[i] = i, out_w[i] = w[i];
   // k_kv4_move may set itself up.  (Not beside many heads: its CTAs would fill the SMs
-  // whose heads are short, and start there, not where memory is idle: 113 us, not 92.)
-  if (SEL == 1024) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // whose heads are short, and start there, not where memory is idle: 113 us, not 92; beside
+  // 1024 threads a head, 48 sequences to 20032, 104.5, not 101.7.)
+  if (few) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (long long i = n + tid; i < out_cap; i += SEL) out_w[i] = 0.f;
   if (len <= a.keep) return;
   int need = n - (len - old);
@@ -293,12 +294,13 @@ gptq_status kv4_evict_run(int dim, bool in_place, const EvictArgs& a, cudaStream
     // their keys do (measured before the listing's last form: one sequence to 16384 19.4 us with
     // 1024 threads, 23 with 512; 48 of them 95 and 92, 48 to 4096 45 and 42).
     const unsigned grid = (unsigned)(a.seqs * a.heads), bytes = cap <= kStaged ? (unsigned)cap * 4 : 0;
+    const bool few = grid <= 2u * (unsigned)num_sms();
     if (bytes == 0)
-      k_kv4_select<false, 1024><<<grid, 1024, 0, s>>>(a);
-    else if (grid <= 2u * (unsigned)num_sms() || bytes > 65 << 10)
-      k_kv4_select<true, 1024><<<grid, 1024, bytes, s>>>(a);
+      k_kv4_select<false, 1024><<<grid, 1024, 0, s>>>(a, few);
+    else if (few || bytes > 65 << 10)
+      k_kv4_select<true, 1024><<<grid, 1024, bytes, s>>>(a, few);
     else
-      k_kv4_select<true, 512><<<grid, 512, bytes, s>>>(a);
+      k_kv4_select<true, 512><<<grid, 512, bytes, s>>>(a, false);
     GQ_LAUNCHED();
   }
   if (dim == 64) return in_place ? move_launch<64, true>(a, s) : move_launch<64, false>(a, s);
