@@ -588,8 +588,12 @@ gptq_status gptq_kv4_attention_lse(int dtype, const void* Q, long long q_ts, lon
  *   ws       >= gptq_kv4_attention_weights_workspace_bytes(...) of this call
  *            (max_len: table_stride * page_size), which is 0 for few query rows and
  *            for many tokens (ws may then be NULL).
- * f32 scores, exponentials and sums, each place's in one fixed order.  A key that
- * is NaN makes its own place NaN.
+ * f32 scores, exponentials and sums, each place's in one fixed order (a total that is
+ * subnormal may count as zero).  Where lse is NaN, so is all that its row sees.  The
+ * attention over a cache that has a key without numbers returns such an lse for every
+ * row that sees that key: the totals of that head of that sequence are then NaN,
+ * and stay so, and eviction, for which they are all alike, keeps its first tokens beside
+ * the `recent` ones.  With an lse that is finite such a key makes its own place NaN alone.
  */
 size_t gptq_kv4_attention_weights_workspace_bytes(int dim, int heads, int group, int max_q, int seqs,
                                                   long long max_len);
