@@ -53,57 +53,11 @@ constexpr int CLIST = 512;   // (sequence, row block) pairs of one launch at mos
 constexpr int CSTART = 3;    // what a tile's start and end cost, in steps
 constexpr float kNone = -1e30f;
 
-template <class T>
-struct MmaFormat;
-template <>
-struct MmaFormat<__nv_bfloat16> {
-  static constexpr uint32_t k = 1u;
-};
-template <>
-struct MmaFormat<__half> {
-  static constexpr uint32_t k = 0u;
-};
-
-// Two f32 numbers as one operand.
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-
 // Scores past column `lim` count nothing.
 __device__ __forceinline__ void hide(uint32_t (&v)[32], int lim) {
 #pragma unroll
   for (int i = 0; i < 32; ++i)
     if (i > lim) v[i] = 0xff800000u;  // -inf
-}
-
-// Barrier of tile x's 256 softmax threads, AND-reducing: they go on or leave
-// together.
-__device__ __forceinline__ bool tile_all(int x, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.and.pred po, %2, 256, pi;\n"
-      " selp.u32 %0, 1, 0, po;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)p), "r"(1 + x)
-      : "memory");
-  return r != 0u;
 }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {

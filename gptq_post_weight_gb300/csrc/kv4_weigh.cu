@@ -54,17 +54,6 @@ constexpr int kTurns = D == 256 ? 2 : 4;
 template <int D>
 constexpr int kMostRows = D == 256 ? 64 : 128;  // query rows of a tile (shared memory)
 
-template <class T>
-struct WFormat;
-template <>
-struct WFormat<__nv_bfloat16> {
-  static constexpr uint32_t k = 1u;
-};
-template <>
-struct WFormat<__half> {
-  static constexpr uint32_t k = 0u;
-};
-
 struct WeighArgs {
   const float* lse;
   float* weights;
@@ -74,32 +63,6 @@ struct WeighArgs {
   float* part;      // their sums, `apart` floats from part to part, laid out like the weights
   long long apart;
 };
-
-__device__ __forceinline__ uint64_t pair2(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 both(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
 
 // wait_bar_warp, suspended for up to a microsecond a try: 26 warps that look again
 // at once take the issue slots of the ones at work.
@@ -136,19 +99,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "r"(taddr));
 }
 
-// Barrier of the 256 threads that sum tile x of a step, AND-reducing.
-__device__ __forceinline__ bool tile_all(int x, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.and.pred po, %2, 256, pi;\n"
-      " selp.u32 %0, 1, 0, po;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)p), "r"(1 + x)
-      : "memory");
-  return r != 0u;
-}
-
-// Waits on three barriers at once.
 __device__ __forceinline__ bool look_at(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -158,6 +108,7 @@ __device__ __forceinline__ bool look_at(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0u;
 }
+// Waits on three barriers at once.
 __device__ __forceinline__ bool wait_three(uint64_t* x, uint32_t xp, uint64_t* y, uint32_t yp, uint64_t* z, uint32_t zp,
                                            volatile int* abort, uint64_t limit) {
   const bool ok = (look_at(x, xp) & look_at(y, yp) & look_at(z, zp)) ||
@@ -359,7 +310,7 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const long long cap = (long long)a.table_stride * a.page_size;
     const float scale = a.scale_log2;  // (here the plain scale: see the launch)
-    const uint64_t scale2 = pair2(scale, scale), log2e2 = pair2(1.4426950408889634f, 1.4426950408889634f);
+    const uint64_t scale2 = pack2(scale, scale), log2e2 = pack2(1.4426950408889634f, 1.4426950408889634f);
     int d = 0, qn = MANY ? -1 : 0, turn = 0;
     uint32_t dph = 0u;
     bool ok = true;
@@ -386,12 +337,12 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
 #pragma unroll
             for (int k = 0; k < N; ++k) {
               const float4 l = *reinterpret_cast<const float4*>(nl + c + 4 * k);  // (the same for every lane)
-              const float2 e = both(mul2(fma2(pair2(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1])), scale2,
-                                              pair2(l.x, l.y)), log2e2));
-              const float2 f = both(mul2(fma2(pair2(__uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3])), scale2,
-                                              pair2(l.z, l.w)), log2e2));
-              sum2[0] = add2(sum2[0], pair2(ex2(e.x), ex2(e.y)));
-              sum2[1] = add2(sum2[1], pair2(ex2(f.x), ex2(f.y)));
+              const float2 e = unpack2(mul2(fma2(pack2(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1])), scale2,
+                                                 pack2(l.x, l.y)), log2e2));
+              const float2 f = unpack2(mul2(fma2(pack2(__uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3])), scale2,
+                                                 pack2(l.z, l.w)), log2e2));
+              sum2[0] = add2(sum2[0], pack2(ex2(e.x), ex2(e.y)));
+              sum2[1] = add2(sum2[1], pack2(ex2(f.x), ex2(f.y)));
             }
           };
           int c = 0;
@@ -442,7 +393,7 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
         if (++d == w.nd) d = 0, dph ^= 1u;
       }
       if (!MANY && !ok) break;
-      const float2 x = both(sum2[0]), y = both(sum2[1]);
+      const float2 x = unpack2(sum2[0]), y = unpack2(sum2[1]);
       float sum = ((x.x + x.y) + (y.x + y.y)) + masked_sum;
       if (MANY) {
         // (A warp whose wait has run out comes here all the same: a tile's warps leave together.)
@@ -602,7 +553,7 @@ __global__ void __launch_bounds__(wthreads(MANY), 1) k_kv4_weigh(AttnArgs a, Wei
     }
   } else {
     const bool one = elect_one();
-    const uint32_t idesc = (1u << 4) | (WFormat<T>::k << 7) | (WFormat<T>::k << 10) | ((uint32_t)(nt >> 3) << 17) | (8u << 24);
+    const uint32_t idesc = (1u << 4) | (MmaFormat<T>::k << 7) | (MmaFormat<T>::k << 10) | ((uint32_t)(nt >> 3) << 17) | (8u << 24);
     const uint64_t ad = sdesc(smem_u32(asm_)), qd = sdesc(smem_u32(qsm));
     // Every step goes through this warp's loop, and beside 25 others an instruction
     // of it takes some ten cycles and a look at a barrier 200: three barriers are
