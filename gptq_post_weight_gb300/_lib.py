@@ -842,7 +842,8 @@ def _refuse_gated(x, nibbles, rungs, tab, bias, act, out, ws):
 
 def q4tp_gated(x, nibbles, rungs, tab, bias=None, act="silu", out=None, ws=None, stream=None):
     """act(x Wg^T + bg) * (x Wu^T + bu), the first half of a gated feed-forward
-    block, in one launch.  W [2 * inner, n] in q4tp form holds the gate's rows and
+    block, in one launch (bf16 above 8 tokens: two, of which the first brings x to
+    f16).  W [2 * inner, n] in q4tp form holds the gate's rows and
     then the up projection's, as quantize_group returns them for the two matrices
     one above the other; bias [2 * inner].  x [tokens, n] and the result [tokens,
     inner] as in q4tp_linear.  `out` overlaps no input."""

@@ -221,9 +221,9 @@ __global__ void __launch_bounds__(256)
 // cosines serve them all; in the half layout the other channels of its pairs
 // are another lane's, which hands them over (dim / 8 lanes of a warp are a
 // head's).  A lane reads and writes its own octets only: y may be q itself.
-// Measured: 8001 tokens of 32 query and 8 key heads of 128 in 41.2 us, 4.2 TB/s
-// (instructions: 56 % of the issue slots, memory 41 % busy); 64 tokens 3.6 us, one
-// 3.5.
+// Measured: 8001 tokens of 32 query and 8 key heads of 128 in 41.1 us, 4.2 TB/s
+// (55 % of the issue slots, memory 41 % busy, neither of them its limit: a warp waits for
+// its loads); 64 tokens 3.5 us, one 3.5.
 struct TurnedHeads {
   const void* q;
   long long qt, qh;

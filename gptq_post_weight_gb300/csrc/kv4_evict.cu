@@ -13,11 +13,15 @@
 // behind what an earlier one wrote (a token comes from its own place or a
 // later one), so that the barrier is all the order it takes.
 //
-// Measured: 8 heads of 128, one sequence of 4096 tokens to 1024, in place: 12 us,
-// two launches' latencies.  48 sequences of up to 16384 tokens to 2000, into other
+// Measured: 8 heads of 128, one sequence of 4096 tokens to 1024, in place: 13 us,
+// two launches' latencies; of 32768 to 8192 42 us, of 131072 to 8192 148 (eight CTAs
+// select).  48 sequences of up to 16384 tokens to 2000, into other
 // pages: 88 us; the selection is some 32 of them (one CTA a head: 384 of unequal
 // length on 152 SMs, 60 % of the issue slots), the moves 57 (72 % of the memory's
 // cycles: a kept token is four pieces, of which the two of parameters are 16 bytes).
+// Tables wider than the sequences cost: zeros for the weights past the end, and above
+// 16640 places the selection of long heads (one sequence of 4096: 14.3 us in 32768
+// places, 20.2 in 131072; 48 of 16384: 94.6 in 20032, 106 in 65536).
 #include "serve.cuh"
 
 namespace gq {

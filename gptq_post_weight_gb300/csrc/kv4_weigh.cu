@@ -31,12 +31,14 @@
 // order.
 //
 // Measured: 48 sequences of up to 16384 tokens, 8 key heads of 128 with 8 query
-// heads each, one new token: 89.5 us, 3.4 TB/s of codes and weights; instructions
-// bound it (59 % of the issue slots, half of them decoding).  2 sequences of 2048
-// queries of 32 heads, contexts to 8192: 251 us, 0.60 PFLOP/s; issue slots 63 %, shared
-// memory 51, tensor cores 33, ex2 34.  (A quarter of the exponentials as a polynomial
+// heads each, one new token: 88.5 us, 3.4 TB/s of codes and weights.  No unit is at its
+// limit (issue slots 59 %, a third of that the decoding's arithmetic; memory 34 %): the
+// warps wait for one another and for their codes.  2 sequences of 2048
+// queries of 32 heads, contexts to 8192: 250 us, 0.60 PFLOP/s; issue slots 63 %, shared
+// memory 51, tensor cores 33, ex2 34, none of them a limit either: the products run two
+// steps' sums ahead at most.  (A quarter of the exponentials as a polynomial
 // made that 287: the unit for them is not what is waited for.)  One prompt's last 64
-// queries of 32 heads of 64 over 4001 tokens: 9.9 us.
+// queries of 32 heads of 64 over 4001 tokens: 9.6 us.
 #include "serve.cuh"
 
 namespace gq {
@@ -638,7 +640,10 @@ int many_rows(int dim) { return dim == 256 ? kMostRows<256> : kMostRows<128>; }
 
 // Parts that a step's rows are cut into: the least time of the CTA with the most
 // to do, in tiles of rows (four of them at least a part; a part costs two more, for
-// its keys).  The lengths are on the device: the table's width is what is looked at.
+// its keys).  The lengths are on the device: the table's width is what is looked at, so that
+// short contexts in a wide table are cut too little.  Measured, 8 x 4 heads of 128, 2048
+// queries over 2048 tokens: 57 us in a table of 2048 places, 102 in one of 32768 and more;
+// 512 queries: 23 and 33.
 int split_of(int dim, int heads, int group, int max_q, int seqs, long long max_len) {
   const long long rows = (long long)max_q * group;
   if (rows <= many_rows(dim)) return 1;

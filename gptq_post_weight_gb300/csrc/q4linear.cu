@@ -40,11 +40,13 @@
 // x enters as f16 times a power of two a token (k_q4_scale_x): eight bits of
 // significand fit f16's eleven, down to 2^-32 of the token's largest element.  In
 // f16 itself eleven bits raised the error from 0.00021 to 0.00036; there half of the
-// columns' weights enter with what their rounding leaves (FINE: 0.00029).
-// Measured, 14336 outputs, n = 4096: one token 17.0 us (3.9 TB/s), 45 tokens of f16 55 us
-// (224 tiles on 152 SMs: two rounds of the plain product's one), 4096 tokens 658 us, 1.46
-// PFLOP/s (tensor cores 64 %: with 4096 columns a tile's end is a quarter of it), of
-// f16 1050.
+// columns' weights (0 to 127 of every 256) enter with what their rounding leaves (FINE:
+// 0.00026).
+// Measured, 14336 outputs, n = 4096, weights from memory: one token 18.9 us (3.5 TB/s), 2, 4
+// and 8 tokens 22.6, 31.5 and 34.2, 45 tokens 49 us (224 tiles on 152 SMs: two rounds of the
+// plain product's one), of f16 60, 4096 tokens 651 us, 1.48 PFLOP/s (tensor cores 64 %: with
+// 4096 columns a tile's end is a quarter of it), of f16 1045.  Two plain products and a
+// multiplication take 41 us for 45 tokens and 783 for 4096, in either type.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -168,9 +170,11 @@ __device__ __forceinline__ void finish8(const LinearArgs& a, int tok, int r, boo
   }
 }
 
-// The activation of a gate, by the approximate exponential and reciprocal (2^-22
-// of the result): with a full division an output took some forty instructions,
-// which the writing warps of k_q4_many share their issue slots for.
+// The activation of a gate, by the approximate exponential and reciprocal: each good to
+// 2^-22 of the result, and for a negative v the exponent's rounding at its own size, some
+// 1.5 |v| 2^-24 (SiLU; of the tanh form's u 6 |u| 2^-24), comes on top.  With a full
+// division an output took some forty instructions, which the writing warps of k_q4_many
+// share their issue slots for.
 __device__ __forceinline__ float gate(float v, int act) {
   if (act != GPTQ_ACT_SILU && act != GPTQ_ACT_GELU_TANH) return activate(v, act);
   const float u = act == GPTQ_ACT_SILU ? v : 1.5957691216057308f * (v + 0.044715f * v * v * v);
@@ -1612,7 +1616,13 @@ gptq_status some_tokens(const LinearArgs& a, cudaStream_t s) {
   long long rounds;
   many_tile(a.tokens, (a.rows + 2 * QROWS - 1) / (2 * QROWS), num_sms() / 2, rounds);
   // FINE decodes and multiplies half of the stages twice: 45 tokens, 14336 outputs of
-  // 4096, 44.5 -> 55 us in the first, 4096 tokens 651 -> 1050 in the other.
+  // 4096, 44.5 -> 55 us in the first (weights in the second-level cache), 4096 tokens 651 ->
+  // 1050 in the other.  Measured with it, first and other: 14336 outputs of 4096, 128 tokens
+  // 65 and 68 us, 256 97 and 94, 300 118 and 109 (the first is chosen), 512 149 and 138; 8704
+  // of 5120, 200 tokens 52 and 54, 300 90 and 85 (the first is chosen); 4096 of 4096, 300
+  // tokens 38 and 39, 700 92 and 80; 2048 of 8192, 512 tokens 54 and 62, 700 84 and 73.  With
+  // 1024 columns the other's end is shorter than said here: 1000 outputs, 256 tokens 22
+  // and 13 in either type, and the first is chosen.
   const double many = (double)rounds * ((a.n / GROUP + 7) / 8 * 4 * (FINE ? 870.0 : 540.0) + 13000.0);
   return ms.cycles * (FINE ? 1.25 : 1.0) <= many ? mid_launch<T, GATED, TO, FINE>(a, ms, s) : many_launch<T, GATED, TO, FINE>(a, s);
 }

@@ -5,7 +5,7 @@
 // cosines, some 200 instructions, are taken once for all of them, and what is
 // left a head is two 16-byte loads, 32 multiplications and two stores.  Both
 // octets of a pair are the thread's own, so that the call may write over its
-// input.  Bytes bound it: 16001 tokens of 40 heads of 128 in 58.6 us, 5.6 TB/s
+// input.  Bytes bound it: 16001 tokens of 40 heads of 128 in 58.3 us, 5.6 TB/s
 // read and written; one token 2.5 us.
 #include "rotary.cuh"
 

@@ -429,12 +429,13 @@ gptq_status gptq_q4tp_linear(int dtype, const void* X, long long ldx, int tokens
                              long long ldr, void* Y, long long ldy, uint32_t* status, void* stream);
 
 /*
- * gptq_q4tp_gated -- Y = act(X Wg^T + bg) * (X Wu^T + bu) in one launch, with
- * the gate's `inner` rows and then the up projection's in one q4tp matrix W of
- * 2 * inner rows (one Hessian group: both read X).  Sums, activation and the
+ * gptq_q4tp_gated -- Y = act(X Wg^T + bg) * (X Wu^T + bu) in one launch (bf16 above 8
+ * tokens: one more, which brings X to f16 in the workspace), with the gate's
+ * `inner` rows and then the up projection's in one q4tp matrix W of 2 * inner rows
+ * (one Hessian group: both read X).  Sums, activation and the
  * product in f32, one rounding to T.  Up to 8 tokens no weight is rounded; above
  * that to 11 bits, in either type, those of rungs below 2^-22 of their row's largest to
- * 2^-33 of that one (bf16: X is taken as f16 times a power of two a token, exact down
+ * 2^-32 of that one (bf16: X is taken as f16 times a power of two a token, exact down
  * to 2^-32 of its largest element; f16: columns 0 to 127 of every 256 to some 21
  * bits).
  *
@@ -618,7 +619,7 @@ gptq_status gptq_kv4_attention_weights(int dtype, const void* Q, long long q_ts,
  *               (and not `table` again): those of `table` itself.  A page that takes tokens is one sequence's
  *               and, unless out_table is NULL, in no row of `table` (pages that
  *               only lose tokens may be shared).  Tokens for an entry outside the
- *               pool are dropped.
+ *               pool are dropped; those of one are page 0's, as for the attention.
  *   kv_lens     in  i32 [seqs], at most table_stride * page_size counts;  out_lens
  *               out i32 [seqs]: min(kv_lens, keep).
  *   weights     in  f32 [seqs][heads][table_stride * page_size].
